@@ -23,9 +23,9 @@
  *    legacy default stream) and runs asynchronously; a call returns as soon as
  *    its kernels are enqueued.
  *  - The enqueueing calls (mdn_chunk_fwd and its variants, mdn_decode_step,
- *    mdn_prepare_inputs) may be captured into a CUDA graph once one call has
- *    run on the device (the first call looks up the device's status word with
- *    cudaGetSymbolAddress); a replay reads the pointers given at capture.
+ *    mdn_prepare_inputs, and the state-space layer's operators) may be
+ *    captured into a CUDA graph once one call has run on the device (the first
+ *    call looks up the device's status word with cudaGetSymbolAddress); a replay reads the pointers given at capture.
  *    mdn_get_device_status synchronises and must not be captured.
  *  - Gates and states are fp32.  q, k, v, o share one element type `dtype`.
  *    Accumulation is fp32.  Inputs are never modified (except the in-place
@@ -465,6 +465,212 @@ mdn_status mdn_decode_step(const void *q, const void *k, const void *v,
                            const float *eta, const float *beta, float *S,
                            float *M, void *o, int N, int H, int dk, int dv,
                            mdn_dtype dtype, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The selective state-space layer's operators: the short causal convolution,
+ * the selective scan, and the norms around a block.  Inputs marked "rows" may
+ * be slices of a wider array: their innermost dimension is contiguous and
+ * consecutive tokens lie ld_* elements apart (ld_* at least the row's width);
+ * everything else is dense.  Tensors need only their element's alignment;
+ * rows on 16-byte boundaries move in wider packets.  Outputs overlap nothing
+ * else unless stated.  Malformed cu_seqlens are reported as for
+ * mdn_chunk_fwd (status word, every sequence treated as empty: no token's
+ * outputs are written, final states receive the initial ones, the gradients
+ * of parameters are zero).  The calls are deterministic: same inputs, same
+ * bits.
+ * ---------------------------------------------------------------------- */
+
+/* What follows the short convolution's sum. */
+typedef enum mdn_conv_act {
+    MDN_CONV_NONE = 0,
+    MDN_CONV_SILU = 1
+} mdn_conv_act;
+
+/*
+ * mdn_short_conv_fwd — causal depthwise convolution along the tokens:
+ *   pre_t = bias + sum_{j<width} w[:, j] x_{t - (width - 1 - j)}
+ *   y_t   = act(pre_t)
+ * where tokens before a sequence's first are its initial state (older
+ * tokens first) or zero.
+ *
+ * Layout: x rows [B * T, D] (dtype, ld_x); w [D, width] fp32, width 2..4;
+ *   bias [D] fp32 or NULL; state0, state_T [n_seq, width - 1, D] (dtype),
+ *   NULL for zero / to skip; y [B * T, D] (dtype).  cu_seqlens, n_seq, B, T
+ *   as mdn_chunk_fwd.  state_T holds the sequence's last width - 1 inputs (a
+ *   shorter sequence keeps the newest of its initial state); it must not be
+ *   state0.
+ * Errors: MDN_ERR_INVALID_ARG (missing or misaligned pointer, bad size or
+ *   row stride, an output that aliases), MDN_ERR_UNSUPPORTED (width, device),
+ *   MDN_ERR_CUDA.
+ */
+mdn_status mdn_short_conv_fwd(const void *x, const float *w, const float *bias,
+                              const void *state0, void *y, void *state_T,
+                              const int32_t *cu_seqlens, int n_seq, int B, int T,
+                              int D, int width, mdn_conv_act act, int64_t ld_x,
+                              mdn_dtype dtype, void *stream);
+
+/* Bytes of device workspace mdn_short_conv_bwd needs (0 for invalid sizes). */
+size_t mdn_short_conv_bwd_workspace_size(int T_total, int D, int width, mdn_dtype dtype);
+
+/*
+ * mdn_short_conv_bwd — gradient of mdn_short_conv_fwd from its inputs:
+ *   dpre = dy act'(pre),  dx_t = sum_j w[:, j] dpre_{t + (width - 1 - j)},
+ *   dw[:, j] = sum_t dpre_t x_{t - (width - 1 - j)},  dbias = sum_t dpre_t,
+ * and dstate0 the same sum for the tokens before the first.
+ *
+ * Arguments as the forward, plus dy rows [B * T, D] (ld_dy), dstate_T
+ *   [n_seq, width - 1, D] (dtype, the adjoint of state_T) or NULL for zero;
+ *   dx [B * T, D] (dtype); dw [D, width], dbias [D] fp32; dstate0 (dtype) or
+ *   NULL to skip.  dbias NULL to skip.  workspace 256-byte aligned.
+ */
+mdn_status mdn_short_conv_bwd(const void *x, const float *w, const float *bias,
+                              const void *state0, const void *dy, const void *dstate_T,
+                              void *dx, float *dw, float *dbias, void *dstate0,
+                              const int32_t *cu_seqlens, int n_seq, int B, int T,
+                              int D, int width, mdn_conv_act act, int64_t ld_x,
+                              int64_t ld_dy, mdn_dtype dtype, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/*
+ * mdn_short_conv_step — the convolution of one new token for each of N
+ * sequences: x rows [N, D] (ld_x), y [N, D]; state [N, width - 1, D] holds the
+ * tokens before it and state_out receives it shifted by one (state_out may be
+ * state: in place).
+ */
+mdn_status mdn_short_conv_step(const void *x, const float *w, const float *bias,
+                               const void *state, void *state_out, void *y, int N,
+                               int D, int width, mdn_conv_act act, int64_t ld_x,
+                               mdn_dtype dtype, void *stream);
+
+/* Tokens between two saved states of mdn_ssm_scan_fwd. */
+#define MDN_SSM_CHUNK 32
+
+/* Slots of the saved states: B * ceil(T / 32), or packed floor(B * T / 32) +
+ * n_seq (an upper bound).  0 for negative sizes. */
+size_t mdn_ssm_state_slots(int n_seq, int B, int T, int packed);
+
+/* Bytes of device workspace mdn_ssm_scan_fwd / mdn_ssm_scan_bwd need (a
+ * multiple of 256; 0 for invalid sizes).  T_total = B * T. */
+size_t mdn_ssm_scan_fwd_workspace_size(int n_seq, int T_total, int D, int G, int N,
+                                       mdn_dtype dtype);
+size_t mdn_ssm_scan_bwd_workspace_size(int n_seq, int T_total, int D, int G, int N,
+                                       mdn_dtype dtype);
+
+/*
+ * mdn_ssm_scan_fwd — the selective scan over whole sequences.  Per channel d
+ * (of group g = d / (D / G)) and state n:
+ *   delta_t = dt_t + dt_bias, or softplus of that
+ *   h_t[n]  = exp(delta_t A[d, n]) h_{t-1}[n] + delta_t u_t B_t[g, n]
+ *   y_t     = (sum_n C_t[g, n] h_t[n] + D_skip u_t) silu(z_t)
+ *
+ * Layout: u, dt, z rows [B * T, D] (dtype; ld_u, ld_dt, ld_z); Bm, Cm rows
+ *   [B * T, G * N] (dtype; ld_B, ld_C); A [D, N], D_skip [D], dt_bias [D]
+ *   fp32; h0, h_T [n_seq, D, N] fp32; y [B * T, D] (dtype).  z, D_skip,
+ *   dt_bias, h0 may be NULL (no gate, zero); h_T NULL to skip it; it may be
+ *   h0.  N in 1..128, G divides D.  cu_seqlens, n_seq, B, T as mdn_chunk_fwd.
+ *   h_chunks: NULL, or [mdn_ssm_state_slots(...), D, N] fp32, 16-byte
+ *   aligned: receives the state before every 32nd token of each sequence
+ *   (chunk c of sequence s at slot s * ceil(T / 32) + c, or packed at
+ *   sum_{s' < s} ceil(L_s' / 32) + c), which the gradient starts from.
+ *   softplus: nonzero to apply it.
+ * States and sums are fp32; a decay exp(delta A) below 2^-126, the smallest
+ * normal fp32 number, is taken as zero.  A is expected to be at most zero; larger values
+ * are computed as written and may overflow.
+ * Errors: as mdn_short_conv_fwd; MDN_ERR_UNSUPPORTED for N above 128.
+ */
+mdn_status mdn_ssm_scan_fwd(const void *u, const void *dt, const float *A,
+                            const void *Bm, const void *Cm, const float *D_skip,
+                            const void *z, const float *dt_bias, const float *h0,
+                            void *y, float *h_T, float *h_chunks,
+                            const int32_t *cu_seqlens, int n_seq, int B, int T,
+                            int D, int G, int N, int softplus, int64_t ld_u,
+                            int64_t ld_dt, int64_t ld_B, int64_t ld_C, int64_t ld_z,
+                            mdn_dtype dtype, void *workspace, size_t workspace_bytes,
+                            void *stream);
+
+/*
+ * mdn_ssm_scan_bwd — gradient of mdn_ssm_scan_fwd from its inputs, its saved
+ * states h_chunks, the adjoint dy rows [B * T, D] (ld_dy) of y and dh_T
+ * ([n_seq, D, N] fp32 or NULL) of the final states.
+ *   du, ddt, dz [B * T, D], dB, dC [B * T, G, N] (dtype); dA [D, N],
+ *   dD_skip [D], ddt_bias [D], dh0 [n_seq, D, N] fp32.  dz is required with
+ *   z; dD_skip, ddt_bias and dh0 may be NULL to skip them.
+ * Groups' gradients are summed over their channels, parameters' over all
+ * tokens, in fp32 and in a fixed order.
+ */
+mdn_status mdn_ssm_scan_bwd(const void *u, const void *dt, const float *A,
+                            const void *Bm, const void *Cm, const float *D_skip,
+                            const void *z, const float *dt_bias, const float *h_chunks,
+                            const void *dy, const float *dh_T, void *du, void *ddt,
+                            float *dA, void *dB, void *dC, float *dD_skip, void *dz,
+                            float *ddt_bias, float *dh0, const int32_t *cu_seqlens,
+                            int n_seq, int B, int T, int D, int G, int N, int softplus,
+                            int64_t ld_u, int64_t ld_dt, int64_t ld_B, int64_t ld_C,
+                            int64_t ld_z, int64_t ld_dy, mdn_dtype dtype,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * mdn_ssm_scan_step — one token for each of n sequences: u, dt, z rows [n, D],
+ * Bm, Cm rows [n, G * N], y [n, D]; h [n, D, N] fp32 is the state before the
+ * token and h_out receives the state after it (h_out may be h: in place).
+ */
+mdn_status mdn_ssm_scan_step(const void *u, const void *dt, const float *A,
+                             const void *Bm, const void *Cm, const float *D_skip,
+                             const void *z, const float *dt_bias, const float *h,
+                             float *h_out, void *y, int n, int D, int G, int N,
+                             int softplus, int64_t ld_u, int64_t ld_dt, int64_t ld_B,
+                             int64_t ld_C, int64_t ld_z, mdn_dtype dtype, void *stream);
+
+/* The gate of mdn_norm_residual_fwd. */
+typedef enum mdn_gate_act {
+    MDN_GATE_SIGMOID = 0,
+    MDN_GATE_SILU = 1
+} mdn_gate_act;
+
+/*
+ * mdn_norm_residual_fwd — the end of one block and the start of the next in
+ * one pass over the rows: with y the block's output and x the residual,
+ *   r1    = (mean(y^2) + eps)^(-1/2)
+ *   b     = y r1 w_post act(gate)
+ *   x_out = x + scale b
+ *   r2    = (mean(x_out^2) + eps)^(-1/2)
+ *   h     = x_out r2 w_pre
+ * w_post NULL: no norm of y (r1 = 1).  gate NULL: no gate.  scale NULL: 1.
+ * w_pre NULL: no h (and h may be NULL).  h is taken from x_out before its
+ * rounding to dtype.
+ *
+ * Layout: y, x, gate rows [rows, D] (dtype; ld_y, ld_x, ld_gate); w_post,
+ *   w_pre, scale [D] fp32; x_out, h [rows, D] (dtype); stats [rows, 2] fp32
+ *   (r1, r2; 8-byte aligned) or NULL to skip.  x_out may be x when ld_x = D.
+ *   D at most 16384.
+ */
+mdn_status mdn_norm_residual_fwd(const void *y, const void *x, const void *gate,
+                                 const float *w_post, const float *w_pre,
+                                 const float *scale, void *x_out, void *h,
+                                 float *stats, int rows, int D, mdn_gate_act gate_act,
+                                 float eps, int64_t ld_y, int64_t ld_x,
+                                 int64_t ld_gate, mdn_dtype dtype, void *stream);
+
+/* Bytes of device workspace mdn_norm_residual_bwd needs (0 for invalid sizes). */
+size_t mdn_norm_residual_bwd_workspace_size(int rows, int D, mdn_dtype dtype);
+
+/*
+ * mdn_norm_residual_bwd — gradient of mdn_norm_residual_fwd from its inputs,
+ * its stats and the adjoints dx_out, dh (rows [rows, D]; dh required with
+ * w_pre): dy, dx, dgate [rows, D] (dtype), dw_post, dw_pre, dscale [D] fp32.
+ * dgate is required with gate, each parameter's gradient with the parameter.
+ * dx may be dx_out when ld_dx_out = D.
+ */
+mdn_status mdn_norm_residual_bwd(const void *y, const void *x, const void *gate,
+                                 const float *w_post, const float *w_pre,
+                                 const float *scale, const float *stats,
+                                 const void *dx_out, const void *dh, void *dy,
+                                 void *dx, void *dgate, float *dw_post,
+                                 float *dw_pre, float *dscale, int rows, int D,
+                                 mdn_gate_act gate_act, int64_t ld_y, int64_t ld_x,
+                                 int64_t ld_gate, int64_t ld_dx_out, int64_t ld_dh,
+                                 mdn_dtype dtype, void *workspace,
+                                 size_t workspace_bytes, void *stream);
 
 /*
  * Synchronises `stream`, then reads and clears the device status word of the

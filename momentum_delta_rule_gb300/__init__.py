@@ -20,6 +20,10 @@ Entry points (same names as the C ABI):
   workspace_size(n_seq, T_total, H, D, dtype)
   device_status(stream=None), wait_selftest(limit_us), abi_version(),
   status_string(code)
+
+The state-space layer's operators (``momentum_delta_rule_gb300.ssm``, under
+the same names here): short_conv_fwd / _bwd / _step, ssm_scan_fwd / _bwd /
+_step, ssm_state_slots, norm_residual_fwd / _bwd.
 """
 import ctypes
 import os
@@ -29,7 +33,9 @@ import torch
 __all__ = ["chunk_fwd", "chunk_fwd_kernel_count", "chunk_bwd", "block_fwd", "chunk_bwd_workspace_size", "chunk_state_slots", "decode_step", "prepare_inputs", "workspace_size",
            "device_status", "wait_selftest",
            "abi_version", "status_string", "MdnError", "lib", "LIB_PATH",
-           "EXPORTED_SYMBOLS"]
+           "EXPORTED_SYMBOLS",
+           "short_conv_fwd", "short_conv_bwd", "short_conv_step", "ssm_scan_fwd", "ssm_scan_bwd",
+           "ssm_scan_step", "ssm_state_slots", "norm_residual_fwd", "norm_residual_bwd"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmdn.so")
@@ -51,7 +57,13 @@ EXPORTED_SYMBOLS = ["mdn_abi_version", "mdn_status_string",
                     "mdn_decode_step", "mdn_get_device_status",
                     "mdn_wait_selftest", "mdn_chunk_bwd_workspace_size",
                     "mdn_chunk_bwd", "mdn_block_fwd_workspace_size", "mdn_block_fwd",
-                    "mdn_chunk_fwd_kernel_count"]
+                    "mdn_chunk_fwd_kernel_count",
+                    "mdn_short_conv_fwd", "mdn_short_conv_bwd_workspace_size",
+                    "mdn_short_conv_bwd", "mdn_short_conv_step", "mdn_ssm_state_slots",
+                    "mdn_ssm_scan_fwd_workspace_size", "mdn_ssm_scan_bwd_workspace_size",
+                    "mdn_ssm_scan_fwd", "mdn_ssm_scan_bwd", "mdn_ssm_scan_step",
+                    "mdn_norm_residual_fwd", "mdn_norm_residual_bwd_workspace_size",
+                    "mdn_norm_residual_bwd"]
 MDN_PATH_CUDA_CORE = 0
 MDN_PATH_TENSOR_CORE = 1
 
@@ -122,6 +134,7 @@ def lib():
     L.mdn_chunk_bwd_workspace_size.argtypes = [c_int] * 6
     L.mdn_chunk_bwd.restype = c_int
     L.mdn_chunk_bwd.argtypes = [vp] * 23 + [c_int] * 8 + [vp, c_size, vp]
+    ssm.declare(L)
     _LIB = L
     return L
 
@@ -529,3 +542,8 @@ def device_status(stream=None, device=None):
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
     with torch.cuda.device(dev):
         return lib().mdn_get_device_status(_stream_handle(dev, stream))
+
+
+from . import ssm  # noqa: E402  (uses the helpers above)
+from .ssm import (norm_residual_bwd, norm_residual_fwd, short_conv_bwd, short_conv_fwd,  # noqa: E402
+                  short_conv_step, ssm_scan_bwd, ssm_scan_fwd, ssm_scan_step, ssm_state_slots)

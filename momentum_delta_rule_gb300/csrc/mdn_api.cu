@@ -86,6 +86,10 @@ long chunk_slots_bound(int n_seq, int T_total) {
 
 }  // namespace
 
+namespace mdn {
+mdn_status current_device_status(int **status) { return current_device(status); }
+}  // namespace mdn
+
 extern "C" {
 
 int mdn_abi_version(void) { return MDN_ABI_VERSION; }

@@ -15,6 +15,8 @@ Contents
                rebuilt from the saved residuals), for the backward pass
   chunkwise_backward  fp64 gradient of the chunkwise form (per-chunk dense
                products, state adjoints carried backwards across chunks)
+  ssm          fp64 state-space layer operators (short convolution, selective
+               scan, norms around a block) and their gradients
   build        compiles the C oracle with gcc (building the checker is not
                using it)
 
