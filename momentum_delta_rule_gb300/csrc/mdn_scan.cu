@@ -4,6 +4,8 @@
 //   delta_t = softplus(dt_t + dt_bias);   a_t[n] = exp(delta_t A[n])
 //   h_t[n]  = a_t[n] h_{t-1}[n] + delta_t u_t B_t[n]
 //   y_t     = (sum_n C_t[n] h_t[n] + D_skip u_t) silu(z_t)
+#include <algorithm>
+
 #include "mdn_scan.cuh"
 
 namespace mdn {
@@ -12,234 +14,393 @@ namespace {
 
 // ------------------------------------------------------------------ layout
 
-// One block: checks cu_seqlens, writes the slot offsets (chunks of kTokens
-// from each sequence's own start) and the sequences longest first (for up to
-// kMaxOrdered of them).  A malformed array sets the status word and leaves
-// every sequence without slots.
+// One block: checks cu_seqlens, writes the first saved-state slot of each
+// sequence (chunks of kTokens from its own start) and the tables of items,
+// sequences longest first (for up to kMaxOrdered of them).  A malformed array
+// sets the status word and leaves one empty item per sequence.
 constexpr int kMaxOrdered = 1024;
 
+__device__ __forceinline__ int block_scan(int mine, int32_t *part, int &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) part[warp] = incl;
+    __syncthreads();
+    int before = 0;
+    total = 0;
+    for (int w = 0; w < 32; ++w) {
+        if (w < warp) before += part[w];
+        total += part[w];
+    }
+    __syncthreads();
+    return before + incl - mine;
+}
+
 __global__ void __launch_bounds__(1024)
-layout_kernel(const int32_t *cu, int n_seq, int T_total, int32_t *off, int32_t *order, int *status) {
+layout_kernel(const int32_t *cu, int n_seq, int T_total, int cut, int trigger, int32_t *off,
+              int32_t *order, Item *item, Item *pre_item, int32_t *count, int *status) {
     __shared__ int32_t part[32];
     if (!cu_well_formed(cu, n_seq, T_total)) {
         for (int s = threadIdx.x; s <= n_seq; s += blockDim.x) {
             off[s] = 0;
-            if (s < n_seq) order[s] = s;
+            if (s < n_seq) item[s] = Item{s, 0, 0, 0};
         }
-        if (threadIdx.x == 0) atomicExch(status, (int)MDN_ERR_INVALID_ARG);
+        if (threadIdx.x == 0) {
+            count[0] = n_seq;
+            count[1] = 0;
+            atomicExch(status, (int)MDN_ERR_INVALID_ARG);
+        }
         return;
     }
-    for (int s = threadIdx.x; s < n_seq; s += blockDim.x) {
-        int rank = s;
-        if (n_seq <= kMaxOrdered) {
-            const int mine = cu[s + 1] - cu[s];
-            rank = 0;
-            for (int o = 0; o < n_seq; ++o) {
-                const int len = cu[o + 1] - cu[o];
-                rank += len > mine || (len == mine && o < s);
-            }
-        }
-        order[rank] = s;
-    }
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int32_t carry = 0;
+    int slots = 0;
     for (int base = 0; base < n_seq; base += 1024) {
         const int s = base + threadIdx.x;
-        int32_t mine = s < n_seq ? (cu[s + 1] - cu[s] + kTokens - 1) / kTokens : 0;
-        int32_t incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
+        int total;
+        const int at = block_scan(s < n_seq ? (cu[s + 1] - cu[s] + kTokens - 1) / kTokens : 0, part, total);
+        if (s < n_seq) {
+            off[s] = slots + at;
+            int rank = s;
+            if (n_seq <= kMaxOrdered) {
+                const int mine = cu[s + 1] - cu[s];
+                rank = 0;
+                for (int o = 0; o < n_seq; ++o) {
+                    const int len = cu[o + 1] - cu[o];
+                    rank += len > mine || (len == mine && o < s);
+                }
+            }
+            order[rank] = s;
         }
-        if (lane == 31) part[warp] = incl;
-        __syncthreads();
-        int32_t before = carry, total = 0;
-        for (int w = 0; w < 32; ++w) {
-            if (w < warp) before += part[w];
-            total += part[w];
-        }
-        if (s < n_seq) off[s] = before + incl - mine;
-        carry += total;
-        __syncthreads();
+        slots += total;
     }
-    if (threadIdx.x == 0) off[n_seq] = carry;
+    if (threadIdx.x == 0) off[n_seq] = slots;
+    __syncthreads();
+    int items = 0, pres = 0;
+    for (int base = 0; base < n_seq; base += 1024) {
+        const int r = base + threadIdx.x;
+        int s = 0, len = 0, segs = 0, total, pre_total;
+        if (r < n_seq) {
+            s = order[r];
+            len = cu[s + 1] - cu[s];
+            segs = segments_of(len, cut, trigger);
+        }
+        const int at = items + block_scan(segs, part, total);
+        const int pre = pres + block_scan(segs > 0 ? segs - 1 : 0, part, pre_total);
+        for (int k = 0; k < segs; ++k) {
+            const Item it{s, k * cut, segs == 1 ? len : min(cut, len - k * cut), pre};
+            item[at + k] = it;
+            if (k < segs - 1) pre_item[pre + k] = it;
+        }
+        items += total;
+        pres += pre_total;
+    }
+    if (threadIdx.x == 0) {
+        count[0] = items;
+        count[1] = pres;
+    }
 }
 
 // ----------------------------------------------------------------- forward
 
-template <typename S>
+constexpr int kStage = 16;            // tokens per stage
+constexpr int kAhead = 2;             // stages whose copies are in flight
+constexpr int kRing = kAhead + 3;     // staged, in flight, and waiting for their outputs
+
+template <typename T, typename S, int V>
 struct FwdSmem {
-    float delta[kTokens][S::CB];      // delta, later unused
-    float du[kTokens][S::CB];         // delta u
-    float y[kTokens][S::CB];
-    float B[kTokens][S::NP], C[kTokens][S::NP];
+    static constexpr int QC = S::CB / V;                                   // packets per token
+    static constexpr int PS = (kStage * QC + S::HT - 1) / S::HT;           // packets per helper
+    static constexpr int QB = S::NP / 4;
+    static constexpr int PB = (kStage * QB + S::HT - 1) / S::HT;           // of B, of C
+    static_assert(S::HT % QC == 0, "a helper keeps its columns");
+    float delta[2][kStage][S::CB];
+    float du[2][kStage][S::CB];       // delta u, then sum_n C h of the same token
+    float B[2][kStage][S::NP], C[2][kStage][S::NP];
+    // the inputs as they are, one place for each packet of each helper
+    Packet<T, V> u[kRing][PS][S::HT], dt[kRing][PS][S::HT], z[kRing][PS][S::HT];
+    Packet<T, 4> b[kRing][PB][S::HT], c[kRing][PB][S::HT];
 };
 
-// One block takes CB channels of one group through one whole sequence, in
-// stages of kTokens tokens: every thread turns its share of the stage's u and
-// dt into fp32 delta and delta u in shared memory, the warps run the
-// recurrence, and the threads that hold u finish y.
-template <typename T, typename S, int V>
-__global__ void __launch_bounds__(S::NT) scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
+// One block takes CB channels of one group through one item, in stages of
+// kStage tokens with two buffers: while the recurrence warps run a stage, the
+// helper warps finish the outputs of the stage before and turn the inputs of
+// the next into fp32 delta and delta u.  A helper copies the packets it will
+// use itself, kAhead stages early, so that only it has to wait for them.
+// PRE: the first pass over a cut segment, whose end state and sum of delta are
+// all it leaves.
+template <typename T, typename S, int V, bool PRE>
+__global__ void __launch_bounds__(S::NT + S::HT, S::NT + S::HT <= 256 ? 3 : 2)
+scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
+    using Sm = FwdSmem<T, S, V>;
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    FwdSmem<S> &sm = *reinterpret_cast<FwdSmem<S> *>(smem_raw);
-    constexpr int QC = S::CB / V;                    // column packets per token
-    constexpr int PS = (kTokens * QC + S::NT - 1) / S::NT;
+    Sm &sm = *reinterpret_cast<Sm *>(smem_raw);
     const int Dg = p.D / p.G;
     const int gtiles = tiles / p.G;
     const int tile = blockIdx.x % tiles;
-    const int seq = p.cu ? l.order[blockIdx.x / tiles] : blockIdx.x / tiles;
     const int g = tile / gtiles;
     const int c0 = (tile % gtiles) * S::CB;          // first channel, within the group
     const long d0 = (long)g * Dg + c0;
+    Item it;
     long t0, slot0;
-    int len;
-    sequence(p, l, seq, t0, len, slot0);
+    if (!find_item(p, l, blockIdx.x / tiles, PRE, it, t0, slot0)) return;
+    const int stages = (it.len + kStage - 1) / kStage;
 
+    if (threadIdx.x >= S::NT) {
+        // ---------------------------------------------------------- helpers
+        const int hid = threadIdx.x - S::NT;
+        const int row = hid / Sm::QC, col = hid % Sm::QC * V;
+        constexpr int RS = S::HT / Sm::QC;               // tokens between a helper's packets
+        const bool qlive = c0 + col < Dg;
+        const T *up = static_cast<const T *>(p.u) + t0 * p.ld_u + d0 + col;
+        const T *dp = static_cast<const T *>(p.dt) + t0 * p.ld_dt + d0 + col;
+        const T *zp = p.z ? static_cast<const T *>(p.z) + t0 * p.ld_z + d0 + col : nullptr;
+        const T *Bp = static_cast<const T *>(p.Bm) + t0 * p.ld_B + (long)g * p.N;
+        const T *Cp = static_cast<const T *>(p.Cm) + t0 * p.ld_C + (long)g * p.N;
+        T *yp = static_cast<T *>(p.y) + t0 * p.D + d0 + col;
+        float bias[V], skip[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            bias[v] = qlive && p.dt_bias ? p.dt_bias[d0 + col + v] : 0.f;
+            skip[v] = qlive && p.D_skip ? p.D_skip[d0 + col + v] : 0.f;
+        }
+        auto issue = [&](int k) {
+            const int tk = k * kStage, n = it.len - tk, r = k % kRing;
+            if (n > 0) {
+#pragma unroll
+                for (int i = 0; i < Sm::PS; ++i) {
+                    const int t = i * RS + row;
+                    if (t < n && t < kStage && qlive) {
+                        copy_packet<T, V>(&sm.u[r][i][hid], up + (long)(tk + t) * p.ld_u);
+                        copy_packet<T, V>(&sm.dt[r][i][hid], dp + (long)(tk + t) * p.ld_dt);
+                        if (!PRE && zp) copy_packet<T, V>(&sm.z[r][i][hid], zp + (long)(tk + t) * p.ld_z);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < Sm::PB; ++i) {
+                    const int j = i * S::HT + hid, t = j / Sm::QB, m = j % Sm::QB * 4;
+                    if (t >= n || t >= kStage || m >= p.N) continue;
+                    const T *bp = Bp + (long)(tk + t) * p.ld_B + m, *cp = Cp + (long)(tk + t) * p.ld_C + m;
+                    if (p.bc_wide) {
+                        copy_packet<T, 4>(&sm.b[r][i][hid], bp);
+                        if (!PRE) copy_packet<T, 4>(&sm.c[r][i][hid], cp);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            sm.b[r][i][hid].e[e] = m + e < p.N ? bp[e] : from_f32<T>(0.f);
+                            sm.c[r][i][hid].e[e] = m + e < p.N ? cp[e] : from_f32<T>(0.f);
+                        }
+                    }
+                }
+            }
+            commit_copies();
+        };
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) issue(k);
+        // round -1 only stages stage 0, round `stages` only finishes the last
+        for (int k = -1; k <= stages; ++k) {
+            issue(k + 1 + kAhead);
+            const int nb = (k + 1) & 1;                      // the next stage's buffer
+            if (!PRE && k >= 1 && qlive) {
+                const int tk = (k - 1) * kStage, n = min(kStage, it.len - tk), r = (k - 1) % kRing;
+#pragma unroll
+                for (int i = 0; i < Sm::PS; ++i) {
+                    const int t = i * RS + row;
+                    if (t >= n) break;
+                    float u[V], z[V], o[V];
+                    unpack<T, V>(sm.u[r][i][hid], u);
+                    if (zp) unpack<T, V>(sm.z[r][i][hid], z);
+                    const auto sum = load_packet<float, V>(&sm.du[nb][t][col]);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        o[v] = fmaf(skip[v], u[v], sum.e[v]);
+                        if (zp) o[v] *= z[v] * sigmoid_f(z[v]);
+                    }
+                    store_packet<T, V>(yp + (long)(tk + t) * p.D, pack<T, V>(o));
+                }
+            }
+            wait_copies<kAhead>();
+            if (k + 1 < stages) {
+                const int n = min(kStage, it.len - (k + 1) * kStage), r = (k + 1) % kRing;
+                const int n_zero = (n + S::TB - 1) / S::TB * S::TB;     // zeros up to a whole batch
+#pragma unroll
+                for (int i = 0; i < Sm::PS; ++i) {
+                    const int t = i * RS + row;
+                    if (t >= n_zero) break;
+                    float u[V], d[V];
+#pragma unroll
+                    for (int v = 0; v < V; ++v) u[v] = d[v] = 0.f;
+                    if (qlive && t < n) {
+                        unpack<T, V>(sm.u[r][i][hid], u);
+                        unpack<T, V>(sm.dt[r][i][hid], d);
+#pragma unroll
+                        for (int v = 0; v < V; ++v) {
+                            d[v] += bias[v];
+                            if (p.softplus) d[v] = softplus_rel(d[v]);
+                            u[v] *= d[v];
+                        }
+                    }
+                    store_packet<float, V>(&sm.delta[nb][t][col], pack<float, V>(d));
+                    store_packet<float, V>(&sm.du[nb][t][col], pack<float, V>(u));
+                }
+#pragma unroll
+                for (int i = 0; i < Sm::PB; ++i) {
+                    const int j = i * S::HT + hid, t = j / Sm::QB, m = j % Sm::QB * 4;
+                    if (t >= n_zero) break;
+                    const bool in = t < n && m < p.N;
+                    float f[4] = {0.f, 0.f, 0.f, 0.f};
+                    if (in) unpack<T, 4>(sm.b[r][i][hid], f);
+                    store_packet<float, 4>(&sm.B[nb][t][m], pack<float, 4>(f));
+                    if (PRE) continue;
+                    if (in) unpack<T, 4>(sm.c[r][i][hid], f);
+                    store_packet<float, 4>(&sm.C[nb][t][m], pack<float, 4>(f));
+                }
+            }
+            if (k < stages) __syncthreads();
+        }
+        wait_copies<0>();
+        return;
+    }
+    // ------------------------------------------------------------ recurrence
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int nl = lane % S::NL;
+    const int nl = lane % S::NL, n0 = nl * kStates;
     const int cw = warp * S::WC + lane / S::NL * S::CPT;     // lane's first channel in the block
-    float a2[S::CPT][kStates], h[S::CPT][kStates];
+    float a2[S::CPT][kStates], h[S::CPT][kStates], sum[S::CPT];
+    bool live[S::CPT];
 #pragma unroll
     for (int c = 0; c < S::CPT; ++c) {
-        const bool live = c0 + cw + c < Dg && nl * kStates < p.N;
+        live[c] = c0 + cw + c < Dg && n0 < p.N;
+        sum[c] = 0.f;
 #pragma unroll
         for (int i = 0; i < kStates; ++i) a2[c][i] = h[c][i] = 0.f;
-        if (live) {
-            load_states(p.A, d0 + cw + c, nl * kStates, p.N, a2[c]);
-            if (p.h0) load_states(p.h0 + (long)seq * p.D * p.N, d0 + cw + c, nl * kStates, p.N, h[c]);
+        if (live[c]) {
+            load_states(p.A, d0 + cw + c, n0, p.N, a2[c]);
+            if (!PRE && p.h0) load_states(p.h0 + (long)it.seq * p.D * p.N, d0 + cw + c, n0, p.N, h[c]);
         }
 #pragma unroll
         for (int i = 0; i < kStates; ++i) a2[c][i] *= kLog2e;
-    }
-    // the thread's column packet of the stage
-    const int qc = threadIdx.x % QC;
-    const bool qlive = c0 + qc * V < Dg;
-    float bias[V], skip[V];
+        if (!PRE && live[c]) {
+            // the state before this segment, through those before it
+            const int before = it.tok0 / l.cut;
+#pragma unroll 4
+            for (int k = 0; k < before; ++k) {
+                float end[kStates];
+                load_states(l.pre_h + (long)(it.pre + k) * p.D * p.N, d0 + cw + c, n0, p.N, end);
+                const float s = l.pre_sum[(long)(it.pre + k) * p.D + d0 + cw + c];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        bias[v] = qlive && p.dt_bias ? p.dt_bias[d0 + qc * V + v] : 0.f;
-        skip[v] = qlive && p.D_skip ? p.D_skip[d0 + qc * V + v] : 0.f;
-    }
-    for (int tb = 0; tb < len; tb += kTokens) {
-        const int n = min(kTokens, len - tb);
-        Packet<T, V> u[PS];
-#pragma unroll
-        for (int i = 0; i < PS; ++i) {
-            const int t = (i * S::NT + threadIdx.x) / QC;
-            if (t >= n) continue;
-            float uf[V], df[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) uf[v] = df[v] = 0.f;
-            if (qlive) {
-                const long row = t0 + tb + t, col = d0 + qc * V;
-                u[i] = load_packet<T, V>(static_cast<const T *>(p.u) + row * p.ld_u + col);
-                unpack<T, V>(u[i], uf);
-                unpack<T, V>(load_packet<T, V>(static_cast<const T *>(p.dt) + row * p.ld_dt + col), df);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    df[v] += bias[v];
-                    if (p.softplus) df[v] = softplus_rel(df[v]);
-                }
-            }
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                sm.delta[t][qc * V + v] = df[v];
-                sm.du[t][qc * V + v] = df[v] * uf[v];
+                for (int i = 0; i < kStates; ++i) h[c][i] = fmaf(ex2(s * a2[c][i]), h[c][i], end[i]);
             }
         }
-        stage_bc<T, S::NP>(p, t0 + tb, n, g, &sm.B[0][0], &sm.C[0][0]);
-        __syncthreads();
-        if (p.h_chunks) {
-            float *hc = p.h_chunks + (slot0 + tb / kTokens) * p.D * p.N;
+    }
+    __syncthreads();
+    for (int k = 0; k < stages; ++k) {
+        const int buf = k & 1;
+        const int n = min(kStage, it.len - k * kStage);
+        if (!PRE && p.h_chunks && k * kStage % kTokens == 0) {
+            float *hc = p.h_chunks + (slot0 + k * kStage / kTokens) * p.D * p.N;
 #pragma unroll
             for (int c = 0; c < S::CPT; ++c)
-                if (c0 + cw + c < Dg && nl * kStates < p.N)
-                    store_states(hc, d0 + cw + c, nl * kStates, p.N, h[c]);
+                if (live[c]) store_states(hc, d0 + cw + c, n0, p.N, h[c]);
         }
-#pragma unroll 4
-        for (int t = 0; t < n; ++t) {
-            const float4 Bv = *reinterpret_cast<const float4 *>(&sm.B[t][nl * kStates]);
-            const float4 Cv = *reinterpret_cast<const float4 *>(&sm.C[t][nl * kStates]);
-            const float bv[kStates] = {Bv.x, Bv.y, Bv.z, Bv.w};
-            const float cv[kStates] = {Cv.x, Cv.y, Cv.z, Cv.w};
-            float acc[S::CPT];
+        // tokens past n are zero and change nothing
+#pragma unroll 1
+        for (int t = 0; t < n; t += S::TB) {
+            // every input of the batch first: the sums go back into du, which
+            // would hold up loads of later tokens behind them
+            Packet<float, kStates> bv[S::TB], cv[S::TB];
+            Packet<float, S::CPT> dl[S::TB], du[S::TB];
 #pragma unroll
-            for (int c = 0; c < S::CPT; ++c) {
-                const float delta = sm.delta[t][cw + c], du = sm.du[t][cw + c];
-                acc[c] = 0.f;
-#pragma unroll
-                for (int i = 0; i < kStates; ++i) {
-                    h[c][i] = fmaf(ex2(delta * a2[c][i]), h[c][i], du * bv[i]);
-                    acc[c] = fmaf(h[c][i], cv[i], acc[c]);
-                }
-#pragma unroll
-                for (int o = S::NL / 2; o > 0; o >>= 1)
-                    acc[c] += __shfl_xor_sync(0xffffffffu, acc[c], o);
+            for (int j = 0; j < S::TB; ++j) {
+                bv[j] = load_packet<float, kStates>(&sm.B[buf][t + j][n0]);
+                if (!PRE) cv[j] = load_packet<float, kStates>(&sm.C[buf][t + j][n0]);
+                dl[j] = load_packet<float, S::CPT>(&sm.delta[buf][t + j][cw]);
+                du[j] = load_packet<float, S::CPT>(&sm.du[buf][t + j][cw]);
             }
-            if (nl == 0)
+            float acc[S::TB * S::CPT];
 #pragma unroll
-                for (int c = 0; c < S::CPT; ++c) sm.y[t][cw + c] = acc[c];
+            for (int j = 0; j < S::TB; ++j)
+#pragma unroll
+                for (int c = 0; c < S::CPT; ++c) {
+                    float y = 0.f;
+                    if (PRE) sum[c] += dl[j].e[c];
+#pragma unroll
+                    for (int i = 0; i < kStates; ++i) {
+                        h[c][i] = fmaf(ex2(dl[j].e[c] * a2[c][i]), h[c][i], du[j].e[c] * bv[j].e[i]);
+                        if (!PRE) y = fmaf(h[c][i], cv[j].e[i], y);
+                    }
+                    acc[j * S::CPT + c] = y;
+                }
+            if (!PRE) {
+                constexpr int M = S::TB * S::CPT, R = M > S::NL ? M / S::NL : 1;
+                static_assert(R <= S::CPT, "a lane's sums belong to one token");
+                reduce_lanes<S::NL, M>(acc, nl);
+                const int first = reduced_first<S::NL, M>(nl);
+                if (S::NL <= M || nl < M)
+                    store_packet<float, R>(&sm.du[buf][t + first / S::CPT][cw + first % S::CPT],
+                                           pack<float, R>(acc));
+            }
         }
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < PS; ++i) {
-            const int t = (i * S::NT + threadIdx.x) / QC;
-            if (t >= n || !qlive) continue;
-            const long row = t0 + tb + t, col = d0 + qc * V;
-            float uf[V], o[V], z[V];
-            unpack<T, V>(u[i], uf);
-            if (p.z) unpack<T, V>(load_packet<T, V>(static_cast<const T *>(p.z) + row * p.ld_z + col), z);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                o[v] = fmaf(skip[v], uf[v], sm.y[t][qc * V + v]);
-                if (p.z) o[v] *= z[v] * sigmoid_f(z[v]);
-            }
-            store_packet<T, V>(static_cast<T *>(p.y) + row * p.D + col, pack<T, V>(o));
-        }
-        // the next stage writes delta and du, which every warp has read, and y
-        // only after the barrier that follows that
     }
-    if (p.h_T)
+    float *out = PRE ? l.pre_h + (long)(it.pre + it.tok0 / l.cut) * p.D * p.N
+                     : p.h_T + (long)it.seq * p.D * p.N;
+    // only the item that ends the sequence knows its final state
+    const int seq_len = p.cu ? p.cu[it.seq + 1] - p.cu[it.seq] : p.T;
+    if (PRE || (p.h_T && (it.len == 0 || it.tok0 + it.len == seq_len)))
 #pragma unroll
         for (int c = 0; c < S::CPT; ++c)
-            if (c0 + cw + c < Dg && nl * kStates < p.N)
-                store_states(p.h_T + (long)seq * p.D * p.N, d0 + cw + c, nl * kStates, p.N, h[c]);
+            if (live[c]) store_states(out, d0 + cw + c, n0, p.N, h[c]);
+    if (PRE && nl == 0)
+#pragma unroll
+        for (int c = 0; c < S::CPT; ++c)
+            if (c0 + cw + c < Dg)
+                l.pre_sum[(long)(it.pre + it.tok0 / l.cut) * p.D + d0 + cw + c] = sum[c];
 }
 
 template <typename T, typename S, int V>
 cudaError_t fwd_t(const ScanProblem &p, const Layout &l, cudaStream_t st) {
     const int Dg = p.D / p.G;
     const long tiles = (long)p.G * ((Dg + S::CB - 1) / S::CB);
-    const long blocks = tiles * p.n_seq;
-    if (blocks > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-    auto k = scan_fwd_kernel<T, S, V>;
-    cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           (int)sizeof(FwdSmem<S>));
-    if (err != cudaSuccess) return err;
-    k<<<(unsigned)blocks, S::NT, sizeof(FwdSmem<S>), st>>>(p, l, (int)tiles);
+    if (tiles * l.items > 0x7fffffffL) return cudaErrorInvalidConfiguration;
+    constexpr int bytes = (int)sizeof(FwdSmem<T, S, V>);
+    auto main = scan_fwd_kernel<T, S, V, false>;
+    auto pre = scan_fwd_kernel<T, S, V, true>;
+    if (bytes > 48 * 1024) {
+        cudaError_t err = cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (err == cudaSuccess)
+            err = cudaFuncSetAttribute(pre, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (err != cudaSuccess) return err;
+    }
+    if (l.pres > 0) {
+        pre<<<(unsigned)(tiles * l.pres), S::NT + S::HT, bytes, st>>>(p, l, (int)tiles);
+        const cudaError_t err = cudaGetLastError();
+        if (err != cudaSuccess) return err;
+    }
+    main<<<(unsigned)(tiles * l.items), S::NT + S::HT, bytes, st>>>(p, l, (int)tiles);
     return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t fwd_dispatch(const ScanProblem &p, const Layout &l, cudaStream_t st) {
-    constexpr int V = 4;
-    const int bytes = V * (int)sizeof(T);
-    const bool wide = (p.D / p.G) % V == 0 && rows_aligned(p.u, p.ld_u, sizeof(T), bytes) &&
-                      rows_aligned(p.dt, p.ld_dt, sizeof(T), bytes) &&
-                      rows_aligned(p.z, p.ld_z, sizeof(T), bytes) &&
-                      rows_aligned(p.y, p.D, sizeof(T), bytes);
-#define MDN_SCAN_CASE(NL)                                       \
-    case NL:                                                    \
-        return wide ? fwd_t<T, Shape<NL, 2>, V>(p, l, st)       \
-                    : fwd_t<T, Shape<NL, 2>, 1>(p, l, st);
+    // 16-byte packets where every row starts on a 16-byte boundary, single
+    // elements otherwise
+    constexpr int V = 16 / (int)sizeof(T);
+    const bool wide = (p.D / p.G) % V == 0 && rows_aligned(p.u, p.ld_u, sizeof(T), 16) &&
+                      rows_aligned(p.dt, p.ld_dt, sizeof(T), 16) &&
+                      rows_aligned(p.z, p.ld_z, sizeof(T), 16) &&
+                      rows_aligned(p.y, p.D, sizeof(T), 16);
+#define MDN_SCAN_CASE(NL, CPT, NW, HW)                                \
+    case NL:                                                          \
+        return wide ? fwd_t<T, Shape<NL, CPT, NW, HW>, V>(p, l, st)   \
+                    : fwd_t<T, Shape<NL, CPT, NW, HW>, 1>(p, l, st);
     switch (lanes_of_states(p.N)) {
-        MDN_SCAN_CASE(2)
-        MDN_SCAN_CASE(4)
-        MDN_SCAN_CASE(8)
-        MDN_SCAN_CASE(16)
-        MDN_SCAN_CASE(32)
+        MDN_SCAN_CASE(2, 2, 2, 4)
+        MDN_SCAN_CASE(4, 2, 4, 4)
+        MDN_SCAN_CASE(8, 2, 8, 4)
+        MDN_SCAN_CASE(16, 4, 8, 4)
+        MDN_SCAN_CASE(32, 4, 8, 4)
     }
 #undef MDN_SCAN_CASE
     return cudaErrorInvalidValue;
@@ -319,14 +480,84 @@ __global__ void states_copy_kernel(const float *from, float *to, long n) {
 
 }  // namespace
 
-cudaError_t launch_layout(const ScanProblem &p, Layout &l, cudaStream_t st) {
-    l.slot_off = l.order = nullptr;
-    if (!p.cu) return cudaSuccess;
-    int32_t *off = reinterpret_cast<int32_t *>(p.ws);
-    int32_t *order = reinterpret_cast<int32_t *>(p.ws + layout_bytes(p.n_seq) / 2);
+// Warps of the recurrence that one item of `D` channels keeps busy, and the
+// warp schedulers of the device (152 SMs of four).  One warp alone takes a
+// token in about 1.3 times the issue time its work needs, so a sequence is
+// worth cutting, at the price of running its cut part twice, where it alone
+// would outlast twice the whole batch's work spread over the device; it is
+// then cut so that three warps meet on each scheduler.
+constexpr long kSchedulers = 152 * 4;
+
+void choose_cut(int T_total, int D, int N, int &cut, int &trigger) {
+    const long warps = std::max(1L, (long)D * lanes_of_states(N) / 64);
+    const long most = std::max(128L, 13 * T_total * warps / (10 * kSchedulers));
+    long len = std::max(64L, T_total * warps / (3 * kSchedulers));
+    len = (len + kTokens - 1) / kTokens * kTokens;
+    cut = (int)std::min<long>(len, 1 << 30);
+    trigger = (int)std::min<long>(std::max(most, len), 0x7fffffff);
+}
+
+namespace {
+
+struct LayoutBytes {
+    size_t off, order, item, pre_item, count, pre_h, pre_sum, total;
+    long items, pres;
+};
+LayoutBytes layout_plan(int n_seq, int T_total, int D, int N, int cut, int trigger, bool packed) {
+    LayoutBytes b;
+    size_t at = 0;
+    auto take = [&](size_t bytes) { const size_t o = at; at += round256(bytes); return o; };
+    // every segment but a sequence's last holds `cut` tokens
+    const long pres = T_total > trigger ? T_total / cut : 0;
+    b.pres = pres;
+    b.items = n_seq + pres;
+    const size_t n = packed ? (size_t)n_seq : 0;
+    b.off = take(n ? sizeof(int32_t) * (n + 1) : 0);
+    b.order = take(sizeof(int32_t) * n);
+    b.item = take(n ? sizeof(Item) * (size_t)b.items : 0);
+    b.pre_item = take(n ? sizeof(Item) * (size_t)pres : 0);
+    b.count = take(n ? 2 * sizeof(int32_t) : 0);
+    b.pre_h = take(sizeof(float) * (size_t)pres * D * N);
+    b.pre_sum = take(sizeof(float) * (size_t)pres * D);
+    b.total = at;
+    return b;
+}
+
+}  // namespace
+
+size_t layout_bytes(int n_seq, int T_total, int D, int N) {
+    int cut, trigger;
+    choose_cut(T_total, D, N, cut, trigger);
+    return layout_plan(n_seq, T_total, D, N, cut, trigger, true).total;
+}
+
+cudaError_t make_layout(const ScanProblem &p, Layout &l, cudaStream_t st, bool cut) {
+    choose_cut(p.T_total, p.D, p.N, l.cut, l.trigger);
+    if (!cut) l.trigger = 0x7fffffff;
+    const LayoutBytes b = layout_plan(p.n_seq, p.T_total, p.D, p.N, l.cut, l.trigger, p.cu != nullptr);
+    l.pre_h = reinterpret_cast<float *>(p.ws + b.pre_h);
+    l.pre_sum = reinterpret_cast<float *>(p.ws + b.pre_sum);
+    l.slot_off = l.count = nullptr;
+    l.item = l.pre_item = nullptr;
+    if (!p.cu) {
+        const int segs = segments_of(p.T, l.cut, l.trigger);
+        l.items = p.n_seq * segs;
+        l.pres = p.n_seq * (segs - 1);
+        return cudaSuccess;
+    }
+    l.items = (int)b.items;
+    l.pres = (int)b.pres;
+    int32_t *off = reinterpret_cast<int32_t *>(p.ws + b.off);
+    int32_t *count = reinterpret_cast<int32_t *>(p.ws + b.count);
+    Item *item = reinterpret_cast<Item *>(p.ws + b.item);
+    Item *pre_item = reinterpret_cast<Item *>(p.ws + b.pre_item);
     l.slot_off = off;
-    l.order = order;
-    layout_kernel<<<1, 1024, 0, st>>>(p.cu, p.n_seq, p.T_total, off, order, p.status);
+    l.count = count;
+    l.item = item;
+    l.pre_item = pre_item;
+    layout_kernel<<<1, 1024, 0, st>>>(p.cu, p.n_seq, p.T_total, l.cut, l.trigger, off,
+                                      reinterpret_cast<int32_t *>(p.ws + b.order), item, pre_item,
+                                      count, p.status);
     return cudaGetLastError();
 }
 
@@ -340,14 +571,14 @@ cudaError_t launch_states_copy(const float *from, float *to, long n, cudaStream_
 }  // namespace scan
 
 size_t scan_fwd_workspace(int n_seq, int T_total, int D, int G, int N, mdn_dtype dtype) {
-    return scan::layout_bytes(n_seq);
+    return scan::layout_bytes(n_seq, T_total, D, N);
 }
 
 cudaError_t launch_scan_fwd(const ScanProblem &p, cudaStream_t st) {
     if (p.n_seq == 0) return cudaSuccess;
     if (p.T_total == 0) return scan::launch_states_copy(p.h0, p.h_T, (long)p.n_seq * p.D * p.N, st);
     scan::Layout l;
-    const cudaError_t err = scan::launch_layout(p, l, st);
+    const cudaError_t err = scan::make_layout(p, l, st, true);
     if (err != cudaSuccess) return err;
     return p.dtype == MDN_BF16 ? scan::fwd_dispatch<__nv_bfloat16>(p, l, st)
                                : scan::fwd_dispatch<float>(p, l, st);

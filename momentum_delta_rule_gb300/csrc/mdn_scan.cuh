@@ -12,14 +12,18 @@ constexpr int kStates = 4;                // states a lane holds of each of its 
 // How a block covers channels and states.  A channel's (padded) states lie
 // across NL lanes, four each; the other lanes of a warp take other channels,
 // CPT neighbouring ones each.  Padded states have A = B = C = 0 and stay 0.
-template <int NL_, int CPT_>
+// NW warps run the recurrence; HW more stage their inputs and finish their
+// outputs.
+template <int NL_, int CPT_, int NW_, int HW_>
 struct Shape {
-    static constexpr int NL = NL_, CPT = CPT_;
+    static constexpr int NL = NL_, CPT = CPT_, NW = NW_, HW = HW_;
     static constexpr int NP = NL * kStates;              // padded states
     static constexpr int WC = 32 / NL * CPT;             // channels per warp
-    static constexpr int NW = NL >= 16 ? 8 : 4;          // warps per block
-    static constexpr int NT = NW * 32;
     static constexpr int CB = WC * NW;                   // channels per block
+    static constexpr int NT = NW * 32;                   // recurrence threads
+    static constexpr int HT = HW * 32;                   // helper threads
+    // tokens whose inputs are read and whose sums are exchanged together
+    static constexpr int TB = NL < 4 ? NL : 4;
 };
 
 inline int lanes_of_states(int N) {
@@ -28,33 +32,60 @@ inline int lanes_of_states(int N) {
     return nl;
 }
 
-// Device arrays that describe the work: where each sequence's saved states
-// begin, and the sequences longest first.
-struct Layout {
-    const int32_t *slot_off;      // [n_seq + 1], packed sequences only
-    const int32_t *order;         // [n_seq]
+// A stretch of one sequence's tokens that a block runs on its own: the whole
+// sequence, or one of the segments a long sequence is cut into.
+struct Item {
+    int seq, tok0, len;       // tokens tok0 .. tok0 + len of the sequence
+    int pre;                  // first slot of the sequence's cut segments
 };
-inline size_t layout_bytes(int n_seq) {
-    return 2 * round256(sizeof(int32_t) * ((size_t)n_seq + 1));
-}
-// Fills them (packed sequences; one block).
-cudaError_t launch_layout(const ScanProblem &p, Layout &l, cudaStream_t st);
+
+// The work, as the kernels see it.  Sequences longer than `trigger` tokens
+// run as segments of `cut` tokens: a first pass takes every segment but the
+// last from a zero state and leaves its end state and its sum of delta in the
+// sequence's slots; the main pass chains those (h <- exp(A sum delta) h + end)
+// up to its own segment.  Shorter sequences have one item and no first pass.
+struct Layout {
+    int cut, trigger;
+    int items, pres;                  // launch bounds; the packed arrays say how many there are
+    const int32_t *slot_off;          // packed: [n_seq + 1] first saved state of each sequence
+    const Item *item, *pre_item;      // packed: tables
+    const int32_t *count;             // packed: items, pre items
+    float *pre_h, *pre_sum;           // [slot][D][N], [slot][D]
+};
+
+// Cuts for these sizes (a function of the totals alone, so that packed
+// sequences need no lengths on the host).
+void choose_cut(int T_total, int D, int N, int &cut, int &trigger);
+size_t layout_bytes(int n_seq, int T_total, int D, int N);
+// Describes the work of p in its workspace (packed: one small kernel), with
+// long sequences cut or whole.
+cudaError_t make_layout(const ScanProblem &p, Layout &l, cudaStream_t st, bool cut);
 // to <- from, or zero where from is null.
 cudaError_t launch_states_copy(const float *from, float *to, long n, cudaStream_t st);
 
-// The tokens of sequence s and its first slot.  Malformed packed offsets left
-// every sequence without slots: it then has no tokens.
-__device__ __forceinline__ void sequence(const ScanProblem &p, const Layout &l, int s, long &t0,
-                                         int &len, long &slot0) {
-    if (!p.cu) {
-        t0 = (long)s * p.T;
-        len = p.T;
-        slot0 = (long)s * ((p.T + kTokens - 1) / kTokens);
-    } else {
-        t0 = p.cu[s];
-        slot0 = l.slot_off[s];
-        len = max(0, min(p.cu[s + 1] - (int)t0, (l.slot_off[s + 1] - (int)slot0) * kTokens));
+__host__ __device__ inline int segments_of(int len, int cut, int trigger) {
+    return len > trigger ? (len + cut - 1) / cut : 1;
+}
+
+// Item i of the main or the first pass; false past the end.
+__device__ __forceinline__ bool find_item(const ScanProblem &p, const Layout &l, int i, bool pre,
+                                          Item &it, long &t0, long &slot0) {
+    if (p.cu) {
+        if (i >= l.count[pre]) return false;
+        it = pre ? l.pre_item[i] : l.item[i];
+        t0 = (long)p.cu[it.seq] + it.tok0;
+        slot0 = (long)l.slot_off[it.seq] + it.tok0 / kTokens;
+        return true;
     }
+    const int segs = segments_of(p.T, l.cut, l.trigger) - (pre ? 1 : 0);
+    it.seq = i / segs;
+    const int k = i - it.seq * segs;
+    it.tok0 = k * l.cut;
+    it.len = segs + pre == 1 ? p.T : min(l.cut, p.T - it.tok0);
+    it.pre = it.seq * (segments_of(p.T, l.cut, l.trigger) - 1);
+    t0 = (long)it.seq * p.T + it.tok0;
+    slot0 = (long)it.seq * ((p.T + kTokens - 1) / kTokens) + it.tok0 / kTokens;
+    return it.seq < p.n_seq;
 }
 
 // A lane's A, states or gradients of one channel (four of N): [D, N] row d.
@@ -72,20 +103,66 @@ __device__ __forceinline__ void store_states(float *base, long d, int n, int N, 
         if (n + i < N) base[d * N + n + i] = f[i];
 }
 
-// Stages the B and C rows of tokens t0 .. t0 + n (group g) as fp32 [token][NP].
-template <typename T, int NP>
-__device__ __forceinline__ void stage_bc(const ScanProblem &p, long t0, int n, int g, float *Bs,
-                                         float *Cs) {
-    for (int i = threadIdx.x; i < n * NP; i += blockDim.x) {
-        const int t = i / NP, k = i % NP;
-        float b = 0.f, c = 0.f;
-        if (k < p.N) {
-            b = to_f32(static_cast<const T *>(p.Bm)[(t0 + t) * p.ld_B + (long)g * p.N + k]);
-            c = to_f32(static_cast<const T *>(p.Cm)[(t0 + t) * p.ld_C + (long)g * p.N + k]);
+// Stages B (and C) rows of tokens t0 .. t0 + n, group g, as fp32 [token][NP]
+// by the `nt` threads tid = 0 .. nt - 1; rows n .. n_zero are zeroed.
+template <typename T, int NP, bool B_, bool C_>
+__device__ __forceinline__ void stage_bc(const ScanProblem &p, long t0, int n, int n_zero, int g,
+                                         int tid, int nt, float *Bs, float *Cs) {
+    for (int i = tid; i < n_zero * (NP / 4); i += nt) {
+        const int t = i / (NP / 4), k = i % (NP / 4) * 4;
+        const T *bp = static_cast<const T *>(p.Bm) + (t0 + t) * p.ld_B + (long)g * p.N + k;
+        const T *cp = static_cast<const T *>(p.Cm) + (t0 + t) * p.ld_C + (long)g * p.N + k;
+        float b[4], c[4];
+        if (p.bc_wide && t < n && k < p.N) {
+            if (B_) unpack<T, 4>(load_packet<T, 4>(bp), b);
+            if (C_) unpack<T, 4>(load_packet<T, 4>(cp), c);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool in = t < n && k + j < p.N;
+                b[j] = B_ && in ? to_f32(bp[j]) : 0.f;
+                c[j] = C_ && in ? to_f32(cp[j]) : 0.f;
+            }
         }
-        Bs[i] = b;
-        Cs[i] = c;
+        if (B_) *reinterpret_cast<float4 *>(Bs + t * NP + k) = make_float4(b[0], b[1], b[2], b[3]);
+        if (C_) *reinterpret_cast<float4 *>(Cs + t * NP + k) = make_float4(c[0], c[1], c[2], c[3]);
     }
+}
+
+// Sums v[0 .. M) over NL lanes, halving the values a lane carries at each
+// exchange: lane nl ends with the M / NL (at least one) values from
+// reduced_first(nl) on, in v[0 ..]; where NL > M only lanes nl < M own theirs.
+template <int NL, int M>
+__device__ __forceinline__ void reduce_lanes(float *v, int nl) {
+    int left = M;
+#pragma unroll
+    for (int o = 1; o < NL; o <<= 1) {
+        if (left > 1) {
+            left /= 2;
+            const bool up = nl & o;
+#pragma unroll
+            for (int i = 0; i < M / 2; ++i) {
+                if (i < left) {
+                    const float send = up ? v[i] : v[i + left];
+                    const float keep = up ? v[i + left] : v[i];
+                    v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                }
+            }
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+        }
+    }
+}
+template <int NL, int M>
+__device__ __forceinline__ int reduced_first(int nl) {
+    int at = 0, left = M;
+#pragma unroll
+    for (int o = 1; o < NL; o <<= 1) {
+        if (left == 1) break;
+        left /= 2;
+        if (nl & o) at += left;
+    }
+    return at;
 }
 
 }  // namespace scan

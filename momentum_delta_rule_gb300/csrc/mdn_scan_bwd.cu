@@ -81,11 +81,11 @@ __global__ void __launch_bounds__(S::NT) scan_bwd_kernel(ScanProblem p, Layout l
         dD[v] = dbias[v] = 0.f;
     }
 
-    for (int k = slot; k < p.n_seq; k += w.slots) {
-        const int seq = p.cu ? l.order[k] : k;
+    for (int k = slot; k < l.items; k += w.slots) {
+        Item it;
         long t0, slot0;
-        int len;
-        sequence(p, l, seq, t0, len, slot0);
+        if (!find_item(p, l, k, false, it, t0, slot0)) break;
+        const int seq = it.seq, len = it.len;
         const long sbase = (long)seq * p.D * p.N;
         float gc[S::CPT][kStates];                   // a_{t+1} g_{t+1}
 #pragma unroll
@@ -128,9 +128,7 @@ __global__ void __launch_bounds__(S::NT) scan_bwd_kernel(ScanProblem p, Layout l
                     sm.e[t][qc * V + v] = ef[v];
                 }
             }
-            stage_bc<T, S::NP>(p, t0 + tb, n, g, &sm.B[0][0], &sm.C[0][0]);
-            for (int i = n * S::NP + threadIdx.x; i < n4 * S::NP; i += S::NT)
-                (&sm.B[0][0])[i] = (&sm.C[0][0])[i] = 0.f;
+            stage_bc<T, S::NP, true, true>(p, t0 + tb, n, n4, g, threadIdx.x, S::NT, &sm.B[0][0], &sm.C[0][0]);
             __syncthreads();
             // forward: the state before every fourth token
             {
@@ -356,11 +354,11 @@ scan_reduce_params_kernel(BwdPartials w, long dn, int D, float *dA, float *dD, f
 
 int bwd_block_channels(int N) {
     switch (lanes_of_states(N)) {
-        case 2: return Shape<2, 2>::CB;
-        case 4: return Shape<4, 2>::CB;
-        case 8: return Shape<8, 2>::CB;
-        case 16: return Shape<16, 2>::CB;
-        default: return Shape<32, 2>::CB;
+        case 2: return Shape<2, 2, 4, 0>::CB;
+        case 4: return Shape<4, 2, 4, 0>::CB;
+        case 8: return Shape<8, 2, 4, 0>::CB;
+        case 16: return Shape<16, 2, 8, 0>::CB;
+        default: return Shape<32, 2, 8, 0>::CB;
     }
 }
 
@@ -378,7 +376,7 @@ BwdPlan bwd_plan(int n_seq, int T_total, int D, int G, int N) {
     const long want = (152L * 4 + b.tiles - 1) / b.tiles;
     b.slots = (int)(n_seq < want ? n_seq : want);
     if (b.slots < 1) b.slots = 1;
-    b.base = layout_bytes(n_seq);
+    b.base = layout_bytes(n_seq, T_total, D, N);
     b.bc = round256((size_t)b.gtiles * T_total * G * 2 * N * sizeof(float));
     b.A = round256((size_t)b.slots * D * N * sizeof(float));
     b.D = round256((size_t)b.slots * D * sizeof(float));
@@ -411,17 +409,17 @@ cudaError_t bwd_dispatch(const ScanProblem &p, const Layout &l, const BwdPartial
     const void *dense[] = {p.du, p.ddt, p.dz};
     for (const void *ptr : dense) wide = wide && rows_aligned(ptr, p.D, sizeof(T), bytes);
     cudaError_t err = cudaErrorInvalidValue;
-#define MDN_SCAN_CASE(NL)                                              \
+#define MDN_SCAN_CASE(NL, NW)                                          \
     case NL:                                                           \
-        err = wide ? bwd_t<T, Shape<NL, 2>, V>(p, l, w, b, st)         \
-                   : bwd_t<T, Shape<NL, 2>, 1>(p, l, w, b, st);        \
+        err = wide ? bwd_t<T, Shape<NL, 2, NW, 0>, V>(p, l, w, b, st)     \
+                   : bwd_t<T, Shape<NL, 2, NW, 0>, 1>(p, l, w, b, st);    \
         break;
     switch (lanes_of_states(p.N)) {
-        MDN_SCAN_CASE(2)
-        MDN_SCAN_CASE(4)
-        MDN_SCAN_CASE(8)
-        MDN_SCAN_CASE(16)
-        MDN_SCAN_CASE(32)
+        MDN_SCAN_CASE(2, 4)
+        MDN_SCAN_CASE(4, 4)
+        MDN_SCAN_CASE(8, 4)
+        MDN_SCAN_CASE(16, 8)
+        MDN_SCAN_CASE(32, 8)
     }
 #undef MDN_SCAN_CASE
     if (err != cudaSuccess) return err;
@@ -457,7 +455,7 @@ cudaError_t launch_scan_bwd(const ScanProblem &p, cudaStream_t st) {
         return scan::launch_states_copy(p.dh_T, p.dh0, (long)p.n_seq * p.D * p.N, st);
     }
     scan::Layout l;
-    const cudaError_t err = scan::launch_layout(p, l, st);
+    const cudaError_t err = scan::make_layout(p, l, st, false);
     if (err != cudaSuccess) return err;
     const scan::BwdPlan b = scan::bwd_plan(p.n_seq, p.T_total, p.D, p.G, p.N);
     scan::BwdPartials w;

@@ -33,6 +33,7 @@ struct ScanProblem {
     long ld_u, ld_dt, ld_z, ld_B, ld_C, ld_dy;
     const int32_t *cu;
     int n_seq, T, T_total, D, G, N, softplus;
+    bool bc_wide;                   // four neighbouring states of B and C make one packet
     mdn_dtype dtype;
     int *status;
     unsigned char *ws;
@@ -102,6 +103,28 @@ __device__ __forceinline__ void store_packet(T *dst, const Packet<T, V> &p) {
     *reinterpret_cast<Packet<T, V> *>(dst) = p;
 }
 
+// Copies one packet from global to shared memory: asynchronously (visible to
+// this thread after wait_copies) where it is 4, 8 or 16 bytes, at once
+// otherwise.
+template <typename T, int V>
+__device__ __forceinline__ void copy_packet(Packet<T, V> *dst, const T *src) {
+    constexpr int bytes = V * (int)sizeof(T);
+    if constexpr (bytes >= 4) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(
+                         static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                     "l"(src), "n"(bytes)
+                     : "memory");
+    } else {
+        *dst = load_packet<T, V>(src);
+    }
+}
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most N of this thread's committed groups are in flight.
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -113,22 +136,20 @@ constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
 // log(1 + e^x) = max(x, 0) + log(1 + e), e = e^{-|x|} in (0, 1], with
-// log(1 + e) = 2 atanh(r), r = e / (2 + e) <= 1/3, from the series
-// 2 r (1 + r^2/3 + r^4/5 + ...): its terms up to r^14 leave out less than
-// 1e-8 of the sum, and a small e keeps its relative accuracy, which
-// log(1.f + e) would lose in rounding the sum.
+// log(1 + e) = 2 atanh(r), r = e / (2 + e) <= 1/3, so that a small e keeps its
+// relative accuracy, which log(1.f + e) would lose in rounding the sum.
+// atanh(r) / r is a polynomial in r^2 through the five Chebyshev points of
+// [0, 1/9]: within 4.1e-9 of it there.  e is 2^(-|x| log2 e) with the argument
+// rounded once: |x| 2^-24 of relative error, and e itself vanishes as |x| grows.
 __device__ __forceinline__ float softplus_rel(float x) {
-    const float e = expf(-fabsf(x));
+    const float e = ex2(-fabsf(x) * kLog2e);
     const float r = __fdividef(e, 2.f + e);
     const float q = r * r;
-    float s = fmaf(q, 1.f / 15.f, 1.f / 13.f);
-    s = fmaf(q, s, 1.f / 11.f);
-    s = fmaf(q, s, 1.f / 9.f);
-    s = fmaf(q, s, 1.f / 7.f);
-    s = fmaf(q, s, 1.f / 5.f);
-    s = fmaf(q, s, 1.f / 3.f);
-    s = fmaf(q, s, 1.f);
-    return fmaf(2.f * r, s, fmaxf(x, 0.f));
+    float s = fmaf(q, 0.14078889f, 0.13982579f);
+    s = fmaf(q, s, 0.20012298f);
+    s = fmaf(q, s, 0.33333161f);
+    s = fmaf(q, s, 1.0000000038f);
+    return fmaf(r + r, s, fmaxf(x, 0.f));
 }
 
 // The sequence that token t of a packed batch belongs to: the largest s with

@@ -61,6 +61,10 @@ mdn_status finish(cudaError_t err) {
     return MDN_ERR_CUDA;
 }
 
+bool bc_wide(const void *Bm, const void *Cm, int64_t ld_B, int64_t ld_C, int N, int el) {
+    return N % 4 == 0 && rows_aligned(Bm, ld_B, el, 4 * el) && rows_aligned(Cm, ld_C, el, 4 * el);
+}
+
 bool workspace_ok(const void *ws, size_t bytes, size_t need) {
     return need == 0 || (ws && bytes >= need && !((uintptr_t)ws & 255u));
 }
@@ -214,7 +218,9 @@ mdn_status mdn_ssm_scan_fwd(const void *u, const void *dt, const float *A, const
     p.dt_bias = dt_bias; p.h0 = h0; p.y = y; p.h_T = h_T; p.h_chunks = h_chunks;
     p.ld_u = ld_u; p.ld_dt = ld_dt; p.ld_B = ld_B; p.ld_C = ld_C; p.ld_z = ld_z;
     p.cu = some ? cu_seqlens : nullptr; p.n_seq = n_seq; p.T = T; p.T_total = (int)L;
-    p.D = D; p.G = G; p.N = N; p.softplus = softplus != 0; p.dtype = dtype; p.status = status;
+    p.D = D; p.G = G; p.N = N; p.softplus = softplus != 0;
+    p.bc_wide = bc_wide(Bm, Cm, ld_B, ld_C, N, el);
+    p.dtype = dtype; p.status = status;
     p.ws = static_cast<unsigned char *>(workspace);
     return finish(launch_scan_fwd(p, static_cast<cudaStream_t>(stream)));
 }
@@ -260,7 +266,9 @@ mdn_status mdn_ssm_scan_bwd(const void *u, const void *dt, const float *A, const
     p.ddt_bias = ddt_bias; p.dh0 = dh0;
     p.ld_u = ld_u; p.ld_dt = ld_dt; p.ld_B = ld_B; p.ld_C = ld_C; p.ld_z = ld_z; p.ld_dy = ld_dy;
     p.cu = some ? cu_seqlens : nullptr; p.n_seq = n_seq; p.T = T; p.T_total = (int)L;
-    p.D = D; p.G = G; p.N = N; p.softplus = softplus != 0; p.dtype = dtype; p.status = status;
+    p.D = D; p.G = G; p.N = N; p.softplus = softplus != 0;
+    p.bc_wide = bc_wide(Bm, Cm, ld_B, ld_C, N, el);
+    p.dtype = dtype; p.status = status;
     p.ws = static_cast<unsigned char *>(workspace);
     return finish(launch_scan_bwd(p, static_cast<cudaStream_t>(stream)));
 }
@@ -290,6 +298,7 @@ mdn_status mdn_ssm_scan_step(const void *u, const void *dt, const float *A, cons
     p.dt_bias = dt_bias; p.h0 = h; p.h_T = h_out; p.y = y;
     p.ld_u = ld_u; p.ld_dt = ld_dt; p.ld_B = ld_B; p.ld_C = ld_C; p.ld_z = ld_z;
     p.n_seq = n; p.T = 1; p.T_total = n; p.D = D; p.G = G; p.N = N; p.softplus = softplus != 0;
+    p.bc_wide = bc_wide(Bm, Cm, ld_B, ld_C, N, el);
     p.dtype = dtype; p.status = status;
     return finish(launch_scan_step(p, static_cast<cudaStream_t>(stream)));
 }
