@@ -106,7 +106,8 @@ layout_kernel(const int32_t *cu, int n_seq, int T_total, int cut, int trigger, i
 // ----------------------------------------------------------------- forward
 
 constexpr int kStage = 16;            // tokens per stage
-constexpr int kAhead = 2;             // stages whose copies are in flight
+enum class Pass { kMain, kEnds, kAdjoint };
+constexpr int kAhead = 1;             // stages whose copies are in flight
 constexpr int kRing = kAhead + 3;     // staged, in flight, and waiting for their outputs
 
 template <typename T, typename S, int V>
@@ -129,12 +130,14 @@ struct FwdSmem {
 // helper warps finish the outputs of the stage before and turn the inputs of
 // the next into fp32 delta and delta u.  A helper copies the packets it will
 // use itself, kAhead stages early, so that only it has to wait for them.
-// PRE: the first pass over a cut segment, whose end state and sum of delta are
-// all it leaves.
-template <typename T, typename S, int V, bool PRE>
+// kEnds: the first pass over a cut segment, whose end state and sum of delta are
+// all it leaves.  kAdjoint: the same for the gradient's adjoint of the state,
+// which runs through the tokens last first, r <- a_t (r + C_t e_t).
+template <typename T, typename S, int V, Pass PASS>
 __global__ void __launch_bounds__(S::NT + S::HT, S::NT + S::HT <= 256 ? 3 : 2)
 scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
     using Sm = FwdSmem<T, S, V>;
+    constexpr bool PRE = PASS != Pass::kMain, REV = PASS == Pass::kAdjoint;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Sm &sm = *reinterpret_cast<Sm *>(smem_raw);
     const int Dg = p.D / p.G;
@@ -145,7 +148,7 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
     const long d0 = (long)g * Dg + c0;
     Item it;
     long t0, slot0;
-    if (!find_item(p, l, blockIdx.x / tiles, PRE, it, t0, slot0)) return;
+    if (!find_item<PASS != Pass::kMain, REV>(p, l, blockIdx.x / tiles, it, t0, slot0)) return;
     const int stages = (it.len + kStage - 1) / kStage;
 
     if (threadIdx.x >= S::NT) {
@@ -154,10 +157,12 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
         const int row = hid / Sm::QC, col = hid % Sm::QC * V;
         constexpr int RS = S::HT / Sm::QC;               // tokens between a helper's packets
         const bool qlive = c0 + col < Dg;
-        const T *up = static_cast<const T *>(p.u) + t0 * p.ld_u + d0 + col;
+        // the adjoint has dy and C where the state has u and B
+        const long ld_u = REV ? p.ld_dy : p.ld_u, ld_B = REV ? p.ld_C : p.ld_B;
+        const T *up = static_cast<const T *>(REV ? p.dy : p.u) + t0 * ld_u + d0 + col;
         const T *dp = static_cast<const T *>(p.dt) + t0 * p.ld_dt + d0 + col;
         const T *zp = p.z ? static_cast<const T *>(p.z) + t0 * p.ld_z + d0 + col : nullptr;
-        const T *Bp = static_cast<const T *>(p.Bm) + t0 * p.ld_B + (long)g * p.N;
+        const T *Bp = static_cast<const T *>(REV ? p.Cm : p.Bm) + t0 * ld_B + (long)g * p.N;
         const T *Cp = static_cast<const T *>(p.Cm) + t0 * p.ld_C + (long)g * p.N;
         T *yp = static_cast<T *>(p.y) + t0 * p.D + d0 + col;
         float bias[V], skip[V];
@@ -167,22 +172,22 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
             skip[v] = qlive && p.D_skip ? p.D_skip[d0 + col + v] : 0.f;
         }
         auto issue = [&](int k) {
-            const int tk = k * kStage, n = it.len - tk, r = k % kRing;
-            if (n > 0) {
+            const int tk = (REV ? stages - 1 - k : k) * kStage, n = it.len - tk, r = k % kRing;
+            if (k < stages) {
 #pragma unroll
                 for (int i = 0; i < Sm::PS; ++i) {
                     const int t = i * RS + row;
                     if (t < n && t < kStage && qlive) {
-                        copy_packet<T, V>(&sm.u[r][i][hid], up + (long)(tk + t) * p.ld_u);
+                        copy_packet<T, V>(&sm.u[r][i][hid], up + (long)(tk + t) * ld_u);
                         copy_packet<T, V>(&sm.dt[r][i][hid], dp + (long)(tk + t) * p.ld_dt);
-                        if (!PRE && zp) copy_packet<T, V>(&sm.z[r][i][hid], zp + (long)(tk + t) * p.ld_z);
+                        if ((!PRE || REV) && zp) copy_packet<T, V>(&sm.z[r][i][hid], zp + (long)(tk + t) * p.ld_z);
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < Sm::PB; ++i) {
                     const int j = i * S::HT + hid, t = j / Sm::QB, m = j % Sm::QB * 4;
                     if (t >= n || t >= kStage || m >= p.N) continue;
-                    const T *bp = Bp + (long)(tk + t) * p.ld_B + m, *cp = Cp + (long)(tk + t) * p.ld_C + m;
+                    const T *bp = Bp + (long)(tk + t) * ld_B + m, *cp = Cp + (long)(tk + t) * p.ld_C + m;
                     if (p.bc_wide) {
                         copy_packet<T, 4>(&sm.b[r][i][hid], bp);
                         if (!PRE) copy_packet<T, 4>(&sm.c[r][i][hid], cp);
@@ -190,7 +195,7 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             sm.b[r][i][hid].e[e] = m + e < p.N ? bp[e] : from_f32<T>(0.f);
-                            sm.c[r][i][hid].e[e] = m + e < p.N ? cp[e] : from_f32<T>(0.f);
+                            if (!PRE) sm.c[r][i][hid].e[e] = m + e < p.N ? cp[e] : from_f32<T>(0.f);
                         }
                     }
                 }
@@ -223,7 +228,7 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
             }
             wait_copies<kAhead>();
             if (k + 1 < stages) {
-                const int n = min(kStage, it.len - (k + 1) * kStage), r = (k + 1) % kRing;
+                const int n = min(kStage, it.len - (REV ? stages - 2 - k : k + 1) * kStage), r = (k + 1) % kRing;
                 const int n_zero = (n + S::TB - 1) / S::TB * S::TB;     // zeros up to a whole batch
 #pragma unroll
                 for (int i = 0; i < Sm::PS; ++i) {
@@ -239,7 +244,13 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
                         for (int v = 0; v < V; ++v) {
                             d[v] += bias[v];
                             if (p.softplus) d[v] = softplus_rel(d[v]);
-                            u[v] *= d[v];
+                            if (!REV) u[v] *= d[v];
+                        }
+                        if (REV && zp) {
+                            float z[V];
+                            unpack<T, V>(sm.z[r][i][hid], z);
+#pragma unroll
+                            for (int v = 0; v < V; ++v) u[v] *= z[v] * sigmoid_f(z[v]);
                         }
                     }
                     store_packet<float, V>(&sm.delta[nb][t][col], pack<float, V>(d));
@@ -267,46 +278,65 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nl = lane % S::NL, n0 = nl * kStates;
     const int cw = warp * S::WC + lane / S::NL * S::CPT;     // lane's first channel in the block
-    float a2[S::CPT][kStates], h[S::CPT][kStates], sum[S::CPT];
+    // two neighbouring channels to a pair
+    Pair a2[S::CPT / 2][kStates], h[S::CPT / 2][kStates];
+    float sum[S::CPT];
     bool live[S::CPT];
+    {
+        float a[S::CPT][kStates], s0[S::CPT][kStates];
 #pragma unroll
-    for (int c = 0; c < S::CPT; ++c) {
-        live[c] = c0 + cw + c < Dg && n0 < p.N;
-        sum[c] = 0.f;
+        for (int c = 0; c < S::CPT; ++c) {
+            live[c] = c0 + cw + c < Dg && n0 < p.N;
+            sum[c] = 0.f;
 #pragma unroll
-        for (int i = 0; i < kStates; ++i) a2[c][i] = h[c][i] = 0.f;
-        if (live[c]) {
-            load_states(p.A, d0 + cw + c, n0, p.N, a2[c]);
-            if (!PRE && p.h0) load_states(p.h0 + (long)it.seq * p.D * p.N, d0 + cw + c, n0, p.N, h[c]);
-        }
+            for (int i = 0; i < kStates; ++i) a[c][i] = s0[c][i] = 0.f;
+            if (live[c]) {
+                load_states(p.A, d0 + cw + c, n0, p.N, a[c]);
+                if (!PRE && p.h0) load_states(p.h0 + (long)it.seq * p.D * p.N, d0 + cw + c, n0, p.N, s0[c]);
+            }
 #pragma unroll
-        for (int i = 0; i < kStates; ++i) a2[c][i] *= kLog2e;
-        if (!PRE && live[c]) {
-            // the state before this segment, through those before it
-            const int before = it.tok0 / l.cut;
+            for (int i = 0; i < kStates; ++i) a[c][i] *= kLog2e;
+            if (!PRE && live[c]) {
+                // the state before this segment, through those before it
+                const int before = it.tok0 / l.cut;
 #pragma unroll 4
-            for (int k = 0; k < before; ++k) {
-                float end[kStates];
-                load_states(l.pre_h + (long)(it.pre + k) * p.D * p.N, d0 + cw + c, n0, p.N, end);
-                const float s = l.pre_sum[(long)(it.pre + k) * p.D + d0 + cw + c];
+                for (int k = 0; k < before; ++k) {
+                    float end[kStates];
+                    load_states(l.pre_h + (long)(it.pre + k) * p.D * p.N, d0 + cw + c, n0, p.N, end);
+                    const float s = l.pre_sum[(long)(it.pre + k) * p.D + d0 + cw + c];
 #pragma unroll
-                for (int i = 0; i < kStates; ++i) h[c][i] = fmaf(ex2(s * a2[c][i]), h[c][i], end[i]);
+                    for (int i = 0; i < kStates; ++i) s0[c][i] = fmaf(ex2(s * a[c][i]), s0[c][i], end[i]);
+                }
             }
         }
+#pragma unroll
+        for (int c = 0; c < S::CPT; c += 2)
+#pragma unroll
+            for (int i = 0; i < kStates; ++i) {
+                a2[c / 2][i] = make_pair(a[c][i], a[c + 1][i]);
+                h[c / 2][i] = make_pair(s0[c][i], s0[c + 1][i]);
+            }
     }
+    auto store_h = [&](float *base) {
+#pragma unroll
+        for (int c = 0; c < S::CPT; c += 2) {
+            float x[kStates], y[kStates];
+#pragma unroll
+            for (int i = 0; i < kStates; ++i) split_pair(h[c / 2][i], x[i], y[i]);
+            if (live[c]) store_states(base, d0 + cw + c, n0, p.N, x);
+            if (live[c + 1]) store_states(base, d0 + cw + c + 1, n0, p.N, y);
+        }
+    };
     __syncthreads();
     for (int k = 0; k < stages; ++k) {
         const int buf = k & 1;
-        const int n = min(kStage, it.len - k * kStage);
-        if (!PRE && p.h_chunks && k * kStage % kTokens == 0) {
-            float *hc = p.h_chunks + (slot0 + k * kStage / kTokens) * p.D * p.N;
-#pragma unroll
-            for (int c = 0; c < S::CPT; ++c)
-                if (live[c]) store_states(hc, d0 + cw + c, n0, p.N, h[c]);
-        }
+        const int n = min(kStage, it.len - (REV ? stages - 1 - k : k) * kStage);
+        if (!PRE && p.h_chunks && k * kStage % kTokens == 0)
+            store_h(p.h_chunks + (slot0 + k * kStage / kTokens) * p.D * p.N);
         // tokens past n are zero and change nothing
 #pragma unroll 1
-        for (int t = 0; t < n; t += S::TB) {
+        for (int step = 0; step < n; step += S::TB) {
+            const int t = REV ? (n - 1) / S::TB * S::TB - step : step;
             // every input of the batch first: the sums go back into du, which
             // would hold up loads of later tokens behind them
             Packet<float, kStates> bv[S::TB], cv[S::TB];
@@ -320,18 +350,39 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
             }
             float acc[S::TB * S::CPT];
 #pragma unroll
-            for (int j = 0; j < S::TB; ++j)
+            for (int jj = 0; jj < S::TB; ++jj) {
+                const int j = REV ? S::TB - 1 - jj : jj;
 #pragma unroll
-                for (int c = 0; c < S::CPT; ++c) {
-                    float y = 0.f;
-                    if (PRE) sum[c] += dl[j].e[c];
+                for (int c = 0; c < S::CPT; c += 2) {
+                    const Pair d = make_pair(dl[j].e[c], dl[j].e[c + 1]);
+                    float y0 = 0.f, y1 = 0.f;
+                    if (PRE) {
+                        sum[c] += dl[j].e[c];
+                        sum[c + 1] += dl[j].e[c + 1];
+                    }
 #pragma unroll
                     for (int i = 0; i < kStates; ++i) {
-                        h[c][i] = fmaf(ex2(dl[j].e[c] * a2[c][i]), h[c][i], du[j].e[c] * bv[j].e[i]);
-                        if (!PRE) y = fmaf(h[c][i], cv[j].e[i], y);
+                        float e0, e1;
+                        split_pair(mul2(d, a2[c / 2][i]), e0, e1);
+                        const Pair a = make_pair(ex2(e0), ex2(e1));
+                        if (REV) {
+                            split_pair(h[c / 2][i], e0, e1);
+                            h[c / 2][i] = mul2(a, make_pair(fmaf(du[j].e[c], bv[j].e[i], e0),
+                                                            fmaf(du[j].e[c + 1], bv[j].e[i], e1)));
+                            continue;
+                        }
+                        h[c / 2][i] = fma2(a, h[c / 2][i],
+                                           make_pair(du[j].e[c] * bv[j].e[i], du[j].e[c + 1] * bv[j].e[i]));
+                        if (!PRE) {
+                            split_pair(h[c / 2][i], e0, e1);
+                            y0 = fmaf(e0, cv[j].e[i], y0);
+                            y1 = fmaf(e1, cv[j].e[i], y1);
+                        }
                     }
-                    acc[j * S::CPT + c] = y;
+                    acc[j * S::CPT + c] = y0;
+                    acc[j * S::CPT + c + 1] = y1;
                 }
+            }
             if (!PRE) {
                 constexpr int M = S::TB * S::CPT, R = M > S::NL ? M / S::NL : 1;
                 static_assert(R <= S::CPT, "a lane's sums belong to one token");
@@ -344,57 +395,57 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
         }
         __syncthreads();
     }
-    float *out = PRE ? l.pre_h + (long)(it.pre + it.tok0 / l.cut) * p.D * p.N
+    // a first pass's slot: segments 0 .. of the states, 1 .. of the adjoints
+    const long pre_slot = (long)it.pre + it.tok0 / l.cut - (REV ? 1 : 0);
+    float *out = PRE ? l.pre_h + pre_slot * p.D * p.N
                      : p.h_T + (long)it.seq * p.D * p.N;
     // only the item that ends the sequence knows its final state
     const int seq_len = p.cu ? p.cu[it.seq + 1] - p.cu[it.seq] : p.T;
-    if (PRE || (p.h_T && (it.len == 0 || it.tok0 + it.len == seq_len)))
-#pragma unroll
-        for (int c = 0; c < S::CPT; ++c)
-            if (live[c]) store_states(out, d0 + cw + c, n0, p.N, h[c]);
+    if (PRE || (p.h_T && (it.len == 0 || it.tok0 + it.len == seq_len))) store_h(out);
     if (PRE && nl == 0)
 #pragma unroll
         for (int c = 0; c < S::CPT; ++c)
             if (c0 + cw + c < Dg)
-                l.pre_sum[(long)(it.pre + it.tok0 / l.cut) * p.D + d0 + cw + c] = sum[c];
+                l.pre_sum[pre_slot * p.D + d0 + cw + c] = sum[c];
 }
 
-template <typename T, typename S, int V>
-cudaError_t fwd_t(const ScanProblem &p, const Layout &l, cudaStream_t st) {
+template <typename T, typename S, int V, Pass PASS>
+cudaError_t fwd_launch(const ScanProblem &p, const Layout &l, int blocks_per_tile, cudaStream_t st) {
+    if (blocks_per_tile == 0) return cudaSuccess;
     const int Dg = p.D / p.G;
     const long tiles = (long)p.G * ((Dg + S::CB - 1) / S::CB);
-    if (tiles * l.items > 0x7fffffffL) return cudaErrorInvalidConfiguration;
+    if (tiles * blocks_per_tile > 0x7fffffffL) return cudaErrorInvalidConfiguration;
     constexpr int bytes = (int)sizeof(FwdSmem<T, S, V>);
-    auto main = scan_fwd_kernel<T, S, V, false>;
-    auto pre = scan_fwd_kernel<T, S, V, true>;
+    auto k = scan_fwd_kernel<T, S, V, PASS>;
     if (bytes > 48 * 1024) {
-        cudaError_t err = cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (err == cudaSuccess)
-            err = cudaFuncSetAttribute(pre, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        const cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (err != cudaSuccess) return err;
     }
-    if (l.pres > 0) {
-        pre<<<(unsigned)(tiles * l.pres), S::NT + S::HT, bytes, st>>>(p, l, (int)tiles);
-        const cudaError_t err = cudaGetLastError();
-        if (err != cudaSuccess) return err;
-    }
-    main<<<(unsigned)(tiles * l.items), S::NT + S::HT, bytes, st>>>(p, l, (int)tiles);
+    k<<<(unsigned)(tiles * blocks_per_tile), S::NT + S::HT, bytes, st>>>(p, l, (int)tiles);
     return cudaGetLastError();
 }
 
+template <typename T, typename S, int V>
+cudaError_t fwd_t(const ScanProblem &p, const Layout &l, Pass pass, cudaStream_t st) {
+    if (pass == Pass::kAdjoint) return fwd_launch<T, S, V, Pass::kAdjoint>(p, l, l.pres, st);
+    const cudaError_t err = fwd_launch<T, S, V, Pass::kEnds>(p, l, l.pres, st);
+    return err != cudaSuccess ? err : fwd_launch<T, S, V, Pass::kMain>(p, l, l.items, st);
+}
+
 template <typename T>
-cudaError_t fwd_dispatch(const ScanProblem &p, const Layout &l, cudaStream_t st) {
+cudaError_t fwd_dispatch(const ScanProblem &p, const Layout &l, Pass pass, cudaStream_t st) {
     // 16-byte packets where every row starts on a 16-byte boundary, single
     // elements otherwise
     constexpr int V = 16 / (int)sizeof(T);
     const bool wide = (p.D / p.G) % V == 0 && rows_aligned(p.u, p.ld_u, sizeof(T), 16) &&
                       rows_aligned(p.dt, p.ld_dt, sizeof(T), 16) &&
                       rows_aligned(p.z, p.ld_z, sizeof(T), 16) &&
-                      rows_aligned(p.y, p.D, sizeof(T), 16);
+                      rows_aligned(p.y, p.D, sizeof(T), 16) &&
+                      rows_aligned(p.dy, p.ld_dy, sizeof(T), 16);
 #define MDN_SCAN_CASE(NL, CPT, NW, HW)                                \
     case NL:                                                          \
-        return wide ? fwd_t<T, Shape<NL, CPT, NW, HW>, V>(p, l, st)   \
-                    : fwd_t<T, Shape<NL, CPT, NW, HW>, 1>(p, l, st);
+        return wide ? fwd_t<T, Shape<NL, CPT, NW, HW>, V>(p, l, pass, st)   \
+                    : fwd_t<T, Shape<NL, CPT, NW, HW>, 1>(p, l, pass, st);
     switch (lanes_of_states(p.N)) {
         MDN_SCAN_CASE(2, 2, 2, 4)
         MDN_SCAN_CASE(4, 2, 4, 4)
@@ -531,9 +582,8 @@ size_t layout_bytes(int n_seq, int T_total, int D, int N) {
     return layout_plan(n_seq, T_total, D, N, cut, trigger, true).total;
 }
 
-cudaError_t make_layout(const ScanProblem &p, Layout &l, cudaStream_t st, bool cut) {
+cudaError_t make_layout(const ScanProblem &p, Layout &l, cudaStream_t st) {
     choose_cut(p.T_total, p.D, p.N, l.cut, l.trigger);
-    if (!cut) l.trigger = 0x7fffffff;
     const LayoutBytes b = layout_plan(p.n_seq, p.T_total, p.D, p.N, l.cut, l.trigger, p.cu != nullptr);
     l.pre_h = reinterpret_cast<float *>(p.ws + b.pre_h);
     l.pre_sum = reinterpret_cast<float *>(p.ws + b.pre_sum);
@@ -561,6 +611,11 @@ cudaError_t make_layout(const ScanProblem &p, Layout &l, cudaStream_t st, bool c
     return cudaGetLastError();
 }
 
+cudaError_t launch_adjoint_ends(const ScanProblem &p, const Layout &l, cudaStream_t st) {
+    return p.dtype == MDN_BF16 ? fwd_dispatch<__nv_bfloat16>(p, l, Pass::kAdjoint, st)
+                               : fwd_dispatch<float>(p, l, Pass::kAdjoint, st);
+}
+
 cudaError_t launch_states_copy(const float *from, float *to, long n, cudaStream_t st) {
     if (!to || n == 0 || from == to) return cudaSuccess;
     const long blocks = (n + 255) / 256;
@@ -578,10 +633,10 @@ cudaError_t launch_scan_fwd(const ScanProblem &p, cudaStream_t st) {
     if (p.n_seq == 0) return cudaSuccess;
     if (p.T_total == 0) return scan::launch_states_copy(p.h0, p.h_T, (long)p.n_seq * p.D * p.N, st);
     scan::Layout l;
-    const cudaError_t err = scan::make_layout(p, l, st, true);
+    const cudaError_t err = scan::make_layout(p, l, st);
     if (err != cudaSuccess) return err;
-    return p.dtype == MDN_BF16 ? scan::fwd_dispatch<__nv_bfloat16>(p, l, st)
-                               : scan::fwd_dispatch<float>(p, l, st);
+    return p.dtype == MDN_BF16 ? scan::fwd_dispatch<__nv_bfloat16>(p, l, scan::Pass::kMain, st)
+                               : scan::fwd_dispatch<float>(p, l, scan::Pass::kMain, st);
 }
 
 cudaError_t launch_scan_step(const ScanProblem &p, cudaStream_t st) {

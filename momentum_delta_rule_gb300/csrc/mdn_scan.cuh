@@ -57,9 +57,11 @@ struct Layout {
 // sequences need no lengths on the host).
 void choose_cut(int T_total, int D, int N, int &cut, int &trigger);
 size_t layout_bytes(int n_seq, int T_total, int D, int N);
-// Describes the work of p in its workspace (packed: one small kernel), with
-// long sequences cut or whole.
-cudaError_t make_layout(const ScanProblem &p, Layout &l, cudaStream_t st, bool cut);
+// Describes the work of p in its workspace (packed: one small kernel).
+cudaError_t make_layout(const ScanProblem &p, Layout &l, cudaStream_t st);
+// The gradient's first pass over cut segments: what each segment but the first
+// hands back to the one before it, from a zero adjoint.
+cudaError_t launch_adjoint_ends(const ScanProblem &p, const Layout &l, cudaStream_t st);
 // to <- from, or zero where from is null.
 cudaError_t launch_states_copy(const float *from, float *to, long n, cudaStream_t st);
 
@@ -67,25 +69,35 @@ __host__ __device__ inline int segments_of(int len, int cut, int trigger) {
     return len > trigger ? (len + cut - 1) / cut : 1;
 }
 
-// Item i of the main or the first pass; false past the end.
-__device__ __forceinline__ bool find_item(const ScanProblem &p, const Layout &l, int i, bool pre,
-                                          Item &it, long &t0, long &slot0) {
+// Item i of the main pass, or of a first pass (every segment but the last, or
+// of the adjoints but the first); false past the end.
+template <bool PRE, bool REV>
+__device__ __forceinline__ bool find_item(const ScanProblem &p, const Layout &l, int i, Item &it,
+                                          long &t0, long &slot0) {
+    int len = p.T;                    // of the whole sequence
     if (p.cu) {
-        if (i >= l.count[pre]) return false;
-        it = pre ? l.pre_item[i] : l.item[i];
-        t0 = (long)p.cu[it.seq] + it.tok0;
-        slot0 = (long)l.slot_off[it.seq] + it.tok0 / kTokens;
-        return true;
+        if (i >= l.count[PRE]) return false;
+        it = PRE ? l.pre_item[i] : l.item[i];
+        t0 = p.cu[it.seq];
+        slot0 = l.slot_off[it.seq];
+        if (REV) len = p.cu[it.seq + 1] - (int)t0;
+    } else {
+        const int all = segments_of(p.T, l.cut, l.trigger), segs = PRE ? all - 1 : all;
+        it.seq = i / segs;
+        if (it.seq >= p.n_seq) return false;
+        it.tok0 = (i - it.seq * segs) * l.cut;
+        it.len = all == 1 ? p.T : min(l.cut, p.T - it.tok0);
+        it.pre = it.seq * (all - 1);
+        t0 = (long)it.seq * p.T;
+        slot0 = (long)it.seq * ((p.T + kTokens - 1) / kTokens);
     }
-    const int segs = segments_of(p.T, l.cut, l.trigger) - (pre ? 1 : 0);
-    it.seq = i / segs;
-    const int k = i - it.seq * segs;
-    it.tok0 = k * l.cut;
-    it.len = segs + pre == 1 ? p.T : min(l.cut, p.T - it.tok0);
-    it.pre = it.seq * (segments_of(p.T, l.cut, l.trigger) - 1);
-    t0 = (long)it.seq * p.T + it.tok0;
-    slot0 = (long)it.seq * ((p.T + kTokens - 1) / kTokens) + it.tok0 / kTokens;
-    return it.seq < p.n_seq;
+    if (REV) {
+        it.tok0 += l.cut;
+        it.len = min(l.cut, len - it.tok0);
+    }
+    t0 += it.tok0;
+    slot0 += it.tok0 / kTokens;
+    return true;
 }
 
 // A lane's A, states or gradients of one channel (four of N): [D, N] row d.
@@ -132,7 +144,8 @@ __device__ __forceinline__ void stage_bc(const ScanProblem &p, long t0, int n, i
 // Sums v[0 .. M) over NL lanes, halving the values a lane carries at each
 // exchange: lane nl ends with the M / NL (at least one) values from
 // reduced_first(nl) on, in v[0 ..]; where NL > M only lanes nl < M own theirs.
-template <int NL, int M>
+// The lanes lie STEP apart in the warp.
+template <int NL, int M, int STEP = 1>
 __device__ __forceinline__ void reduce_lanes(float *v, int nl) {
     int left = M;
 #pragma unroll
@@ -145,11 +158,11 @@ __device__ __forceinline__ void reduce_lanes(float *v, int nl) {
                 if (i < left) {
                     const float send = up ? v[i] : v[i + left];
                     const float keep = up ? v[i + left] : v[i];
-                    v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                    v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o * STEP);
                 }
             }
         } else {
-            v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], o * STEP);
         }
     }
 }

@@ -14,6 +14,8 @@
 // saved: one pass forward keeps the state before every fourth token in shared
 // memory, then each group of four tokens, last first, is run forward again
 // with its states and decays in registers and walked back.
+#include <algorithm>
+
 #include "mdn_scan.cuh"
 
 namespace mdn {
@@ -23,30 +25,70 @@ namespace {
 constexpr int kSub = 4;                       // tokens walked back at a time
 constexpr int kSubs = kTokens / kSub;
 
-template <typename S>
+template <typename T, typename S, int V>
 struct BwdSmem {
+    static constexpr int QC = S::CB / V;                             // packets per token
+    static constexpr int PS = (kTokens * QC + S::NT - 1) / S::NT;    // packets per thread
+    static constexpr int QB = S::NP / 4;
+    static constexpr int PB = (kTokens * QB + S::NT - 1) / S::NT;    // of B, of C
+    static_assert(S::NT % QC == 0, "a thread keeps its columns");
     float delta[kTokens][S::CB];      // delta; then ddelta
     float u[kTokens][S::CB];          // u; then du
     float e[kTokens][S::CB];          // e; then y before the gate
     float B[kTokens][S::NP], C[kTokens][S::NP];
-    float4 sub[kSubs][S::CPT][S::NT];         // state before every fourth token
+    float4 sub[kSubs - 1][S::CPT][S::NT];     // state before every fourth token but the first
     float bc[2][S::NW][kSub][2][S::NP];       // the warps' dB, dC of four tokens
+    // the next chunk's inputs as they are, one place for each thread's packets
+    Packet<T, V> in_u[PS][S::NT], in_dt[PS][S::NT], in_dy[PS][S::NT], in_z[PS][S::NT];
+    Packet<T, 4> in_b[PB][S::NT], in_c[PB][S::NT];
 };
 
 struct BwdPartials {
     float *bc;        // [tile of the group][T_total][G][2][N]
     float *A;         // [slot][D][N]
     float *D, *bias;  // [slot][D]
-    int slots;        // blocks that share a tile's sequences
+    int slots;        // blocks that share a tile's items
 };
 
+// The values a lane adds up over the NL lanes of its channels: per token and
+// channel sum_n g B, sum_n A w, sum_n C h (in that order).  Lanes exchange
+// halves while the count stays whole and leave the rest in every lane.
+template <int NL, int M>
+__device__ __forceinline__ int reduce_triples(float *v, int nl) {
+    int left = M, at = 0;
+#pragma unroll
+    for (int o = 1; o < NL; o <<= 1) {
+        if (left % 6 == 0) {
+            left /= 2;
+            const bool up = nl & o;
+            if (up) at += left;
+#pragma unroll
+            for (int i = 0; i < M / 2; ++i) {
+                if (i < left) {
+                    const float send = up ? v[i] : v[i + left];
+                    const float keep = up ? v[i + left] : v[i];
+                    v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 3; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        }
+    }
+    return at / 3;                    // first (token, channel) of this lane's
+}
+
+// One block takes CB channels of one group through its items, each item's
+// chunks last first.  Channels are held two to a pair of registers.
 template <typename T, typename S, int V>
-__global__ void __launch_bounds__(S::NT) scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
+__global__ void __launch_bounds__(S::NT, S::NT <= 128 ? 3 : 1)
+scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
+    using Sm = BwdSmem<T, S, V>;
+    static_assert(S::CPT == 2, "one pair of channels a lane");
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    BwdSmem<S> &sm = *reinterpret_cast<BwdSmem<S> *>(smem_raw);
-    constexpr int QC = S::CB / V;
-    constexpr int RS = S::NT / QC;                   // token rows per pass
-    static_assert(S::NT % QC == 0, "a thread keeps its columns");
+    Sm &sm = *reinterpret_cast<Sm *>(smem_raw);
+    constexpr int RS = S::NT / Sm::QC;               // tokens between a thread's packets
+    const int tid = threadIdx.x;
     const int Dg = p.D / p.G;
     const int gtiles = tiles / p.G;
     const int tile = blockIdx.x % tiles;
@@ -55,62 +97,125 @@ __global__ void __launch_bounds__(S::NT) scan_bwd_kernel(ScanProblem p, Layout l
     const int c0 = (tile % gtiles) * S::CB;
     const long d0 = (long)g * Dg + c0;
 
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int nl = lane % S::NL;
-    const int n0 = nl * kStates;
-    const int cw = warp * S::WC + lane / S::NL * S::CPT;
-    float a2[S::CPT][kStates], dA[S::CPT][kStates], skip[S::CPT];
-    bool live[S::CPT];
+    const int lane = tid & 31, warp = tid >> 5;
+    const int nl = lane % S::NL, n0 = nl * kStates;
+    const int cw = warp * S::WC + lane / S::NL * 2;  // the lane's first channel in the block
+    const bool live0 = c0 + cw < Dg && n0 < p.N, live1 = c0 + cw + 1 < Dg && n0 < p.N;
+    const float skip0 = c0 + cw < Dg && p.D_skip ? p.D_skip[d0 + cw] : 0.f;
+    const float skip1 = c0 + cw + 1 < Dg && p.D_skip ? p.D_skip[d0 + cw + 1] : 0.f;
+    auto load_pairs = [&](const float *base, Pair *out) {
+        float x[kStates] = {0.f, 0.f, 0.f, 0.f}, y[kStates] = {0.f, 0.f, 0.f, 0.f};
+        if (live0) load_states(base, d0 + cw, n0, p.N, x);
+        if (live1) load_states(base, d0 + cw + 1, n0, p.N, y);
 #pragma unroll
-    for (int c = 0; c < S::CPT; ++c) {
-        live[c] = c0 + cw + c < Dg && n0 < p.N;
-        skip[c] = c0 + cw + c < Dg && p.D_skip ? p.D_skip[d0 + cw + c] : 0.f;
+        for (int i = 0; i < kStates; ++i) out[i] = make_pair(x[i], y[i]);
+    };
+    auto store_pairs = [&](float *base, const Pair *v) {
+        float x[kStates], y[kStates];
 #pragma unroll
-        for (int i = 0; i < kStates; ++i) a2[c][i] = dA[c][i] = 0.f;
-        if (live[c]) load_states(p.A, d0 + cw + c, n0, p.N, a2[c]);
+        for (int i = 0; i < kStates; ++i) split_pair(v[i], x[i], y[i]);
+        if (live0) store_states(base, d0 + cw, n0, p.N, x);
+        if (live1) store_states(base, d0 + cw + 1, n0, p.N, y);
+    };
+    Pair a2[kStates], dA[kStates];
+    load_pairs(p.A, a2);
 #pragma unroll
-        for (int i = 0; i < kStates; ++i) a2[c][i] *= kLog2e;
+    for (int i = 0; i < kStates; ++i) {
+        a2[i] = mul2(a2[i], make_pair(kLog2e, kLog2e));
+        dA[i] = make_pair(0.f, 0.f);
     }
-    const int qc = threadIdx.x % QC, qrow = threadIdx.x / QC;
-    const bool qlive = c0 + qc * V < Dg;
-    const long col = d0 + qc * V;
+    const int row = tid / Sm::QC, qcol = tid % Sm::QC * V;
+    const bool qlive = c0 + qcol < Dg;
+    const long col = d0 + qcol;
     float bias[V], dD[V], dbias[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         bias[v] = qlive && p.dt_bias ? p.dt_bias[col + v] : 0.f;
         dD[v] = dbias[v] = 0.f;
     }
+    // copies tokens t0 .. t0 + n, this thread's packets
+    auto issue = [&](long t0, int n) {
+#pragma unroll
+        for (int i = 0; i < Sm::PS; ++i) {
+            const int t = i * RS + row;
+            if (t >= n || !qlive) break;
+            copy_packet<T, V>(&sm.in_u[i][tid], static_cast<const T *>(p.u) + (t0 + t) * p.ld_u + col);
+            copy_packet<T, V>(&sm.in_dt[i][tid], static_cast<const T *>(p.dt) + (t0 + t) * p.ld_dt + col);
+            copy_packet<T, V>(&sm.in_dy[i][tid], static_cast<const T *>(p.dy) + (t0 + t) * p.ld_dy + col);
+            if (p.z)
+                copy_packet<T, V>(&sm.in_z[i][tid], static_cast<const T *>(p.z) + (t0 + t) * p.ld_z + col);
+        }
+#pragma unroll
+        for (int i = 0; i < Sm::PB; ++i) {
+            const int j = i * S::NT + tid, t = j / Sm::QB, m = j % Sm::QB * 4;
+            if (t >= n || m >= p.N) continue;
+            const T *bp = static_cast<const T *>(p.Bm) + (t0 + t) * p.ld_B + (long)g * p.N + m;
+            const T *cp = static_cast<const T *>(p.Cm) + (t0 + t) * p.ld_C + (long)g * p.N + m;
+            if (p.bc_wide) {
+                copy_packet<T, 4>(&sm.in_b[i][tid], bp);
+                copy_packet<T, 4>(&sm.in_c[i][tid], cp);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    sm.in_b[i][tid].e[e] = m + e < p.N ? bp[e] : from_f32<T>(0.f);
+                    sm.in_c[i][tid].e[e] = m + e < p.N ? cp[e] : from_f32<T>(0.f);
+                }
+            }
+        }
+        commit_copies();
+    };
 
     for (int k = slot; k < l.items; k += w.slots) {
         Item it;
         long t0, slot0;
-        if (!find_item(p, l, k, false, it, t0, slot0)) break;
-        const int seq = it.seq, len = it.len;
-        const long sbase = (long)seq * p.D * p.N;
-        float gc[S::CPT][kStates];                   // a_{t+1} g_{t+1}
+        if (!find_item<false, false>(p, l, k, it, t0, slot0)) break;
+        const long sbase = (long)it.seq * p.D * p.N;
+        const int seq_len = p.cu ? p.cu[it.seq + 1] - p.cu[it.seq] : p.T;
+        const int chunks = (it.len + kTokens - 1) / kTokens;
+        if (chunks > 0) issue(t0 + (chunks - 1) * kTokens, it.len - (chunks - 1) * kTokens);
+        Pair gc[kStates];                            // a_{t+1} g_{t+1}
+        if (p.dh_T) {
+            load_pairs(p.dh_T + sbase, gc);
+        } else {
 #pragma unroll
-        for (int c = 0; c < S::CPT; ++c) {
-#pragma unroll
-            for (int i = 0; i < kStates; ++i) gc[c][i] = 0.f;
-            if (live[c] && p.dh_T) load_states(p.dh_T + sbase, d0 + cw + c, n0, p.N, gc[c]);
+            for (int i = 0; i < kStates; ++i) gc[i] = make_pair(0.f, 0.f);
         }
-        for (int chunk = (len + kTokens - 1) / kTokens - 1; chunk >= 0; --chunk) {
+        // the adjoint behind this segment, through those that follow it
+        const int segs = it.len > 0 ? segments_of(seq_len, l.cut, l.trigger) : 1;
+        for (int q = segs - 1; q > it.tok0 / l.cut; --q) {
+            const long at = it.pre + q - 1;
+            Pair r[kStates];
+            load_pairs(l.pre_h + at * p.D * p.N, r);
+            const float s0 = live0 ? l.pre_sum[at * p.D + d0 + cw] : 0.f;
+            const float s1 = live1 ? l.pre_sum[at * p.D + d0 + cw + 1] : 0.f;
+#pragma unroll
+            for (int i = 0; i < kStates; ++i) {
+                float x, y;
+                split_pair(mul2(make_pair(s0, s1), a2[i]), x, y);
+                gc[i] = fma2(make_pair(ex2(x), ex2(y)), gc[i], r[i]);
+            }
+        }
+        for (int chunk = chunks - 1; chunk >= 0; --chunk) {
             const int tb = chunk * kTokens;
-            const int n = min(kTokens, len - tb);
+            const int n = min(kTokens, it.len - tb);
             const int n4 = (n + kSub - 1) / kSub * kSub;
-            // stage the chunk; tokens n .. n4 are zero and change nothing
-            for (int t = qrow; t < n4; t += RS) {
+            // this chunk's inputs to fp32 (tokens n .. n4 are zero and change
+            // nothing), then the copies of the one before it
+            wait_copies<0>();
+#pragma unroll
+            for (int i = 0; i < Sm::PS; ++i) {
+                const int t = i * RS + row;
+                if (t >= n4) break;
                 float df[V], uf[V], ef[V];
 #pragma unroll
                 for (int v = 0; v < V; ++v) df[v] = uf[v] = ef[v] = 0.f;
                 if (t < n && qlive) {
-                    const long row = t0 + tb + t;
-                    unpack<T, V>(load_packet<T, V>(static_cast<const T *>(p.u) + row * p.ld_u + col), uf);
-                    unpack<T, V>(load_packet<T, V>(static_cast<const T *>(p.dt) + row * p.ld_dt + col), df);
-                    unpack<T, V>(load_packet<T, V>(static_cast<const T *>(p.dy) + row * p.ld_dy + col), ef);
+                    unpack<T, V>(sm.in_u[i][tid], uf);
+                    unpack<T, V>(sm.in_dt[i][tid], df);
+                    unpack<T, V>(sm.in_dy[i][tid], ef);
                     if (p.z) {
                         float z[V];
-                        unpack<T, V>(load_packet<T, V>(static_cast<const T *>(p.z) + row * p.ld_z + col), z);
+                        unpack<T, V>(sm.in_z[i][tid], z);
 #pragma unroll
                         for (int v = 0; v < V; ++v) ef[v] *= z[v] * sigmoid_f(z[v]);
                     }
@@ -121,131 +226,152 @@ __global__ void __launch_bounds__(S::NT) scan_bwd_kernel(ScanProblem p, Layout l
                         dD[v] = fmaf(ef[v], uf[v], dD[v]);
                     }
                 }
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    sm.delta[t][qc * V + v] = df[v];
-                    sm.u[t][qc * V + v] = uf[v];
-                    sm.e[t][qc * V + v] = ef[v];
-                }
+                store_packet<float, V>(&sm.delta[t][qcol], pack<float, V>(df));
+                store_packet<float, V>(&sm.u[t][qcol], pack<float, V>(uf));
+                store_packet<float, V>(&sm.e[t][qcol], pack<float, V>(ef));
             }
-            stage_bc<T, S::NP, true, true>(p, t0 + tb, n, n4, g, threadIdx.x, S::NT, &sm.B[0][0], &sm.C[0][0]);
+#pragma unroll
+            for (int i = 0; i < Sm::PB; ++i) {
+                const int j = i * S::NT + tid, t = j / Sm::QB, m = j % Sm::QB * 4;
+                if (t >= n4) break;
+                float b[4] = {0.f, 0.f, 0.f, 0.f}, c[4] = {0.f, 0.f, 0.f, 0.f};
+                if (t < n && m < p.N) {
+                    unpack<T, 4>(sm.in_b[i][tid], b);
+                    unpack<T, 4>(sm.in_c[i][tid], c);
+                }
+                store_packet<float, 4>(&sm.B[t][m], pack<float, 4>(b));
+                store_packet<float, 4>(&sm.C[t][m], pack<float, 4>(c));
+            }
+            if (chunk > 0) issue(t0 + tb - kTokens, kTokens);
             __syncthreads();
+            const float *hc = p.h_chunks + (slot0 + chunk) * p.D * p.N;
             // forward: the state before every fourth token
             {
-                const float *hc = p.h_chunks + (slot0 + chunk) * p.D * p.N;
-                float h[S::CPT][kStates];
-#pragma unroll
-                for (int c = 0; c < S::CPT; ++c) {
-#pragma unroll
-                    for (int i = 0; i < kStates; ++i) h[c][i] = 0.f;
-                    if (live[c]) load_states(hc, d0 + cw + c, n0, p.N, h[c]);
-                }
-                for (int s = 0; s < n4 / kSub; ++s) {
-#pragma unroll
-                    for (int c = 0; c < S::CPT; ++c)
-                        sm.sub[s][c][threadIdx.x] = make_float4(h[c][0], h[c][1], h[c][2], h[c][3]);
-                    if (s == n4 / kSub - 1) break;
+                Pair h[kStates];
+                load_pairs(hc, h);
+#pragma unroll 1
+                for (int s = 0; s < n4 / kSub - 1; ++s) {
 #pragma unroll
                     for (int j = 0; j < kSub; ++j) {
                         const int t = s * kSub + j;
-                        const float4 Bv = *reinterpret_cast<const float4 *>(&sm.B[t][n0]);
-                        const float bv[kStates] = {Bv.x, Bv.y, Bv.z, Bv.w};
+                        const auto bv = load_packet<float, kStates>(&sm.B[t][n0]);
+                        const auto dl = load_packet<float, 2>(&sm.delta[t][cw]);
+                        const auto uv = load_packet<float, 2>(&sm.u[t][cw]);
+                        const float x0 = dl.e[0] * uv.e[0], x1 = dl.e[1] * uv.e[1];
 #pragma unroll
-                        for (int c = 0; c < S::CPT; ++c) {
-                            const float delta = sm.delta[t][cw + c];
-                            const float du = delta * sm.u[t][cw + c];
-#pragma unroll
-                            for (int i = 0; i < kStates; ++i)
-                                h[c][i] = fmaf(ex2(delta * a2[c][i]), h[c][i], du * bv[i]);
+                        for (int i = 0; i < kStates; ++i) {
+                            float e0, e1;
+                            split_pair(mul2(make_pair(dl.e[0], dl.e[1]), a2[i]), e0, e1);
+                            h[i] = fma2(make_pair(ex2(e0), ex2(e1)), h[i],
+                                        make_pair(x0 * bv.e[i], x1 * bv.e[i]));
                         }
                     }
+                    float x[kStates], y[kStates];
+#pragma unroll
+                    for (int i = 0; i < kStates; ++i) split_pair(h[i], x[i], y[i]);
+                    sm.sub[s][0][tid] = make_float4(x[0], x[1], x[2], x[3]);
+                    sm.sub[s][1][tid] = make_float4(y[0], y[1], y[2], y[3]);
                 }
             }
-            float dAc[S::CPT][kStates];              // this chunk's dA
+            Pair dAc[kStates];                       // this chunk's dA
 #pragma unroll
-            for (int c = 0; c < S::CPT; ++c)
-#pragma unroll
-                for (int i = 0; i < kStates; ++i) dAc[c][i] = 0.f;
+            for (int i = 0; i < kStates; ++i) dAc[i] = make_pair(0.f, 0.f);
+#pragma unroll 1
             for (int s = n4 / kSub - 1; s >= 0; --s) {
-                float h[kSub + 1][S::CPT][kStates], a[kSub][S::CPT][kStates];
-#pragma unroll
-                for (int c = 0; c < S::CPT; ++c) {
-                    const float4 v = sm.sub[s][c][threadIdx.x];
-                    h[0][c][0] = v.x; h[0][c][1] = v.y; h[0][c][2] = v.z; h[0][c][3] = v.w;
+                Pair h[kSub + 1][kStates], a[kSub][kStates];
+                if (s > 0) {
+                    const float4 x = sm.sub[s - 1][0][tid], y = sm.sub[s - 1][1][tid];
+                    h[0][0] = make_pair(x.x, y.x); h[0][1] = make_pair(x.y, y.y);
+                    h[0][2] = make_pair(x.z, y.z); h[0][3] = make_pair(x.w, y.w);
+                } else {
+                    load_pairs(hc, h[0]);
                 }
 #pragma unroll
                 for (int j = 0; j < kSub; ++j) {
                     const int t = s * kSub + j;
-                    const float4 Bv = *reinterpret_cast<const float4 *>(&sm.B[t][n0]);
-                    const float bv[kStates] = {Bv.x, Bv.y, Bv.z, Bv.w};
+                    const auto bv = load_packet<float, kStates>(&sm.B[t][n0]);
+                    const auto dl = load_packet<float, 2>(&sm.delta[t][cw]);
+                    const auto uv = load_packet<float, 2>(&sm.u[t][cw]);
+                    const float x0 = dl.e[0] * uv.e[0], x1 = dl.e[1] * uv.e[1];
 #pragma unroll
-                    for (int c = 0; c < S::CPT; ++c) {
-                        const float delta = sm.delta[t][cw + c];
-                        const float du = delta * sm.u[t][cw + c];
-#pragma unroll
-                        for (int i = 0; i < kStates; ++i) {
-                            a[j][c][i] = ex2(delta * a2[c][i]);
-                            h[j + 1][c][i] = fmaf(a[j][c][i], h[j][c][i], du * bv[i]);
-                        }
+                    for (int i = 0; i < kStates; ++i) {
+                        float e0, e1;
+                        split_pair(mul2(make_pair(dl.e[0], dl.e[1]), a2[i]), e0, e1);
+                        a[j][i] = make_pair(ex2(e0), ex2(e1));
+                        h[j + 1][i] = fma2(a[j][i], h[j][i], make_pair(x0 * bv.e[i], x1 * bv.e[i]));
                     }
                 }
+                float tri[kSub * 6], bc[kSub * 2 * kStates];
 #pragma unroll
                 for (int j = kSub - 1; j >= 0; --j) {
                     const int t = s * kSub + j;
-                    const float4 Bv = *reinterpret_cast<const float4 *>(&sm.B[t][n0]);
-                    const float4 Cv = *reinterpret_cast<const float4 *>(&sm.C[t][n0]);
-                    const float bv[kStates] = {Bv.x, Bv.y, Bv.z, Bv.w};
-                    const float cv[kStates] = {Cv.x, Cv.y, Cv.z, Cv.w};
-                    float dB[kStates], dC[kStates];
+                    const auto bv = load_packet<float, kStates>(&sm.B[t][n0]);
+                    const auto cv = load_packet<float, kStates>(&sm.C[t][n0]);
+                    const auto dl = load_packet<float, 2>(&sm.delta[t][cw]);
+                    const auto uv = load_packet<float, 2>(&sm.u[t][cw]);
+                    const auto ev = load_packet<float, 2>(&sm.e[t][cw]);
+                    const Pair dlp = make_pair(dl.e[0], dl.e[1]);
+                    const float x0 = dl.e[0] * uv.e[0], x1 = dl.e[1] * uv.e[1];
+                    Pair s2 = make_pair(0.f, 0.f);
+                    float s1a = 0.f, s1b = 0.f, ya = 0.f, yb = 0.f;
 #pragma unroll
-                    for (int i = 0; i < kStates; ++i) dB[i] = dC[i] = 0.f;
-#pragma unroll
-                    for (int c = 0; c < S::CPT; ++c) {
-                        const float delta = sm.delta[t][cw + c], u = sm.u[t][cw + c];
-                        const float e = sm.e[t][cw + c], du = delta * u;
-                        float s1 = 0.f, s2 = 0.f, y = 0.f;
-#pragma unroll
-                        for (int i = 0; i < kStates; ++i) {
-                            const float gg = fmaf(cv[i], e, gc[c][i]);
-                            dB[i] = fmaf(gg, du, dB[i]);
-                            dC[i] = fmaf(e, h[j + 1][c][i], dC[i]);
-                            y = fmaf(cv[i], h[j + 1][c][i], y);
-                            s1 = fmaf(gg, bv[i], s1);
-                            gc[c][i] = a[j][c][i] * gg;
-                            const float wv = gc[c][i] * h[j][c][i];
-                            s2 = fmaf(a2[c][i], wv, s2);
-                            dAc[c][i] = fmaf(delta, wv, dAc[c][i]);
-                        }
-#pragma unroll
-                        for (int o = S::NL / 2; o > 0; o >>= 1) {
-                            s1 += __shfl_xor_sync(0xffffffffu, s1, o);
-                            s2 += __shfl_xor_sync(0xffffffffu, s2, o);
-                            y += __shfl_xor_sync(0xffffffffu, y, o);
-                        }
-                        __syncwarp();
-                        if (nl == 0) {
-                            sm.delta[t][cw + c] = fmaf(u, s1, s2 * (1.f / kLog2e));
-                            sm.u[t][cw + c] = fmaf(delta, s1, skip[c] * e);
-                            sm.e[t][cw + c] = fmaf(skip[c], u, y);
-                        }
+                    for (int i = 0; i < kStates; ++i) {
+                        float g0, g1, h0, h1;
+                        split_pair(gc[i], g0, g1);
+                        split_pair(h[j + 1][i], h0, h1);
+                        g0 = fmaf(cv.e[i], ev.e[0], g0);
+                        g1 = fmaf(cv.e[i], ev.e[1], g1);
+                        bc[(j * 2 + 0) * kStates + i] = fmaf(g1, x1, g0 * x0);
+                        bc[(j * 2 + 1) * kStates + i] = fmaf(ev.e[1], h1, ev.e[0] * h0);
+                        ya = fmaf(cv.e[i], h0, ya);
+                        yb = fmaf(cv.e[i], h1, yb);
+                        s1a = fmaf(g0, bv.e[i], s1a);
+                        s1b = fmaf(g1, bv.e[i], s1b);
+                        gc[i] = mul2(a[j][i], make_pair(g0, g1));
+                        const Pair wv = mul2(gc[i], h[j][i]);
+                        s2 = fma2(a2[i], wv, s2);
+                        dAc[i] = fma2(dlp, wv, dAc[i]);
                     }
+                    tri[j * 6 + 0] = s1a;
+                    tri[j * 6 + 2] = ya;
+                    tri[j * 6 + 3] = s1b;
+                    tri[j * 6 + 5] = yb;
+                    split_pair(s2, tri[j * 6 + 1], tri[j * 6 + 4]);
+                }
+                // a lane ends with R (token, channel) triples and finishes them
+                // where it owns them; the row's readers are all past it
+                {
+                    constexpr int M = kSub * 2, R = M > S::NL ? M / S::NL : 1;
+                    const int first = reduce_triples<S::NL, kSub * 6>(tri, nl);
+                    __syncwarp();
+                    if (S::NL <= M || nl < M)
 #pragma unroll
-                    for (int i = 0; i < kStates; ++i)
-#pragma unroll
-                        for (int o = S::NL; o < 32; o <<= 1) {
-                            dB[i] += __shfl_xor_sync(0xffffffffu, dB[i], o);
-                            dC[i] += __shfl_xor_sync(0xffffffffu, dC[i], o);
-                        }
-                    if (lane < S::NL)
-#pragma unroll
-                        for (int i = 0; i < kStates; ++i) {
-                            sm.bc[s & 1][warp][j][0][n0 + i] = dB[i];
-                            sm.bc[s & 1][warp][j][1][n0 + i] = dC[i];
+                        for (int r = 0; r < R; ++r) {
+                            const int t = s * kSub + (first + r) / 2, c = (first + r) & 1;
+                            const float dl = sm.delta[t][cw + c], u = sm.u[t][cw + c], e = sm.e[t][cw + c];
+                            const float skip = c ? skip1 : skip0;
+                            sm.delta[t][cw + c] = fmaf(u, tri[3 * r], tri[3 * r + 1] * (1.f / kLog2e));
+                            sm.u[t][cw + c] = fmaf(dl, tri[3 * r], skip * e);
+                            sm.e[t][cw + c] = fmaf(skip, u, tri[3 * r + 2]);
                         }
                 }
+                // the same over the lanes of other channels, for dB and dC
+                {
+                    constexpr int CL = 32 / S::NL, M = kSub * 2 * kStates, R = M / CL;
+                    const int cl = lane / S::NL;
+                    reduce_lanes<CL, M, S::NL>(bc, cl);
+                    const int first = reduced_first<CL, M>(cl);
+                    float *dst = &sm.bc[s & 1][warp][0][0][0];
+#pragma unroll
+                    for (int r = 0; r < R; r += R < 4 ? R : 4) {
+                        constexpr int P = R < 4 ? R : 4;
+                        const int at = first + r;
+                        store_packet<float, P>(dst + at / kStates * S::NP + n0 + at % kStates,
+                                               pack<float, P>(bc + r));
+                    }
+                }
                 __syncthreads();
-                // the block's dB, dC of the four tokens
-                for (int i = threadIdx.x; i < kSub * 2 * S::NP; i += S::NT) {
+                for (int i = tid; i < kSub * 2 * S::NP; i += S::NT) {
                     const int j = i / (2 * S::NP), which = i / S::NP % 2, m = i % S::NP;
                     const int t = s * kSub + j;
                     if (t >= n || m >= p.N) continue;
@@ -256,58 +382,57 @@ __global__ void __launch_bounds__(S::NT) scan_bwd_kernel(ScanProblem p, Layout l
                 }
             }
 #pragma unroll
-            for (int c = 0; c < S::CPT; ++c)
-#pragma unroll
-                for (int i = 0; i < kStates; ++i) dA[c][i] += dAc[c][i];
+            for (int i = 0; i < kStates; ++i) dA[i] = fma2(dAc[i], make_pair(1.f, 1.f), dA[i]);
             // the last barrier above stands between the results in shared
             // memory and here
-            for (int t = qrow; t < n && qlive; t += RS) {
-                const long row = t0 + tb + t;
-                float o[V], x[V];
+            if (qlive)
 #pragma unroll
-                for (int v = 0; v < V; ++v) o[v] = sm.u[t][qc * V + v];
-                store_packet<T, V>(static_cast<T *>(p.du) + row * p.D + col, pack<T, V>(o));
-                unpack<T, V>(load_packet<T, V>(static_cast<const T *>(p.dt) + row * p.ld_dt + col), x);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    o[v] = sm.delta[t][qc * V + v];
-                    if (p.softplus) o[v] *= sigmoid_f(x[v] + bias[v]);
-                    dbias[v] += o[v];
-                }
-                store_packet<T, V>(static_cast<T *>(p.ddt) + row * p.D + col, pack<T, V>(o));
-                if (p.z) {
-                    float z[V];
-                    unpack<T, V>(load_packet<T, V>(static_cast<const T *>(p.dy) + row * p.ld_dy + col), x);
-                    unpack<T, V>(load_packet<T, V>(static_cast<const T *>(p.z) + row * p.ld_z + col), z);
+                for (int i = 0; i < Sm::PS; ++i) {
+                    const int t = i * RS + row;
+                    if (t >= n) break;
+                    const long tok = t0 + tb + t;
+                    float o[V], x[V];
+                    auto r = load_packet<float, V>(&sm.u[t][qcol]);
+                    unpack<float, V>(r, o);
+                    store_packet<T, V>(static_cast<T *>(p.du) + tok * p.D + col, pack<T, V>(o));
+                    r = load_packet<float, V>(&sm.delta[t][qcol]);
+                    unpack<T, V>(load_packet<T, V>(static_cast<const T *>(p.dt) + tok * p.ld_dt + col), x);
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
-                        const float sg = sigmoid_f(z[v]);
-                        o[v] = x[v] * sm.e[t][qc * V + v] * sg * fmaf(z[v], 1.f - sg, 1.f);
+                        o[v] = r.e[v];
+                        if (p.softplus) o[v] *= sigmoid_f(x[v] + bias[v]);
+                        dbias[v] += o[v];
                     }
-                    store_packet<T, V>(static_cast<T *>(p.dz) + row * p.D + col, pack<T, V>(o));
+                    store_packet<T, V>(static_cast<T *>(p.ddt) + tok * p.D + col, pack<T, V>(o));
+                    if (p.z) {
+                        float z[V];
+                        r = load_packet<float, V>(&sm.e[t][qcol]);
+                        unpack<T, V>(load_packet<T, V>(static_cast<const T *>(p.dy) + tok * p.ld_dy + col), x);
+                        unpack<T, V>(load_packet<T, V>(static_cast<const T *>(p.z) + tok * p.ld_z + col), z);
+#pragma unroll
+                        for (int v = 0; v < V; ++v) {
+                            const float sg = sigmoid_f(z[v]);
+                            o[v] = x[v] * r.e[v] * sg * fmaf(z[v], 1.f - sg, 1.f);
+                        }
+                        store_packet<T, V>(static_cast<T *>(p.dz) + tok * p.D + col, pack<T, V>(o));
+                    }
                 }
-            }
             __syncthreads();
         }
-        if (p.dh0)
-#pragma unroll
-            for (int c = 0; c < S::CPT; ++c)
-                if (live[c]) store_states(p.dh0 + sbase, d0 + cw + c, n0, p.N, gc[c]);
+        if (p.dh0 && it.tok0 == 0) store_pairs(p.dh0 + sbase, gc);
     }
     const long pbase = (long)slot * p.D;
-#pragma unroll
-    for (int c = 0; c < S::CPT; ++c)
-        if (live[c]) store_states(w.A + pbase * p.N, d0 + cw + c, n0, p.N, dA[c]);
+    store_pairs(w.A + pbase * p.N, dA);
     // the threads of a column packet add up in order
     __syncthreads();
 #pragma unroll
     for (int v = 0; v < V; ++v)
-        if (qrow < kTokens) {                        // later rows hold no token
-            sm.delta[qrow][qc * V + v] = dD[v];
-            sm.u[qrow][qc * V + v] = dbias[v];
+        if (row < kTokens) {                         // later rows hold no token
+            sm.delta[row][qcol + v] = dD[v];
+            sm.u[row][qcol + v] = dbias[v];
         }
     __syncthreads();
-    for (int c = threadIdx.x; c < S::CB; c += S::NT) {
+    for (int c = tid; c < S::CB; c += S::NT) {
         if (c0 + c >= Dg) continue;
         float x = 0.f, y = 0.f;
         for (int r = 0; r < RS && r < kTokens; ++r) {
@@ -352,20 +477,28 @@ scan_reduce_params_kernel(BwdPartials w, long dn, int D, float *dA, float *dD, f
     }
 }
 
+// The shapes by lanes per channel: 64 channels a block while eight warps allow.
+template <int NL> struct BwdShape;
+template <> struct BwdShape<2> { using S = Shape<2, 2, 2, 0>; };
+template <> struct BwdShape<4> { using S = Shape<4, 2, 4, 0>; };
+template <> struct BwdShape<8> { using S = Shape<8, 2, 4, 0>; };
+template <> struct BwdShape<16> { using S = Shape<16, 2, 8, 0>; };
+template <> struct BwdShape<32> { using S = Shape<32, 2, 8, 0>; };
+
 int bwd_block_channels(int N) {
     switch (lanes_of_states(N)) {
-        case 2: return Shape<2, 2, 4, 0>::CB;
-        case 4: return Shape<4, 2, 4, 0>::CB;
-        case 8: return Shape<8, 2, 4, 0>::CB;
-        case 16: return Shape<16, 2, 8, 0>::CB;
-        default: return Shape<32, 2, 8, 0>::CB;
+        case 2: return BwdShape<2>::S::CB;
+        case 4: return BwdShape<4>::S::CB;
+        case 8: return BwdShape<8>::S::CB;
+        case 16: return BwdShape<16>::S::CB;
+        default: return BwdShape<32>::S::CB;
     }
 }
 
 struct BwdPlan {
     long tiles, gtiles;
     int slots;
-    size_t bc, A, D, bytes;       // float offsets; bytes of the whole workspace
+    size_t bc, A, D, bytes;       // bytes of each part, and of the whole workspace
     size_t base;
 };
 BwdPlan bwd_plan(int n_seq, int T_total, int D, int G, int N) {
@@ -373,9 +506,12 @@ BwdPlan bwd_plan(int n_seq, int T_total, int D, int G, int N) {
     const int Dg = D / G, CB = bwd_block_channels(N);
     b.gtiles = (Dg + CB - 1) / CB;
     b.tiles = b.gtiles * G;
+    // blocks for four on each SM, and no more than there can be items
+    int cut, trigger;
+    choose_cut(T_total, D, N, cut, trigger);
+    const long items = n_seq + (T_total > trigger ? T_total / cut : 0);
     const long want = (152L * 4 + b.tiles - 1) / b.tiles;
-    b.slots = (int)(n_seq < want ? n_seq : want);
-    if (b.slots < 1) b.slots = 1;
+    b.slots = (int)std::max(1L, std::min(items, want));
     b.base = layout_bytes(n_seq, T_total, D, N);
     b.bc = round256((size_t)b.gtiles * T_total * G * 2 * N * sizeof(float));
     b.A = round256((size_t)b.slots * D * N * sizeof(float));
@@ -391,17 +527,16 @@ cudaError_t bwd_t(const ScanProblem &p, const Layout &l, const BwdPartials &w, c
     if (blocks > 0x7fffffffL) return cudaErrorInvalidConfiguration;
     auto k = scan_bwd_kernel<T, S, V>;
     cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           (int)sizeof(BwdSmem<S>));
+                                           (int)sizeof(BwdSmem<T, S, V>));
     if (err != cudaSuccess) return err;
-    k<<<(unsigned)blocks, S::NT, sizeof(BwdSmem<S>), st>>>(p, l, w, (int)b.tiles);
+    k<<<(unsigned)blocks, S::NT, sizeof(BwdSmem<T, S, V>), st>>>(p, l, w, (int)b.tiles);
     return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t bwd_dispatch(const ScanProblem &p, const Layout &l, const BwdPartials &w,
                          const BwdPlan &b, cudaStream_t st) {
-    constexpr int V = 4;
-    const int bytes = V * (int)sizeof(T);
+    constexpr int V = 16 / (int)sizeof(T), bytes = 16;
     bool wide = (p.D / p.G) % V == 0 && rows_aligned(p.u, p.ld_u, sizeof(T), bytes) &&
                 rows_aligned(p.dt, p.ld_dt, sizeof(T), bytes) &&
                 rows_aligned(p.z, p.ld_z, sizeof(T), bytes) &&
@@ -409,17 +544,17 @@ cudaError_t bwd_dispatch(const ScanProblem &p, const Layout &l, const BwdPartial
     const void *dense[] = {p.du, p.ddt, p.dz};
     for (const void *ptr : dense) wide = wide && rows_aligned(ptr, p.D, sizeof(T), bytes);
     cudaError_t err = cudaErrorInvalidValue;
-#define MDN_SCAN_CASE(NL, NW)                                          \
-    case NL:                                                           \
-        err = wide ? bwd_t<T, Shape<NL, 2, NW, 0>, V>(p, l, w, b, st)     \
-                   : bwd_t<T, Shape<NL, 2, NW, 0>, 1>(p, l, w, b, st);    \
+#define MDN_SCAN_CASE(NL)                                                    \
+    case NL:                                                                 \
+        err = wide ? bwd_t<T, BwdShape<NL>::S, V>(p, l, w, b, st)            \
+                   : bwd_t<T, BwdShape<NL>::S, 1>(p, l, w, b, st);           \
         break;
     switch (lanes_of_states(p.N)) {
-        MDN_SCAN_CASE(2, 4)
-        MDN_SCAN_CASE(4, 4)
-        MDN_SCAN_CASE(8, 4)
-        MDN_SCAN_CASE(16, 8)
-        MDN_SCAN_CASE(32, 8)
+        MDN_SCAN_CASE(2)
+        MDN_SCAN_CASE(4)
+        MDN_SCAN_CASE(8)
+        MDN_SCAN_CASE(16)
+        MDN_SCAN_CASE(32)
     }
 #undef MDN_SCAN_CASE
     if (err != cudaSuccess) return err;
@@ -455,7 +590,8 @@ cudaError_t launch_scan_bwd(const ScanProblem &p, cudaStream_t st) {
         return scan::launch_states_copy(p.dh_T, p.dh0, (long)p.n_seq * p.D * p.N, st);
     }
     scan::Layout l;
-    const cudaError_t err = scan::make_layout(p, l, st, false);
+    cudaError_t err = scan::make_layout(p, l, st);
+    if (err == cudaSuccess) err = scan::launch_adjoint_ends(p, l, st);
     if (err != cudaSuccess) return err;
     const scan::BwdPlan b = scan::bwd_plan(p.n_seq, p.T_total, p.D, p.G, p.N);
     scan::BwdPartials w;
