@@ -37,9 +37,14 @@ struct BwdSmem {
     float e[kTokens][S::CB];          // e; then y before the gate
     float B[kTokens][S::NP], C[kTokens][S::NP];
     float4 sub[kSubs - 1][S::CPT][S::NT];     // state before every fourth token but the first
+    float4 entry[2][S::CPT][S::NT];           // saved states: of this chunk and the next
     float bc[2][S::NW][kSub][2][S::NP];       // the warps' dB, dC of four tokens
-    // the next chunk's inputs as they are, one place for each thread's packets
-    Packet<T, V> in_u[PS][S::NT], in_dt[PS][S::NT], in_dy[PS][S::NT], in_z[PS][S::NT];
+    // the inputs as they are, one place for each thread's packets: the next
+    // chunk's, and with two slots this one's until its gradients are out (in
+    // fp32 that would leave an SM with one block; there they are read again)
+    static constexpr int kSlots = sizeof(T) == 2 ? 2 : 1;
+    Packet<T, V> in_u[PS][S::NT];
+    Packet<T, V> in_dt[kSlots][PS][S::NT], in_dy[kSlots][PS][S::NT], in_z[kSlots][PS][S::NT];
     Packet<T, 4> in_b[PB][S::NT], in_c[PB][S::NT];
 };
 
@@ -81,7 +86,7 @@ __device__ __forceinline__ int reduce_triples(float *v, int nl) {
 // One block takes CB channels of one group through its items, each item's
 // chunks last first.  Channels are held two to a pair of registers.
 template <typename T, typename S, int V>
-__global__ void __launch_bounds__(S::NT, S::NT <= 128 ? 3 : 1)
+__global__ void __launch_bounds__(S::NT, S::NT <= 128 ? 2 : 1)
 scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
     using Sm = BwdSmem<T, S, V>;
     static_assert(S::CPT == 2, "one pair of channels a lane");
@@ -133,17 +138,32 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
         bias[v] = qlive && p.dt_bias ? p.dt_bias[col + v] : 0.f;
         dD[v] = dbias[v] = 0.f;
     }
-    // copies tokens t0 .. t0 + n, this thread's packets
-    auto issue = [&](long t0, int n) {
+    // copies tokens t0 .. t0 + n of the chunk whose saved states lie at hc, this
+    // thread's packets
+    auto issue = [&](long t0, int n, const float *hc, int chunk) {
+        const int r = chunk % Sm::kSlots;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            float4 *dst = &sm.entry[chunk & 1][c][tid];
+            if (!(c ? live1 : live0)) {
+                *dst = make_float4(0.f, 0.f, 0.f, 0.f);
+            } else if (p.N % kStates == 0) {
+                copy_packet<float, 4>(reinterpret_cast<Packet<float, 4> *>(dst), hc + (d0 + cw + c) * p.N + n0);
+            } else {
+                float f[kStates];
+                load_states(hc, d0 + cw + c, n0, p.N, f);
+                *dst = make_float4(f[0], f[1], f[2], f[3]);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < Sm::PS; ++i) {
             const int t = i * RS + row;
             if (t >= n || !qlive) break;
             copy_packet<T, V>(&sm.in_u[i][tid], static_cast<const T *>(p.u) + (t0 + t) * p.ld_u + col);
-            copy_packet<T, V>(&sm.in_dt[i][tid], static_cast<const T *>(p.dt) + (t0 + t) * p.ld_dt + col);
-            copy_packet<T, V>(&sm.in_dy[i][tid], static_cast<const T *>(p.dy) + (t0 + t) * p.ld_dy + col);
+            copy_packet<T, V>(&sm.in_dt[r][i][tid], static_cast<const T *>(p.dt) + (t0 + t) * p.ld_dt + col);
+            copy_packet<T, V>(&sm.in_dy[r][i][tid], static_cast<const T *>(p.dy) + (t0 + t) * p.ld_dy + col);
             if (p.z)
-                copy_packet<T, V>(&sm.in_z[i][tid], static_cast<const T *>(p.z) + (t0 + t) * p.ld_z + col);
+                copy_packet<T, V>(&sm.in_z[r][i][tid], static_cast<const T *>(p.z) + (t0 + t) * p.ld_z + col);
         }
 #pragma unroll
         for (int i = 0; i < Sm::PB; ++i) {
@@ -172,7 +192,11 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
         const long sbase = (long)it.seq * p.D * p.N;
         const int seq_len = p.cu ? p.cu[it.seq + 1] - p.cu[it.seq] : p.T;
         const int chunks = (it.len + kTokens - 1) / kTokens;
-        if (chunks > 0) issue(t0 + (chunks - 1) * kTokens, it.len - (chunks - 1) * kTokens);
+        const long hstep = (long)p.D * p.N;
+        const float *hc = p.h_chunks + slot0 * hstep;
+        if (chunks > 0)
+            issue(t0 + (chunks - 1) * kTokens, it.len - (chunks - 1) * kTokens,
+                  hc + (chunks - 1) * hstep, chunks - 1);
         Pair gc[kStates];                            // a_{t+1} g_{t+1}
         if (p.dh_T) {
             load_pairs(p.dh_T + sbase, gc);
@@ -201,6 +225,7 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
             const int n4 = (n + kSub - 1) / kSub * kSub;
             // this chunk's inputs to fp32 (tokens n .. n4 are zero and change
             // nothing), then the copies of the one before it
+            const int r = chunk % Sm::kSlots;
             wait_copies<0>();
 #pragma unroll
             for (int i = 0; i < Sm::PS; ++i) {
@@ -211,11 +236,11 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
                 for (int v = 0; v < V; ++v) df[v] = uf[v] = ef[v] = 0.f;
                 if (t < n && qlive) {
                     unpack<T, V>(sm.in_u[i][tid], uf);
-                    unpack<T, V>(sm.in_dt[i][tid], df);
-                    unpack<T, V>(sm.in_dy[i][tid], ef);
+                    unpack<T, V>(sm.in_dt[r][i][tid], df);
+                    unpack<T, V>(sm.in_dy[r][i][tid], ef);
                     if (p.z) {
                         float z[V];
-                        unpack<T, V>(sm.in_z[i][tid], z);
+                        unpack<T, V>(sm.in_z[r][i][tid], z);
 #pragma unroll
                         for (int v = 0; v < V; ++v) ef[v] *= z[v] * sigmoid_f(z[v]);
                     }
@@ -242,13 +267,18 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
                 store_packet<float, 4>(&sm.B[t][m], pack<float, 4>(b));
                 store_packet<float, 4>(&sm.C[t][m], pack<float, 4>(c));
             }
-            if (chunk > 0) issue(t0 + tb - kTokens, kTokens);
+            if (chunk > 0) issue(t0 + tb - kTokens, kTokens, hc + (chunk - 1) * hstep, chunk - 1);
             __syncthreads();
-            const float *hc = p.h_chunks + (slot0 + chunk) * p.D * p.N;
+            // a lane's saved states (its own copies), or those of sub s
+            auto load_sub = [&](const float4 (*from)[S::NT], Pair *h) {
+                const float4 x = from[0][tid], y = from[1][tid];
+                h[0] = make_pair(x.x, y.x); h[1] = make_pair(x.y, y.y);
+                h[2] = make_pair(x.z, y.z); h[3] = make_pair(x.w, y.w);
+            };
             // forward: the state before every fourth token
             {
                 Pair h[kStates];
-                load_pairs(hc, h);
+                load_sub(sm.entry[chunk & 1], h);
 #pragma unroll 1
                 for (int s = 0; s < n4 / kSub - 1; ++s) {
 #pragma unroll
@@ -279,13 +309,7 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
 #pragma unroll 1
             for (int s = n4 / kSub - 1; s >= 0; --s) {
                 Pair h[kSub + 1][kStates], a[kSub][kStates];
-                if (s > 0) {
-                    const float4 x = sm.sub[s - 1][0][tid], y = sm.sub[s - 1][1][tid];
-                    h[0][0] = make_pair(x.x, y.x); h[0][1] = make_pair(x.y, y.y);
-                    h[0][2] = make_pair(x.z, y.z); h[0][3] = make_pair(x.w, y.w);
-                } else {
-                    load_pairs(hc, h[0]);
-                }
+                load_sub(s > 0 ? sm.sub[s - 1] : sm.entry[chunk & 1], h[0]);
 #pragma unroll
                 for (int j = 0; j < kSub; ++j) {
                     const int t = s * kSub + j;
@@ -392,27 +416,30 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
                     if (t >= n) break;
                     const long tok = t0 + tb + t;
                     float o[V], x[V];
-                    auto r = load_packet<float, V>(&sm.u[t][qcol]);
-                    unpack<float, V>(r, o);
+                    auto q = load_packet<float, V>(&sm.u[t][qcol]);
+                    unpack<float, V>(q, o);
                     store_packet<T, V>(static_cast<T *>(p.du) + tok * p.D + col, pack<T, V>(o));
-                    r = load_packet<float, V>(&sm.delta[t][qcol]);
-                    unpack<T, V>(load_packet<T, V>(static_cast<const T *>(p.dt) + tok * p.ld_dt + col), x);
+                    q = load_packet<float, V>(&sm.delta[t][qcol]);
+                    unpack<T, V>(Sm::kSlots == 2 ? sm.in_dt[r][i][tid]
+                                                 : load_packet<T, V>(static_cast<const T *>(p.dt) + tok * p.ld_dt + col), x);
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
-                        o[v] = r.e[v];
+                        o[v] = q.e[v];
                         if (p.softplus) o[v] *= sigmoid_f(x[v] + bias[v]);
                         dbias[v] += o[v];
                     }
                     store_packet<T, V>(static_cast<T *>(p.ddt) + tok * p.D + col, pack<T, V>(o));
                     if (p.z) {
                         float z[V];
-                        r = load_packet<float, V>(&sm.e[t][qcol]);
-                        unpack<T, V>(load_packet<T, V>(static_cast<const T *>(p.dy) + tok * p.ld_dy + col), x);
-                        unpack<T, V>(load_packet<T, V>(static_cast<const T *>(p.z) + tok * p.ld_z + col), z);
+                        q = load_packet<float, V>(&sm.e[t][qcol]);
+                        unpack<T, V>(Sm::kSlots == 2 ? sm.in_dy[r][i][tid]
+                                                     : load_packet<T, V>(static_cast<const T *>(p.dy) + tok * p.ld_dy + col), x);
+                        unpack<T, V>(Sm::kSlots == 2 ? sm.in_z[r][i][tid]
+                                                     : load_packet<T, V>(static_cast<const T *>(p.z) + tok * p.ld_z + col), z);
 #pragma unroll
                         for (int v = 0; v < V; ++v) {
                             const float sg = sigmoid_f(z[v]);
-                            o[v] = x[v] * r.e[v] * sg * fmaf(z[v], 1.f - sg, 1.f);
+                            o[v] = x[v] * q.e[v] * sg * fmaf(z[v], 1.f - sg, 1.f);
                         }
                         store_packet<T, V>(static_cast<T *>(p.dz) + tok * p.D + col, pack<T, V>(o));
                     }
