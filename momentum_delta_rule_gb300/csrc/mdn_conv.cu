@@ -6,15 +6,24 @@
 //   dw_j  = sum_t dpre_t x_{t-(W-1-j)};  dbias = sum_t dpre_t
 //
 // Tokens before a sequence's first are its W - 1 initial-state rows.  Memory
-// bound (2 W + 4 flops against 2 elements moved): a thread owns a packet of
-// channels and a run of consecutive tokens, keeps the last W - 1 inputs in
-// registers, and issues several rows' loads before it uses the first.
+// bound (2 W + 4 flops against 2 elements moved): a thread owns four
+// neighbouring channels and a run of consecutive tokens, keeps the last W - 1
+// inputs in registers, and copies the rows ahead of it asynchronously into
+// shared memory that only it reads.  A batch of rows inside one sequence runs
+// without a branch.  Runs are cut so that one wave of blocks covers the
+// tokens: what a run starts with (weights, the rows before it, the search for
+// its sequence) costs as much as a dozen tokens.
+#include <algorithm>
+
 #include "mdn_ssm.cuh"
 
 namespace mdn {
 namespace {
 
-constexpr int kConvThreads = 256;
+constexpr int kConvThreads = 128;
+// Blocks that an SM holds (the launch bounds give them the registers) and that
+// one wave of the forward and of the gradient has on each.
+constexpr int kFwdBlocks = 6, kBwdBlocks = 4;
 
 __device__ __forceinline__ float conv_act(float v, int act) {
     return act == MDN_CONV_SILU ? v * sigmoid_f(v) : v;
@@ -40,7 +49,35 @@ struct SeqWalk {
             end = start + p.T;
         }
     }
+    // The next sequence with tokens.
+    __device__ __forceinline__ void next(const ConvProblem &p) {
+        do {
+            ++s;
+            start = end;
+            end = p.cu ? (long)p.cu[s + 1] : start + p.T;
+        } while (end == start);
+    }
 };
+
+// The weights [tap][channel] and the bias of channels c .. c + V.
+template <int V, int W>
+__device__ __forceinline__ void load_weights(const ConvProblem &p, int c, float (*w)[V], float *bias) {
+    float f[V * W];
+    const float *src = p.w + (long)c * W;
+    if constexpr (V == 4) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) unpack<float, 4>(load_packet<float, 4>(src + 4 * i), f + 4 * i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V * W; ++i) f[i] = src[i];
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[j][v] = f[v * W + j];
+        bias[v] = p.bias ? p.bias[c + v] : 0.f;
+    }
+}
 
 // Input at position `pos` of sequence w (pos >= start - (W - 1)): a token, an
 // initial-state row or zero.
@@ -89,9 +126,53 @@ struct ConvGrid {
     long nruns;
 };
 
+// Rows of a batch: 64 bytes of a thread's packets, so that a block's copies
+// ahead take as much shared memory in either type.
+template <typename T, int V>
+constexpr int kBatch = V * sizeof(T) == 16 ? 4 : 8;
+constexpr int kConvAhead = 2;          // batches in flight
+
+// This thread's rows ahead: batch k of a run in slot k % (kConvAhead + 1).
+template <typename T, int V>
+struct RowRing {
+    static constexpr int kRows = kBatch<T, V>;
+    Packet<T, V> (*at)[kRows][kConvThreads];
+    const T *src;                      // the run's first row, this thread's channels
+    long ld;
+    __device__ __forceinline__ void issue(int k, long rows) const {
+        const int slot = k % (kConvAhead + 1);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+            if (k * kRows + i < rows)
+                copy_packet<T, V>(&at[slot][i][threadIdx.x], src + (long)(k * kRows + i) * ld);
+    }
+    __device__ __forceinline__ void row(int k, int i, float *f) const {
+        unpack<T, V>(at[k % (kConvAhead + 1)][i][threadIdx.x], f);
+    }
+};
+
+template <int V, int W>
+__device__ __forceinline__ void conv_sum(const float (*w)[V], const float *bias, const float (*win)[V],
+                                         const float *x, float *pre) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        pre[v] = fmaf(w[W - 1][v], x[v], bias[v]);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) pre[v] = fmaf(w[j][v], win[j][v], pre[v]);
+    }
+}
+template <int V, int W>
+__device__ __forceinline__ void push_row(float (*win)[V], const float *x) {
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int v = 0; v < V; ++v) win[j][v] = j + 1 < W - 1 ? win[j + 1][v] : x[v];
+}
+
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvProblem p, ConvGrid g) {
-    constexpr int UN = 8;          // rows loaded ahead
+__global__ void __launch_bounds__(kConvThreads, kFwdBlocks) conv_fwd_kernel(ConvProblem p, ConvGrid g) {
+    constexpr int kRows = kBatch<T, V>;
+    __shared__ Packet<T, V> ring[kConvAhead + 1][kRows][kConvThreads];
     const int lane = threadIdx.x & (g.cl - 1);
     const int ct = blockIdx.x % g.ctiles;
     const long row = (long)(blockIdx.x / g.ctiles) * (kConvThreads / g.cl) + threadIdx.x / g.cl;
@@ -106,13 +187,15 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvProblem p, C
     if (row >= g.nruns || c >= p.D) return;
     const long t0 = row * g.run;
     const long t1 = min(t0 + g.run, (long)p.T_total);
-    float w[W][V], bias[V];
+    const RowRing<T, V> rx{ring, static_cast<const T *>(p.x) + t0 * p.ld_x + c, p.ld_x};
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) w[j][v] = p.w[(long)(c + v) * W + j];
-        bias[v] = p.bias ? p.bias[c + v] : 0.f;
+    for (int k = 0; k < kConvAhead; ++k) {
+        rx.issue(k, t1 - t0);
+        commit_copies();
     }
+    T *yp = static_cast<T *>(p.y) + c;
+    float w[W][V], bias[V];
+    load_weights<V, W>(p, c, w, bias);
     SeqWalk q;
     q.find(p, t0);
     if (t0 == 0 && p.state_T)           // empty sequences before the first token
@@ -120,189 +203,227 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvProblem p, C
     float win[W - 1][V];                // inputs t - (W - 1) .. t - 1
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) conv_input<T, V, W>(p, q, t0 - (W - 1) + j, c, win[j]);
-    const T *xp = static_cast<const T *>(p.x) + c;
-    T *yp = static_cast<T *>(p.y) + c;
-    for (long tb = t0; tb < t1; tb += UN) {
-        Packet<T, V> in[UN];
+    auto finish = [&]() {               // q ended: its state, and those of empty ones that follow
+        if (!p.state_T) return;
 #pragma unroll
-        for (int i = 0; i < UN; ++i)
-            if (tb + i < t1) in[i] = load_packet<T, V>(xp + (tb + i) * p.ld_x);
+        for (int j = 0; j < W - 1; ++j)
+            store_packet<T, V>(static_cast<T *>(p.state_T) + ((long)q.s * (W - 1) + j) * p.D + c,
+                               pack<T, V>(win[j]));
+        if (p.cu)
+            for (int s = q.s + 1; s < p.n_seq && p.cu[s + 1] == q.end; ++s)
+                copy_state<T, V, W>(p.state0, p.state_T, s, p.D, c);
+    };
+    auto token = [&](long t, const float *x) {
+        float o[V];
+        conv_sum<V, W>(w, bias, win, x, o);
 #pragma unroll
-        for (int i = 0; i < UN; ++i) {
-            const long t = tb + i;
-            if (t >= t1) break;
-            if (t == q.end) {           // the next sequence with tokens
-                do {
-                    ++q.s;
-                    q.start = q.end;
-                    q.end = p.cu ? (long)p.cu[q.s + 1] : q.start + p.T;
-                } while (q.end == q.start);
+        for (int v = 0; v < V; ++v) o[v] = conv_act(o[v], p.act);
+        store_packet<T, V>(yp + t * p.D, pack<T, V>(o));
+        push_row<V, W>(win, x);
+    };
+    int k = 0;
+    for (long tb = t0; tb < t1; tb += kRows, ++k) {
+        rx.issue(k + kConvAhead, t1 - t0);
+        commit_copies();
+        wait_copies<kConvAhead>();
+        if (tb + kRows <= t1 && tb + kRows <= q.end) {
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j)
-                    conv_input<T, V, W>(p, q, t - (W - 1) + j, c, win[j]);
+            for (int i = 0; i < kRows; ++i) {
+                float x[V];
+                rx.row(k, i, x);
+                token(tb + i, x);
             }
-            float x[V], o[V];
-            unpack<T, V>(in[i], x);
+            if (tb + kRows == q.end) finish();
+        } else {
+#pragma unroll 1
+            for (long t = tb; t < tb + kRows && t < t1; ++t) {
+                if (t == q.end) {       // the next sequence with tokens
+                    q.next(p);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float a = fmaf(w[W - 1][v], x[v], bias[v]);
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) a = fmaf(w[j][v], win[j][v], a);
-                o[v] = conv_act(a, p.act);
-            }
-            store_packet<T, V>(yp + t * p.D, pack<T, V>(o));
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-                for (int v = 0; v < V; ++v) win[j][v] = j + 1 < W - 1 ? win[j + 1][v] : x[v];
-            if (p.state_T && t == q.end - 1) {
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j)
-                    store_packet<T, V>(static_cast<T *>(p.state_T) +
-                                           ((long)q.s * (W - 1) + j) * p.D + c,
-                                       pack<T, V>(win[j]));
-                if (p.cu)               // empty sequences that follow
-                    for (int s = q.s + 1; s < p.n_seq && p.cu[s + 1] == q.end; ++s)
-                        copy_state<T, V, W>(p.state0, p.state_T, s, p.D, c);
+                    for (int j = 0; j < W - 1; ++j)
+                        conv_input<T, V, W>(p, q, t - (W - 1) + j, c, win[j]);
+                }
+                float x[V];
+                rx.row(k, (int)(t - tb), x);
+                token(t, x);
+                if (t + 1 == q.end) finish();
             }
         }
+        // a batch that begins a sequence starts from its state
+        if (tb + kRows < t1 && tb + kRows == q.end) {
+            q.next(p);
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+                conv_input<T, V, W>(p, q, q.start - (W - 1) + j, c, win[j]);
+        }
     }
+    wait_copies<0>();
 }
 
-// dstate of a sequence without tokens is the adjoint of the state it hands on.
-// dx of positions [a - (W - 1), ..] lags dpre by W - 1 tokens: the loop runs
-// W - 1 tokens past the run (recomputing dpre there, the next run's first
-// rows) and a run that holds a sequence's start also produces the W - 1
-// positions before it, the initial state's gradient.
+// dx lags dpre by W - 1 tokens: at token t the output is position t - (W - 1).
+// A run goes W - 1 tokens past its end (recomputing dpre there, the next run's
+// first rows; zero behind a sequence's end), and where it holds a sequence's
+// start it also produces the W - 1 positions before that, the gradient of the
+// initial state.  dstate of a sequence without tokens is the adjoint of the
+// state it hands on.
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(ConvProblem p, ConvGrid g, long rows) {
-    constexpr int UN = 4;
+__global__ void __launch_bounds__(kConvThreads, kBwdBlocks) conv_bwd_kernel(ConvProblem p, ConvGrid g) {
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    constexpr int kRows = kBatch<T, V>;
+    using Ring = Packet<T, V>[kConvAhead + 1][kRows][kConvThreads];
     const int lane = threadIdx.x & (g.cl - 1);
     const int ct = blockIdx.x % g.ctiles;
     const long row = (long)(blockIdx.x / g.ctiles) * (kConvThreads / g.cl) + threadIdx.x / g.cl;
     const int c = (ct * g.cl + lane) * V;
     const bool ok = !p.cu || cu_well_formed(p.cu, p.n_seq, p.T_total);
-    if (row >= rows || c >= p.D) return;
-    float w[W][V], bias[V], dw[W][V], db[V];
+    if (c >= p.D) return;
+    float dw[W][V], db[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            w[j][v] = p.w[(long)(c + v) * W + j];
-            dw[j][v] = 0.f;
-        }
-        bias[v] = p.bias ? p.bias[c + v] : 0.f;
+        for (int j = 0; j < W; ++j) dw[j][v] = 0.f;
         db[v] = 0.f;
     }
     if (!ok) {
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicExch(p.status, (int)MDN_ERR_INVALID_ARG);
         if (p.dstate0)
-            for (long s = row; s < p.n_seq; s += rows)
+            for (long s = row; s < p.n_seq; s += g.nruns)
                 copy_state<T, V, W>(p.dstate_T, p.dstate0, (int)s, p.D, c);
-    }
-    const T *xp = static_cast<const T *>(p.x) + c;
-    const T *dyp = static_cast<const T *>(p.dy) + c;
-    for (long r = row; ok && r < g.nruns; r += rows) {
-        const long t0 = r * g.run;
+    } else if (row < g.nruns) {
+        const long t0 = row * g.run;
         const long t1 = min(t0 + g.run, (long)p.T_total);
+        const T *xp = static_cast<const T *>(p.x) + c, *dyp = static_cast<const T *>(p.dy) + c;
+        Ring *ring = reinterpret_cast<Ring *>(smem_raw);
+        const RowRing<T, V> rx{ring[0], xp + t0 * p.ld_x, p.ld_x};
+        const RowRing<T, V> ry{ring[1], dyp + t0 * p.ld_dy, p.ld_dy};
+#pragma unroll
+        for (int k = 0; k < kConvAhead; ++k) {
+            rx.issue(k, t1 - t0);
+            ry.issue(k, t1 - t0);
+            commit_copies();
+        }
+        float w[W][V], bias[V];
+        load_weights<V, W>(p, c, w, bias);
         SeqWalk q;
         q.find(p, t0);
         if (t0 == 0 && p.dstate0)
             for (int s = 0; s < q.s; ++s) copy_state<T, V, W>(p.dstate_T, p.dstate0, s, p.D, c);
-        long a = t0;                    // first token of the piece
-        while (a < t1) {
-            const long b = min(t1, q.end);
-            const bool at_start = a == q.start;
-            float win[W - 1][V], dp[W][V];    // dp[k]: dpre_{t-(W-1)+k}
+        long a = t0;                     // first token of this run in sequence q
+        float win[W - 1][V], dp[W - 1][V];     // inputs, and dpre, of the W - 1 tokens before t
+        auto begin = [&]() {
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j) conv_input<T, V, W>(p, q, a - (W - 1) + j, c, win[j]);
+            for (int j = 0; j < W - 1; ++j) {
+                conv_input<T, V, W>(p, q, a - (W - 1) + j, c, win[j]);
 #pragma unroll
-            for (int k = 0; k < W; ++k)
+                for (int v = 0; v < V; ++v) dp[j][v] = 0.f;
+            }
+        };
+        begin();
+        // dpre of a token; its part of dw and db
+        auto dpre = [&](const float *x, const float *d, bool mine, float *e) {
+            conv_sum<V, W>(w, bias, win, x, e);
 #pragma unroll
-                for (int v = 0; v < V; ++v) dp[k][v] = 0.f;
-            const long stop = b + W - 1;
-            for (long tb = a; tb < stop; tb += UN) {
-                Packet<T, V> in[UN], dn[UN];
+            for (int v = 0; v < V; ++v) {
+                e[v] = d[v] * conv_dact(e[v], p.act);
+                if (mine) {
+                    db[v] += e[v];
+                    dw[W - 1][v] = fmaf(e[v], x[v], dw[W - 1][v]);
 #pragma unroll
-                for (int i = 0; i < UN; ++i)
-                    if (tb + i < stop && tb + i < q.end) {
-                        in[i] = load_packet<T, V>(xp + (tb + i) * p.ld_x);
-                        dn[i] = load_packet<T, V>(dyp + (tb + i) * p.ld_dy);
-                    }
-#pragma unroll
-                for (int i = 0; i < UN; ++i) {
-                    const long t = tb + i;
-                    if (t >= stop) break;
-#pragma unroll
-                    for (int k = 0; k < W - 1; ++k)
-#pragma unroll
-                        for (int v = 0; v < V; ++v) dp[k][v] = dp[k + 1][v];
-                    if (t < q.end) {
-                        float x[V], d[V];
-                        unpack<T, V>(in[i], x);
-                        unpack<T, V>(dn[i], d);
-#pragma unroll
-                        for (int v = 0; v < V; ++v) {
-                            float pre = fmaf(w[W - 1][v], x[v], bias[v]);
-#pragma unroll
-                            for (int j = 0; j < W - 1; ++j) pre = fmaf(w[j][v], win[j][v], pre);
-                            const float e = d[v] * conv_dact(pre, p.act);
-                            dp[W - 1][v] = e;
-                            if (t < b) {
-                                db[v] += e;
-                                dw[W - 1][v] = fmaf(e, x[v], dw[W - 1][v]);
-#pragma unroll
-                                for (int j = 0; j < W - 1; ++j)
-                                    dw[j][v] = fmaf(e, win[j][v], dw[j][v]);
-                            }
-                        }
-#pragma unroll
-                        for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-                            for (int v = 0; v < V; ++v)
-                                win[j][v] = j + 1 < W - 1 ? win[j + 1][v] : x[v];
-                    } else {
-#pragma unroll
-                        for (int v = 0; v < V; ++v) dp[W - 1][v] = 0.f;
-                    }
-                    const long pos = t - (W - 1);
-                    if (pos < a && !(at_start && p.dstate0)) continue;
-                    float o[V];
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        o[v] = 0.f;
-#pragma unroll
-                        for (int k = 0; k < W; ++k) o[v] = fmaf(w[W - 1 - k][v], dp[k][v], o[v]);
-                    }
-                    if (p.dstate_T && pos >= q.end - (W - 1)) {
-                        float e[V];
-                        unpack<T, V>(load_packet<T, V>(
-                                         static_cast<const T *>(p.dstate_T) +
-                                         ((long)q.s * (W - 1) + (pos - (q.end - (W - 1)))) * p.D + c),
-                                     e);
-#pragma unroll
-                        for (int v = 0; v < V; ++v) o[v] += e[v];
-                    }
-                    T *dst = pos >= a ? static_cast<T *>(p.dx) + pos * p.D + c
-                                      : static_cast<T *>(p.dstate0) +
-                                            ((long)q.s * (W - 1) + (W - 1) + (pos - q.start)) * p.D + c;
-                    store_packet<T, V>(dst, pack<T, V>(o));
+                    for (int j = 0; j < W - 1; ++j) dw[j][v] = fmaf(e[v], win[j][v], dw[j][v]);
                 }
             }
-            if (b == q.end && p.dstate0 && p.cu)
+            push_row<V, W>(win, x);
+        };
+        // dx of position t - (W - 1) once dpre_t is known
+        auto back = [&](const float *e, float *o) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                o[v] = w[0][v] * e[v];
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) o[v] = fmaf(w[W - 1 - j][v], dp[j][v], o[v]);
+            }
+            push_row<V, W>(dp, e);
+        };
+        auto output = [&](long pos, float *o) {
+            if (pos < a && !(a == q.start && p.dstate0)) return;
+            if (p.dstate_T && pos >= q.end - (W - 1)) {
+                float e[V];
+                unpack<T, V>(load_packet<T, V>(static_cast<const T *>(p.dstate_T) +
+                                               ((long)q.s * (W - 1) + (pos - (q.end - (W - 1)))) * p.D + c),
+                             e);
+#pragma unroll
+                for (int v = 0; v < V; ++v) o[v] += e[v];
+            }
+            T *dst = pos >= a ? static_cast<T *>(p.dx) + pos * p.D + c
+                              : static_cast<T *>(p.dstate0) +
+                                    ((long)q.s * (W - 1) + (W - 1) + (pos - q.start)) * p.D + c;
+            store_packet<T, V>(dst, pack<T, V>(o));
+        };
+        // the W - 1 positions still open at token t (the run's or q's end)
+        auto drain = [&](long t) {
+#pragma unroll 1
+            for (int i = 0; i < W - 1; ++i, ++t) {
+                float e[V], o[V];
+                if (t < q.end) {
+                    float x[V], d[V];
+                    unpack<T, V>(load_packet<T, V>(xp + t * p.ld_x), x);
+                    unpack<T, V>(load_packet<T, V>(dyp + t * p.ld_dy), d);
+                    dpre(x, d, false, e);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) e[v] = 0.f;
+                }
+                back(e, o);
+                output(t - (W - 1), o);
+            }
+            if (t >= q.end + (W - 1) && p.dstate0 && p.cu)      // empty sequences that follow
                 for (int s = q.s + 1; s < p.n_seq && p.cu[s + 1] == q.end; ++s)
                     copy_state<T, V, W>(p.dstate_T, p.dstate0, s, p.D, c);
-            a = b;
-            if (a < t1) q.find(p, a);
+        };
+        int k = 0;
+        for (long tb = t0; tb < t1; tb += kRows, ++k) {
+            rx.issue(k + kConvAhead, t1 - t0);
+            ry.issue(k + kConvAhead, t1 - t0);
+            commit_copies();
+            wait_copies<kConvAhead>();
+            if (tb >= a + W - 1 && tb + kRows <= t1 && tb + kRows <= q.end) {
+                // all outputs are the run's own, and none is within
+                // W - 1 of the sequence's end
+                T *dst = static_cast<T *>(p.dx) + (tb - (W - 1)) * p.D + c;
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) {
+                    float x[V], d[V], e[V], o[V];
+                    rx.row(k, i, x);
+                    ry.row(k, i, d);
+                    dpre(x, d, true, e);
+                    back(e, o);
+                    store_packet<T, V>(dst + (long)i * p.D, pack<T, V>(o));
+                }
+            } else {
+#pragma unroll 1
+                for (long t = tb; t < tb + kRows && t < t1; ++t) {
+                    if (t == q.end) {
+                        drain(t);
+                        q.next(p);
+                        a = t;
+                        begin();
+                    }
+                    float x[V], d[V], e[V], o[V];
+                    rx.row(k, (int)(t - tb), x);
+                    ry.row(k, (int)(t - tb), d);
+                    dpre(x, d, true, e);
+                    back(e, o);
+                    output(t - (W - 1), o);
+                }
+            }
         }
+        wait_copies<0>();
+        drain(t1);
     }
     float *part = p.partial + row * (long)(W + 1) * p.D + c;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) part[(long)j * p.D + v] = dw[j][v];
-        part[(long)W * p.D + v] = db[v];
-    }
+    for (int j = 0; j < W; ++j) store_packet<float, V>(part + (long)j * p.D, pack<float, V>(dw[j]));
+    store_packet<float, V>(part + (long)W * p.D, pack<float, V>(db));
 }
 
 // Sums the rows' partial sums in order: 8 threads per column, a warp's 32
@@ -339,15 +460,14 @@ __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvProblem p, 
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) row[j] = load_packet<T, V>(st + (long)j * p.D);
     row[W - 1] = load_packet<T, V>(static_cast<const T *>(p.x) + n * p.ld_x + c);
-    float o[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) o[v] = p.bias ? p.bias[c + v] : 0.f;
+    float w[W][V], o[V];
+    load_weights<V, W>(p, c, w, o);
 #pragma unroll
     for (int j = 0; j < W; ++j) {
         float x[V];
         unpack<T, V>(row[j], x);
 #pragma unroll
-        for (int v = 0; v < V; ++v) o[v] = fmaf(p.w[(long)(c + v) * W + j], x[v], o[v]);
+        for (int v = 0; v < V; ++v) o[v] = fmaf(w[j][v], x[v], o[v]);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) o[v] = conv_act(o[v], p.act);
@@ -372,33 +492,30 @@ cudaError_t copy_states(const void *from, void *to, long n, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-ConvGrid conv_grid(int D, int V, int run, long T_total) {
+// Runs such that `blocks` blocks cover the tokens, of at least `least` tokens.
+ConvGrid conv_grid(int D, int V, long T_total, long blocks, int least) {
     ConvGrid g;
     const int packets = (D + V - 1) / V;
     g.cl = 1;
     while (g.cl < packets && g.cl < kConvThreads) g.cl *= 2;
     g.ctiles = (packets + g.cl - 1) / g.cl;
-    g.run = run;
-    g.nruns = (T_total + run - 1) / run;
+    const long rows = std::max(1L, blocks / g.ctiles) * (kConvThreads / g.cl);
+    g.run = (int)std::max<long>(least, (T_total + rows - 1) / rows);
+    g.nruns = (T_total + g.run - 1) / g.run;
     return g;
 }
-
-// Rows of partial sums of the gradient: enough token runs in flight to fill
-// the device (two blocks of 256 threads on each of 152 SMs), no more than the
-// tokens need.
-constexpr int kBwdRun = 32;
+// One wave on 152 SMs.  The gradient recomputes W - 1 tokens a run, so its
+// shortest runs are longer; each run leaves one row of partial sums.
+ConvGrid conv_fwd_grid(int D, int V, long T_total) { return conv_grid(D, V, T_total, 152L * kFwdBlocks, 8); }
+ConvGrid conv_bwd_grid(int D, int V, long T_total) { return conv_grid(D, V, T_total, 152L * kBwdBlocks, 16); }
 long conv_bwd_rows(const ConvGrid &g) {
     const int per = kConvThreads / g.cl;
-    long blocks = (152L * 2 + g.ctiles - 1) / g.ctiles;
-    if (blocks < 1) blocks = 1;
-    long rows = blocks * per;
-    const long most = (g.nruns + per - 1) / per * per;
-    return rows < most ? rows : (most > 0 ? most : per);
+    return std::max(1L, (g.nruns + per - 1) / per) * per;
 }
 
 template <typename T, int V, int W>
 cudaError_t conv_fwd_t(const ConvProblem &p, cudaStream_t st) {
-    const ConvGrid g = conv_grid(p.D, V, 16, p.T_total);
+    const ConvGrid g = conv_fwd_grid(p.D, V, p.T_total);
     const long blocks = (g.nruns + kConvThreads / g.cl - 1) / (kConvThreads / g.cl) * g.ctiles;
     if (blocks > 0x7fffffffL) return cudaErrorInvalidConfiguration;
     conv_fwd_kernel<T, V, W><<<(unsigned)blocks, kConvThreads, 0, st>>>(p, g);
@@ -406,10 +523,17 @@ cudaError_t conv_fwd_t(const ConvProblem &p, cudaStream_t st) {
 }
 template <typename T, int V, int W>
 cudaError_t conv_bwd_t(const ConvProblem &p, cudaStream_t st) {
-    const ConvGrid g = conv_grid(p.D, V, kBwdRun, p.T_total);
+    const ConvGrid g = conv_bwd_grid(p.D, V, p.T_total);
     const long rows = conv_bwd_rows(g);
     const long blocks = rows / (kConvThreads / g.cl) * g.ctiles;
-    conv_bwd_kernel<T, V, W><<<(unsigned)blocks, kConvThreads, 0, st>>>(p, g, rows);
+    if (blocks > 0x7fffffffL) return cudaErrorInvalidConfiguration;
+    constexpr int bytes = 2 * (kConvAhead + 1) * kBatch<T, V> * kConvThreads * (int)sizeof(Packet<T, V>);
+    if (bytes > 48 * 1024) {
+        const cudaError_t err = cudaFuncSetAttribute(conv_bwd_kernel<T, V, W>,
+                                                     cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (err != cudaSuccess) return err;
+    }
+    conv_bwd_kernel<T, V, W><<<(unsigned)blocks, kConvThreads, bytes, st>>>(p, g);
     cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     const long cols = (long)(W + 1) * p.D;
@@ -446,23 +570,23 @@ cudaError_t conv_width(const ConvProblem &p, cudaStream_t st) {
 
 template <ConvKind K, typename T>
 cudaError_t conv_dispatch(const ConvProblem &p, cudaStream_t st) {
-    // 16-byte packets where every row of every array starts on a 16-byte
-    // boundary, single elements otherwise
-    constexpr int V = 16 / (int)sizeof(T);
-    bool wide = p.D % V == 0 && rows_aligned(p.x, p.ld_x, sizeof(T), 16);
-    if (K == ConvKind::kBwd) wide = wide && rows_aligned(p.dy, p.ld_dy, sizeof(T), 16);
+    // packets of four channels where every row of every array starts on a
+    // packet's boundary, single elements otherwise
+    constexpr int V = 4, bytes = V * (int)sizeof(T);
+    bool wide = p.D % V == 0 && rows_aligned(p.x, p.ld_x, sizeof(T), bytes) &&
+                rows_aligned(p.w, 4, 4, 16);
+    if (K == ConvKind::kBwd) wide = wide && rows_aligned(p.dy, p.ld_dy, sizeof(T), bytes);
     const void *dense[] = {p.state0, p.dstate_T, p.y, p.state_T, p.dx, p.dstate0};
-    for (const void *ptr : dense) wide = wide && rows_aligned(ptr, p.D, sizeof(T), 16);
+    for (const void *ptr : dense) wide = wide && rows_aligned(ptr, p.D, sizeof(T), bytes);
     return wide ? conv_width<K, T, V>(p, st) : conv_width<K, T, 1>(p, st);
 }
 
 }  // namespace
 
 size_t conv_bwd_workspace(int T_total, int D, int width, mdn_dtype dtype) {
-    const int V = dtype == MDN_BF16 ? 8 : 4;
     size_t most = 0;
-    for (int v : {V, 1}) {
-        const long rows = conv_bwd_rows(conv_grid(D, v, kBwdRun, T_total));
+    for (int v : {4, 1}) {
+        const long rows = conv_bwd_rows(conv_bwd_grid(D, v, T_total));
         const size_t need = (size_t)rows * (width + 1) * D * sizeof(float);
         most = need > most ? need : most;
     }
