@@ -10,8 +10,12 @@
 //   dw_pre = sum dh X r2;  dscale = sum dX b;  dw_post = sum dn y r1
 //
 // Memory bound: a row's elements stay in registers between its reductions, so
-// every array is read or written once.  The gradient's blocks each take many
-// rows and keep the columns' parameter sums in registers.
+// every array is read or written once.  Blocks take rows in turn, and every
+// thread copies its packets of the rows ahead into shared memory that only it
+// reads, so that the reductions of one row do not hold up the loads of the
+// next.  The gradient keeps the columns' parameter sums in registers.
+#include <algorithm>
+
 #include "mdn_ssm.cuh"
 
 namespace mdn {
@@ -25,14 +29,14 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float *red, int &turn
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if (tpr == 32) return v;
-    float *r = red + turn * 32;
-    turn ^= 1;
-    const int warp = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0) r[warp] = v;
+    float *r = red + turn;
+    turn ^= 32;
+    if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = v;
     __syncthreads();
-    const int wpr = tpr >> 5, first = warp / wpr * wpr;
-    v = 0.f;
-    for (int w = 0; w < wpr; ++w) v += r[first + w];
+    // the row's warps: lane j takes warp j's sum, of tpr / 32 that repeat
+    const int wpr = tpr >> 5;
+    v = r[((threadIdx.x >> 5) & ~(wpr - 1)) + (threadIdx.x & (wpr - 1))];
+    for (int o = wpr >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
@@ -51,192 +55,292 @@ __device__ __forceinline__ void gate_act_d(float g, int act, float &a, float &d)
     }
 }
 
-template <typename T, int V, int NI>
-__global__ void __launch_bounds__(512) norm_fwd_kernel(NormProblem p, int tpr) {
-    __shared__ float red[64];
-    int turn = 0;
-    const int tid = threadIdx.x & (tpr - 1);
-    const long row = (long)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
-    const bool live = row < p.rows;
-    float y[NI][V], x[NI][V], g[NI][V];
+// V weights from column c on, in packets of 16 bytes where V has them; `none`
+// where there are no weights or no such column.
+template <int V>
+__device__ __forceinline__ void load_cols(const float *w, int c, int D, float none, float *f) {
+    constexpr int P = V < 4 ? V : 4;
+    if (w && c < D) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int c = (i * tpr + tid) * V;
-        if (live && c < p.D) {
-            const auto py = load_packet<T, V>(static_cast<const T *>(p.y) + row * p.ld_y + c);
-            const auto px = load_packet<T, V>(static_cast<const T *>(p.x) + row * p.ld_x + c);
-            if (p.gate)
-                unpack<T, V>(load_packet<T, V>(static_cast<const T *>(p.gate) + row * p.ld_gate + c), g[i]);
-            unpack<T, V>(py, y[i]);
-            unpack<T, V>(px, x[i]);
-        } else {
+        for (int i = 0; i < V; i += P) unpack<float, P>(load_packet<float, P>(w + c + i), f + i);
+    } else {
 #pragma unroll
-            for (int v = 0; v < V; ++v) y[i][v] = x[i][v] = g[i][v] = 0.f;
-        }
+        for (int i = 0; i < V; ++i) f[i] = none;
     }
-    const float inv_d = 1.f / (float)p.D;
-    float r1 = 1.f, r2 = 1.f;
-    if (p.w_post) {
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-#pragma unroll
-            for (int v = 0; v < V; ++v) ss = fmaf(y[i][v], y[i][v], ss);
-        r1 = rsqrtf(fmaf(row_sum(ss, tpr, red, turn), inv_d, p.eps));
-    }
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int c = (i * tpr + tid) * V;
-        if (c >= p.D) continue;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float b = y[i][v];
-            if (p.w_post) b *= r1 * p.w_post[c + v];
-            if (p.gate) b *= gate_act(g[i][v], p.gate_act);
-            const float X = p.scale ? fmaf(p.scale[c + v], b, x[i][v]) : x[i][v] + b;
-            x[i][v] = X;
-            ss = fmaf(X, X, ss);
-        }
-        if (live)
-            store_packet<T, V>(static_cast<T *>(p.x_out) + row * p.D + c, pack<T, V>(x[i]));
-    }
-    if (p.w_pre) {
-        r2 = rsqrtf(fmaf(row_sum(ss, tpr, red, turn), inv_d, p.eps));
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int c = (i * tpr + tid) * V;
-            if (!live || c >= p.D) continue;
-#pragma unroll
-            for (int v = 0; v < V; ++v) x[i][v] *= r2 * p.w_pre[c + v];
-            store_packet<T, V>(static_cast<T *>(p.h) + row * p.D + c, pack<T, V>(x[i]));
-        }
-    }
-    if (p.stats && live && tid == 0)
-        *reinterpret_cast<float2 *>(p.stats + 2 * row) = make_float2(r1, r2);
 }
 
-template <typename T, int V, int NI, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormProblem p, int tpr) {
+// Rows ahead by the bytes of a thread's packets of one array, so that 512
+// threads of the forward and 1024 of the gradient fit their copies; negative:
+// the rows are read where they are used.
+__host__ __device__ constexpr int fwd_ahead(int bytes) { return bytes <= 32 ? 2 : bytes <= 64 ? 1 : 0; }
+__host__ __device__ constexpr int bwd_ahead(int bytes) { return bytes <= 16 ? 1 : bytes <= 32 ? 0 : -1; }
+
+// This thread's packets of one array: of its rows in turn, copied AHEAD rows
+// early into AHEAD + 1 slots of shared memory that only it reads.
+template <typename T, int V, int NI, int AHEAD>
+struct RowStream {
+    const T *next;                    // the next row to copy (AHEAD < 0: to read)
+    long step;                        // elements to the row after
+    Packet<T, V> *ring;               // [AHEAD + 1][NI][blockDim.x], this thread's
+    int D, tpr, tid;
+
+    __device__ __forceinline__ RowStream(const void *src, long ld, long row, long rows_step, unsigned char *smem,
+                                         int which, int D_, int tpr_, int tid_)
+        : next(static_cast<const T *>(src) + row * ld + tid_ * V), step(rows_step * ld),
+          ring(reinterpret_cast<Packet<T, V> *>(smem) + which * (AHEAD + 1) * NI * blockDim.x + threadIdx.x),
+          D(D_), tpr(tpr_), tid(tid_) {}
+    __device__ __forceinline__ bool in(int i) const { return (i * tpr + tid) * V < D; }
+    // Copies the next row into `slot` (not past the last row).
+    __device__ __forceinline__ void issue(int slot, bool live) {
+        if constexpr (AHEAD >= 0) {
+            if (live) {
+                if constexpr (V * sizeof(T) >= 4) {
+#pragma unroll
+                    for (int i = 0; i < NI; ++i)
+                        if (in(i)) copy_packet<T, V>(&ring[(slot * NI + i) * blockDim.x], next + i * tpr * V);
+                } else {
+                    // too small to copy asynchronously: all loads, then the stores
+                    Packet<T, V> f[NI];
+#pragma unroll
+                    for (int i = 0; i < NI; ++i)
+                        if (in(i)) f[i] = load_packet<T, V>(next + i * tpr * V);
+#pragma unroll
+                    for (int i = 0; i < NI; ++i)
+                        if (in(i)) ring[(slot * NI + i) * blockDim.x] = f[i];
+                }
+            }
+            next += step;
+        }
+    }
+    // Packet i of the row in `slot` (zeros past the row's end).
+    __device__ __forceinline__ void get(int slot, int i, bool live, float *f) const {
+        if (live && in(i)) {
+            if constexpr (AHEAD >= 0) unpack<T, V>(ring[(slot * NI + i) * blockDim.x], f);
+            else unpack<T, V>(load_packet<T, V>(next + i * tpr * V), f);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) f[v] = 0.f;
+        }
+    }
+    __device__ __forceinline__ void done() {
+        if constexpr (AHEAD < 0) next += step;
+    }
+};
+
+// One row at a time per group of tpr threads; the columns' weights stay in
+// registers (w_post and scale meet as one factor).
+template <typename T, int V, int NI, bool GATE>
+__global__ void __launch_bounds__(512) norm_fwd_kernel(NormProblem p, int tpr) {
+    extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float red[64];
+    constexpr int AHEAD = fwd_ahead(NI * V * (int)sizeof(T));
     int turn = 0;
-    const int tid = threadIdx.x & (tpr - 1);
-    const int rpb = blockDim.x / tpr;
-    const long first = (long)blockIdx.x * rpb + threadIdx.x / tpr;
+    const int tid = threadIdx.x & (tpr - 1), mine = threadIdx.x / tpr;
+    const long rpb = blockDim.x / tpr, step = gridDim.x * rpb;
+    long row = blockIdx.x * rpb + mine;
+    using Stream = RowStream<T, V, NI, AHEAD>;
+    Stream sy(p.y, p.ld_y, row, step, smem, 0, p.D, tpr, tid);
+    Stream sx(p.x, p.ld_x, row, step, smem, 1, p.D, tpr, tid);
+    Stream sg(p.gate, p.ld_gate, row, step, smem, 2, p.D, tpr, tid);
+    auto issue = [&](int slot, bool live) {
+        sy.issue(slot, live);
+        sx.issue(slot, live);
+        if (GATE) sg.issue(slot, live);
+        commit_copies();
+    };
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) issue(k, row + k * step < p.rows);
+    float ws[NI][V], wpre[NI][V];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int c = (i * tpr + tid) * V;
+        float sc[V];
+        load_cols<V>(p.w_post, c, p.D, 1.f, ws[i]);
+        load_cols<V>(p.scale, c, p.D, 1.f, sc);
+        load_cols<V>(p.w_pre, c, p.D, 0.f, wpre[i]);
+#pragma unroll
+        for (int v = 0; v < V; ++v) ws[i][v] *= sc[v];
+    }
+    T *xo = static_cast<T *>(p.x_out) + row * p.D + tid * V;
+    T *ho = static_cast<T *>(p.h) + row * p.D + tid * V;
+    const long out_step = step * p.D;
     const float inv_d = 1.f / (float)p.D;
+    // every thread of a block makes the same number of rounds (the sums wait
+    // for the whole block)
+    int get = 0, put = AHEAD;
+    for (long base = blockIdx.x * rpb; base < p.rows; base += step) {
+        const bool live = row < p.rows;
+        issue(put, row + AHEAD * step < p.rows);
+        wait_copies<AHEAD>();
+        float y[NI][V], x[NI][V];
+        float r1 = 1.f, r2 = 1.f, ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            sy.get(get, i, live, y[i]);
+#pragma unroll
+            for (int v = 0; v < V; ++v) ss = fmaf(y[i][v], y[i][v], ss);
+        }
+        if (p.w_post) r1 = rsqrtf(fmaf(row_sum(ss, tpr, red, turn), inv_d, p.eps));
+        ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            float g[V];
+            sx.get(get, i, live, x[i]);
+            if (GATE) sg.get(get, i, live, g);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float b = y[i][v] * r1;
+                if (GATE) b *= gate_act(g[v], p.gate_act);
+                x[i][v] = fmaf(b, ws[i][v], x[i][v]);
+                ss = fmaf(x[i][v], x[i][v], ss);
+            }
+            if (live && sy.in(i)) store_packet<T, V>(xo + i * tpr * V, pack<T, V>(x[i]));
+        }
+        if (p.w_pre) {
+            r2 = rsqrtf(fmaf(row_sum(ss, tpr, red, turn), inv_d, p.eps));
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) x[i][v] *= r2 * wpre[i][v];
+                if (live && sy.in(i)) store_packet<T, V>(ho + i * tpr * V, pack<T, V>(x[i]));
+            }
+        }
+        if (p.stats && live && tid == 0)
+            *reinterpret_cast<float2 *>(p.stats + 2 * row) = make_float2(r1, r2);
+        row += step;
+        xo += out_step;
+        ho += out_step;
+        get = get == AHEAD ? 0 : get + 1;
+        put = put == AHEAD ? 0 : put + 1;
+    }
+    wait_copies<0>();
+}
+
+template <typename T, int V, int NI, bool GATE, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormProblem p, int tpr) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ float red[64];
+    constexpr int AHEAD = bwd_ahead(NI * V * (int)sizeof(T));
+    int turn = 0;
+    const int tid = threadIdx.x & (tpr - 1), mine = threadIdx.x / tpr;
+    const long rpb = blockDim.x / tpr, step = gridDim.x * rpb;
+    const long first = blockIdx.x * rpb + mine;
+    long row = first;
+    using Stream = RowStream<T, V, NI, AHEAD>;
+    Stream sy(p.y, p.ld_y, row, step, smem, 0, p.D, tpr, tid);
+    Stream sx(p.x, p.ld_x, row, step, smem, 1, p.D, tpr, tid);
+    Stream sd(p.dx_out, p.ld_dx_out, row, step, smem, 2, p.D, tpr, tid);
+    Stream sh(p.dh, p.ld_dh, row, step, smem, 3, p.D, tpr, tid);
+    Stream sg(p.gate, p.ld_gate, row, step, smem, 4, p.D, tpr, tid);
+    const bool pre = p.w_pre != nullptr;
+    auto issue = [&](int slot, bool live) {
+        sy.issue(slot, live);
+        sx.issue(slot, live);
+        sd.issue(slot, live);
+        sh.issue(slot, live && pre);
+        if (GATE) sg.issue(slot, live);
+        commit_copies();
+    };
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) issue(k, row + k * step < p.rows);
+    float wpost[NI][V], wpre[NI][V], sc[NI][V];
     float a_post[NI][V], a_pre[NI][V], a_scale[NI][V];
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
+    for (int i = 0; i < NI; ++i) {
+        const int c = (i * tpr + tid) * V;
+        load_cols<V>(p.w_post, c, p.D, 1.f, wpost[i]);
+        load_cols<V>(p.scale, c, p.D, 1.f, sc[i]);
+        load_cols<V>(p.w_pre, c, p.D, 0.f, wpre[i]);
 #pragma unroll
         for (int v = 0; v < V; ++v) a_post[i][v] = a_pre[i][v] = a_scale[i][v] = 0.f;
-    // every thread of a block makes the same number of rounds (the sums below
-    // wait for the whole block)
-    for (long base = (long)blockIdx.x * rpb; base < p.rows; base += (long)gridDim.x * rpb) {
-        const long row = base + threadIdx.x / tpr;
+    }
+    long at = row * p.D + tid * V;
+    const float inv_d = 1.f / (float)p.D;
+    int get = 0, put = AHEAD < 0 ? 0 : AHEAD;
+    for (long base = blockIdx.x * rpb; base < p.rows; base += step) {
         const bool live = row < p.rows;
         const float r1 = live ? p.stats[2 * row] : 0.f;
         const float r2 = live ? p.stats[2 * row + 1] : 0.f;
+        issue(put, row + AHEAD * step < p.rows);
+        wait_copies<(AHEAD < 0 ? 0 : AHEAD)>();
         float y[NI][V], X[NI][V], g[NI][V], dX[NI][V], dh[NI][V];
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int c = (i * tpr + tid) * V;
-            if (live && c < p.D) {
-                const auto py = load_packet<T, V>(static_cast<const T *>(p.y) + row * p.ld_y + c);
-                const auto px = load_packet<T, V>(static_cast<const T *>(p.x) + row * p.ld_x + c);
-                const auto pd =
-                    load_packet<T, V>(static_cast<const T *>(p.dx_out) + row * p.ld_dx_out + c);
-                if (p.gate)
-                    unpack<T, V>(load_packet<T, V>(static_cast<const T *>(p.gate) + row * p.ld_gate + c), g[i]);
-                if (p.w_pre)
-                    unpack<T, V>(load_packet<T, V>(static_cast<const T *>(p.dh) + row * p.ld_dh + c), dh[i]);
-                unpack<T, V>(py, y[i]);
-                unpack<T, V>(px, X[i]);
-                unpack<T, V>(pd, dX[i]);
-            } else {
-#pragma unroll
-                for (int v = 0; v < V; ++v) y[i][v] = X[i][v] = g[i][v] = dX[i][v] = dh[i][v] = 0.f;
-            }
-        }
         // X again, and mean(dh w_pre X)
         float s2 = 0.f;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int c = (i * tpr + tid) * V;
-            if (c >= p.D) continue;
+            sy.get(get, i, live, y[i]);
+            sx.get(get, i, live, X[i]);
+            sd.get(get, i, live, dX[i]);
+            sh.get(get, i, live && pre, dh[i]);
+            if (GATE) sg.get(get, i, live, g[i]);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                float b = y[i][v];
-                if (p.w_post) b *= r1 * p.w_post[c + v];
-                if (p.gate) b *= gate_act(g[i][v], p.gate_act);
-                X[i][v] = p.scale ? fmaf(p.scale[c + v], b, X[i][v]) : X[i][v] + b;
-                if (p.w_pre) {
-                    a_pre[i][v] = fmaf(dh[i][v] * r2, X[i][v], a_pre[i][v]);
-                    dh[i][v] *= p.w_pre[c + v];
-                    s2 = fmaf(dh[i][v], X[i][v], s2);
-                }
+                float b = y[i][v] * (r1 * wpost[i][v]);
+                if (GATE) b *= gate_act(g[i][v], p.gate_act);
+                X[i][v] = fmaf(sc[i][v], b, X[i][v]);
+                a_pre[i][v] = fmaf(dh[i][v] * r2, X[i][v], a_pre[i][v]);
+                dh[i][v] *= wpre[i][v];
+                s2 = fmaf(dh[i][v], X[i][v], s2);
             }
         }
-        if (p.w_pre) {
-            const float k = row_sum(s2, tpr, red, turn) * inv_d * r2 * r2;
+        if (pre) {
+            const float m = row_sum(s2, tpr, red, turn) * inv_d * r2 * r2;
 #pragma unroll
             for (int i = 0; i < NI; ++i)
 #pragma unroll
                 for (int v = 0; v < V; ++v)
-                    dX[i][v] = fmaf(r2, fmaf(-k, X[i][v], dh[i][v]), dX[i][v]);
+                    dX[i][v] = fmaf(r2, fmaf(-m, X[i][v], dh[i][v]), dX[i][v]);
         }
         // through the residual sum, the scale and the gate; mean(dn w_post y)
         float s1 = 0.f;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int c = (i * tpr + tid) * V;
-            if (c >= p.D) continue;
+            const bool here = live && sy.in(i);
+            const long o = at + i * tpr * V;
+            if (here) store_packet<T, V>(static_cast<T *>(p.dx) + o, pack<T, V>(dX[i]));
             float dg[V];
-            if (live)
-                store_packet<T, V>(static_cast<T *>(p.dx) + row * p.D + c, pack<T, V>(dX[i]));
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float n = p.w_post ? y[i][v] * r1 * p.w_post[c + v] : y[i][v];
+                const float n = y[i][v] * (r1 * wpost[i][v]);
                 float act = 1.f, dact = 0.f;
-                if (p.gate) gate_act_d(g[i][v], p.gate_act, act, dact);
-                float db = dX[i][v];
-                if (p.scale) {
-                    a_scale[i][v] = fmaf(db, n * act, a_scale[i][v]);
-                    db *= p.scale[c + v];
-                }
+                if (GATE) gate_act_d(g[i][v], p.gate_act, act, dact);
+                a_scale[i][v] = fmaf(dX[i][v], n * act, a_scale[i][v]);
+                const float db = dX[i][v] * sc[i][v];
                 dg[v] = db * n * dact;
-                float dn = db * act;
-                if (p.w_post) {
-                    a_post[i][v] = fmaf(dn * r1, y[i][v], a_post[i][v]);
-                    dn *= p.w_post[c + v];
-                    s1 = fmaf(dn, y[i][v], s1);
-                }
-                dX[i][v] = dn;
+                const float dn = db * act;
+                a_post[i][v] = fmaf(dn * r1, y[i][v], a_post[i][v]);
+                dX[i][v] = dn * wpost[i][v];
+                s1 = fmaf(dX[i][v], y[i][v], s1);
             }
-            if (p.gate && live)
-                store_packet<T, V>(static_cast<T *>(p.dgate) + row * p.D + c, pack<T, V>(dg));
+            if (GATE && here) store_packet<T, V>(static_cast<T *>(p.dgate) + o, pack<T, V>(dg));
         }
-        const float k = p.w_post ? row_sum(s1, tpr, red, turn) * inv_d * r1 * r1 : 0.f;
+        // without w_post r1 is 1 and y passes on as it is
+        const float m = p.w_post ? row_sum(s1, tpr, red, turn) * inv_d * r1 * r1 : 0.f;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int c = (i * tpr + tid) * V;
-            if (!live || c >= p.D) continue;
-            if (p.w_post) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) dX[i][v] = r1 * fmaf(-k, y[i][v], dX[i][v]);
-            }
-            store_packet<T, V>(static_cast<T *>(p.dy) + row * p.D + c, pack<T, V>(dX[i]));
+            for (int v = 0; v < V; ++v) dX[i][v] = r1 * fmaf(-m, y[i][v], dX[i][v]);
+            if (live && sy.in(i))
+                store_packet<T, V>(static_cast<T *>(p.dy) + at + i * tpr * V, pack<T, V>(dX[i]));
         }
+        row += step;
+        at += step * p.D;
+        get = AHEAD <= 0 || get == AHEAD ? 0 : get + 1;
+        put = AHEAD <= 0 || put == AHEAD ? 0 : put + 1;
+        sy.done(); sx.done(); sd.done(); sh.done(); sg.done();
     }
-    float *part = p.partial + first * 3L * p.D;
+    wait_copies<0>();
+    float *part = p.partial + first * 3L * p.D + tid * V;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-        const int c = (i * tpr + tid) * V;
-        if (c >= p.D) continue;
+        if (!sy.in(i)) continue;
+        constexpr int P = V < 4 ? V : 4;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            part[c + v] = a_post[i][v];
-            part[p.D + c + v] = a_pre[i][v];
-            part[2L * p.D + c + v] = a_scale[i][v];
+        for (int v = 0; v < V; v += P) {
+            float *o = part + i * tpr * V + v;
+            store_packet<float, P>(o, pack<float, P>(a_post[i] + v));
+            store_packet<float, P>(o + p.D, pack<float, P>(a_pre[i] + v));
+            store_packet<float, P>(o + 2L * p.D, pack<float, P>(a_scale[i] + v));
         }
     }
 }
@@ -283,38 +387,56 @@ NormShape norm_shape(int D, int V, int soft, int most) {
     s.threads = s.tpr < 128 ? 128 : s.tpr;
     return s;
 }
-// The forward holds three arrays of a row, the gradient five and three sums.
-NormShape norm_fwd_shape(int D, int V) { return norm_shape(D, V, 16, 512); }
-NormShape norm_bwd_shape(int D, int V) { return norm_shape(D, V, 8, 1024); }
-int norm_bwd_blocks(int rows, const NormShape &s) {
-    const int rpb = s.threads / s.tpr;
-    const long most = ((long)rows + rpb - 1) / rpb;
-    const long want = 152L * (s.threads >= 512 ? 1 : 512 / s.threads);
-    return (int)(most < want ? most : want);
+// The forward holds two arrays of a row, the gradient five and three sums.
+// Few rows (less than two for each SM) take more threads and fewer values:
+// their time is the latency of one row.
+NormShape norm_fwd_shape(int rows, int D, int V) {
+    return rows < 2 * 152 ? norm_shape(D, V, V, 512) : norm_shape(D, V, 16, 512);
 }
+NormShape norm_bwd_shape(int D, int V) { return norm_shape(D, V, 8, 1024); }
+// Blocks that share the rows: as many threads on each of 152 SMs as their
+// registers allow, where there are rows for them.
+int norm_blocks(int rows, const NormShape &s, int threads) {
+    const long rpb = s.threads / s.tpr, most = (rows + rpb - 1) / rpb;
+    return (int)std::min(most, 152L * std::max(1, threads / s.threads));
+}
+int fwd_threads(const NormShape &s, int V) { return s.ni * V <= 16 ? 640 : 512; }
+constexpr int kBwdThreads = 512;
 
 template <bool BWD, typename T, int V, int NI>
 cudaError_t norm_launch(const NormProblem &p, const NormShape &s, cudaStream_t st) {
+    const int blocks = norm_blocks(p.rows, s, BWD ? kBwdThreads : fwd_threads(s, V));
+    constexpr int each = NI * V * (int)sizeof(T);
+    constexpr int slots = BWD ? 5 * (bwd_ahead(each) + 1) : 3 * (fwd_ahead(each) + 1);
+    const int bytes = slots * each * s.threads;
+    auto launch = [&](auto kernel) {
+        if (bytes > 48 * 1024) {
+            const cudaError_t err =
+                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+            if (err != cudaSuccess) return err;
+        }
+        kernel<<<blocks, s.threads, bytes, st>>>(p, s.tpr);
+        return cudaGetLastError();
+    };
+    const bool gate = p.gate != nullptr;
     if constexpr (BWD) {
-        const int blocks = norm_bwd_blocks(p.rows, s);
-        if (s.threads <= 512)
-            norm_bwd_kernel<T, V, NI, 512><<<blocks, s.threads, 0, st>>>(p, s.tpr);
-        else
-            norm_bwd_kernel<T, V, NI, 1024><<<blocks, s.threads, 0, st>>>(p, s.tpr);
-        cudaError_t err = cudaGetLastError();
+        const cudaError_t err =
+            s.threads <= 512 ? (gate ? launch(norm_bwd_kernel<T, V, NI, true, 512>)
+                                     : launch(norm_bwd_kernel<T, V, NI, false, 512>))
+                             : (gate ? launch(norm_bwd_kernel<T, V, NI, true, 1024>)
+                                     : launch(norm_bwd_kernel<T, V, NI, false, 1024>));
         if (err != cudaSuccess) return err;
         norm_reduce_kernel<<<(3 * p.D + 31) / 32, 256, 0, st>>>(
             p.partial, blocks * (s.threads / s.tpr), p.D, p.dw_post, p.dw_pre, p.dscale);
+        return cudaGetLastError();
     } else {
-        const int rpb = s.threads / s.tpr;
-        norm_fwd_kernel<T, V, NI><<<(p.rows + rpb - 1) / rpb, s.threads, 0, st>>>(p, s.tpr);
+        return gate ? launch(norm_fwd_kernel<T, V, NI, true>) : launch(norm_fwd_kernel<T, V, NI, false>);
     }
-    return cudaGetLastError();
 }
 
 template <bool BWD, typename T, int V>
 cudaError_t norm_items(const NormProblem &p, cudaStream_t st) {
-    const NormShape s = BWD ? norm_bwd_shape(p.D, V) : norm_fwd_shape(p.D, V);
+    const NormShape s = BWD ? norm_bwd_shape(p.D, V) : norm_fwd_shape(p.rows, p.D, V);
     constexpr int kMost = (BWD ? 16 : 32) / V;      // D = 16384
     if (s.ni == 1) return norm_launch<BWD, T, V, 1>(p, s, st);
     if (s.ni == 2) return norm_launch<BWD, T, V, 2>(p, s, st);
@@ -338,6 +460,7 @@ cudaError_t norm_dispatch(const NormProblem &p, cudaStream_t st) {
     if (BWD)
         wide = wide && rows_aligned(p.dx_out, p.ld_dx_out, sizeof(T), 16) &&
                rows_aligned(p.dh, p.ld_dh, sizeof(T), 16);
+    for (const float *w : {p.w_post, p.w_pre, p.scale}) wide = wide && rows_aligned(w, 0, 4, 16);
     const void *dense[] = {p.x_out, p.h, p.dy, p.dx, p.dgate};
     for (const void *ptr : dense) wide = wide && rows_aligned(ptr, p.D, sizeof(T), 16);
     return wide ? norm_items<BWD, T, V>(p, st) : norm_items<BWD, T, 1>(p, st);
@@ -350,7 +473,7 @@ size_t norm_bwd_workspace(int rows, int D, mdn_dtype dtype) {
     for (int v : {dtype == MDN_BF16 ? 8 : 4, 1}) {
         const NormShape s = norm_bwd_shape(D, v);
         const size_t need =
-            (size_t)norm_bwd_blocks(rows, s) * (s.threads / s.tpr) * 3 * D * sizeof(float);
+            (size_t)norm_blocks(rows, s, kBwdThreads) * (s.threads / s.tpr) * 3 * D * sizeof(float);
         most = need > most ? need : most;
     }
     return round256(most);
