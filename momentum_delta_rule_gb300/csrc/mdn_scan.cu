@@ -363,7 +363,7 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
 #pragma unroll
                     for (int i = 0; i < kStates; ++i) {
                         float e0, e1;
-                        split_pair(mul2(d, a2[c / 2][i]), e0, e1);
+                        split_pair(fma2(d, a2[c / 2][i], make_pair(kDecayBias, kDecayBias)), e0, e1);
                         const Pair a = make_pair(ex2(e0), ex2(e1));
                         if (REV) {
                             split_pair(h[c / 2][i], e0, e1);
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanProblem p) {
         for (int i = 0; i < kStates; ++i) {
             const bool in = n0 + i < p.N;
             const float b = in ? to_f32(Bp[i]) : 0.f, c = in ? to_f32(Cp[i]) : 0.f;
-            h[i] = fmaf(ex2(delta * (a[i] * kLog2e)), h[i], delta * u * b);
+            h[i] = fmaf(ex2(fmaf(delta, a[i] * kLog2e, kDecayBias)), h[i], delta * u * b);
             acc = fmaf(h[i], c, acc);
         }
         store_states(p.h_T, ch, n0, p.N, h);

@@ -291,7 +291,7 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
 #pragma unroll
                         for (int i = 0; i < kStates; ++i) {
                             float e0, e1;
-                            split_pair(mul2(make_pair(dl.e[0], dl.e[1]), a2[i]), e0, e1);
+                            split_pair(fma2(make_pair(dl.e[0], dl.e[1]), a2[i], make_pair(kDecayBias, kDecayBias)), e0, e1);
                             h[i] = fma2(make_pair(ex2(e0), ex2(e1)), h[i],
                                         make_pair(x0 * bv.e[i], x1 * bv.e[i]));
                         }
@@ -320,7 +320,7 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
 #pragma unroll
                     for (int i = 0; i < kStates; ++i) {
                         float e0, e1;
-                        split_pair(mul2(make_pair(dl.e[0], dl.e[1]), a2[i]), e0, e1);
+                        split_pair(fma2(make_pair(dl.e[0], dl.e[1]), a2[i], make_pair(kDecayBias, kDecayBias)), e0, e1);
                         a[j][i] = make_pair(ex2(e0), ex2(e1));
                         h[j + 1][i] = fma2(a[j][i], h[j][i], make_pair(x0 * bv.e[i], x1 * bv.e[i]));
                     }
@@ -471,36 +471,35 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
     }
 }
 
-// dB, dC [T_total, G, N]: the tiles' partial sums, in order.  Nothing is
-// written where malformed packed offsets left no slots (total_slots 0).
+// Sums what the blocks left, in order: dB, dC [rows, N] over the group's tiles
+// (rows = T_total * G; nothing is written where malformed packed offsets left
+// no slots, total_slots 0), then dA, dD_skip and ddt_bias over the blocks that
+// shared a tile.
 template <typename T>
 __global__ void __launch_bounds__(256)
-scan_reduce_bc_kernel(const int32_t *total_slots, const float *part, int gtiles, long rows, int N, T *dB, T *dC) {
-    if (total_slots && *total_slots == 0) return;
-    const long per = rows * 2 * N;
-    for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < per; i += (long)gridDim.x * 256) {
+scan_reduce_kernel(const int32_t *total_slots, BwdPartials w, int gtiles, long rows, int D, int N,
+                   T *dB, T *dC, float *dA, float *dD, float *dbias) {
+    const long per = rows * 2 * N, dn = (long)D * N;
+    const bool tokens = !total_slots || *total_slots != 0;
+    for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < per + dn + 2L * D; i += (long)gridDim.x * 256) {
         float v = 0.f;
-        for (int k = 0; k < gtiles; ++k) v += part[k * per + i];
-        const long row = i / (2 * N);
-        const int m = (int)(i - row * 2 * N);
-        if (m < N) dB[row * N + m] = from_f32<T>(v);
-        else dC[row * N + m - N] = from_f32<T>(v);
-    }
-}
-
-// out[i] = sum over the slots, in order, of part[slot][i].
-__global__ void __launch_bounds__(256)
-scan_reduce_params_kernel(BwdPartials w, long dn, int D, float *dA, float *dD, float *dbias) {
-    const long total = dn + 2L * D;
-    for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long)gridDim.x * 256) {
-        const float *src = i < dn ? w.A + i : i < dn + D ? w.D + (i - dn) : w.bias + (i - dn - D);
-        const long step = i < dn ? dn : D;
-        float *out = i < dn ? dA + i : i < dn + D ? dD : dbias;
+        if (i < per) {
+            if (!tokens) continue;
+#pragma unroll 4
+            for (int k = 0; k < gtiles; ++k) v += w.bc[k * per + i];
+            const long row = i / (2 * N);
+            const int m = (int)(i - row * 2 * N);
+            if (m < N) dB[row * N + m] = from_f32<T>(v);
+            else dC[row * N + m - N] = from_f32<T>(v);
+            continue;
+        }
+        const long q = i - per;
+        const float *src = q < dn ? w.A + q : q < dn + D ? w.D + (q - dn) : w.bias + (q - dn - D);
+        float *out = q < dn ? dA + q : q < dn + D ? dD : dbias;
         if (!out) continue;
-        float v = 0.f;
-        for (int s = 0; s < w.slots; ++s) v += src[s * step];
-        if (i < dn) *out = v;
-        else out[i < dn + D ? i - dn : i - dn - D] = v;
+        for (int s = 0; s < w.slots; ++s) v += src[s * (q < dn ? dn : D)];
+        if (q < dn) *out = v;
+        else out[q < dn + D ? q - dn : q - dn - D] = v;
     }
 }
 
@@ -585,16 +584,11 @@ cudaError_t bwd_dispatch(const ScanProblem &p, const Layout &l, const BwdPartial
     }
 #undef MDN_SCAN_CASE
     if (err != cudaSuccess) return err;
-    const long rows = (long)p.T_total * p.G, per = rows * 2 * p.N;
-    const long blocks = (per + 255) / 256;
-    scan_reduce_bc_kernel<T><<<(unsigned)(blocks < 152 * 8 ? blocks : 152 * 8), 256, 0, st>>>(
-        l.slot_off ? l.slot_off + p.n_seq : nullptr, w.bc, (int)b.gtiles, rows, p.N, static_cast<T *>(p.dB), static_cast<T *>(p.dC));
-    err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
-    const long dn = (long)p.D * p.N;
-    const long pb = (dn + 2L * p.D + 255) / 256;
-    scan_reduce_params_kernel<<<(unsigned)(pb < 152 * 8 ? pb : 152 * 8), 256, 0, st>>>(w, dn, p.D, p.dA, p.dD,
-                                                                                  p.ddt_bias);
+    const long rows = (long)p.T_total * p.G;
+    const long blocks = (rows * 2 * p.N + (long)p.D * (p.N + 2) + 255) / 256;
+    scan_reduce_kernel<T><<<(unsigned)std::min(blocks, 152L * 8), 256, 0, st>>>(
+        l.slot_off ? l.slot_off + p.n_seq : nullptr, w, (int)b.gtiles, rows, p.D, p.N,
+        static_cast<T *>(p.dB), static_cast<T *>(p.dC), p.dA, p.dD, p.ddt_bias);
     return cudaGetLastError();
 }
 

@@ -155,6 +155,13 @@ __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
+// Added to the arguments of the decays 2^(delta A log2 e), in the same fma.
+// ex2.approx falls short of 2^x by 1.5e-8 on average for x in [-0.5, 0]
+// (measured over 4 M arguments), and a decay a that enters 1 / (1 - a) times
+// turns that into up to 1e-5 of a state; raising the argument by 1.5e-8 / ln 2
+// takes the mean out.  Errors of dA at 8 x 2048 tokens against 64 bits: 1.8e-6
+// without it, 7.7e-7 with.  2^kDecayBias rounds to 1: delta = 0 changes nothing.
+constexpr float kDecayBias = 2.2e-8f;
 
 // 1 / (1 + e^{-x}); a large e^{-x} gives 0.
 __device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }

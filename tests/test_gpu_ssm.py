@@ -186,6 +186,19 @@ def test_scan_extreme_steps(dtype):
     check_scan(c, train=True)
 
 
+def test_scan_state_without_decay_or_input_is_kept():
+    # A = 0 or delta = 0 (exp(0) = 1), and B = 0: the state stays, bit for bit
+    import momentum_delta_rule_gb300 as mdn
+    c = _dev(scan_case("fp32", [501, 3], D=64, N=16, seed=14, softplus=False, bias=False))
+    zero = torch.zeros_like(c["Bm"])
+    for dt, A in ((c["dt"], torch.zeros_like(c["A"])), (torch.zeros_like(c["dt"]), c["A"])):
+        _, hT = mdn.ssm_scan_fwd(c["u"], dt, A, zero, c["Cm"], h0=c["h0"], **_scan_kw(c))
+        assert torch.equal(hT, c["h0"])
+        h = c["h0"].clone()
+        mdn.ssm_scan_step(c["u"][0, :2], dt[0, :2], A, zero[0, :2], c["Cm"][0, :2], h, softplus=False)
+        assert torch.equal(h, c["h0"])
+
+
 def test_scan_unaligned_rows():
     # rows and bases on no packet boundary
     c = scan_case("bf16", [37, 20], D=40, N=16, seed=8)
