@@ -459,68 +459,136 @@ cudaError_t fwd_dispatch(const ScanProblem &p, const Layout &l, Pass pass, cudaS
 
 // -------------------------------------------------------------------- step
 
-// Memory bound by the states (read and written once, in order): a thread
-// holds four states of one channel.
+constexpr int kStepWarps = 4;
+
+// Memory bound by the states, read and written once.  A warp takes 32
+// channels of one group and sequence: lane j prepares channel j's delta and
+// delta u once, the states then pass in steps of 32 / NL channels (whole
+// lines), K of them in flight, and the exchange that adds up a channel's
+// states leaves each owner lane one channel's output to finish.
 template <typename T, int NL>
-__global__ void __launch_bounds__(256) scan_step_kernel(ScanProblem p) {
-    const long idx = ((long)blockIdx.x * 256 + threadIdx.x);
-    const long ch = idx / NL;                        // sequence * D + channel
-    const int n0 = (int)(idx % NL) * kStates;
-    const bool live = ch < (long)p.n_seq * p.D;
-    const long s = live ? ch / p.D : 0;
-    const int d = live ? (int)(ch - s * p.D) : 0;
-    const bool mine = live && n0 < p.N;
-    float a[kStates], h[kStates], acc = 0.f, u = 0.f;
-    if (mine) {
-        load_states(p.A, d, n0, p.N, a);
-        if (p.N % kStates == 0) {
-            const float4 v = *reinterpret_cast<const float4 *>(p.h0 + ch * p.N + n0);
-            h[0] = v.x; h[1] = v.y; h[2] = v.z; h[3] = v.w;
-        } else {
-            load_states(p.h0, ch, n0, p.N, h);
-        }
-        u = to_f32(static_cast<const T *>(p.u)[s * p.ld_u + d]);
-        float delta = to_f32(static_cast<const T *>(p.dt)[s * p.ld_dt + d]);
-        if (p.dt_bias) delta += p.dt_bias[d];
+__global__ void __launch_bounds__(32 * kStepWarps) scan_step_kernel(ScanProblem p, int tiles) {
+    constexpr int CL = 32 / NL, K = NL < 4 ? NL : 4, STEPS = NL;
+    const int lane = threadIdx.x & 31;
+    const int tile = blockIdx.x * kStepWarps + (threadIdx.x >> 5);
+    if (tile >= tiles) return;
+    const int Dg = p.D / p.G, gtiles = tiles / p.G;
+    const int g = p.G == 1 ? 0 : tile / gtiles;
+    const int c0 = (tile - g * gtiles) * 32;         // first channel, within the group
+    const int d0 = g * Dg + c0;
+    const long s = blockIdx.y;
+    const int nl = lane % NL, cl = lane / NL, n0 = nl * kStates;
+    const bool whole = p.N % kStates == 0;
+    const T *up = static_cast<const T *>(p.u) + s * p.ld_u + d0;
+    const T *zp = static_cast<const T *>(p.z) + s * p.ld_z + d0;
+    const float *hp = p.h0 + (s * p.D + d0) * p.N, *ap = p.A + (long)d0 * p.N;
+    float *ho = p.h_T + (s * p.D + d0) * p.N;
+    float delta = 0.f, du = 0.f;
+    if (c0 + lane < Dg) {
+        const float u = to_f32(up[lane]);
+        delta = to_f32(static_cast<const T *>(p.dt)[s * p.ld_dt + d0 + lane]);
+        if (p.dt_bias) delta += p.dt_bias[d0 + lane];
         if (p.softplus) delta = softplus_rel(delta);
-        const long gb = (long)(d / (p.D / p.G)) * p.N + n0;
-        const T *Bp = static_cast<const T *>(p.Bm) + s * p.ld_B + gb;
-        const T *Cp = static_cast<const T *>(p.Cm) + s * p.ld_C + gb;
-#pragma unroll
-        for (int i = 0; i < kStates; ++i) {
-            const bool in = n0 + i < p.N;
-            const float b = in ? to_f32(Bp[i]) : 0.f, c = in ? to_f32(Cp[i]) : 0.f;
-            h[i] = fmaf(ex2(fmaf(delta, a[i] * kLog2e, kDecayBias)), h[i], delta * u * b);
-            acc = fmaf(h[i], c, acc);
-        }
-        store_states(p.h_T, ch, n0, p.N, h);
+        du = delta * u;
     }
+    float b[kStates] = {0.f, 0.f, 0.f, 0.f}, c[kStates] = {0.f, 0.f, 0.f, 0.f};
+    if (n0 < p.N) {
+        const T *bp = static_cast<const T *>(p.Bm) + s * p.ld_B + g * p.N + n0;
+        const T *cp = static_cast<const T *>(p.Cm) + s * p.ld_C + g * p.N + n0;
+        if (p.bc_wide) {
+            unpack<T, kStates>(load_packet<T, kStates>(bp), b);
+            unpack<T, kStates>(load_packet<T, kStates>(cp), c);
+        } else {
 #pragma unroll
-    for (int o = NL / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (live && n0 == 0) {
-        if (p.D_skip) acc = fmaf(p.D_skip[d], u, acc);
-        if (p.z) {
-            const float z = to_f32(static_cast<const T *>(p.z)[s * p.ld_z + d]);
-            acc *= z * sigmoid_f(z);
+            for (int i = 0; i < kStates; ++i)
+                if (n0 + i < p.N) {
+                    b[i] = to_f32(bp[i]);
+                    c[i] = to_f32(cp[i]);
+                }
         }
-        static_cast<T *>(p.y)[ch] = from_f32<T>(acc);
     }
+#pragma unroll 1
+    for (int st = 0; st < STEPS; st += K) {
+        float h[K][kStates], a[K][kStates], acc[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int ch = (st + k) * CL + cl;
+#pragma unroll
+            for (int i = 0; i < kStates; ++i) h[k][i] = a[k][i] = 0.f;
+            if (c0 + ch >= Dg || n0 >= p.N) continue;
+            if (whole) {
+                const float4 v = __ldcs(reinterpret_cast<const float4 *>(hp + ch * p.N + n0));
+                h[k][0] = v.x; h[k][1] = v.y; h[k][2] = v.z; h[k][3] = v.w;
+                unpack<float, kStates>(load_packet<float, kStates>(ap + ch * p.N + n0), a[k]);
+            } else {
+                load_states(hp, ch, n0, p.N, h[k]);
+                load_states(ap, ch, n0, p.N, a[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int ch = (st + k) * CL + cl;
+            const float dk = __shfl_sync(0xffffffffu, delta, ch), duk = __shfl_sync(0xffffffffu, du, ch);
+            acc[k] = 0.f;
+#pragma unroll
+            for (int i = 0; i < kStates; ++i) {
+                h[k][i] = fmaf(ex2(fmaf(dk, a[k][i] * kLog2e, kDecayBias)), h[k][i], duk * b[i]);
+                acc[k] = fmaf(h[k][i], c[i], acc[k]);
+            }
+            if (c0 + ch >= Dg || n0 >= p.N) continue;
+            if (whole) __stcs(reinterpret_cast<float4 *>(ho + ch * p.N + n0), make_float4(h[k][0], h[k][1], h[k][2], h[k][3]));
+            else store_states(ho, ch, n0, p.N, h[k]);
+        }
+        reduce_lanes<NL, K>(acc, nl);
+        const int ch = (st + reduced_first<NL, K>(nl)) * CL + cl;
+        if (nl < K && c0 + ch < Dg) {
+            float y = acc[0];
+            if (p.D_skip) y = fmaf(p.D_skip[d0 + ch], to_f32(up[ch]), y);
+            if (p.z) {
+                const float z = to_f32(zp[ch]);
+                y *= z * sigmoid_f(z);
+            }
+            static_cast<T *>(p.y)[s * p.D + d0 + ch] = from_f32<T>(y);
+        }
+    }
+}
+
+template <typename T, int NL>
+cudaError_t step_t(const ScanProblem &p, cudaStream_t st) {
+    const int tiles = p.G * ((p.D / p.G + 31) / 32);
+    const unsigned blocks = (unsigned)((tiles + kStepWarps - 1) / kStepWarps);
+    // the grid's second dimension ends at 65535
+    for (long s0 = 0; s0 < p.n_seq; s0 += 65535L) {
+        ScanProblem q = p;
+        auto rows = [&](const void *x, long ld) -> const void * {
+            return x ? static_cast<const T *>(x) + s0 * ld : nullptr;
+        };
+        q.u = rows(p.u, p.ld_u);
+        q.dt = rows(p.dt, p.ld_dt);
+        q.z = rows(p.z, p.ld_z);
+        q.Bm = rows(p.Bm, p.ld_B);
+        q.Cm = rows(p.Cm, p.ld_C);
+        q.y = const_cast<void *>(rows(p.y, p.D));
+        q.h0 = p.h0 + s0 * p.D * p.N;
+        q.h_T = p.h_T + s0 * p.D * p.N;
+        const dim3 grid(blocks, (unsigned)std::min(65535L, p.n_seq - s0));
+        scan_step_kernel<T, NL><<<grid, 32 * kStepWarps, 0, st>>>(q, tiles);
+        const cudaError_t err = cudaGetLastError();
+        if (err != cudaSuccess) return err;
+    }
+    return cudaSuccess;
 }
 
 template <typename T>
 cudaError_t step_dispatch(const ScanProblem &p, cudaStream_t st) {
-    const int nl = lanes_of_states(p.N);
-    const long blocks = ((long)p.n_seq * p.D * nl + 255) / 256;
-    if (blocks > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-    switch (nl) {
-        case 2: scan_step_kernel<T, 2><<<(unsigned)blocks, 256, 0, st>>>(p); break;
-        case 4: scan_step_kernel<T, 4><<<(unsigned)blocks, 256, 0, st>>>(p); break;
-        case 8: scan_step_kernel<T, 8><<<(unsigned)blocks, 256, 0, st>>>(p); break;
-        case 16: scan_step_kernel<T, 16><<<(unsigned)blocks, 256, 0, st>>>(p); break;
-        case 32: scan_step_kernel<T, 32><<<(unsigned)blocks, 256, 0, st>>>(p); break;
-        default: return cudaErrorInvalidValue;
+    switch (lanes_of_states(p.N)) {
+        case 2: return step_t<T, 2>(p, st);
+        case 4: return step_t<T, 4>(p, st);
+        case 8: return step_t<T, 8>(p, st);
+        case 16: return step_t<T, 16>(p, st);
+        case 32: return step_t<T, 32>(p, st);
     }
-    return cudaGetLastError();
+    return cudaErrorInvalidValue;
 }
 
 // to <- from, or zero (the states of a call without tokens).
