@@ -219,10 +219,8 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
                     if (zp) unpack<T, V>(sm.z[r][i][hid], z);
                     const auto sum = load_packet<float, V>(&sm.du[nb][t][col]);
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        o[v] = fmaf(skip[v], u[v], sum.e[v]);
-                        if (zp) o[v] *= z[v] * sigmoid_f(z[v]);
-                    }
+                    for (int v = 0; v < V; ++v) o[v] = fmaf(skip[v], u[v], sum.e[v]);
+                    if (zp) apply_gate<V>(o, z);
                     store_packet<T, V>(yp + (long)(tk + t) * p.D, pack<T, V>(o));
                 }
             }
@@ -240,17 +238,14 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
                     if (qlive && t < n) {
                         unpack<T, V>(sm.u[r][i][hid], u);
                         unpack<T, V>(sm.dt[r][i][hid], d);
+                        step_sizes<V>(d, bias, p.softplus);
+                        if (!REV) {
 #pragma unroll
-                        for (int v = 0; v < V; ++v) {
-                            d[v] += bias[v];
-                            if (p.softplus) d[v] = softplus_rel(d[v]);
-                            if (!REV) u[v] *= d[v];
-                        }
-                        if (REV && zp) {
+                            for (int v = 0; v < V; ++v) u[v] *= d[v];
+                        } else if (zp) {
                             float z[V];
                             unpack<T, V>(sm.z[r][i][hid], z);
-#pragma unroll
-                            for (int v = 0; v < V; ++v) u[v] *= z[v] * sigmoid_f(z[v]);
+                            apply_gate<V>(u, z);
                         }
                     }
                     store_packet<float, V>(&sm.delta[nb][t][col], pack<float, V>(d));

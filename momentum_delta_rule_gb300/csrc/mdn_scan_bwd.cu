@@ -241,15 +241,11 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
                     if (p.z) {
                         float z[V];
                         unpack<T, V>(sm.in_z[r][i][tid], z);
-#pragma unroll
-                        for (int v = 0; v < V; ++v) ef[v] *= z[v] * sigmoid_f(z[v]);
+                        apply_gate<V>(ef, z);
                     }
+                    step_sizes<V>(df, bias, p.softplus);
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        df[v] += bias[v];
-                        if (p.softplus) df[v] = softplus_rel(df[v]);
-                        dD[v] = fmaf(ef[v], uf[v], dD[v]);
-                    }
+                    for (int v = 0; v < V; ++v) dD[v] = fmaf(ef[v], uf[v], dD[v]);
                 }
                 store_packet<float, V>(&sm.delta[t][qcol], pack<float, V>(df));
                 store_packet<float, V>(&sm.u[t][qcol], pack<float, V>(uf));
@@ -422,12 +418,19 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
                     q = load_packet<float, V>(&sm.delta[t][qcol]);
                     unpack<T, V>(Sm::kSlots == 2 ? sm.in_dt[r][i][tid]
                                                  : load_packet<T, V>(static_cast<const T *>(p.dt) + tok * p.ld_dt + col), x);
+                    float sg[V];
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
                         o[v] = q.e[v];
-                        if (p.softplus) o[v] *= sigmoid_f(x[v] + bias[v]);
-                        dbias[v] += o[v];
+                        x[v] += bias[v];
                     }
+                    if (p.softplus) {
+                        sigmoids<V>(x, sg);
+#pragma unroll
+                        for (int v = 0; v < V; ++v) o[v] *= sg[v];
+                    }
+#pragma unroll
+                    for (int v = 0; v < V; ++v) dbias[v] += o[v];
                     store_packet<T, V>(static_cast<T *>(p.ddt) + tok * p.D + col, pack<T, V>(o));
                     if (p.z) {
                         float z[V];
@@ -436,11 +439,10 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
                                                      : load_packet<T, V>(static_cast<const T *>(p.dy) + tok * p.ld_dy + col), x);
                         unpack<T, V>(Sm::kSlots == 2 ? sm.in_z[r][i][tid]
                                                      : load_packet<T, V>(static_cast<const T *>(p.z) + tok * p.ld_z + col), z);
+                        sigmoids<V>(z, sg);
 #pragma unroll
-                        for (int v = 0; v < V; ++v) {
-                            const float sg = sigmoid_f(z[v]);
-                            o[v] = x[v] * q.e[v] * sg * fmaf(z[v], 1.f - sg, 1.f);
-                        }
+                        for (int v = 0; v < V; ++v)
+                            o[v] = x[v] * q.e[v] * (sg[v] * fmaf(z[v], 1.f - sg[v], 1.f));
                         store_packet<T, V>(static_cast<T *>(p.dz) + tok * p.D + col, pack<T, V>(o));
                     }
                 }

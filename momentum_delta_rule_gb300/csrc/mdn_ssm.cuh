@@ -148,6 +148,11 @@ __device__ __forceinline__ Pair mul2(Pair a, Pair b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
     return d;
 }
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    Pair d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
 __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
     Pair d;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
@@ -181,6 +186,68 @@ __device__ __forceinline__ float softplus_rel(float x) {
     s = fmaf(q, s, 0.33333161f);
     s = fmaf(q, s, 1.0000000038f);
     return fmaf(r + r, s, fmaxf(x, 0.f));
+}
+
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The same functions for V values, two to an instruction where V is even.
+// x <- softplus(x + bias), or x + bias.
+template <int V>
+__device__ __forceinline__ void step_sizes(float *x, const float *bias, bool softplus) {
+    if constexpr (V % 2 == 0) {
+        auto two = [](float c) { return make_pair(c, c); };
+#pragma unroll
+        for (int v = 0; v < V; v += 2) {
+            const Pair s = add2(make_pair(x[v], x[v + 1]), make_pair(bias[v], bias[v + 1]));
+            split_pair(s, x[v], x[v + 1]);
+            if (!softplus) continue;
+            float e0, e1, d0, d1;
+            split_pair(mul2(make_pair(fabsf(x[v]), fabsf(x[v + 1])), two(-kLog2e)), e0, e1);
+            const Pair e = make_pair(ex2(e0), ex2(e1));
+            split_pair(add2(e, two(2.f)), d0, d1);
+            const Pair r = mul2(e, make_pair(rcp(d0), rcp(d1))), q = mul2(r, r);
+            Pair p = fma2(q, two(0.14078889f), two(0.13982579f));
+            p = fma2(q, p, two(0.20012298f));
+            p = fma2(q, p, two(0.33333161f));
+            p = fma2(q, p, two(1.0000000038f));
+            split_pair(fma2(add2(r, r), p, make_pair(fmaxf(x[v], 0.f), fmaxf(x[v + 1], 0.f))), x[v], x[v + 1]);
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            x[v] += bias[v];
+            if (softplus) x[v] = softplus_rel(x[v]);
+        }
+    }
+}
+// s <- sigmoid(x)
+template <int V>
+__device__ __forceinline__ void sigmoids(const float *x, float *s) {
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int v = 0; v < V; v += 2) {
+            float e0, e1;
+            split_pair(mul2(make_pair(x[v], x[v + 1]), make_pair(-kLog2e, -kLog2e)), e0, e1);
+            split_pair(add2(make_pair(ex2(e0), ex2(e1)), make_pair(1.f, 1.f)), e0, e1);
+            s[v] = rcp(e0);
+            s[v + 1] = rcp(e1);
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[v] = sigmoid_f(x[v]);
+    }
+}
+// y <- y z sigmoid(z)
+template <int V>
+__device__ __forceinline__ void apply_gate(float *y, const float *z) {
+    float s[V];
+    sigmoids<V>(z, s);
+#pragma unroll
+    for (int v = 0; v < V; ++v) y[v] *= z[v] * s[v];
 }
 
 // The sequence that token t of a packed batch belongs to: the largest s with
