@@ -410,7 +410,8 @@ cudaError_t norm_launch(const NormProblem &p, const NormShape &s, cudaStream_t s
     constexpr int slots = BWD ? 5 * (bwd_ahead(each) + 1) : 3 * (fwd_ahead(each) + 1);
     const int bytes = slots * each * s.threads;
     auto launch = [&](auto kernel) {
-        if (bytes > 48 * 1024) {
+        // the kernels' own static arrays count towards the 48 KiB too
+        if (bytes > 47 * 1024) {
             const cudaError_t err =
                 cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
             if (err != cudaSuccess) return err;

@@ -455,6 +455,13 @@ def test_norm_widths(dtype, D):
     check_norm(dtype, 5, D, seed=D)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("D", [3, 96, 130, 513, 1026, 2047, 2048, 3000, 4097, 8190, 16384])
+def test_norm_widths_of_many_rows(dtype, D):
+    # more rows than the kernels' small-batch shapes take
+    check_norm(dtype, 640, D, gate="silu", seed=D)
+
+
 @pytest.mark.parametrize("post,pre,scale", [(True, False, False), (False, True, True), (False, False, True), (True, True, False)])
 @pytest.mark.parametrize("gate", [None, "sigmoid", "silu"])
 def test_norm_options(post, pre, scale, gate):
