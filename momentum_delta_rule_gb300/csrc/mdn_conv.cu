@@ -139,12 +139,20 @@ struct RowRing {
     Packet<T, V> (*at)[kRows][kConvThreads];
     const T *src;                      // the run's first row, this thread's channels
     long ld;
-    __device__ __forceinline__ void issue(int k, long rows) const {
+    Copies<T, V, kRows> copies;
+    __device__ __forceinline__ RowRing(Packet<T, V> (*at_)[kRows][kConvThreads], const T *src_, long ld_)
+        : at(at_), src(src_), ld(ld_) {
+        copies.clear();
+    }
+    // Batch k, two ahead of the one in use: a copy that goes through registers
+    // reaches shared memory with the next issue, still one ahead.
+    __device__ __forceinline__ void issue(int k, long rows) {
         const int slot = k % (kConvAhead + 1);
+        copies.put();
 #pragma unroll
         for (int i = 0; i < kRows; ++i)
             if (k * kRows + i < rows)
-                copy_packet<T, V>(&at[slot][i][threadIdx.x], src + (long)(k * kRows + i) * ld);
+                copies.get(i, &at[slot][i][threadIdx.x], src + (long)(k * kRows + i) * ld);
     }
     __device__ __forceinline__ void row(int k, int i, float *f) const {
         unpack<T, V>(at[k % (kConvAhead + 1)][i][threadIdx.x], f);
@@ -187,7 +195,7 @@ __global__ void __launch_bounds__(kConvThreads, kFwdBlocks) conv_fwd_kernel(Conv
     if (row >= g.nruns || c >= p.D) return;
     const long t0 = row * g.run;
     const long t1 = min(t0 + g.run, (long)p.T_total);
-    const RowRing<T, V> rx{ring, static_cast<const T *>(p.x) + t0 * p.ld_x + c, p.ld_x};
+    RowRing<T, V> rx{ring, static_cast<const T *>(p.x) + t0 * p.ld_x + c, p.ld_x};
 #pragma unroll
     for (int k = 0; k < kConvAhead; ++k) {
         rx.issue(k, t1 - t0);
@@ -294,8 +302,8 @@ __global__ void __launch_bounds__(kConvThreads, kBwdBlocks) conv_bwd_kernel(Conv
         const long t1 = min(t0 + g.run, (long)p.T_total);
         const T *xp = static_cast<const T *>(p.x) + c, *dyp = static_cast<const T *>(p.dy) + c;
         Ring *ring = reinterpret_cast<Ring *>(smem_raw);
-        const RowRing<T, V> rx{ring[0], xp + t0 * p.ld_x, p.ld_x};
-        const RowRing<T, V> ry{ring[1], dyp + t0 * p.ld_dy, p.ld_dy};
+        RowRing<T, V> rx{ring[0], xp + t0 * p.ld_x, p.ld_x};
+        RowRing<T, V> ry{ring[1], dyp + t0 * p.ld_dy, p.ld_dy};
 #pragma unroll
         for (int k = 0; k < kConvAhead; ++k) {
             rx.issue(k, t1 - t0);
@@ -570,22 +578,27 @@ cudaError_t conv_width(const ConvProblem &p, cudaStream_t st) {
 
 template <ConvKind K, typename T>
 cudaError_t conv_dispatch(const ConvProblem &p, cudaStream_t st) {
-    // packets of four channels where every row of every array starts on a
-    // packet's boundary, single elements otherwise
-    constexpr int V = 4, bytes = V * (int)sizeof(T);
-    bool wide = p.D % V == 0 && rows_aligned(p.x, p.ld_x, sizeof(T), bytes) &&
-                rows_aligned(p.w, 4, 4, 16);
-    if (K == ConvKind::kBwd) wide = wide && rows_aligned(p.dy, p.ld_dy, sizeof(T), bytes);
-    const void *dense[] = {p.state0, p.dstate_T, p.y, p.state_T, p.dx, p.dstate0};
-    for (const void *ptr : dense) wide = wide && rows_aligned(ptr, p.D, sizeof(T), bytes);
-    return wide ? conv_width<K, T, V>(p, st) : conv_width<K, T, 1>(p, st);
+    // packets of four channels (or two) where every row of every array starts
+    // on a packet's boundary, single elements otherwise
+    const int V = packet_width(4, sizeof(T), [&](int v, int bytes) {
+        bool ok = p.D % v == 0 && rows_aligned(p.x, p.ld_x, sizeof(T), bytes) &&
+                  rows_aligned(p.w, 4, 4, v == 4 ? 16 : 4);
+        if (K == ConvKind::kBwd) ok = ok && rows_aligned(p.dy, p.ld_dy, sizeof(T), bytes);
+        const void *dense[] = {p.state0, p.dstate_T, p.y, p.state_T, p.dx, p.dstate0};
+        for (const void *ptr : dense) ok = ok && rows_aligned(ptr, p.D, sizeof(T), bytes);
+        return ok;
+    });
+    if (V == 4) return conv_width<K, T, 4>(p, st);
+    if constexpr (sizeof(T) == 2)
+        if (V == 2) return conv_width<K, T, 2>(p, st);
+    return conv_width<K, T, 1>(p, st);
 }
 
 }  // namespace
 
 size_t conv_bwd_workspace(int T_total, int D, int width, mdn_dtype dtype) {
     size_t most = 0;
-    for (int v : {4, 1}) {
+    for (int v : {4, 2, 1}) {
         const long rows = conv_bwd_rows(conv_bwd_grid(D, v, T_total));
         const size_t need = (size_t)rows * (width + 1) * D * sizeof(float);
         most = need > most ? need : most;

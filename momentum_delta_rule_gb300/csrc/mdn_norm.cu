@@ -83,32 +83,27 @@ struct RowStream {
     long step;                        // elements to the row after
     Packet<T, V> *ring;               // [AHEAD + 1][NI][blockDim.x], this thread's
     int D, tpr, tid;
+    Copies<T, V, AHEAD < 0 ? 1 : NI> copies;
 
     __device__ __forceinline__ RowStream(const void *src, long ld, long row, long rows_step, unsigned char *smem,
                                          int which, int D_, int tpr_, int tid_)
         : next(static_cast<const T *>(src) + row * ld + tid_ * V), step(rows_step * ld),
           ring(reinterpret_cast<Packet<T, V> *>(smem) + which * (AHEAD + 1) * NI * blockDim.x + threadIdx.x),
-          D(D_), tpr(tpr_), tid(tid_) {}
+          D(D_), tpr(tpr_), tid(tid_) {
+        copies.clear();
+    }
     __device__ __forceinline__ bool in(int i) const { return (i * tpr + tid) * V < D; }
-    // Copies the next row into `slot` (not past the last row).
+    // Copies the next row into `slot` (not past the last row).  A copy that goes
+    // through registers reaches shared memory with the next one.
     __device__ __forceinline__ void issue(int slot, bool live) {
         if constexpr (AHEAD >= 0) {
+            copies.put();
             if (live) {
-                if constexpr (V * sizeof(T) >= 4) {
 #pragma unroll
-                    for (int i = 0; i < NI; ++i)
-                        if (in(i)) copy_packet<T, V>(&ring[(slot * NI + i) * blockDim.x], next + i * tpr * V);
-                } else {
-                    // too small to copy asynchronously: all loads, then the stores
-                    Packet<T, V> f[NI];
-#pragma unroll
-                    for (int i = 0; i < NI; ++i)
-                        if (in(i)) f[i] = load_packet<T, V>(next + i * tpr * V);
-#pragma unroll
-                    for (int i = 0; i < NI; ++i)
-                        if (in(i)) ring[(slot * NI + i) * blockDim.x] = f[i];
-                }
+                for (int i = 0; i < NI; ++i)
+                    if (in(i)) copies.get(i, &ring[(slot * NI + i) * blockDim.x], next + i * tpr * V);
             }
+            if (AHEAD == 0) copies.put();
             next += step;
         }
     }
@@ -391,9 +386,9 @@ NormShape norm_shape(int D, int V, int soft, int most) {
 // Few rows (less than two for each SM) take more threads and fewer values:
 // their time is the latency of one row.
 NormShape norm_fwd_shape(int rows, int D, int V) {
-    return rows < 2 * 152 ? norm_shape(D, V, V, 512) : norm_shape(D, V, 16, 512);
+    return rows < 2 * 152 ? norm_shape(D, V, V, 512) : norm_shape(D, V, V < 4 ? 4 * V : 2 * V, 512);
 }
-NormShape norm_bwd_shape(int D, int V) { return norm_shape(D, V, 8, 1024); }
+NormShape norm_bwd_shape(int D, int V) { return norm_shape(D, V, V < 4 ? 4 * V : 8, V < 4 ? 512 : 1024); }
 // Blocks that share the rows: as many threads on each of 152 SMs as their
 // registers allow, where there are rows for them.
 int norm_blocks(int rows, const NormShape &s, int threads) {
@@ -454,24 +449,30 @@ cudaError_t norm_items(const NormProblem &p, cudaStream_t st) {
 
 template <bool BWD, typename T>
 cudaError_t norm_dispatch(const NormProblem &p, cudaStream_t st) {
-    constexpr int V = 16 / (int)sizeof(T);
-    bool wide = p.D % V == 0 && rows_aligned(p.y, p.ld_y, sizeof(T), 16) &&
-                rows_aligned(p.x, p.ld_x, sizeof(T), 16) &&
-                rows_aligned(p.gate, p.ld_gate, sizeof(T), 16);
-    if (BWD)
-        wide = wide && rows_aligned(p.dx_out, p.ld_dx_out, sizeof(T), 16) &&
-               rows_aligned(p.dh, p.ld_dh, sizeof(T), 16);
-    for (const float *w : {p.w_post, p.w_pre, p.scale}) wide = wide && rows_aligned(w, 0, 4, 16);
-    const void *dense[] = {p.x_out, p.h, p.dy, p.dx, p.dgate};
-    for (const void *ptr : dense) wide = wide && rows_aligned(ptr, p.D, sizeof(T), 16);
-    return wide ? norm_items<BWD, T, V>(p, st) : norm_items<BWD, T, 1>(p, st);
+    constexpr int MOST = 16 / (int)sizeof(T);
+    const int V = packet_width(MOST, sizeof(T), [&](int v, int bytes) {
+        bool ok = p.D % v == 0 && rows_aligned(p.y, p.ld_y, sizeof(T), bytes) &&
+                  rows_aligned(p.x, p.ld_x, sizeof(T), bytes) &&
+                  rows_aligned(p.gate, p.ld_gate, sizeof(T), bytes);
+        if (BWD)
+            ok = ok && rows_aligned(p.dx_out, p.ld_dx_out, sizeof(T), bytes) &&
+                 rows_aligned(p.dh, p.ld_dh, sizeof(T), bytes);
+        for (const float *w : {p.w_post, p.w_pre, p.scale}) ok = ok && rows_aligned(w, 0, 4, v >= 4 ? 16 : 4 * v);
+        const void *dense[] = {p.x_out, p.h, p.dy, p.dx, p.dgate};
+        for (const void *ptr : dense) ok = ok && rows_aligned(ptr, p.D, sizeof(T), bytes);
+        return ok;
+    });
+    if (V == MOST) return norm_items<BWD, T, MOST>(p, st);
+    if constexpr (sizeof(T) == 2)
+        if (V == 2) return norm_items<BWD, T, 2>(p, st);
+    return norm_items<BWD, T, 1>(p, st);
 }
 
 }  // namespace
 
 size_t norm_bwd_workspace(int rows, int D, mdn_dtype dtype) {
     size_t most = 0;
-    for (int v : {dtype == MDN_BF16 ? 8 : 4, 1}) {
+    for (int v : {dtype == MDN_BF16 ? 8 : 4, 2, 1}) {
         const NormShape s = norm_bwd_shape(D, v);
         const size_t need =
             (size_t)norm_blocks(rows, s, kBwdThreads) * (s.threads / s.tpr) * 3 * D * sizeof(float);

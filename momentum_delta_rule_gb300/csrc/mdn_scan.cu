@@ -121,7 +121,7 @@ struct FwdSmem {
     float du[2][kStage][S::CB];       // delta u, then sum_n C h of the same token
     float B[2][kStage][S::NP], C[2][kStage][S::NP];
     // the inputs as they are, one place for each packet of each helper
-    Packet<T, V> u[kRing][PS][S::HT], dt[kRing][PS][S::HT], z[kRing][PS][S::HT];
+    Slot<T, V> u[kRing][PS][S::HT], dt[kRing][PS][S::HT], z[kRing][PS][S::HT];
     Packet<T, 4> b[kRing][PB][S::HT], c[kRing][PB][S::HT];
 };
 
@@ -171,6 +171,9 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
             bias[v] = qlive && p.dt_bias ? p.dt_bias[d0 + col + v] : 0.f;
             skip[v] = qlive && p.D_skip ? p.D_skip[d0 + col + v] : 0.f;
         }
+        const Span<T> us = span_of<T>(REV ? p.dy : p.u, p.T_total, ld_u, p.D);
+        const Span<T> ds = span_of<T>(p.dt, p.T_total, p.ld_dt, p.D);
+        const Span<T> zs = span_of<T>(p.z, p.T_total, p.ld_z, p.D);
         auto issue = [&](int k) {
             const int tk = (REV ? stages - 1 - k : k) * kStage, n = it.len - tk, r = k % kRing;
             if (k < stages) {
@@ -178,9 +181,10 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
                 for (int i = 0; i < Sm::PS; ++i) {
                     const int t = i * RS + row;
                     if (t < n && t < kStage && qlive) {
-                        copy_packet<T, V>(&sm.u[r][i][hid], up + (long)(tk + t) * ld_u);
-                        copy_packet<T, V>(&sm.dt[r][i][hid], dp + (long)(tk + t) * p.ld_dt);
-                        if ((!PRE || REV) && zp) copy_packet<T, V>(&sm.z[r][i][hid], zp + (long)(tk + t) * p.ld_z);
+                        copy_slot<T, V>(&sm.u[r][i][hid], up + (long)(tk + t) * ld_u, us);
+                        copy_slot<T, V>(&sm.dt[r][i][hid], dp + (long)(tk + t) * p.ld_dt, ds);
+                        if ((!PRE || REV) && zp)
+                            copy_slot<T, V>(&sm.z[r][i][hid], zp + (long)(tk + t) * p.ld_z, zs);
                     }
                 }
 #pragma unroll
@@ -215,8 +219,8 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
                     const int t = i * RS + row;
                     if (t >= n) break;
                     float u[V], z[V], o[V];
-                    unpack<T, V>(sm.u[r][i][hid], u);
-                    if (zp) unpack<T, V>(sm.z[r][i][hid], z);
+                    unpack_slot<T, V>(sm.u[r][i][hid], up + (long)(tk + t) * ld_u, u);
+                    if (zp) unpack_slot<T, V>(sm.z[r][i][hid], zp + (long)(tk + t) * p.ld_z, z);
                     const auto sum = load_packet<float, V>(&sm.du[nb][t][col]);
 #pragma unroll
                     for (int v = 0; v < V; ++v) o[v] = fmaf(skip[v], u[v], sum.e[v]);
@@ -226,7 +230,8 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
             }
             wait_copies<kAhead>();
             if (k + 1 < stages) {
-                const int n = min(kStage, it.len - (REV ? stages - 2 - k : k + 1) * kStage), r = (k + 1) % kRing;
+                const int tk = (REV ? stages - 2 - k : k + 1) * kStage;
+                const int n = min(kStage, it.len - tk), r = (k + 1) % kRing;
                 const int n_zero = (n + S::TB - 1) / S::TB * S::TB;     // zeros up to a whole batch
 #pragma unroll
                 for (int i = 0; i < Sm::PS; ++i) {
@@ -236,15 +241,15 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
 #pragma unroll
                     for (int v = 0; v < V; ++v) u[v] = d[v] = 0.f;
                     if (qlive && t < n) {
-                        unpack<T, V>(sm.u[r][i][hid], u);
-                        unpack<T, V>(sm.dt[r][i][hid], d);
+                        unpack_slot<T, V>(sm.u[r][i][hid], up + (long)(tk + t) * ld_u, u);
+                        unpack_slot<T, V>(sm.dt[r][i][hid], dp + (long)(tk + t) * p.ld_dt, d);
                         step_sizes<V>(d, bias, p.softplus);
                         if (!REV) {
 #pragma unroll
                             for (int v = 0; v < V; ++v) u[v] *= d[v];
                         } else if (zp) {
                             float z[V];
-                            unpack<T, V>(sm.z[r][i][hid], z);
+                            unpack_slot<T, V>(sm.z[r][i][hid], zp + (long)(tk + t) * p.ld_z, z);
                             apply_gate<V>(u, z);
                         }
                     }
@@ -429,18 +434,21 @@ cudaError_t fwd_t(const ScanProblem &p, const Layout &l, Pass pass, cudaStream_t
 
 template <typename T>
 cudaError_t fwd_dispatch(const ScanProblem &p, const Layout &l, Pass pass, cudaStream_t st) {
-    // 16-byte packets where every row starts on a 16-byte boundary, single
-    // elements otherwise
-    constexpr int V = 16 / (int)sizeof(T);
-    const bool wide = (p.D / p.G) % V == 0 && rows_aligned(p.u, p.ld_u, sizeof(T), 16) &&
-                      rows_aligned(p.dt, p.ld_dt, sizeof(T), 16) &&
-                      rows_aligned(p.z, p.ld_z, sizeof(T), 16) &&
-                      rows_aligned(p.y, p.D, sizeof(T), 16) &&
-                      rows_aligned(p.dy, p.ld_dy, sizeof(T), 16);
+    // 16-byte packets (or pairs of two-byte elements) where every row starts on
+    // a packet's boundary, single elements otherwise
+    constexpr int MOST = 16 / (int)sizeof(T);
+    const int V = packet_width(MOST, sizeof(T), [&](int v, int bytes) {
+        return (p.D / p.G) % v == 0 && rows_aligned(p.u, p.ld_u, sizeof(T), bytes) &&
+               rows_aligned(p.dt, p.ld_dt, sizeof(T), bytes) &&
+               rows_aligned(p.z, p.ld_z, sizeof(T), bytes) &&
+               rows_aligned(p.y, p.D, sizeof(T), bytes) && rows_aligned(p.dy, p.ld_dy, sizeof(T), bytes);
+    });
 #define MDN_SCAN_CASE(NL, CPT, NW, HW)                                \
     case NL:                                                          \
-        return wide ? fwd_t<T, Shape<NL, CPT, NW, HW>, V>(p, l, pass, st)   \
-                    : fwd_t<T, Shape<NL, CPT, NW, HW>, 1>(p, l, pass, st);
+        if (V == MOST) return fwd_t<T, Shape<NL, CPT, NW, HW>, MOST>(p, l, pass, st); \
+        if constexpr (sizeof(T) == 2)                                 \
+            if (V == 2) return fwd_t<T, Shape<NL, CPT, NW, HW>, 2>(p, l, pass, st); \
+        return fwd_t<T, Shape<NL, CPT, NW, HW>, 1>(p, l, pass, st);
     switch (lanes_of_states(p.N)) {
         MDN_SCAN_CASE(2, 2, 2, 4)
         MDN_SCAN_CASE(4, 2, 4, 4)

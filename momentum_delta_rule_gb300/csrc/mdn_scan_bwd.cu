@@ -564,18 +564,22 @@ cudaError_t bwd_t(const ScanProblem &p, const Layout &l, const BwdPartials &w, c
 template <typename T>
 cudaError_t bwd_dispatch(const ScanProblem &p, const Layout &l, const BwdPartials &w,
                          const BwdPlan &b, cudaStream_t st) {
-    constexpr int V = 16 / (int)sizeof(T), bytes = 16;
-    bool wide = (p.D / p.G) % V == 0 && rows_aligned(p.u, p.ld_u, sizeof(T), bytes) &&
-                rows_aligned(p.dt, p.ld_dt, sizeof(T), bytes) &&
-                rows_aligned(p.z, p.ld_z, sizeof(T), bytes) &&
-                rows_aligned(p.dy, p.ld_dy, sizeof(T), bytes);
-    const void *dense[] = {p.du, p.ddt, p.dz};
-    for (const void *ptr : dense) wide = wide && rows_aligned(ptr, p.D, sizeof(T), bytes);
+    constexpr int MOST = 16 / (int)sizeof(T);
+    const int V = packet_width(MOST, sizeof(T), [&](int v, int bytes) {
+        bool ok = (p.D / p.G) % v == 0 && rows_aligned(p.u, p.ld_u, sizeof(T), bytes) &&
+                  rows_aligned(p.dt, p.ld_dt, sizeof(T), bytes) &&
+                  rows_aligned(p.z, p.ld_z, sizeof(T), bytes) &&
+                  rows_aligned(p.dy, p.ld_dy, sizeof(T), bytes);
+        const void *dense[] = {p.du, p.ddt, p.dz};
+        for (const void *ptr : dense) ok = ok && rows_aligned(ptr, p.D, sizeof(T), bytes);
+        return ok;
+    });
     cudaError_t err = cudaErrorInvalidValue;
 #define MDN_SCAN_CASE(NL)                                                    \
     case NL:                                                                 \
-        err = wide ? bwd_t<T, BwdShape<NL>::S, V>(p, l, w, b, st)            \
-                   : bwd_t<T, BwdShape<NL>::S, 1>(p, l, w, b, st);           \
+        if (V == MOST) err = bwd_t<T, BwdShape<NL>::S, MOST>(p, l, w, b, st); \
+        else if (V == 2) err = bwd_t<T, BwdShape<NL>::S, sizeof(T) == 2 ? 2 : 1>(p, l, w, b, st); \
+        else err = bwd_t<T, BwdShape<NL>::S, 1>(p, l, w, b, st);             \
         break;
     switch (lanes_of_states(p.N)) {
         MDN_SCAN_CASE(2)

@@ -2,6 +2,8 @@
 // structs, launchers, packets of elements and the elementwise functions.
 #pragma once
 
+#include <type_traits>
+
 #include "mdn_internal.cuh"
 
 namespace mdn {
@@ -68,6 +70,14 @@ mdn_status current_device_status(int **status);
 
 inline size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// The widest packet (elements: `most`, 2 or 1) for which `fits(bytes)` holds;
+// 2 only for two-byte elements, which it lets be copied asynchronously.
+template <typename F>
+inline int packet_width(int most, int el, F fits) {
+    if (fits(most, most * el)) return most;
+    return el == 2 && fits(2, 4) ? 2 : 1;
+}
+
 // Whether `bytes`-wide packets reach every row of a [rows, width] array of
 // `el`-byte elements whose rows lie ld elements apart.
 inline bool rows_aligned(const void *ptr, long ld, int el, int bytes) {
@@ -103,19 +113,100 @@ __device__ __forceinline__ void store_packet(T *dst, const Packet<T, V> &p) {
     *reinterpret_cast<Packet<T, V> *>(dst) = p;
 }
 
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "n"(BYTES)
+                 : "memory");
+}
 // Copies one packet from global to shared memory: asynchronously (visible to
 // this thread after wait_copies) where it is 4, 8 or 16 bytes, at once
 // otherwise.
 template <typename T, int V>
 __device__ __forceinline__ void copy_packet(Packet<T, V> *dst, const T *src) {
-    constexpr int bytes = V * (int)sizeof(T);
-    if constexpr (bytes >= 4) {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(
-                         static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
-                     "l"(src), "n"(bytes)
-                     : "memory");
+    if constexpr (V * sizeof(T) >= 4) cp_async<V * (int)sizeof(T)>(dst, src);
+    else *dst = load_packet<T, V>(src);
+}
+// The same for N packets at a time, without a wait whatever their size: packets
+// too small for an asynchronous copy are loaded into registers, and stored when
+// the next N are asked for (or by `put`), by when they have arrived.
+template <typename T, int V, int N>
+struct Copies {
+    static constexpr bool kAsync = V * sizeof(T) >= 4;
+    static constexpr uint32_t kNone = 0xffffffffu;
+    Packet<T, V> held[kAsync ? 1 : N];
+    uint32_t at[kAsync ? 1 : N];      // shared-memory addresses, kNone for none
+
+    __device__ __forceinline__ void clear() {
+        if constexpr (!kAsync) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) at[i] = kNone;
+        }
+    }
+    __device__ __forceinline__ void put() {
+        if constexpr (!kAsync) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (at[i] != kNone)
+                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(at[i]),
+                                 "h"(*reinterpret_cast<const unsigned short *>(&held[i]))
+                                 : "memory");
+            clear();
+        }
+    }
+    __device__ __forceinline__ void get(int i, Packet<T, V> *dst, const T *src) {
+        if constexpr (kAsync) {
+            copy_packet<T, V>(dst, src);
+        } else {
+            held[i] = load_packet<T, V>(src);
+            at[i] = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+        }
+    }
+};
+// And without registers: a place for one packet that a thread copies for
+// itself.  Packets of 4,
+// 8 or 16 bytes are copied as they are.  A single two-byte element comes as
+// the aligned word around it; which half it is follows from its address.  The
+// array's first and last elements, whose words may reach past the array, are
+// loaded and stored instead.
+template <typename T, int V>
+struct Slot {
+    static constexpr bool kWord = V * sizeof(T) < 4;
+    Packet<typename std::conditional<kWord, uint32_t, T>::type, V> p;
+};
+// The elements of an array whose words may reach past it.
+template <typename T>
+struct Span {
+    const T *first, *last;
+};
+// `rows` rows of `width` elements, ld apart.
+template <typename T>
+__device__ __forceinline__ Span<T> span_of(const void *base, long rows, long ld, int width) {
+    const T *b = static_cast<const T *>(base);
+    return Span<T>{b, b + (rows - 1) * ld + width - 1};
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void copy_slot(Slot<T, V> *dst, const T *src, const Span<T> &span) {
+    if constexpr (!Slot<T, V>::kWord) {
+        cp_async<V * (int)sizeof(T)>(dst, src);
     } else {
-        *dst = load_packet<T, V>(src);
+        const uintptr_t a = (uintptr_t)src;
+        if (src == span.first || src == span.last)
+            dst->p.e[0] = (uint32_t) * reinterpret_cast<const unsigned short *>(src) << (a & 2 ? 16 : 0);
+        else
+            cp_async<4>(dst, reinterpret_cast<const void *>(a & ~(uintptr_t)3));
+    }
+}
+// `src`: where the slot was copied from.
+template <typename T, int V>
+__device__ __forceinline__ void unpack_slot(const Slot<T, V> &s, const T *src, float *f) {
+    if constexpr (!Slot<T, V>::kWord) {
+        unpack<T, V>(s.p, f);
+    } else {
+        static_assert(std::is_same<T, __nv_bfloat16>::value, "bf16 is the upper half of an fp32");
+        f[0] = __uint_as_float((uintptr_t)src & 2 ? s.p.e[0] & 0xffff0000u : s.p.e[0] << 16);
     }
 }
 __device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
