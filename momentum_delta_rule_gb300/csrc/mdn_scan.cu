@@ -32,7 +32,7 @@ __device__ __forceinline__ int block_scan(int mine, int32_t *part, int &total) {
     __syncthreads();
     int before = 0;
     total = 0;
-    for (int w = 0; w < 32; ++w) {
+    for (int w = 0; w < (int)blockDim.x >> 5; ++w) {
         if (w < warp) before += part[w];
         total += part[w];
     }
@@ -57,7 +57,7 @@ layout_kernel(const int32_t *cu, int n_seq, int T_total, int cut, int trigger, i
         return;
     }
     int slots = 0;
-    for (int base = 0; base < n_seq; base += 1024) {
+    for (int base = 0; base < n_seq; base += blockDim.x) {
         const int s = base + threadIdx.x;
         int total;
         const int at = block_scan(s < n_seq ? (cu[s + 1] - cu[s] + kTokens - 1) / kTokens : 0, part, total);
@@ -79,7 +79,7 @@ layout_kernel(const int32_t *cu, int n_seq, int T_total, int cut, int trigger, i
     if (threadIdx.x == 0) off[n_seq] = slots;
     __syncthreads();
     int items = 0, pres = 0;
-    for (int base = 0; base < n_seq; base += 1024) {
+    for (int base = 0; base < n_seq; base += blockDim.x) {
         const int r = base + threadIdx.x;
         int s = 0, len = 0, segs = 0, total, pre_total;
         if (r < n_seq) {
@@ -610,13 +610,25 @@ __global__ void states_copy_kernel(const float *from, float *to, long n) {
 // then cut so that three warps meet on each scheduler.
 constexpr long kSchedulers = 152 * 4;
 
-void choose_cut(int T_total, int D, int N, int &cut, int &trigger) {
+Cut choose_cut(int T_total, int D, int N) {
     const long warps = std::max(1L, (long)D * lanes_of_states(N) / 64);
     const long most = std::max(128L, 13 * T_total * warps / (10 * kSchedulers));
     long len = std::max(64L, T_total * warps / (3 * kSchedulers));
     len = (len + kTokens - 1) / kTokens * kTokens;
-    cut = (int)std::min<long>(len, 1 << 30);
-    trigger = (int)std::min<long>(std::max(most, len), 0x7fffffff);
+    return Cut{(int)std::min<long>(len, 1 << 30), (int)std::min<long>(std::max(most, len), 0x7fffffff)};
+}
+
+// Blocks come in waves of `held`; where the last one leaves more than a tenth
+// of the device idle, the sequences are cut so that their first parts fill
+// whole waves and the rest, a first pass of a seventh of its cost, the gaps.
+// (8 x 2048 tokens, 2048 channels: 256 blocks of 304, 732 us whole, 671 + 27 us
+// cut.)
+Cut choose_even_cut(int T, long whole, long held) {
+    const long waves = (whole + held - 1) / held;
+    if (whole == 0 || 10 * whole >= 9 * waves * held) return Cut{kTokens, 0x7fffffff};
+    long len = std::max(64L, T * whole / (waves * held));
+    len = (len + kTokens - 1) / kTokens * kTokens;
+    return Cut{(int)std::min<long>(len, 1 << 30), (int)std::min<long>(len, 1 << 30)};
 }
 
 namespace {
@@ -625,49 +637,48 @@ struct LayoutBytes {
     size_t off, order, item, pre_item, count, pre_h, pre_sum, total;
     long items, pres;
 };
-LayoutBytes layout_plan(int n_seq, int T_total, int D, int N, int cut, int trigger, bool packed) {
+LayoutBytes layout_plan(int n_seq, int T_total, int D, int N, Cut cut, bool packed) {
     LayoutBytes b;
     size_t at = 0;
     auto take = [&](size_t bytes) { const size_t o = at; at += round256(bytes); return o; };
-    // every segment but a sequence's last holds `cut` tokens
-    const long pres = T_total > trigger ? T_total / cut : 0;
-    b.pres = pres;
-    b.items = n_seq + pres;
+    if (packed) {
+        // every segment but a sequence's last holds `cut` tokens
+        b.pres = T_total > cut.trigger ? T_total / cut.cut : 0;
+        b.items = n_seq + b.pres;
+    } else {
+        const int segs = n_seq ? segments_of(T_total / n_seq, cut.cut, cut.trigger) : 0;
+        b.items = (long)n_seq * segs;
+        b.pres = n_seq ? (long)n_seq * (segs - 1) : 0;
+    }
     const size_t n = packed ? (size_t)n_seq : 0;
     b.off = take(n ? sizeof(int32_t) * (n + 1) : 0);
     b.order = take(sizeof(int32_t) * n);
     b.item = take(n ? sizeof(Item) * (size_t)b.items : 0);
-    b.pre_item = take(n ? sizeof(Item) * (size_t)pres : 0);
+    b.pre_item = take(n ? sizeof(Item) * (size_t)b.pres : 0);
     b.count = take(n ? 2 * sizeof(int32_t) : 0);
-    b.pre_h = take(sizeof(float) * (size_t)pres * D * N);
-    b.pre_sum = take(sizeof(float) * (size_t)pres * D);
+    b.pre_h = take(sizeof(float) * (size_t)b.pres * D * N);
+    b.pre_sum = take(sizeof(float) * (size_t)b.pres * D);
     b.total = at;
     return b;
 }
 
 }  // namespace
 
-size_t layout_bytes(int n_seq, int T_total, int D, int N) {
-    int cut, trigger;
-    choose_cut(T_total, D, N, cut, trigger);
-    return layout_plan(n_seq, T_total, D, N, cut, trigger, true).total;
+size_t layout_bytes(int n_seq, int T_total, int D, int N, Cut cut, bool packed) {
+    return layout_plan(n_seq, T_total, D, N, cut, packed).total;
 }
 
-cudaError_t make_layout(const ScanProblem &p, Layout &l, cudaStream_t st) {
-    choose_cut(p.T_total, p.D, p.N, l.cut, l.trigger);
-    const LayoutBytes b = layout_plan(p.n_seq, p.T_total, p.D, p.N, l.cut, l.trigger, p.cu != nullptr);
+cudaError_t make_layout(const ScanProblem &p, Cut cut, Layout &l, cudaStream_t st) {
+    l.cut = cut.cut;
+    l.trigger = cut.trigger;
+    const LayoutBytes b = layout_plan(p.n_seq, p.T_total, p.D, p.N, cut, p.cu != nullptr);
+    l.items = (int)b.items;
+    l.pres = (int)b.pres;
     l.pre_h = reinterpret_cast<float *>(p.ws + b.pre_h);
     l.pre_sum = reinterpret_cast<float *>(p.ws + b.pre_sum);
     l.slot_off = l.count = nullptr;
     l.item = l.pre_item = nullptr;
-    if (!p.cu) {
-        const int segs = segments_of(p.T, l.cut, l.trigger);
-        l.items = p.n_seq * segs;
-        l.pres = p.n_seq * (segs - 1);
-        return cudaSuccess;
-    }
-    l.items = (int)b.items;
-    l.pres = (int)b.pres;
+    if (!p.cu) return cudaSuccess;
     int32_t *off = reinterpret_cast<int32_t *>(p.ws + b.off);
     int32_t *count = reinterpret_cast<int32_t *>(p.ws + b.count);
     Item *item = reinterpret_cast<Item *>(p.ws + b.item);
@@ -676,9 +687,10 @@ cudaError_t make_layout(const ScanProblem &p, Layout &l, cudaStream_t st) {
     l.count = count;
     l.item = item;
     l.pre_item = pre_item;
-    layout_kernel<<<1, 1024, 0, st>>>(p.cu, p.n_seq, p.T_total, l.cut, l.trigger, off,
-                                      reinterpret_cast<int32_t *>(p.ws + b.order), item, pre_item,
-                                      count, p.status);
+    const int threads = std::min(1024, (p.n_seq + 31) / 32 * 32);
+    layout_kernel<<<1, threads, 0, st>>>(p.cu, p.n_seq, p.T_total, l.cut, l.trigger, off,
+                                         reinterpret_cast<int32_t *>(p.ws + b.order), item, pre_item,
+                                         count, p.status);
     return cudaGetLastError();
 }
 
@@ -697,14 +709,17 @@ cudaError_t launch_states_copy(const float *from, float *to, long n, cudaStream_
 }  // namespace scan
 
 size_t scan_fwd_workspace(int n_seq, int T_total, int D, int G, int N, mdn_dtype dtype) {
-    return scan::layout_bytes(n_seq, T_total, D, N);
+    // which of the two a call is, its sizes do not tell
+    const scan::Cut cut = scan::choose_cut(T_total, D, N);
+    return std::max(scan::layout_bytes(n_seq, T_total, D, N, cut, true),
+                    scan::layout_bytes(n_seq, T_total, D, N, cut, false));
 }
 
 cudaError_t launch_scan_fwd(const ScanProblem &p, cudaStream_t st) {
     if (p.n_seq == 0) return cudaSuccess;
     if (p.T_total == 0) return scan::launch_states_copy(p.h0, p.h_T, (long)p.n_seq * p.D * p.N, st);
     scan::Layout l;
-    const cudaError_t err = scan::make_layout(p, l, st);
+    const cudaError_t err = scan::make_layout(p, scan::choose_cut(p.T_total, p.D, p.N), l, st);
     if (err != cudaSuccess) return err;
     return p.dtype == MDN_BF16 ? scan::fwd_dispatch<__nv_bfloat16>(p, l, scan::Pass::kMain, st)
                                : scan::fwd_dispatch<float>(p, l, scan::Pass::kMain, st);

@@ -53,12 +53,19 @@ struct Layout {
     float *pre_h, *pre_sum;           // [slot][D][N], [slot][D]
 };
 
-// Cuts for these sizes (a function of the totals alone, so that packed
-// sequences need no lengths on the host).
-void choose_cut(int T_total, int D, int N, int &cut, int &trigger);
-size_t layout_bytes(int n_seq, int T_total, int D, int N);
+// Where sequences are cut.  For packed sequences a function of the totals alone
+// (no lengths on the host).
+struct Cut {
+    int cut, trigger;
+};
+Cut choose_cut(int T_total, int D, int N);
+// The gradient of equal lengths: `whole` blocks for the uncut sequences, of
+// which the device holds `held` at once.
+Cut choose_even_cut(int T, long whole, long held);
+// Bytes of the workspace that make_layout fills with these cuts.
+size_t layout_bytes(int n_seq, int T_total, int D, int N, Cut cut, bool packed);
 // Describes the work of p in its workspace (packed: one small kernel).
-cudaError_t make_layout(const ScanProblem &p, Layout &l, cudaStream_t st);
+cudaError_t make_layout(const ScanProblem &p, Cut cut, Layout &l, cudaStream_t st);
 // The gradient's first pass over cut segments: what each segment but the first
 // hands back to the one before it, from a zero adjoint.
 cudaError_t launch_adjoint_ends(const ScanProblem &p, const Layout &l, cudaStream_t st);
@@ -83,9 +90,11 @@ __device__ __forceinline__ bool find_item(const ScanProblem &p, const Layout &l,
         if (REV) len = p.cu[it.seq + 1] - (int)t0;
     } else {
         const int all = segments_of(p.T, l.cut, l.trigger), segs = PRE ? all - 1 : all;
-        it.seq = i / segs;
-        if (it.seq >= p.n_seq) return false;
-        it.tok0 = (i - it.seq * segs) * l.cut;
+        // first segments first: the last ones are the shorter ones
+        const int k = i / p.n_seq;
+        if (k >= segs) return false;
+        it.seq = i - k * p.n_seq;
+        it.tok0 = k * l.cut;
         it.len = all == 1 ? p.T : min(l.cut, p.T - it.tok0);
         it.pre = it.seq * (all - 1);
         t0 = (long)it.seq * p.T;

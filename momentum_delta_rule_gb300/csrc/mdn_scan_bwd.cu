@@ -523,24 +523,28 @@ int bwd_block_channels(int N) {
     }
 }
 
+int bwd_block_warps(int N) { return lanes_of_states(N) == 2 ? 2 : lanes_of_states(N) <= 8 ? 4 : 8; }
+
 struct BwdPlan {
     long tiles, gtiles;
     int slots;
-    size_t bc, A, D, bytes;       // bytes of each part, and of the whole workspace
-    size_t base;
+    Cut cut;
+    size_t base, bc, A, D, bytes; // bytes of each part, and of the whole workspace
 };
-BwdPlan bwd_plan(int n_seq, int T_total, int D, int G, int N) {
+BwdPlan bwd_plan(int n_seq, int T_total, int D, int G, int N, bool packed) {
     BwdPlan b;
     const int Dg = D / G, CB = bwd_block_channels(N);
     b.gtiles = (Dg + CB - 1) / CB;
     b.tiles = b.gtiles * G;
-    // blocks for four on each SM, and no more than there can be items
-    int cut, trigger;
-    choose_cut(T_total, D, N, cut, trigger);
-    const long items = n_seq + (T_total > trigger ? T_total / cut : 0);
-    const long want = (152L * 4 + b.tiles - 1) / b.tiles;
-    b.slots = (int)std::max(1L, std::min(items, want));
-    b.base = layout_bytes(n_seq, T_total, D, N);
+    // an SM holds eight warps of any shape
+    const long held = 152L * (8 / bwd_block_warps(N));
+    b.cut = packed ? choose_cut(T_total, D, N)
+                   : choose_even_cut(n_seq ? T_total / n_seq : 0, b.tiles * n_seq, held);
+    const long items = packed ? n_seq + (T_total > b.cut.trigger ? T_total / b.cut.cut : 0)
+                              : (long)n_seq * (n_seq ? segments_of(T_total / n_seq, b.cut.cut, b.cut.trigger) : 0);
+    // a block for every item, as far as eight waves of blocks go
+    b.slots = (int)std::max(1L, std::min(items, (8 * held + b.tiles - 1) / b.tiles));
+    b.base = layout_bytes(n_seq, T_total, D, N, b.cut, packed);
     b.bc = round256((size_t)b.gtiles * T_total * G * 2 * N * sizeof(float));
     b.A = round256((size_t)b.slots * D * N * sizeof(float));
     b.D = round256((size_t)b.slots * D * sizeof(float));
@@ -602,7 +606,9 @@ cudaError_t bwd_dispatch(const ScanProblem &p, const Layout &l, const BwdPartial
 }  // namespace scan
 
 size_t scan_bwd_workspace(int n_seq, int T_total, int D, int G, int N, mdn_dtype dtype) {
-    return scan::bwd_plan(n_seq, T_total, D, G, N).bytes;
+    // which of the two a call is, its sizes do not tell
+    return std::max(scan::bwd_plan(n_seq, T_total, D, G, N, true).bytes,
+                    scan::bwd_plan(n_seq, T_total, D, G, N, false).bytes);
 }
 
 cudaError_t launch_scan_bwd(const ScanProblem &p, cudaStream_t st) {
@@ -616,11 +622,11 @@ cudaError_t launch_scan_bwd(const ScanProblem &p, cudaStream_t st) {
             }
         return scan::launch_states_copy(p.dh_T, p.dh0, (long)p.n_seq * p.D * p.N, st);
     }
+    const scan::BwdPlan b = scan::bwd_plan(p.n_seq, p.T_total, p.D, p.G, p.N, p.cu != nullptr);
     scan::Layout l;
-    cudaError_t err = scan::make_layout(p, l, st);
+    cudaError_t err = scan::make_layout(p, b.cut, l, st);
     if (err == cudaSuccess) err = scan::launch_adjoint_ends(p, l, st);
     if (err != cudaSuccess) return err;
-    const scan::BwdPlan b = scan::bwd_plan(p.n_seq, p.T_total, p.D, p.G, p.N);
     scan::BwdPartials w;
     unsigned char *at = p.ws + b.base;
     w.bc = reinterpret_cast<float *>(at);

@@ -212,6 +212,29 @@ def test_scan_single_long_sequence_and_many_short():
     check_scan(scan_case("bf16", [3] * 300, D=16, N=8, seed=12), train=True)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("T,S,D,N,G", [(300, 2, 40, 16, 1), (97, 3, 34, 8, 2), (64, 1, 16, 16, 1), (65, 2, 9, 128, 1), (130, 40, 192, 32, 1)])
+def test_scan_cut_sequences_of_equal_length(dtype, T, S, D, N, G):
+    # few blocks: the forward and the gradient cut them into segments of their own
+    check_scan(scan_case(dtype, [T] * S, D=D, N=N, G=G, packed=False, seed=T), train=True)
+
+
+def test_scan_step_of_many_sequences():
+    # more than the grid's second dimension holds
+    import momentum_delta_rule_gb300 as mdn
+    n = 65535 + 70
+    g = _gen(40)
+    u, dt, z = (torch.randn(n, 2, generator=g).cuda() for _ in range(3))
+    A = -torch.rand(2, 1, generator=g).cuda()
+    Bm, Cm, h = (torch.randn(*s, generator=g).cuda() for s in ((n, 1, 1), (n, 1, 1), (n, 2, 1)))
+    out = torch.empty_like(h)
+    y = mdn.ssm_scan_step(u, dt, A, Bm, Cm, h, z=z, h_out=out)
+    rows = [0, 1, 65534, 65535, 65536, n - 1]
+    part = torch.empty(len(rows), 2, 1, device="cuda")
+    want = mdn.ssm_scan_step(u[rows], dt[rows], A, Bm[rows], Cm[rows], h[rows], z=z[rows], h_out=part)
+    assert torch.equal(y[rows], want) and torch.equal(out[rows], part)
+
+
 def test_scan_without_tokens():
     import momentum_delta_rule_gb300 as mdn
     c = _dev(scan_case("fp32", [0, 0], D=8, N=4, packed=False))
