@@ -536,11 +536,7 @@ cudaError_t conv_bwd_t(const ConvProblem &p, cudaStream_t st) {
     const long blocks = rows / (kConvThreads / g.cl) * g.ctiles;
     if (blocks > 0x7fffffffL) return cudaErrorInvalidConfiguration;
     constexpr int bytes = 2 * (kConvAhead + 1) * kBatch<T, V> * kConvThreads * (int)sizeof(Packet<T, V>);
-    if (bytes > 48 * 1024) {
-        const cudaError_t err = cudaFuncSetAttribute(conv_bwd_kernel<T, V, W>,
-                                                     cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (err != cudaSuccess) return err;
-    }
+    static_assert(bytes <= 48 * 1024, "four blocks an SM");
     conv_bwd_kernel<T, V, W><<<(unsigned)blocks, kConvThreads, bytes, st>>>(p, g);
     cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;

@@ -416,12 +416,10 @@ cudaError_t fwd_launch(const ScanProblem &p, const Layout &l, int blocks_per_til
     const long tiles = (long)p.G * ((Dg + S::CB - 1) / S::CB);
     if (tiles * blocks_per_tile > 0x7fffffffL) return cudaErrorInvalidConfiguration;
     constexpr int bytes = (int)sizeof(FwdSmem<T, S, V>);
-    auto k = scan_fwd_kernel<T, S, V, PASS>;
-    if (bytes > 48 * 1024) {
-        const cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (err != cudaSuccess) return err;
-    }
-    k<<<(unsigned)(tiles * blocks_per_tile), S::NT + S::HT, bytes, st>>>(p, l, (int)tiles);
+    const cudaError_t err = allow_shared<scan_fwd_kernel<T, S, V, PASS>>(bytes);
+    if (err != cudaSuccess) return err;
+    scan_fwd_kernel<T, S, V, PASS>
+        <<<(unsigned)(tiles * blocks_per_tile), S::NT + S::HT, bytes, st>>>(p, l, (int)tiles);
     return cudaGetLastError();
 }
 

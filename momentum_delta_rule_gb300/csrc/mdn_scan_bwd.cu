@@ -557,11 +557,10 @@ cudaError_t bwd_t(const ScanProblem &p, const Layout &l, const BwdPartials &w, c
                   cudaStream_t st) {
     const long blocks = b.tiles * w.slots;
     if (blocks > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-    auto k = scan_bwd_kernel<T, S, V>;
-    cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           (int)sizeof(BwdSmem<T, S, V>));
+    constexpr int bytes = (int)sizeof(BwdSmem<T, S, V>);
+    const cudaError_t err = allow_shared<scan_bwd_kernel<T, S, V>>(bytes);
     if (err != cudaSuccess) return err;
-    k<<<(unsigned)blocks, S::NT, sizeof(BwdSmem<T, S, V>), st>>>(p, l, w, (int)b.tiles);
+    scan_bwd_kernel<T, S, V><<<(unsigned)blocks, S::NT, bytes, st>>>(p, l, w, (int)b.tiles);
     return cudaGetLastError();
 }
 

@@ -70,6 +70,22 @@ mdn_status current_device_status(int **status);
 
 inline size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// Lets a kernel have `bytes` of dynamic shared memory, always the same for one
+// kernel: once on each device.
+template <auto Kernel>
+inline cudaError_t allow_shared(int bytes) {
+    static std::atomic<uint64_t> done{0};
+    if (bytes <= 48 * 1024) return cudaSuccess;
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    err = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return err;
+}
+
 // The widest packet (elements: `most`, 2 or 1) for which `fits(bytes)` holds;
 // 2 only for two-byte elements, which it lets be copied asynchronously.
 template <typename F>

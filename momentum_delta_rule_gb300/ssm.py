@@ -92,7 +92,17 @@ def _rows(name, t, shape, dtype, index, width, tail=1):
     """Checks a rows input and returns its row stride (`width`: of a dense row)."""
     if t is None or t.dtype is not dtype or t.get_device() != index or t.shape != shape:
         _refuse(name, t, shape, dtype, index)
-    return width if t.is_contiguous() else _row_stride(name, t, tail)
+    if t.is_contiguous():
+        return width
+    # a slice of [.., T, wider] rows
+    st = t.stride()
+    lead = len(st) - tail
+    if (lead <= 2 and st[-1] == 1 and (tail == 1 or shape[-2] == 1 or st[-2] == shape[-1])
+            and (lead == 1 or shape[0] == 1 or st[0] == st[1] * shape[1])):
+        ld = st[lead - 1]
+        if ld >= width and shape[lead - 1] > 1:
+            return ld
+    return _row_stride(name, t, tail)
 
 
 def _dense(name, t, shape, dtype, index):
@@ -411,6 +421,8 @@ def _norm_inputs(y, x, gate, w_post, w_pre, scale, gate_act, index):
     if y.dim() < 1 or shape[-1] == 0:
         raise ValueError("y must be [..., D] with at least one column")
     D = shape[-1]
+    if y.numel() > 0x7fffffff * D:
+        raise ValueError("y has more than 2^31 - 1 rows")
     lds = (_rows("y", y, shape, dtype, index, D), _rows("x", x, shape, dtype, index, D),
            _rows("gate", gate, shape, dtype, index, D) if gate is not None else 0)
     ptrs = (y.data_ptr(), x.data_ptr(), _address(gate), _dense("w_post", w_post, (D,), _F32, index),
