@@ -25,13 +25,23 @@ constexpr int kConvThreads = 128;
 // one wave of the forward and of the gradient has on each.
 constexpr int kFwdBlocks = 6, kBwdBlocks = 4;
 
-__device__ __forceinline__ float conv_act(float v, int act) {
-    return act == MDN_CONV_SILU ? v * sigmoid_f(v) : v;
+// v <- act(v)
+template <int V>
+__device__ __forceinline__ void conv_act(float *v, int act) {
+    if (act != MDN_CONV_SILU) return;
+    float s[V];
+    sigmoids<V>(v, s);
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] *= s[i];
 }
-__device__ __forceinline__ float conv_dact(float v, int act) {
-    if (act != MDN_CONV_SILU) return 1.f;
-    const float s = sigmoid_f(v);
-    return s * fmaf(v, 1.f - s, 1.f);
+// v <- act'(v)
+template <int V>
+__device__ __forceinline__ void conv_dact(float *v, int act) {
+    float s[V];
+    if (act == MDN_CONV_SILU) sigmoids<V>(v, s);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        v[i] = act == MDN_CONV_SILU ? s[i] * fmaf(v[i], 1.f - s[i], 1.f) : 1.f;
 }
 
 // Walk over sequences: the one that holds the current token.
@@ -224,8 +234,7 @@ __global__ void __launch_bounds__(kConvThreads, kFwdBlocks) conv_fwd_kernel(Conv
     auto token = [&](long t, const float *x) {
         float o[V];
         conv_sum<V, W>(w, bias, win, x, o);
-#pragma unroll
-        for (int v = 0; v < V; ++v) o[v] = conv_act(o[v], p.act);
+        conv_act<V>(o, p.act);
         store_packet<T, V>(yp + t * p.D, pack<T, V>(o));
         push_row<V, W>(win, x);
     };
@@ -330,9 +339,10 @@ __global__ void __launch_bounds__(kConvThreads, kBwdBlocks) conv_bwd_kernel(Conv
         // dpre of a token; its part of dw and db
         auto dpre = [&](const float *x, const float *d, bool mine, float *e) {
             conv_sum<V, W>(w, bias, win, x, e);
+            conv_dact<V>(e, p.act);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                e[v] = d[v] * conv_dact(e[v], p.act);
+                e[v] *= d[v];
                 if (mine) {
                     db[v] += e[v];
                     dw[W - 1][v] = fmaf(e[v], x[v], dw[W - 1][v]);
@@ -477,8 +487,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvProblem p, 
 #pragma unroll
         for (int v = 0; v < V; ++v) o[v] = fmaf(w[j][v], x[v], o[v]);
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) o[v] = conv_act(o[v], p.act);
+    conv_act<V>(o, p.act);
     store_packet<T, V>(static_cast<T *>(p.y) + n * p.D + c, pack<T, V>(o));
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) store_packet<T, V>(so + (long)j * p.D, row[j + 1]);

@@ -40,18 +40,23 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float *red, int &turn
     return v;
 }
 
-__device__ __forceinline__ float gate_act(float g, int act) {
-    const float s = sigmoid_f(g);
-    return act == MDN_GATE_SILU ? g * s : s;
+// a <- act(g), d <- act'(g)
+template <int V>
+__device__ __forceinline__ void gate_acts(const float *g, int act, float *a) {
+    sigmoids<V>(g, a);
+    if (act == MDN_GATE_SILU)
+#pragma unroll
+        for (int v = 0; v < V; ++v) a[v] *= g[v];
 }
-__device__ __forceinline__ void gate_act_d(float g, int act, float &a, float &d) {
-    const float s = sigmoid_f(g);
-    if (act == MDN_GATE_SILU) {
-        a = g * s;
-        d = s * fmaf(g, 1.f - s, 1.f);
-    } else {
-        a = s;
-        d = s * (1.f - s);
+template <int V>
+__device__ __forceinline__ void gate_acts_d(const float *g, int act, float *a, float *d) {
+    float s[V];
+    sigmoids<V>(g, s);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const bool silu = act == MDN_GATE_SILU;
+        a[v] = silu ? g[v] * s[v] : s[v];
+        d[v] = silu ? s[v] * fmaf(g[v], 1.f - s[v], 1.f) : s[v] * (1.f - s[v]);
     }
 }
 
@@ -179,13 +184,16 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(NormProblem p, int tpr) {
         ss = 0.f;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            float g[V];
+            float g[V], act[V];
             sx.get(get, i, live, x[i]);
-            if (GATE) sg.get(get, i, live, g);
+            if (GATE) {
+                sg.get(get, i, live, g);
+                gate_acts<V>(g, p.gate_act, act);
+            }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 float b = y[i][v] * r1;
-                if (GATE) b *= gate_act(g[v], p.gate_act);
+                if (GATE) b *= act[v];
                 x[i][v] = fmaf(b, ws[i][v], x[i][v]);
                 ss = fmaf(x[i][v], x[i][v], ss);
             }
@@ -258,7 +266,7 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormProblem p, int tpr) 
         const float r2 = live ? p.stats[2 * row + 1] : 0.f;
         issue(put, row + AHEAD * step < p.rows);
         wait_copies<(AHEAD < 0 ? 0 : AHEAD)>();
-        float y[NI][V], X[NI][V], g[NI][V], dX[NI][V], dh[NI][V];
+        float y[NI][V], X[NI][V], g[NI][V], act[NI][V], dact[NI][V], dX[NI][V], dh[NI][V];
         // X again, and mean(dh w_pre X)
         float s2 = 0.f;
 #pragma unroll
@@ -267,11 +275,14 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormProblem p, int tpr) 
             sx.get(get, i, live, X[i]);
             sd.get(get, i, live, dX[i]);
             sh.get(get, i, live && pre, dh[i]);
-            if (GATE) sg.get(get, i, live, g[i]);
+            if (GATE) {
+                sg.get(get, i, live, g[i]);
+                gate_acts_d<V>(g[i], p.gate_act, act[i], dact[i]);
+            }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 float b = y[i][v] * (r1 * wpost[i][v]);
-                if (GATE) b *= gate_act(g[i][v], p.gate_act);
+                if (GATE) b *= act[i][v];
                 X[i][v] = fmaf(sc[i][v], b, X[i][v]);
                 a_pre[i][v] = fmaf(dh[i][v] * r2, X[i][v], a_pre[i][v]);
                 dh[i][v] *= wpre[i][v];
@@ -297,12 +308,11 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormProblem p, int tpr) 
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const float n = y[i][v] * (r1 * wpost[i][v]);
-                float act = 1.f, dact = 0.f;
-                if (GATE) gate_act_d(g[i][v], p.gate_act, act, dact);
-                a_scale[i][v] = fmaf(dX[i][v], n * act, a_scale[i][v]);
+                const float ga = GATE ? act[i][v] : 1.f;
+                a_scale[i][v] = fmaf(dX[i][v], n * ga, a_scale[i][v]);
                 const float db = dX[i][v] * sc[i][v];
-                dg[v] = db * n * dact;
-                const float dn = db * act;
+                if (GATE) dg[v] = db * n * dact[i][v];
+                const float dn = db * ga;
                 a_post[i][v] = fmaf(dn * r1, y[i][v], a_post[i][v]);
                 dX[i][v] = dn * wpost[i][v];
                 s1 = fmaf(dX[i][v], y[i][v], s1);
@@ -395,12 +405,12 @@ int norm_blocks(int rows, const NormShape &s, int threads) {
     const long rpb = s.threads / s.tpr, most = (rows + rpb - 1) / rpb;
     return (int)std::min(most, 152L * std::max(1, threads / s.threads));
 }
-int fwd_threads(const NormShape &s, int V) { return s.ni * V <= 16 ? 640 : 512; }
+int fwd_threads(const NormShape &s, int V, bool gate) { return s.ni * V <= 16 && !gate ? 640 : 512; }
 constexpr int kBwdThreads = 512;
 
 template <bool BWD, typename T, int V, int NI>
 cudaError_t norm_launch(const NormProblem &p, const NormShape &s, cudaStream_t st) {
-    const int blocks = norm_blocks(p.rows, s, BWD ? kBwdThreads : fwd_threads(s, V));
+    const int blocks = norm_blocks(p.rows, s, BWD ? kBwdThreads : fwd_threads(s, V, p.gate != nullptr));
     constexpr int each = NI * V * (int)sizeof(T);
     constexpr int slots = BWD ? 5 * (bwd_ahead(each) + 1) : 3 * (fwd_ahead(each) + 1);
     const int bytes = slots * each * s.threads;
