@@ -376,9 +376,9 @@ struct NormShape {
     int tpr, ni, threads;
 };
 // Threads per row and packets per thread.  A row takes up to 128 threads
-// first, then `soft` values a thread, then up to `most` threads, then more
-// values.
-NormShape norm_shape(int D, int V, int soft, int most) {
+// first, then `soft` values a thread, then up to `most` threads, then `hard`
+// values, then 1024 threads.
+NormShape norm_shape(int D, int V, int soft, int most, int hard) {
     const int packets = (D + V - 1) / V;
     NormShape s;
     s.tpr = 32;
@@ -387,18 +387,25 @@ NormShape norm_shape(int D, int V, int soft, int most) {
         if (s.tpr < 128) s.tpr *= 2;
         else if (s.ni * V < soft) s.ni *= 2;
         else if (s.tpr < most) s.tpr *= 2;
-        else s.ni *= 2;
+        else if (s.ni * V < hard) s.ni *= 2;
+        else s.tpr *= 2;
     }
     s.threads = s.tpr < 128 ? 128 : s.tpr;
     return s;
 }
-// The forward holds two arrays of a row, the gradient five and three sums.
-// Few rows (less than two for each SM) take more threads and fewer values:
-// their time is the latency of one row.
+// The forward holds two arrays of a row and their weights: 32 values and 512
+// threads reach D = 16384.  Few rows (less than two for each SM) take more
+// threads and fewer values: their time is the latency of one row.
 NormShape norm_fwd_shape(int rows, int D, int V) {
-    return rows < 2 * 152 ? norm_shape(D, V, V, 512) : norm_shape(D, V, V < 4 ? 4 * V : 2 * V, 512);
+    return rows < 2 * 152 ? norm_shape(D, V, V, 512, 32) : norm_shape(D, V, V < 4 ? 4 * V : 2 * V, 512, 32);
 }
-NormShape norm_bwd_shape(int D, int V) { return norm_shape(D, V, V < 4 ? 4 * V : 8, V < 4 ? 512 : 1024); }
+// The gradient holds seven arrays, weights and sums: 16 values and 1024
+// threads; a row of more than kSoft values a thread in 512 takes 1024.
+template <int V>
+constexpr int kSoft = V < 4 ? 16 : 8;
+NormShape norm_bwd_shape(int D, int V) {
+    return V < 4 ? norm_shape(D, V, 4 * V, 512, 16) : norm_shape(D, V, 8, 1024, 16);
+}
 // Blocks that share the rows: as many threads on each of 152 SMs as their
 // registers allow, where there are rows for them.
 int norm_blocks(int rows, const NormShape &s, int threads) {
@@ -426,11 +433,15 @@ cudaError_t norm_launch(const NormProblem &p, const NormShape &s, cudaStream_t s
     };
     const bool gate = p.gate != nullptr;
     if constexpr (BWD) {
-        const cudaError_t err =
-            s.threads <= 512 ? (gate ? launch(norm_bwd_kernel<T, V, NI, true, 512>)
-                                     : launch(norm_bwd_kernel<T, V, NI, false, 512>))
-                             : (gate ? launch(norm_bwd_kernel<T, V, NI, true, 1024>)
-                                     : launch(norm_bwd_kernel<T, V, NI, false, 1024>));
+        cudaError_t err = cudaErrorInvalidValue;
+        if constexpr (NI * V <= kSoft<V>)
+            if (s.threads <= 512)
+                err = gate ? launch(norm_bwd_kernel<T, V, NI, true, 512>)
+                           : launch(norm_bwd_kernel<T, V, NI, false, 512>);
+        if constexpr (NI * V >= kSoft<V>)
+            if (s.threads > 512)
+                err = gate ? launch(norm_bwd_kernel<T, V, NI, true, 1024>)
+                           : launch(norm_bwd_kernel<T, V, NI, false, 1024>);
         if (err != cudaSuccess) return err;
         norm_reduce_kernel<<<(3 * p.D + 31) / 32, 256, 0, st>>>(
             p.partial, blocks * (s.threads / s.tpr), p.D, p.dw_post, p.dw_pre, p.dscale);

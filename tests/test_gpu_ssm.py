@@ -479,7 +479,7 @@ def test_norm_widths(dtype, D):
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
-@pytest.mark.parametrize("D", [3, 96, 130, 513, 1026, 2047, 2048, 3000, 4097, 8190, 16384])
+@pytest.mark.parametrize("D", [3, 96, 130, 513, 1026, 2047, 2048, 3000, 4097, 8190, 8192, 10001, 16382, 16383, 16384])
 def test_norm_widths_of_many_rows(dtype, D):
     # more rows than the kernels' small-batch shapes take
     check_norm(dtype, 640, D, gate="silu", seed=D)
