@@ -471,8 +471,10 @@ mdn_status mdn_decode_step(const void *q, const void *k, const void *v,
  * the selective scan, and the norms around a block.  Inputs marked "rows" may
  * be slices of a wider array: their innermost dimension is contiguous and
  * consecutive tokens lie ld_* elements apart (ld_* at least the row's width);
- * everything else is dense.  Tensors need only their element's alignment;
- * rows on 16-byte boundaries move in wider packets.  Outputs overlap nothing
+ * everything else is dense.  Rows, weights and biases need only their
+ * element's alignment (rows on 16-byte boundaries move in wider packets).  A,
+ * dA and the fp32 states h0, h_T, h, h_out, dh_T, dh0 need 16 bytes where N is
+ * a multiple of 4; h_chunks always does, stats 8.  Outputs overlap nothing
  * else unless stated.  Malformed cu_seqlens are reported as for
  * mdn_chunk_fwd (status word, every sequence treated as empty: no token's
  * outputs are written, final states receive the initial ones, the gradients

@@ -283,6 +283,11 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
     float sum[S::CPT];
     bool live[S::CPT];
     {
+        // a cut sequence's initial state, if its final state takes its place
+        float *kept = l.pre_h0 + (long)it.pre * p.D * p.N;
+        const bool cut = !PRE && l.pre_h0 && it.len > 0 &&
+                         it.len < (p.cu ? p.cu[it.seq + 1] - p.cu[it.seq] : p.T);
+        const float *h0 = cut ? kept : p.h0 + (long)it.seq * p.D * p.N;
         float a[S::CPT][kStates], s0[S::CPT][kStates];
 #pragma unroll
         for (int c = 0; c < S::CPT; ++c) {
@@ -292,7 +297,12 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
             for (int i = 0; i < kStates; ++i) a[c][i] = s0[c][i] = 0.f;
             if (live[c]) {
                 load_states(p.A, d0 + cw + c, n0, p.N, a[c]);
-                if (!PRE && p.h0) load_states(p.h0 + (long)it.seq * p.D * p.N, d0 + cw + c, n0, p.N, s0[c]);
+                if (!PRE && p.h0) load_states(h0, d0 + cw + c, n0, p.N, s0[c]);
+                if (PASS == Pass::kEnds && l.pre_h0 && it.tok0 == 0) {
+                    float keep[kStates];
+                    load_states(h0, d0 + cw + c, n0, p.N, keep);
+                    store_states(kept, d0 + cw + c, n0, p.N, keep);
+                }
             }
 #pragma unroll
             for (int i = 0; i < kStates; ++i) a[c][i] *= kLog2e;
@@ -610,7 +620,7 @@ constexpr long kSchedulers = 152 * 4;
 
 Cut choose_cut(int T_total, int D, int N) {
     const long warps = std::max(1L, (long)D * lanes_of_states(N) / 64);
-    const long most = std::max(128L, 13 * T_total * warps / (10 * kSchedulers));
+    const long most = std::max(128L, 13L * T_total * warps / (10 * kSchedulers));
     long len = std::max(64L, T_total * warps / (3 * kSchedulers));
     len = (len + kTokens - 1) / kTokens * kTokens;
     return Cut{(int)std::min<long>(len, 1 << 30), (int)std::min<long>(std::max(most, len), 0x7fffffff)};
@@ -632,10 +642,10 @@ Cut choose_even_cut(int T, long whole, long held) {
 namespace {
 
 struct LayoutBytes {
-    size_t off, order, item, pre_item, count, pre_h, pre_sum, total;
+    size_t off, order, item, pre_item, count, pre_h, pre_sum, pre_h0, total;
     long items, pres;
 };
-LayoutBytes layout_plan(int n_seq, int T_total, int D, int N, Cut cut, bool packed) {
+LayoutBytes layout_plan(int n_seq, int T_total, int D, int N, Cut cut, bool packed, bool h0) {
     LayoutBytes b;
     size_t at = 0;
     auto take = [&](size_t bytes) { const size_t o = at; at += round256(bytes); return o; };
@@ -656,24 +666,28 @@ LayoutBytes layout_plan(int n_seq, int T_total, int D, int N, Cut cut, bool pack
     b.count = take(n ? 2 * sizeof(int32_t) : 0);
     b.pre_h = take(sizeof(float) * (size_t)b.pres * D * N);
     b.pre_sum = take(sizeof(float) * (size_t)b.pres * D);
+    b.pre_h0 = take(h0 ? sizeof(float) * (size_t)b.pres * D * N : 0);
     b.total = at;
     return b;
 }
 
 }  // namespace
 
-size_t layout_bytes(int n_seq, int T_total, int D, int N, Cut cut, bool packed) {
-    return layout_plan(n_seq, T_total, D, N, cut, packed).total;
+size_t layout_bytes(int n_seq, int T_total, int D, int N, Cut cut, bool packed, bool h0) {
+    return layout_plan(n_seq, T_total, D, N, cut, packed, h0).total;
 }
 
 cudaError_t make_layout(const ScanProblem &p, Cut cut, Layout &l, cudaStream_t st) {
     l.cut = cut.cut;
     l.trigger = cut.trigger;
-    const LayoutBytes b = layout_plan(p.n_seq, p.T_total, p.D, p.N, cut, p.cu != nullptr);
+    // the gradient has no h0
+    const bool replaced = p.h0 && p.h0 == p.h_T;
+    const LayoutBytes b = layout_plan(p.n_seq, p.T_total, p.D, p.N, cut, p.cu != nullptr, replaced);
     l.items = (int)b.items;
     l.pres = (int)b.pres;
     l.pre_h = reinterpret_cast<float *>(p.ws + b.pre_h);
     l.pre_sum = reinterpret_cast<float *>(p.ws + b.pre_sum);
+    l.pre_h0 = replaced ? reinterpret_cast<float *>(p.ws + b.pre_h0) : nullptr;
     l.slot_off = l.count = nullptr;
     l.item = l.pre_item = nullptr;
     if (!p.cu) return cudaSuccess;
@@ -709,8 +723,8 @@ cudaError_t launch_states_copy(const float *from, float *to, long n, cudaStream_
 size_t scan_fwd_workspace(int n_seq, int T_total, int D, int G, int N, mdn_dtype dtype) {
     // which of the two a call is, its sizes do not tell
     const scan::Cut cut = scan::choose_cut(T_total, D, N);
-    return std::max(scan::layout_bytes(n_seq, T_total, D, N, cut, true),
-                    scan::layout_bytes(n_seq, T_total, D, N, cut, false));
+    return std::max(scan::layout_bytes(n_seq, T_total, D, N, cut, true, true),
+                    scan::layout_bytes(n_seq, T_total, D, N, cut, false, true));
 }
 
 cudaError_t launch_scan_fwd(const ScanProblem &p, cudaStream_t st) {

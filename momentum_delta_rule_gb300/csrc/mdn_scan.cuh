@@ -51,6 +51,10 @@ struct Layout {
     const Item *item, *pre_item;      // packed: tables
     const int32_t *count;             // packed: items, pre items
     float *pre_h, *pre_sum;           // [slot][D][N], [slot][D]
+    // h0 of the cut sequences at their first slots, where the final states
+    // replace it: the last segment may end before the others have read theirs.
+    // Null where nothing does.
+    float *pre_h0;
 };
 
 // Where sequences are cut.  For packed sequences a function of the totals alone
@@ -63,7 +67,8 @@ Cut choose_cut(int T_total, int D, int N);
 // which the device holds `held` at once.
 Cut choose_even_cut(int T, long whole, long held);
 // Bytes of the workspace that make_layout fills with these cuts.
-size_t layout_bytes(int n_seq, int T_total, int D, int N, Cut cut, bool packed);
+// `h0`: with room for copies of the initial states.
+size_t layout_bytes(int n_seq, int T_total, int D, int N, Cut cut, bool packed, bool h0);
 // Describes the work of p in its workspace (packed: one small kernel).
 cudaError_t make_layout(const ScanProblem &p, Cut cut, Layout &l, cudaStream_t st);
 // The gradient's first pass over cut segments: what each segment but the first

@@ -544,7 +544,7 @@ BwdPlan bwd_plan(int n_seq, int T_total, int D, int G, int N, bool packed) {
                               : (long)n_seq * (n_seq ? segments_of(T_total / n_seq, b.cut.cut, b.cut.trigger) : 0);
     // a block for every item, as far as eight waves of blocks go
     b.slots = (int)std::max(1L, std::min(items, (8 * held + b.tiles - 1) / b.tiles));
-    b.base = layout_bytes(n_seq, T_total, D, N, b.cut, packed);
+    b.base = layout_bytes(n_seq, T_total, D, N, b.cut, packed, false);
     b.bc = round256((size_t)b.gtiles * T_total * G * 2 * N * sizeof(float));
     b.A = round256((size_t)b.slots * D * N * sizeof(float));
     b.D = round256((size_t)b.slots * D * sizeof(float));

@@ -259,6 +259,17 @@ def test_scan_final_state_in_place_and_given_buffers():
     assert h2 is h and y2 is out and torch.equal(h, hT) and torch.equal(out, y)
 
 
+@pytest.mark.parametrize("lens,packed", [([1500, 1500], False), ([2001, 7], True), ([900], False)])
+def test_scan_final_states_of_cut_sequences_in_place(lens, packed):
+    import momentum_delta_rule_gb300 as mdn
+    c = _dev(scan_case("bf16", lens, D=66, N=16, packed=packed, seed=4))
+    args = (c["u"], c["dt"], c["A"], c["Bm"], c["Cm"])
+    y, hT = mdn.ssm_scan_fwd(*args, h0=c["h0"], **_scan_kw(c))
+    h = c["h0"].clone()
+    y2, h2 = mdn.ssm_scan_fwd(*args, h0=h, h_T=h, **_scan_kw(c))
+    assert h2 is h and torch.equal(h, hT) and torch.equal(y2, y)
+
+
 @pytest.mark.parametrize("cu", [[0, 40, 20, 60], [0, 20, 50], [5, 20, 60]])
 def test_malformed_offsets_are_reported(cu):
     import momentum_delta_rule_gb300 as mdn
