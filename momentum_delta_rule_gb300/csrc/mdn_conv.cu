@@ -13,6 +13,14 @@
 // without a branch.  Runs are cut so that one wave of blocks covers the
 // tokens: what a run starts with (weights, the rows before it, the search for
 // its sequence) costs as much as a dozen tokens.
+//
+// Measured, bf16, SiLU, width 4: 32768 tokens of 2048 channels 49 us (5.5 TB/s
+// over the 269 MB read and written once); 16384 tokens of 4096 channels 49 us
+// forward and 90 us gradient (4.5 TB/s over 403 MB).  A copy of the same bytes
+// takes 40, 40 and 59 us.  The forward is held by the latency at the ends of
+// its one wave; the gradient also by issue: SiLU and its derivative beside the
+// 4 W operations of an element.  256 sequences' single tokens at 2048
+// channels: 3.5 us, the latency of one round of loads and stores.
 #include <algorithm>
 
 #include "mdn_ssm.cuh"

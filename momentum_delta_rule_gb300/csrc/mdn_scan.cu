@@ -4,6 +4,19 @@
 //   delta_t = softplus(dt_t + dt_bias);   a_t[n] = exp(delta_t A[n])
 //   h_t[n]  = a_t[n] h_{t-1}[n] + delta_t u_t B_t[n]
 //   y_t     = (sum_n C_t[n] h_t[n] + D_skip u_t) silu(z_t)
+//
+// A depends on channel and state, so the decays a_t[n] do not factor into
+// products of matrices: each (token, channel, state) takes one exponential and
+// four multiplications or fma on the CUDA cores.  At 16 states that is more
+// time than the bytes: 32768 tokens of 2048 channels cost 1.07 G exponentials,
+// 113 us at the measured 62 a nanosecond and SM, against 80 us for 541 MB.
+//
+// Measured, bf16, 16 states: 32768 packed tokens of 2048 channels 360 us
+// (3.0 T exponentials a second, 0.31 of that rate); one sequence of 16384
+// tokens 176 us and 107 us for its first pass.  Bound by issue (71 % of the
+// slots) and the shared-memory pipe (76 %): delta, delta u, B and C come from
+// there for every token.  Four channels a lane instead of two read B and C
+// half as often but leave fewer warps: 360 to 375 us.
 #include <algorithm>
 
 #include "mdn_scan.cuh"
@@ -278,8 +291,9 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nl = lane % S::NL, n0 = nl * kStates;
     const int cw = warp * S::WC + lane / S::NL * S::CPT;     // lane's first channel in the block
-    // two neighbouring channels to a pair
-    Pair a2[S::CPT / 2][kStates], h[S::CPT / 2][kStates];
+    // two neighbouring states to a pair (two channels instead, whose B and C
+    // are scalars, cost 110 us where this costs 107, in the first pass)
+    Pair a2[S::CPT][kStates / 2], h[S::CPT][kStates / 2];
     float sum[S::CPT];
     bool live[S::CPT];
     {
@@ -320,21 +334,20 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
             }
         }
 #pragma unroll
-        for (int c = 0; c < S::CPT; c += 2)
+        for (int c = 0; c < S::CPT; ++c)
 #pragma unroll
-            for (int i = 0; i < kStates; ++i) {
-                a2[c / 2][i] = make_pair(a[c][i], a[c + 1][i]);
-                h[c / 2][i] = make_pair(s0[c][i], s0[c + 1][i]);
+            for (int i = 0; i < kStates / 2; ++i) {
+                a2[c][i] = make_pair(a[c][2 * i], a[c][2 * i + 1]);
+                h[c][i] = make_pair(s0[c][2 * i], s0[c][2 * i + 1]);
             }
     }
     auto store_h = [&](float *base) {
 #pragma unroll
-        for (int c = 0; c < S::CPT; c += 2) {
-            float x[kStates], y[kStates];
+        for (int c = 0; c < S::CPT; ++c) {
+            float x[kStates];
 #pragma unroll
-            for (int i = 0; i < kStates; ++i) split_pair(h[c / 2][i], x[i], y[i]);
+            for (int i = 0; i < kStates / 2; ++i) split_pair(h[c][i], x[2 * i], x[2 * i + 1]);
             if (live[c]) store_states(base, d0 + cw + c, n0, p.N, x);
-            if (live[c + 1]) store_states(base, d0 + cw + c + 1, n0, p.N, y);
         }
     };
     __syncthreads();
@@ -363,34 +376,30 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
             for (int jj = 0; jj < S::TB; ++jj) {
                 const int j = REV ? S::TB - 1 - jj : jj;
 #pragma unroll
-                for (int c = 0; c < S::CPT; c += 2) {
-                    const Pair d = make_pair(dl[j].e[c], dl[j].e[c + 1]);
-                    float y0 = 0.f, y1 = 0.f;
-                    if (PRE) {
-                        sum[c] += dl[j].e[c];
-                        sum[c + 1] += dl[j].e[c + 1];
-                    }
+                for (int c = 0; c < S::CPT; ++c) {
+                    const float dc = dl[j].e[c], duc = du[j].e[c];
+                    if (PRE) sum[c] += dc;
+                    Pair y;
 #pragma unroll
-                    for (int i = 0; i < kStates; ++i) {
+                    for (int i = 0; i < kStates / 2; ++i) {
+                        const Pair b = make_pair(bv[j].e[2 * i], bv[j].e[2 * i + 1]);
                         float e0, e1;
-                        split_pair(fma2(d, a2[c / 2][i], make_pair(kDecayBias, kDecayBias)), e0, e1);
+                        split_pair(fma2(make_pair(dc, dc), a2[c][i], make_pair(kDecayBias, kDecayBias)), e0, e1);
                         const Pair a = make_pair(ex2(e0), ex2(e1));
                         if (REV) {
-                            split_pair(h[c / 2][i], e0, e1);
-                            h[c / 2][i] = mul2(a, make_pair(fmaf(du[j].e[c], bv[j].e[i], e0),
-                                                            fmaf(du[j].e[c + 1], bv[j].e[i], e1)));
+                            h[c][i] = mul2(a, fma2(make_pair(duc, duc), b, h[c][i]));
                             continue;
                         }
-                        h[c / 2][i] = fma2(a, h[c / 2][i],
-                                           make_pair(du[j].e[c] * bv[j].e[i], du[j].e[c + 1] * bv[j].e[i]));
+                        h[c][i] = fma2(a, h[c][i], mul2(make_pair(duc, duc), b));
                         if (!PRE) {
-                            split_pair(h[c / 2][i], e0, e1);
-                            y0 = fmaf(e0, cv[j].e[i], y0);
-                            y1 = fmaf(e1, cv[j].e[i], y1);
+                            const Pair cc = make_pair(cv[j].e[2 * i], cv[j].e[2 * i + 1]);
+                            y = i ? fma2(h[c][i], cc, y) : mul2(h[c][i], cc);
                         }
                     }
-                    acc[j * S::CPT + c] = y0;
-                    acc[j * S::CPT + c + 1] = y1;
+                    if (PRE) continue;
+                    float y0, y1;
+                    split_pair(y, y0, y1);
+                    acc[j * S::CPT + c] = y0 + y1;
                 }
             }
             if (!PRE) {
@@ -476,7 +485,12 @@ constexpr int kStepWarps = 4;
 // channels of one group and sequence: lane j prepares channel j's delta and
 // delta u once, the states then pass in steps of 32 / NL channels (whole
 // lines), K of them in flight, and the exchange that adds up a channel's
-// states leaves each owner lane one channel's output to finish.
+// states leaves each owner lane one channel's output to finish.  The first K
+// steps' states are asked for before anything else and every other input with
+// them, so that a warp waits for memory once.  256 sequences of 2048 channels
+// and 16 states: 12.7 us, 71 MB at 5.6 TB/s (10.5 us at a copy's rate); 15.5 us
+// with the states behind the deltas and the gates behind the sums.  Warps that
+// took several sequences one after another took 20 to 34 us.
 template <typename T, int NL>
 __global__ void __launch_bounds__(32 * kStepWarps) scan_step_kernel(ScanProblem p, int tiles) {
     constexpr int CL = 32 / NL, K = NL < 4 ? NL : 4, STEPS = NL;
@@ -494,13 +508,34 @@ __global__ void __launch_bounds__(32 * kStepWarps) scan_step_kernel(ScanProblem 
     const T *zp = static_cast<const T *>(p.z) + s * p.ld_z + d0;
     const float *hp = p.h0 + (s * p.D + d0) * p.N, *ap = p.A + (long)d0 * p.N;
     float *ho = p.h_T + (s * p.D + d0) * p.N;
-    float delta = 0.f, du = 0.f;
+    // the states of the K steps from st on
+    float h[K][kStates], a[K][kStates];
+    auto load = [&](int st) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int ch = (st + k) * CL + cl;
+#pragma unroll
+            for (int i = 0; i < kStates; ++i) h[k][i] = a[k][i] = 0.f;
+            if (c0 + ch >= Dg || n0 >= p.N) continue;
+            if (whole) {
+                const float4 v = __ldcs(reinterpret_cast<const float4 *>(hp + ch * p.N + n0));
+                h[k][0] = v.x; h[k][1] = v.y; h[k][2] = v.z; h[k][3] = v.w;
+                unpack<float, kStates>(load_packet<float, kStates>(ap + ch * p.N + n0), a[k]);
+            } else {
+                load_states(hp, ch, n0, p.N, h[k]);
+                load_states(ap, ch, n0, p.N, a[k]);
+            }
+        }
+    };
+    load(0);
+    // lane j's channel c0 + j
+    float delta = 0.f, du = 0.f, u = 0.f, skip = 0.f, gate = 0.f;
     if (c0 + lane < Dg) {
-        const float u = to_f32(up[lane]);
+        u = to_f32(up[lane]);
         delta = to_f32(static_cast<const T *>(p.dt)[s * p.ld_dt + d0 + lane]);
+        if (p.D_skip) skip = p.D_skip[d0 + lane];
+        if (p.z) gate = to_f32(zp[lane]);
         if (p.dt_bias) delta += p.dt_bias[d0 + lane];
-        if (p.softplus) delta = softplus_rel(delta);
-        du = delta * u;
     }
     float b[kStates] = {0.f, 0.f, 0.f, 0.f}, c[kStates] = {0.f, 0.f, 0.f, 0.f};
     if (n0 < p.N) {
@@ -518,24 +553,13 @@ __global__ void __launch_bounds__(32 * kStepWarps) scan_step_kernel(ScanProblem 
                 }
         }
     }
+    if (p.softplus) delta = softplus_rel(delta);
+    du = delta * u;
+    gate *= sigmoid_f(gate);
 #pragma unroll 1
     for (int st = 0; st < STEPS; st += K) {
-        float h[K][kStates], a[K][kStates], acc[K];
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int ch = (st + k) * CL + cl;
-#pragma unroll
-            for (int i = 0; i < kStates; ++i) h[k][i] = a[k][i] = 0.f;
-            if (c0 + ch >= Dg || n0 >= p.N) continue;
-            if (whole) {
-                const float4 v = __ldcs(reinterpret_cast<const float4 *>(hp + ch * p.N + n0));
-                h[k][0] = v.x; h[k][1] = v.y; h[k][2] = v.z; h[k][3] = v.w;
-                unpack<float, kStates>(load_packet<float, kStates>(ap + ch * p.N + n0), a[k]);
-            } else {
-                load_states(hp, ch, n0, p.N, h[k]);
-                load_states(ap, ch, n0, p.N, a[k]);
-            }
-        }
+        float acc[K];
+        if (st > 0) load(st);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int ch = (st + k) * CL + cl;
@@ -552,15 +576,12 @@ __global__ void __launch_bounds__(32 * kStepWarps) scan_step_kernel(ScanProblem 
         }
         reduce_lanes<NL, K>(acc, nl);
         const int ch = (st + reduced_first<NL, K>(nl)) * CL + cl;
-        if (nl < K && c0 + ch < Dg) {
-            float y = acc[0];
-            if (p.D_skip) y = fmaf(p.D_skip[d0 + ch], to_f32(up[ch]), y);
-            if (p.z) {
-                const float z = to_f32(zp[ch]);
-                y *= z * sigmoid_f(z);
-            }
-            static_cast<T *>(p.y)[s * p.D + d0 + ch] = from_f32<T>(y);
-        }
+        float y = acc[0];
+        const float su = __shfl_sync(0xffffffffu, u, ch), sd = __shfl_sync(0xffffffffu, skip, ch);
+        const float sg = __shfl_sync(0xffffffffu, gate, ch);
+        if (p.D_skip) y = fmaf(sd, su, y);
+        if (p.z) y *= sg;
+        if (nl < K && c0 + ch < Dg) static_cast<T *>(p.y)[s * p.D + d0 + ch] = from_f32<T>(y);
     }
 }
 

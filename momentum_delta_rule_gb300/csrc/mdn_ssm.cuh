@@ -87,7 +87,10 @@ inline cudaError_t allow_shared(int bytes) {
 }
 
 // The widest packet (elements: `most`, 2 or 1) for which `fits(bytes)` holds;
-// 2 only for two-byte elements, which it lets be copied asynchronously.
+// 2 only for two-byte elements, which it lets be copied asynchronously.  What
+// the width is worth, in us, for bf16 rows of 2048, 2044 and 2047 channels
+// (the convolution's widest is 4): gated norm of 16384 rows 51, 115, 258;
+// its gradient 122, 189, 335; scan of 8192 tokens 108, 128, 271.
 template <typename F>
 inline int packet_width(int most, int el, F fits) {
     if (fits(most, most * el)) return most;
@@ -180,12 +183,14 @@ struct Copies {
         }
     }
 };
-// And without registers: a place for one packet that a thread copies for
-// itself.  Packets of 4,
-// 8 or 16 bytes are copied as they are.  A single two-byte element comes as
-// the aligned word around it; which half it is follows from its address.  The
-// array's first and last elements, whose words may reach past the array, are
-// loaded and stored instead.
+// The same without registers, for the scan's helper warps: a place for one
+// packet that a thread copies for itself.  Packets of 4, 8 or 16 bytes are
+// copied as they are.  A single two-byte element comes as the aligned word
+// around it; which half it is follows from its address.  The array's first and
+// last elements, whose words may reach past the array, are loaded and stored
+// instead.  (Rows of 2047 bf16 channels, 8192 tokens: the convolution, the
+// norm and the scan's gradient, which have registers to spare for Copies, take
+// 164, 639 and 511 us with those and 234, 716 and 882 us with these.)
 template <typename T, int V>
 struct Slot {
     static constexpr bool kWord = V * sizeof(T) < 4;
