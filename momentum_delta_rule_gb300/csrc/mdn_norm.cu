@@ -9,11 +9,18 @@
 //   dy     = r1 (w_post dn - y r1^2 mean(dn w_post y))
 //   dw_pre = sum dh X r2;  dscale = sum dX b;  dw_post = sum dn y r1
 //
-// Memory bound: a row's elements stay in registers between its reductions, so
-// every array is read or written once.  Blocks take rows in turn, and every
+// Memory bound: a row's elements stay in registers (or, of the widest rows, in
+// shared memory) between its reductions, so every array is read or written once.  Blocks take rows in turn, and every
 // thread copies its packets of the rows ahead into shared memory that only it
 // reads, so that the reductions of one row do not hold up the loads of the
 // next.  The gradient keeps the columns' parameter sums in registers.
+//
+// Measured, bf16: 32768 rows of 2048, no gate, 82 us (537 MB, 6.5 TB/s, 96 % of
+// a copy's rate); 16384 rows of 2048 with a gate 51 us (336 MB, 6.5 TB/s), its
+// gradient 122 us (537 MB, 4.4 TB/s) and 6 us for the parameters' partial rows.
+// The gradient is bound by issue: 64 % of the slots, with 16 warps an SM at
+// 128 registers a thread.  64 rows of 1001 in fp32: 3.3 us, the latency of a
+// row's loads and its two sums.
 #include <algorithm>
 
 #include "mdn_ssm.cuh"
@@ -75,10 +82,15 @@ __device__ __forceinline__ void load_cols(const float *w, int c, int D, float no
 }
 
 // Rows ahead by the bytes of a thread's packets of one array, so that 512
-// threads of the forward and 1024 of the gradient fit their copies; negative:
-// the rows are read where they are used.
+// threads of the forward and `threads` of the gradient fit their copies (its
+// five arrays' in 160 KB); negative: the rows are read where they are used.
 __host__ __device__ constexpr int fwd_ahead(int bytes) { return bytes <= 32 ? 2 : bytes <= 64 ? 1 : 0; }
-__host__ __device__ constexpr int bwd_ahead(int bytes) { return bytes <= 16 ? 1 : bytes <= 32 ? 0 : -1; }
+// The gradient's packets that a copy would hold in registers (`held`) are read
+// in place where a thread has many.
+__host__ __device__ constexpr int bwd_ahead(int bytes, int threads, bool held) {
+    if (held) return -1;
+    return bytes * threads <= 16 * 1024 ? 1 : bytes * threads <= 32 * 1024 ? 0 : -1;
+}
 
 // This thread's packets of one array: of its rows in turn, copied AHEAD rows
 // early into AHEAD + 1 slots of shared memory that only it reads.
@@ -219,11 +231,25 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(NormProblem p, int tpr) {
     wait_copies<0>();
 }
 
+// Values of a row that a thread of the gradient has at most.
+constexpr int kBwdValues = 16;
+
+// A thread keeps its row's elements in registers, but not for rows that give
+// it kBwdValues (or half as many single two-byte ones): it reads those again
+// for each of the steps, and the weights with them, since seven arrays, three
+// weights and three sums of 16 values do not fit 128 registers.  In us with
+// both, 67 M bf16 values: rows of 8192 299 and 488, with a gate 405 and 571;
+// 33 M values, rows of 16384 248 and 417; 25 M in rows of 3001 530 and 694.
+__host__ __device__ constexpr bool bwd_lean(int NI, int V, int el) {
+    return NI * V == kBwdValues || (V * el < 4 && 2 * NI * V == kBwdValues);
+}
+
 template <typename T, int V, int NI, bool GATE, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormProblem p, int tpr) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float red[64];
-    constexpr int AHEAD = bwd_ahead(NI * V * (int)sizeof(T));
+    constexpr bool LEAN = bwd_lean(NI, V, (int)sizeof(T));
+    constexpr int AHEAD = bwd_ahead(NI * V * (int)sizeof(T), MAXT, LEAN && V * sizeof(T) < 4);
     int turn = 0;
     const int tid = threadIdx.x & (tpr - 1), mine = threadIdx.x / tpr;
     const long rpb = blockDim.x / tpr, step = gridDim.x * rpb;
@@ -246,14 +272,17 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormProblem p, int tpr) 
     };
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) issue(k, row + k * step < p.rows);
-    float wpost[NI][V], wpre[NI][V], sc[NI][V];
+    auto load_weights = [&](int i, float *post, float *scale, float *before) {
+        const int c = (i * tpr + tid) * V;
+        load_cols<V>(p.w_post, c, p.D, 1.f, post);
+        load_cols<V>(p.scale, c, p.D, 1.f, scale);
+        load_cols<V>(p.w_pre, c, p.D, 0.f, before);
+    };
+    float wpost[LEAN ? 1 : NI][V], wpre[LEAN ? 1 : NI][V], sc[LEAN ? 1 : NI][V];
     float a_post[NI][V], a_pre[NI][V], a_scale[NI][V];
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-        const int c = (i * tpr + tid) * V;
-        load_cols<V>(p.w_post, c, p.D, 1.f, wpost[i]);
-        load_cols<V>(p.scale, c, p.D, 1.f, sc[i]);
-        load_cols<V>(p.w_pre, c, p.D, 0.f, wpre[i]);
+        if (!LEAN) load_weights(i, wpost[LEAN ? 0 : i], sc[LEAN ? 0 : i], wpre[LEAN ? 0 : i]);
 #pragma unroll
         for (int v = 0; v < V; ++v) a_post[i][v] = a_pre[i][v] = a_scale[i][v] = 0.f;
     }
@@ -266,56 +295,66 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormProblem p, int tpr) 
         const float r2 = live ? p.stats[2 * row + 1] : 0.f;
         issue(put, row + AHEAD * step < p.rows);
         wait_copies<(AHEAD < 0 ? 0 : AHEAD)>();
-        float y[NI][V], X[NI][V], g[NI][V], act[NI][V], dact[NI][V], dX[NI][V], dh[NI][V];
-        // X again, and mean(dh w_pre X)
-        float s2 = 0.f;
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            sy.get(get, i, live, y[i]);
-            sx.get(get, i, live, X[i]);
-            sd.get(get, i, live, dX[i]);
-            sh.get(get, i, live && pre, dh[i]);
+        // packet i: its elements, X again and dh w_pre
+        constexpr int K = LEAN ? 1 : NI;
+        float y[K][V], X[K][V], act[K][V], dact[K][V], dh[K][V], dX[NI][V];
+        auto read = [&](int i, float *dx, bool sums) {
+            const int k = LEAN ? 0 : i;
+            if (LEAN) load_weights(i, wpost[k], sc[k], wpre[k]);
+            sy.get(get, i, live, y[k]);
+            sx.get(get, i, live, X[k]);
+            sd.get(get, i, live, dx);
+            sh.get(get, i, live && pre, dh[k]);
             if (GATE) {
-                sg.get(get, i, live, g[i]);
-                gate_acts_d<V>(g[i], p.gate_act, act[i], dact[i]);
+                float g[V];
+                sg.get(get, i, live, g);
+                gate_acts_d<V>(g, p.gate_act, act[k], dact[k]);
             }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                float b = y[i][v] * (r1 * wpost[i][v]);
-                if (GATE) b *= act[i][v];
-                X[i][v] = fmaf(sc[i][v], b, X[i][v]);
-                a_pre[i][v] = fmaf(dh[i][v] * r2, X[i][v], a_pre[i][v]);
-                dh[i][v] *= wpre[i][v];
-                s2 = fmaf(dh[i][v], X[i][v], s2);
+                float b = y[k][v] * (r1 * wpost[k][v]);
+                if (GATE) b *= act[k][v];
+                X[k][v] = fmaf(sc[k][v], b, X[k][v]);
+                if (sums) a_pre[i][v] = fmaf(dh[k][v] * r2, X[k][v], a_pre[i][v]);
+                dh[k][v] *= wpre[k][v];
+            }
+        };
+        // mean(dh w_pre X)
+        float s2 = 0.f;
+        if (!LEAN || pre) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int k = LEAN ? 0 : i;
+                read(i, dX[i], true);
+#pragma unroll
+                for (int v = 0; v < V; ++v) s2 = fmaf(dh[k][v], X[k][v], s2);
             }
         }
-        if (pre) {
-            const float m = row_sum(s2, tpr, red, turn) * inv_d * r2 * r2;
-#pragma unroll
-            for (int i = 0; i < NI; ++i)
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    dX[i][v] = fmaf(r2, fmaf(-m, X[i][v], dh[i][v]), dX[i][v]);
-        }
+        const float m2 = pre ? row_sum(s2, tpr, red, turn) * inv_d * r2 * r2 : 0.f;
         // through the residual sum, the scale and the gate; mean(dn w_post y)
         float s1 = 0.f;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const bool here = live && sy.in(i);
             const long o = at + i * tpr * V;
+            const int k = LEAN ? 0 : i;
+            if (LEAN) read(i, dX[i], false);
+            if (pre)
+#pragma unroll
+                for (int v = 0; v < V; ++v) dX[i][v] = fmaf(r2, fmaf(-m2, X[k][v], dh[k][v]), dX[i][v]);
             if (here) store_packet<T, V>(static_cast<T *>(p.dx) + o, pack<T, V>(dX[i]));
             float dg[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float n = y[i][v] * (r1 * wpost[i][v]);
-                const float ga = GATE ? act[i][v] : 1.f;
+                const float n = y[k][v] * (r1 * wpost[k][v]);
+                const float ga = GATE ? act[k][v] : 1.f;
                 a_scale[i][v] = fmaf(dX[i][v], n * ga, a_scale[i][v]);
-                const float db = dX[i][v] * sc[i][v];
-                if (GATE) dg[v] = db * n * dact[i][v];
+                const float db = dX[i][v] * sc[k][v];
+                if (GATE) dg[v] = db * n * dact[k][v];
                 const float dn = db * ga;
-                a_post[i][v] = fmaf(dn * r1, y[i][v], a_post[i][v]);
-                dX[i][v] = dn * wpost[i][v];
-                s1 = fmaf(dX[i][v], y[i][v], s1);
+                a_post[i][v] = fmaf(dn * r1, y[k][v], a_post[i][v]);
+                dX[i][v] = dn * wpost[k][v];
+                s1 = fmaf(dX[i][v], y[k][v], s1);
             }
             if (GATE && here) store_packet<T, V>(static_cast<T *>(p.dgate) + o, pack<T, V>(dg));
         }
@@ -323,8 +362,10 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormProblem p, int tpr) 
         const float m = p.w_post ? row_sum(s1, tpr, red, turn) * inv_d * r1 * r1 : 0.f;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
+            const int k = LEAN ? 0 : i;
+            if (LEAN) sy.get(get, i, live, y[k]);
 #pragma unroll
-            for (int v = 0; v < V; ++v) dX[i][v] = r1 * fmaf(-m, y[i][v], dX[i][v]);
+            for (int v = 0; v < V; ++v) dX[i][v] = r1 * fmaf(-m, y[k][v], dX[i][v]);
             if (live && sy.in(i))
                 store_packet<T, V>(static_cast<T *>(p.dy) + at + i * tpr * V, pack<T, V>(dX[i]));
         }
@@ -394,18 +435,17 @@ NormShape norm_shape(int D, int V, int soft, int most, int hard) {
     return s;
 }
 // The forward holds two arrays of a row and their weights: 32 values and 512
-// threads reach D = 16384.  Few rows (less than two for each SM) take more
-// threads and fewer values: their time is the latency of one row.
+// threads reach D = 16384.  Few rows (at most one for each SM) take more
+// threads and fewer values: their time is the latency of one row.  In us with
+// the one shape and the other, bf16: 152 rows of 2048 3.1 and 3.3, of 4096 3.7
+// and 3.8; but 303 rows of 4096 5.1 and 4.6, 1000 rows 10.3 and 9.1.
 NormShape norm_fwd_shape(int rows, int D, int V) {
-    return rows < 2 * 152 ? norm_shape(D, V, V, 512, 32) : norm_shape(D, V, V < 4 ? 4 * V : 2 * V, 512, 32);
+    return rows <= 152 ? norm_shape(D, V, V, 512, 32) : norm_shape(D, V, V < 4 ? 4 * V : 2 * V, 512, 32);
 }
-// The gradient holds seven arrays, weights and sums: 16 values and 1024
-// threads; a row of more than kSoft values a thread in 512 takes 1024.
-template <int V>
-constexpr int kSoft = V < 4 ? 16 : 8;
-NormShape norm_bwd_shape(int D, int V) {
-    return V < 4 ? norm_shape(D, V, 4 * V, 512, 16) : norm_shape(D, V, 8, 1024, 16);
-}
+// The gradient holds seven arrays, weights and sums: 16 values and 512
+// threads, and 1024 above D = 8192 (8192 rows of 8192, no gate: 299 us; with
+// 8 values and 1024 threads, in registers, 582 us).
+NormShape norm_bwd_shape(int D, int V) { return norm_shape(D, V, V < 4 ? 4 * V : 8, 512, kBwdValues); }
 // Blocks that share the rows: as many threads on each of 152 SMs as their
 // registers allow, where there are rows for them.
 int norm_blocks(int rows, const NormShape &s, int threads) {
@@ -419,7 +459,8 @@ template <bool BWD, typename T, int V, int NI>
 cudaError_t norm_launch(const NormProblem &p, const NormShape &s, cudaStream_t st) {
     const int blocks = norm_blocks(p.rows, s, BWD ? kBwdThreads : fwd_threads(s, V, p.gate != nullptr));
     constexpr int each = NI * V * (int)sizeof(T);
-    constexpr int slots = BWD ? 5 * (bwd_ahead(each) + 1) : 3 * (fwd_ahead(each) + 1);
+    const int slots = BWD ? 5 * (bwd_ahead(each, s.threads > 512 ? 1024 : 512,
+                                                bwd_lean(NI, V, (int)sizeof(T)) && V * sizeof(T) < 4) + 1) : 3 * (fwd_ahead(each) + 1);
     const int bytes = slots * each * s.threads;
     auto launch = [&](auto kernel) {
         // the kernels' own static arrays count towards the 48 KiB too
@@ -434,11 +475,10 @@ cudaError_t norm_launch(const NormProblem &p, const NormShape &s, cudaStream_t s
     const bool gate = p.gate != nullptr;
     if constexpr (BWD) {
         cudaError_t err = cudaErrorInvalidValue;
-        if constexpr (NI * V <= kSoft<V>)
-            if (s.threads <= 512)
-                err = gate ? launch(norm_bwd_kernel<T, V, NI, true, 512>)
-                           : launch(norm_bwd_kernel<T, V, NI, false, 512>);
-        if constexpr (NI * V >= kSoft<V>)
+        if (s.threads <= 512)
+            err = gate ? launch(norm_bwd_kernel<T, V, NI, true, 512>)
+                       : launch(norm_bwd_kernel<T, V, NI, false, 512>);
+        if constexpr (NI * V == kBwdValues)
             if (s.threads > 512)
                 err = gate ? launch(norm_bwd_kernel<T, V, NI, true, 1024>)
                            : launch(norm_bwd_kernel<T, V, NI, false, 1024>);
@@ -454,7 +494,7 @@ cudaError_t norm_launch(const NormProblem &p, const NormShape &s, cudaStream_t s
 template <bool BWD, typename T, int V>
 cudaError_t norm_items(const NormProblem &p, cudaStream_t st) {
     const NormShape s = BWD ? norm_bwd_shape(p.D, V) : norm_fwd_shape(p.rows, p.D, V);
-    constexpr int kMost = (BWD ? 16 : 32) / V;      // D = 16384
+    constexpr int kMost = (BWD ? kBwdValues : 32) / V;      // D = 16384
     if (s.ni == 1) return norm_launch<BWD, T, V, 1>(p, s, st);
     if (s.ni == 2) return norm_launch<BWD, T, V, 2>(p, s, st);
     if constexpr (kMost >= 4)
