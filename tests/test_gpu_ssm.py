@@ -503,6 +503,12 @@ def test_norm_options(post, pre, scale, gate):
     check_norm("fp32", 3, 700, post, pre, gate, scale, strided=False, seed=2)
 
 
+@pytest.mark.parametrize("dtype,D", [("bf16", 5000), ("bf16", 3001), ("fp32", 4100), ("bf16", 9001)])
+@pytest.mark.parametrize("post,pre,scale,gate", [(True, False, False, "silu"), (False, True, True, None), (False, False, True, "sigmoid")])
+def test_norm_options_of_wide_rows(dtype, D, post, pre, scale, gate):
+    check_norm(dtype, 9, D, post=post, pre=pre, scale=scale, gate=gate, seed=D)
+
+
 @pytest.mark.parametrize("R", [1, 2, 700, 5000])
 def test_norm_rows(R):
     check_norm("bf16", R, 64, seed=R)
