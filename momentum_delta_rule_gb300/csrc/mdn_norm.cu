@@ -453,6 +453,8 @@ int norm_blocks(int rows, const NormShape &s, int threads) {
     const long rpb = s.threads / s.tpr, most = (rows + rpb - 1) / rpb;
     return (int)std::min(most, 152L * std::max(1, threads / s.threads));
 }
+// (16384 rows of 2048 bf16, no gate: 41 us with 640 threads an SM, 43 with 512;
+// with a gate, or 32 values a thread, no more than 512 fit.)
 int fwd_threads(const NormShape &s, int V, bool gate) { return s.ni * V <= 16 && !gate ? 640 : 512; }
 constexpr int kBwdThreads = 512;
 

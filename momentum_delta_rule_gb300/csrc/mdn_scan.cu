@@ -11,12 +11,12 @@
 // time than the bytes: 32768 tokens of 2048 channels cost 1.07 G exponentials,
 // 113 us at the measured 62 a nanosecond and SM, against 80 us for 541 MB.
 //
-// Measured, bf16, 16 states: 32768 packed tokens of 2048 channels 360 us
+// Measured, bf16, 16 states: 32768 packed tokens of 2048 channels 357 us
 // (3.0 T exponentials a second, 0.31 of that rate); one sequence of 16384
-// tokens 176 us and 107 us for its first pass.  Bound by issue (71 % of the
-// slots) and the shared-memory pipe (76 %): delta, delta u, B and C come from
+// tokens 176 us and 107 us for its first pass.  Bound by issue (70 % of the
+// slots) and the shared-memory pipe (75 %): delta, delta u, B and C come from
 // there for every token.  Four channels a lane instead of two read B and C
-// half as often but leave fewer warps: 360 to 375 us.
+// half as often but leave fewer warps: 365 us, and 190 to 215 for 176.
 #include <algorithm>
 
 #include "mdn_scan.cuh"
@@ -636,7 +636,10 @@ __global__ void states_copy_kernel(const float *from, float *to, long n) {
 // token in about 1.3 times the issue time its work needs, so a sequence is
 // worth cutting, at the price of running its cut part twice, where it alone
 // would outlast twice the whole batch's work spread over the device; it is
-// then cut so that three warps meet on each scheduler.
+// then cut so that three warps meet on each scheduler.  Both passes in us, 2048
+// channels: one sequence of 16384 tokens 287, uncut 1063, with two warps a
+// scheduler 364, with four 287; one of 1024 tokens 31, uncut 69; four of 512,
+// which the rule leaves whole, 36, cut 45.
 constexpr long kSchedulers = 152 * 4;
 
 Cut choose_cut(int T_total, int D, int N) {

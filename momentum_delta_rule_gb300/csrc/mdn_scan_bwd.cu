@@ -20,8 +20,8 @@
 // gradient of 8192 tokens of 2044 channels 431 us.  A token, channel and state
 // takes two exponentials and about 20 other operations with its share of the
 // exchanges, 537 M of them: the exponentials alone are 113 us, the bytes (u,
-// dt, B, C, z, dy and the saved states in, five gradients out) 100 us.  Bound
-// by issue, 70 % of the slots of a full SM; 244 registers a thread and 103 KB
+// dt, B, C, z, dy and the saved states in, five gradients out) 80 us.  Bound
+// by issue, 61 % of the slots with eight warps; 244 registers a thread and 100 KB
 // of shared memory hold an SM to two blocks.  Tried: helper warps as in the
 // forward (987 us where this took 903), the same with registers moved from the
 // helpers to the rest (1215 us).
