@@ -553,8 +553,11 @@ BwdPlan bwd_plan(int n_seq, int T_total, int D, int G, int N, bool packed) {
                    : choose_even_cut(n_seq ? T_total / n_seq : 0, b.tiles * n_seq, held);
     const long items = packed ? n_seq + (T_total > b.cut.trigger ? T_total / b.cut.cut : 0)
                               : (long)n_seq * (n_seq ? segments_of(T_total / n_seq, b.cut.cut, b.cut.trigger) : 0);
-    // a block for every item, as far as eight waves of blocks go
-    b.slots = (int)std::max(1L, std::min(items, (8 * held + b.tiles - 1) / b.tiles));
+    // a block for every item, as far as two waves of blocks go: every block
+    // leaves partial sums.  In us with those, with two waves and with eight:
+    // 2048 sequences of 64 tokens, 256 channels, 668 and 706; 100 packed ones of
+    // 16000 tokens, 1024 channels, 330 and 340; 32 of 12000, 2048, 480 and 493
+    b.slots = (int)std::max(1L, std::min(items, (2 * held + b.tiles - 1) / b.tiles));
     b.base = layout_bytes(n_seq, T_total, D, N, b.cut, packed, false);
     b.bc = round256((size_t)b.gtiles * T_total * G * 2 * N * sizeof(float));
     b.A = round256((size_t)b.slots * D * N * sizeof(float));
