@@ -85,13 +85,19 @@ __device__ __forceinline__ void load_cols(const float *w, int c, int D, float no
 // Rows ahead by the bytes of a thread's packets of one array, so that 512
 // threads of the forward and `threads` of the gradient fit their copies (its
 // five arrays' in 160 KB); negative: the rows are read where they are used.
-__host__ __device__ constexpr int fwd_ahead(int bytes) { return bytes <= 32 ? 2 : bytes <= 64 ? 1 : 0; }
-// The gradient's packets that a copy would hold in registers (`held`) are read
-// in place where a thread has many.
+// So are packets that a copy would hold in registers (`held`) where a thread
+// has many.
+__host__ __device__ constexpr int fwd_ahead(int bytes, bool held) {
+    return held ? -1 : bytes <= 32 ? 2 : bytes <= 64 ? 1 : 0;
+}
 __host__ __device__ constexpr int bwd_ahead(int bytes, int threads, bool held) {
     if (held) return -1;
     return bytes * threads <= 16 * 1024 ? 1 : bytes * threads <= 32 * 1024 ? 0 : -1;
 }
+
+// (us in place and copied ahead, bf16: 2048 rows of 12001 240 and 438, but 4096
+// rows of 6001 320 and 180.)
+__host__ __device__ constexpr bool fwd_held(int NI, int V, int el) { return V * el < 4 && NI >= 32; }
 
 // This thread's packets of one array: of its rows in turn, copied AHEAD rows
 // early into AHEAD + 1 slots of shared memory that only it reads.
@@ -146,7 +152,7 @@ template <typename T, int V, int NI, bool GATE>
 __global__ void __launch_bounds__(512) norm_fwd_kernel(NormProblem p, int tpr) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float red[64];
-    constexpr int AHEAD = fwd_ahead(NI * V * (int)sizeof(T));
+    constexpr int AHEAD = fwd_ahead(NI * V * (int)sizeof(T), fwd_held(NI, V, (int)sizeof(T)));
     int turn = 0;
     const int tid = threadIdx.x & (tpr - 1), mine = threadIdx.x / tpr;
     const long rpb = blockDim.x / tpr, step = gridDim.x * rpb;
@@ -180,11 +186,11 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(NormProblem p, int tpr) {
     const float inv_d = 1.f / (float)p.D;
     // every thread of a block makes the same number of rounds (the sums wait
     // for the whole block)
-    int get = 0, put = AHEAD;
+    int get = 0, put = AHEAD < 0 ? 0 : AHEAD;
     for (long base = blockIdx.x * rpb; base < p.rows; base += step) {
         const bool live = row < p.rows;
         issue(put, row + AHEAD * step < p.rows);
-        wait_copies<AHEAD>();
+        wait_copies<(AHEAD < 0 ? 0 : AHEAD)>();
         float y[NI][V], x[NI][V];
         float r1 = 1.f, r2 = 1.f, ss = 0.f;
 #pragma unroll
@@ -226,8 +232,9 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(NormProblem p, int tpr) {
         row += step;
         xo += out_step;
         ho += out_step;
-        get = get == AHEAD ? 0 : get + 1;
-        put = put == AHEAD ? 0 : put + 1;
+        get = AHEAD <= 0 || get == AHEAD ? 0 : get + 1;
+        put = AHEAD <= 0 || put == AHEAD ? 0 : put + 1;
+        sy.done(); sx.done(); sg.done();
     }
     wait_copies<0>();
 }
@@ -463,7 +470,7 @@ cudaError_t norm_launch(const NormProblem &p, const NormShape &s, cudaStream_t s
     const int blocks = norm_blocks(p.rows, s, BWD ? kBwdThreads : fwd_threads(s, V, p.gate != nullptr));
     constexpr int each = NI * V * (int)sizeof(T);
     const int slots = BWD ? 5 * (bwd_ahead(each, s.threads > 512 ? 1024 : 512,
-                                                bwd_lean(NI, V, (int)sizeof(T)) && V * sizeof(T) < 4) + 1) : 3 * (fwd_ahead(each) + 1);
+                                                bwd_lean(NI, V, (int)sizeof(T)) && V * sizeof(T) < 4) + 1) : 3 * (fwd_ahead(each, fwd_held(NI, V, (int)sizeof(T))) + 1);
     const int bytes = slots * each * s.threads;
     auto launch = [&](auto kernel) {
         // the kernels' own static arrays count towards the 48 KiB too
