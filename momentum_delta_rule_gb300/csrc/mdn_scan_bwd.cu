@@ -95,12 +95,13 @@ __device__ __forceinline__ int reduce_triples(float *v, int nl) {
 }
 
 // One block takes CB channels of one group through its items, each item's
-// chunks last first.  Channels are held two to a pair of registers.
+// chunks last first.  A lane's two channels are held as two pairs of states
+// each: pair i has channel i / 2, states 2 (i % 2) and the next.
 template <typename T, typename S, int V>
 __global__ void __launch_bounds__(S::NT, S::NT <= 128 ? 2 : 1)
 scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
     using Sm = BwdSmem<T, S, V>;
-    static_assert(S::CPT == 2, "one pair of channels a lane");
+    static_assert(S::CPT == 2 && kStates == 4, "four pairs a lane");
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Sm &sm = *reinterpret_cast<Sm *>(smem_raw);
     constexpr int RS = S::NT / Sm::QC;               // tokens between a thread's packets
@@ -124,12 +125,18 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
         if (live0) load_states(base, d0 + cw, n0, p.N, x);
         if (live1) load_states(base, d0 + cw + 1, n0, p.N, y);
 #pragma unroll
-        for (int i = 0; i < kStates; ++i) out[i] = make_pair(x[i], y[i]);
+        for (int i = 0; i < 2; ++i) {
+            out[i] = make_pair(x[2 * i], x[2 * i + 1]);
+            out[2 + i] = make_pair(y[2 * i], y[2 * i + 1]);
+        }
     };
     auto store_pairs = [&](float *base, const Pair *v) {
         float x[kStates], y[kStates];
 #pragma unroll
-        for (int i = 0; i < kStates; ++i) split_pair(v[i], x[i], y[i]);
+        for (int i = 0; i < 2; ++i) {
+            split_pair(v[i], x[2 * i], x[2 * i + 1]);
+            split_pair(v[2 + i], y[2 * i], y[2 * i + 1]);
+        }
         if (live0) store_states(base, d0 + cw, n0, p.N, x);
         if (live1) store_states(base, d0 + cw + 1, n0, p.N, y);
     };
@@ -226,7 +233,8 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
 #pragma unroll
             for (int i = 0; i < kStates; ++i) {
                 float x, y;
-                split_pair(mul2(make_pair(s0, s1), a2[i]), x, y);
+                const float sc = i < 2 ? s0 : s1;
+                split_pair(mul2(make_pair(sc, sc), a2[i]), x, y);
                 gc[i] = fma2(make_pair(ex2(x), ex2(y)), gc[i], r[i]);
             }
         }
@@ -279,8 +287,11 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
             // a lane's saved states (its own copies), or those of sub s
             auto load_sub = [&](const float4 (*from)[S::NT], Pair *h) {
                 const float4 x = from[0][tid], y = from[1][tid];
-                h[0] = make_pair(x.x, y.x); h[1] = make_pair(x.y, y.y);
-                h[2] = make_pair(x.z, y.z); h[3] = make_pair(x.w, y.w);
+                h[0] = make_pair(x.x, x.y); h[1] = make_pair(x.z, x.w);
+                h[2] = make_pair(y.x, y.y); h[3] = make_pair(y.z, y.w);
+            };
+            auto state_pair = [](const Packet<float, kStates> &q, int i) {
+                return make_pair(q.e[i % 2 * 2], q.e[i % 2 * 2 + 1]);
             };
             // forward: the state before every fourth token
             {
@@ -297,15 +308,18 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
                         const float x0 = dl.e[0] * uv.e[0], x1 = dl.e[1] * uv.e[1];
 #pragma unroll
                         for (int i = 0; i < kStates; ++i) {
+                            const float d = dl.e[i / 2], x = i < 2 ? x0 : x1;
                             float e0, e1;
-                            split_pair(fma2(make_pair(dl.e[0], dl.e[1]), a2[i], make_pair(kDecayBias, kDecayBias)), e0, e1);
-                            h[i] = fma2(make_pair(ex2(e0), ex2(e1)), h[i],
-                                        make_pair(x0 * bv.e[i], x1 * bv.e[i]));
+                            split_pair(fma2(make_pair(d, d), a2[i], make_pair(kDecayBias, kDecayBias)), e0, e1);
+                            h[i] = fma2(make_pair(ex2(e0), ex2(e1)), h[i], mul2(make_pair(x, x), state_pair(bv, i)));
                         }
                     }
                     float x[kStates], y[kStates];
 #pragma unroll
-                    for (int i = 0; i < kStates; ++i) split_pair(h[i], x[i], y[i]);
+                    for (int i = 0; i < 2; ++i) {
+                        split_pair(h[i], x[2 * i], x[2 * i + 1]);
+                        split_pair(h[2 + i], y[2 * i], y[2 * i + 1]);
+                    }
                     sm.sub[s][0][tid] = make_float4(x[0], x[1], x[2], x[3]);
                     sm.sub[s][1][tid] = make_float4(y[0], y[1], y[2], y[3]);
                 }
@@ -326,10 +340,11 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
                     const float x0 = dl.e[0] * uv.e[0], x1 = dl.e[1] * uv.e[1];
 #pragma unroll
                     for (int i = 0; i < kStates; ++i) {
+                        const float d = dl.e[i / 2], x = i < 2 ? x0 : x1;
                         float e0, e1;
-                        split_pair(fma2(make_pair(dl.e[0], dl.e[1]), a2[i], make_pair(kDecayBias, kDecayBias)), e0, e1);
+                        split_pair(fma2(make_pair(d, d), a2[i], make_pair(kDecayBias, kDecayBias)), e0, e1);
                         a[j][i] = make_pair(ex2(e0), ex2(e1));
-                        h[j + 1][i] = fma2(a[j][i], h[j][i], make_pair(x0 * bv.e[i], x1 * bv.e[i]));
+                        h[j + 1][i] = fma2(a[j][i], h[j][i], mul2(make_pair(x, x), state_pair(bv, i)));
                     }
                 }
                 float tri[kSub * 6], bc[kSub * 2 * kStates];
@@ -341,33 +356,41 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
                     const auto dl = load_packet<float, 2>(&sm.delta[t][cw]);
                     const auto uv = load_packet<float, 2>(&sm.u[t][cw]);
                     const auto ev = load_packet<float, 2>(&sm.e[t][cw]);
-                    const Pair dlp = make_pair(dl.e[0], dl.e[1]);
-                    const float x0 = dl.e[0] * uv.e[0], x1 = dl.e[1] * uv.e[1];
-                    Pair s2 = make_pair(0.f, 0.f);
-                    float s1a = 0.f, s1b = 0.f, ya = 0.f, yb = 0.f;
+                    Pair db[2], dc[2];               // dB, dC of the lane's states
 #pragma unroll
-                    for (int i = 0; i < kStates; ++i) {
-                        float g0, g1, h0, h1;
-                        split_pair(gc[i], g0, g1);
-                        split_pair(h[j + 1][i], h0, h1);
-                        g0 = fmaf(cv.e[i], ev.e[0], g0);
-                        g1 = fmaf(cv.e[i], ev.e[1], g1);
-                        bc[(j * 2 + 0) * kStates + i] = fmaf(g1, x1, g0 * x0);
-                        bc[(j * 2 + 1) * kStates + i] = fmaf(ev.e[1], h1, ev.e[0] * h0);
-                        ya = fmaf(cv.e[i], h0, ya);
-                        yb = fmaf(cv.e[i], h1, yb);
-                        s1a = fmaf(g0, bv.e[i], s1a);
-                        s1b = fmaf(g1, bv.e[i], s1b);
-                        gc[i] = mul2(a[j][i], make_pair(g0, g1));
-                        const Pair wv = mul2(gc[i], h[j][i]);
-                        s2 = fma2(a2[i], wv, s2);
-                        dAc[i] = fma2(dlp, wv, dAc[i]);
+                    for (int c = 0; c < 2; ++c) {
+                        const float xc = dl.e[c] * uv.e[c];
+                        const Pair x = make_pair(xc, xc), e = make_pair(ev.e[c], ev.e[c]);
+                        const Pair d = make_pair(dl.e[c], dl.e[c]);
+                        Pair s1, s2, y;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int i = 2 * c + k;
+                            const Pair b = state_pair(bv, i), cc = state_pair(cv, i), ht = h[j + 1][i];
+                            const Pair gt = fma2(cc, e, gc[i]);
+                            db[k] = c ? fma2(gt, x, db[k]) : mul2(gt, x);
+                            dc[k] = c ? fma2(ht, e, dc[k]) : mul2(ht, e);
+                            y = k ? fma2(cc, ht, y) : mul2(cc, ht);
+                            s1 = k ? fma2(gt, b, s1) : mul2(gt, b);
+                            gc[i] = mul2(a[j][i], gt);
+                            const Pair wv = mul2(gc[i], h[j][i]);
+                            s2 = k ? fma2(a2[i], wv, s2) : mul2(a2[i], wv);
+                            dAc[i] = fma2(d, wv, dAc[i]);
+                        }
+                        float lo, hi;
+                        split_pair(s1, lo, hi);
+                        tri[j * 6 + 3 * c] = lo + hi;
+                        split_pair(s2, lo, hi);
+                        tri[j * 6 + 3 * c + 1] = lo + hi;
+                        split_pair(y, lo, hi);
+                        tri[j * 6 + 3 * c + 2] = lo + hi;
                     }
-                    tri[j * 6 + 0] = s1a;
-                    tri[j * 6 + 2] = ya;
-                    tri[j * 6 + 3] = s1b;
-                    tri[j * 6 + 5] = yb;
-                    split_pair(s2, tri[j * 6 + 1], tri[j * 6 + 4]);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float *o = bc + j * 2 * kStates + 2 * k;
+                        split_pair(db[k], o[0], o[1]);
+                        split_pair(dc[k], o[kStates], o[kStates + 1]);
+                    }
                 }
                 // a lane ends with R (token, channel) triples and finishes them
                 // where it owns them; the row's readers are all past it
