@@ -465,39 +465,42 @@ int norm_blocks(int rows, const NormShape &s, int threads) {
 int fwd_threads(const NormShape &s, int V, bool gate) { return s.ni * V <= 16 && !gate ? 640 : 512; }
 constexpr int kBwdThreads = 512;
 
+// Launches a kernel of at most MAXT threads that keeps `each` bytes a thread.
+template <auto Kernel, int MAXT>
+cudaError_t norm_run(const NormProblem &p, const NormShape &s, int blocks, int each, cudaStream_t st) {
+    const cudaError_t err = allow_shared<Kernel>(each * MAXT);
+    if (err != cudaSuccess) return err;
+    Kernel<<<blocks, s.threads, each * s.threads, st>>>(p, s.tpr);
+    return cudaGetLastError();
+}
+
 template <bool BWD, typename T, int V, int NI>
 cudaError_t norm_launch(const NormProblem &p, const NormShape &s, cudaStream_t st) {
     const int blocks = norm_blocks(p.rows, s, BWD ? kBwdThreads : fwd_threads(s, V, p.gate != nullptr));
     constexpr int each = NI * V * (int)sizeof(T);
-    const int slots = BWD ? 5 * (bwd_ahead(each, s.threads > 512 ? 1024 : 512,
-                                                bwd_lean(NI, V, (int)sizeof(T)) && V * sizeof(T) < 4) + 1) : 3 * (fwd_ahead(each, fwd_held(NI, V, (int)sizeof(T))) + 1);
-    const int bytes = slots * each * s.threads;
-    auto launch = [&](auto kernel) {
-        // the kernels' own static arrays count towards the 48 KiB too
-        if (bytes > 47 * 1024) {
-            const cudaError_t err =
-                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-            if (err != cudaSuccess) return err;
-        }
-        kernel<<<blocks, s.threads, bytes, st>>>(p, s.tpr);
-        return cudaGetLastError();
-    };
     const bool gate = p.gate != nullptr;
     if constexpr (BWD) {
+        constexpr bool held = bwd_lean(NI, V, (int)sizeof(T)) && V * sizeof(T) < 4;
         cudaError_t err = cudaErrorInvalidValue;
-        if (s.threads <= 512)
-            err = gate ? launch(norm_bwd_kernel<T, V, NI, true, 512>)
-                       : launch(norm_bwd_kernel<T, V, NI, false, 512>);
+        if (s.threads <= 512) {
+            constexpr int bytes = 5 * (bwd_ahead(each, 512, held) + 1) * each;
+            err = gate ? norm_run<norm_bwd_kernel<T, V, NI, true, 512>, 512>(p, s, blocks, bytes, st)
+                       : norm_run<norm_bwd_kernel<T, V, NI, false, 512>, 512>(p, s, blocks, bytes, st);
+        }
         if constexpr (NI * V == kBwdValues)
-            if (s.threads > 512)
-                err = gate ? launch(norm_bwd_kernel<T, V, NI, true, 1024>)
-                           : launch(norm_bwd_kernel<T, V, NI, false, 1024>);
+            if (s.threads > 512) {
+                constexpr int bytes = 5 * (bwd_ahead(each, 1024, held) + 1) * each;
+                err = gate ? norm_run<norm_bwd_kernel<T, V, NI, true, 1024>, 1024>(p, s, blocks, bytes, st)
+                           : norm_run<norm_bwd_kernel<T, V, NI, false, 1024>, 1024>(p, s, blocks, bytes, st);
+            }
         if (err != cudaSuccess) return err;
         norm_reduce_kernel<<<(3 * p.D + 31) / 32, 256, 0, st>>>(
             p.partial, blocks * (s.threads / s.tpr), p.D, p.dw_post, p.dw_pre, p.dscale);
         return cudaGetLastError();
     } else {
-        return gate ? launch(norm_fwd_kernel<T, V, NI, true>) : launch(norm_fwd_kernel<T, V, NI, false>);
+        constexpr int bytes = 3 * (fwd_ahead(each, fwd_held(NI, V, (int)sizeof(T))) + 1) * each;
+        return gate ? norm_run<norm_fwd_kernel<T, V, NI, true>, 512>(p, s, blocks, bytes, st)
+                    : norm_run<norm_fwd_kernel<T, V, NI, false>, 512>(p, s, blocks, bytes, st);
     }
 }
 
