@@ -49,3 +49,23 @@ def norm_args(rows, D, dtype, gate=False, bwd=False):
         return (p(0), p(1), g, p(3), p(4), p(5), p(6), p(7), None, rows, D, 0, 1e-6, D, D, D, dtype, None)
     return (p(0), p(1), g, p(3), p(4), p(5), p(6), p(7), p(8), p(9), p(10), p(11) if gate else None, p(12), p(13), p(14),
             rows, D, 0, D, D, D, D, D, dtype, p(15), 1 << 40, None)
+
+
+def conv_args(n_seq, packed, tokens, D, W, dtype, bwd=False):
+    """Arguments of mdn_short_conv_fwd or _bwd."""
+    p = lambda i: ctypes.c_void_p(0x100000 * (i + 1))
+    cu = p(20) if packed else None
+    B, T = (1, tokens) if packed else (n_seq, tokens // n_seq)
+    if not bwd:
+        return (p(0), p(1), p(2), p(3), p(4), p(5), cu, n_seq, B, T, D, W, 1, D, dtype, None)
+    return (p(0), p(1), p(2), p(3), p(4), p(5), p(6), p(7), p(8), p(9), cu, n_seq, B, T, D, W, 1, D, D, dtype, p(10),
+            1 << 40, None)
+
+
+def scan_bwd_args(n_seq, packed, tokens, D, G, N, dtype):
+    """Arguments of mdn_ssm_scan_bwd."""
+    p = lambda i: ctypes.c_void_p(0x100000 * (i + 1))
+    cu = p(30) if packed else None
+    B, T = (1, tokens) if packed else (n_seq, tokens // n_seq)
+    return tuple(p(i) for i in range(20)) + (cu, n_seq, B, T, D, G, N, 1, D, D, G * N, G * N, D, D, dtype, p(40), 1 << 60,
+                                             None)
