@@ -319,7 +319,7 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
                 }
             }
 #pragma unroll
-            for (int i = 0; i < kStates; ++i) a[c][i] *= kLog2e;
+            for (int i = 0; i < kStates; ++i) a[c][i] = decay_rate(a[c][i]);
             if (!PRE && live[c]) {
                 // the state before this segment, through those before it
                 const int before = it.tok0 / l.cut;
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(32 * kStepWarps) scan_step_kernel(ScanProblem 
             acc[k] = 0.f;
 #pragma unroll
             for (int i = 0; i < kStates; ++i) {
-                h[k][i] = fmaf(ex2(fmaf(dk, a[k][i] * kLog2e, kDecayBias)), h[k][i], duk * b[i]);
+                h[k][i] = fmaf(ex2(fmaf(dk, decay_rate(a[k][i]), kDecayBias)), h[k][i], duk * b[i]);
                 acc[k] = fmaf(h[k][i], c[i], acc[k]);
             }
             if (c0 + ch >= Dg || n0 >= p.N) continue;

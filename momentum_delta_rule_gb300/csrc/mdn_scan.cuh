@@ -114,6 +114,15 @@ __device__ __forceinline__ bool find_item(const ScanProblem &p, const Layout &l,
     return true;
 }
 
+// A log2 e, the decays' exponent a unit of delta, kept above -infinity: a token
+// behind a sequence's end has delta = 0 and must change nothing, which 0 times
+// -infinity would.  Any delta above 1e-36 still gives 2^-huge = 0.
+__device__ __forceinline__ float decay_rate(float a) {
+    float x = a * kLog2e;
+    asm("max.NaN.f32 %0, %0, 0fFF7FFFFF;" : "+f"(x));        // -FLT_MAX; NaN stays
+    return x;
+}
+
 // A lane's A, states or gradients of one channel (four of N): [D, N] row d.
 __device__ __forceinline__ void load_states(const float *base, long d, int n, int N, float *f) {
 #pragma unroll

@@ -145,7 +145,9 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
     load_pairs(p.A, a2);
 #pragma unroll
     for (int i = 0; i < kStates; ++i) {
-        a2[i] = mul2(a2[i], make_pair(kLog2e, kLog2e));
+        float x, y;
+        split_pair(a2[i], x, y);
+        a2[i] = make_pair(decay_rate(x), decay_rate(y));
         dA[i] = make_pair(0.f, 0.f);
     }
     const int row = tid / Sm::QC, qcol = tid % Sm::QC * V;
