@@ -330,8 +330,9 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
             Pair dAc[kStates];                       // this chunk's dA
 #pragma unroll
             for (int i = 0; i < kStates; ++i) dAc[i] = make_pair(0.f, 0.f);
-#pragma unroll 1
-            for (int s = n4 / kSub - 1; s >= 0; --s) {
+            // four tokens forward again, and back; LAST: some are behind the end
+            auto walk = [&](int s, auto last) {
+                constexpr bool LAST = decltype(last)::value;
                 Pair h[kSub + 1][kStates], a[kSub][kStates];
                 load_sub(s > 0 ? sm.sub[s - 1] : sm.entry[chunk & 1], h[0]);
 #pragma unroll
@@ -379,6 +380,9 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
                             const Pair wv = mul2(gc[i], h[j][i]);
                             s2 = k ? fma2(a2[i], wv, s2) : mul2(a2[i], wv);
                             dAc[i] = fma2(d, wv, dAc[i]);
+                            // a token behind the end has d = 0, but may
+                            // meet an infinite or NaN state
+                            if (LAST && s * kSub + j >= n) dAc[i] = make_pair(0.f, 0.f);
                         }
                         float lo, hi;
                         split_pair(s1, lo, hi);
@@ -437,7 +441,11 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
                     for (int q = 0; q < S::NW; ++q) v += sm.bc[s & 1][q][j][which][m];
                     w.bc[((((long)(tile % gtiles) * p.T_total + t0 + tb + t) * p.G + g) * 2 + which) * p.N + m] = v;
                 }
-            }
+            };
+            int sub = n4 / kSub - 1;
+            if (n < n4) walk(sub--, std::true_type());
+#pragma unroll 1
+            for (; sub >= 0; --sub) walk(sub, std::false_type());
 #pragma unroll
             for (int i = 0; i < kStates; ++i) dA[i] = fma2(dAc[i], make_pair(1.f, 1.f), dA[i]);
             // the last barrier above stands between the results in shared

@@ -12,6 +12,7 @@ from tests.test_gpu_ssm import _dev, _gen, _np, _scan_kw, _scan_ref, scan_case
 pytestmark = pytest.mark.gpu
 
 INF = float("inf")
+STATES = [8, 16, 32, 64, 128]
 
 
 def _same_kind(name, got, ref, mag, ulps):
@@ -26,6 +27,54 @@ def _same_kind(name, got, ref, mag, ulps):
     at = np.argwhere(bad)
     assert not len(at), "%s: %d of %d, first at %s: %s for %s" % (name, len(at), bad.size, at[0], g[tuple(at[0])],
                                                                   ref[tuple(at[0])])
+
+
+def positive_case(dtype, N, G=1, lens=(7, 34), D=12, seed=0):
+    """Every term of every sum positive (but A): an infinity is not met by its opposite."""
+    c = scan_case(dtype, list(lens), D=D, N=N, G=G, strided=False, seed=seed)
+    for k in ("u", "Bm", "Cm", "z", "h0", "D_skip"):
+        c[k] = c[k].abs() + 0.125
+    return c
+
+
+def check_kind(c, dy_at=None, dh_at=None):
+    import momentum_delta_rule_gb300 as mdn
+    d = _dev(c)
+    D = d["A"].shape[0]
+    args = (d["u"], d["dt"], d["A"], d["Bm"], d["Cm"])
+    y, hT, hc = mdn.ssm_scan_fwd(*args, h0=d["h0"], return_chunk_states=True, **_scan_kw(d))
+    dy = (torch.rand(y.shape, generator=_gen(1)) + 0.125).to(y.dtype)
+    dhT = torch.rand(hT.shape, generator=_gen(2)) + 0.125
+    if dy_at is not None:
+        dy[dy_at] = INF
+    if dh_at is not None:
+        dhT[dh_at] = INF
+    g = mdn.ssm_scan_bwd(*args, hc, dy.cuda(), dh_T=dhT.cuda(), need_dh0=True, **_scan_kw(d))
+    torch.cuda.synchronize()
+    with np.errstate(all="ignore"):
+        ref, mag = (_scan_ref(c, dy=_np(dy).reshape(-1, D), dh_T=_np(dhT), magnitude=m) for m in (False, True))
+    T, L = max(c["lens"]), sum(c["lens"])
+    _same_kind("y", y, ref[0], mag[0], 64 + 16 * T)
+    _same_kind("h_T", hT, ref[1], mag[1], 64 + 16 * T)
+    for k, v in g.items():
+        _same_kind(k, v, ref[3][k], mag[3][k], 2 * (64 + 16 * T) + max(L, D))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("N", STATES)
+def test_infinite_input(dtype, N):
+    # in the middle of a sequence, and as its last token
+    c = positive_case(dtype, N, seed=N)
+    c["u"][0, 3, 2] = INF
+    c["u"][0, 40, 5] = INF
+    check_kind(c)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("N", STATES)
+def test_infinite_adjoint_of_the_final_state(dtype, N):
+    check_kind(positive_case(dtype, N, seed=N), dh_at=(0, 4, N - 1))
+    check_kind(positive_case(dtype, N, seed=N), dh_at=(1, 9, 0))
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
