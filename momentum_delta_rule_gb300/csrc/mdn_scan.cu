@@ -145,8 +145,9 @@ struct FwdSmem {
 // use itself, kAhead stages early, so that only it has to wait for them.
 // kEnds: the first pass over a cut segment, whose end state and sum of delta are
 // all it leaves.  kAdjoint: the same for the gradient's adjoint of the state,
-// which runs through the tokens last first, r <- a_t (r + C_t e_t).
-template <typename T, typename S, int V, Pass PASS>
+// which runs through the tokens last first, r <- a_t (r + C_t e_t).  Neither adds
+// up states, so neither cares for PAD.
+template <typename T, typename S, int V, Pass PASS, Pad PAD>
 __global__ void __launch_bounds__(S::NT + S::HT, S::NT + S::HT <= 256 ? 3 : 2)
 scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
     using Sm = FwdSmem<T, S, V>;
@@ -296,6 +297,9 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
     Pair a2[S::CPT][kStates / 2], h[S::CPT][kStates / 2];
     float sum[S::CPT];
     bool live[S::CPT];
+    bool in[kStates];                    // of the lane's states, the real ones
+#pragma unroll
+    for (int i = 0; i < kStates; ++i) in[i] = n0 + i < p.N;
     {
         // a cut sequence's initial state, if its final state takes its place
         float *kept = l.pre_h0 + (long)it.pre * p.D * p.N;
@@ -391,6 +395,7 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
                             continue;
                         }
                         h[c][i] = fma2(a, h[c][i], mul2(make_pair(duc, duc), b));
+                        if (PAD == Pad::kStates) h[c][i] = real_states(h[c][i], in[2 * i], in[2 * i + 1]);
                         if (!PRE) {
                             const Pair cc = make_pair(cv[j].e[2 * i], cv[j].e[2 * i + 1]);
                             y = i ? fma2(h[c][i], cc, y) : mul2(h[c][i], cc);
@@ -399,7 +404,7 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
                     if (PRE) continue;
                     float y0, y1;
                     split_pair(y, y0, y1);
-                    acc[j * S::CPT + c] = y0 + y1;
+                    acc[j * S::CPT + c] = PAD != Pad::kLanes || in[0] ? y0 + y1 : 0.f;
                 }
             }
             if (!PRE) {
@@ -428,16 +433,16 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
                 l.pre_sum[pre_slot * p.D + d0 + cw + c] = sum[c];
 }
 
-template <typename T, typename S, int V, Pass PASS>
+template <typename T, typename S, int V, Pass PASS, Pad PAD = Pad::kNone>
 cudaError_t fwd_launch(const ScanProblem &p, const Layout &l, int blocks_per_tile, cudaStream_t st) {
     if (blocks_per_tile == 0) return cudaSuccess;
     const int Dg = p.D / p.G;
     const long tiles = (long)p.G * ((Dg + S::CB - 1) / S::CB);
     if (tiles * blocks_per_tile > 0x7fffffffL) return cudaErrorInvalidConfiguration;
     constexpr int bytes = (int)sizeof(FwdSmem<T, S, V>);
-    const cudaError_t err = allow_shared<scan_fwd_kernel<T, S, V, PASS>>(bytes);
+    const cudaError_t err = allow_shared<scan_fwd_kernel<T, S, V, PASS, PAD>>(bytes);
     if (err != cudaSuccess) return err;
-    scan_fwd_kernel<T, S, V, PASS>
+    scan_fwd_kernel<T, S, V, PASS, PAD>
         <<<(unsigned)(tiles * blocks_per_tile), S::NT + S::HT, bytes, st>>>(p, l, (int)tiles);
     return cudaGetLastError();
 }
@@ -446,7 +451,12 @@ template <typename T, typename S, int V>
 cudaError_t fwd_t(const ScanProblem &p, const Layout &l, Pass pass, cudaStream_t st) {
     if (pass == Pass::kAdjoint) return fwd_launch<T, S, V, Pass::kAdjoint>(p, l, l.pres, st);
     const cudaError_t err = fwd_launch<T, S, V, Pass::kEnds>(p, l, l.pres, st);
-    return err != cudaSuccess ? err : fwd_launch<T, S, V, Pass::kMain>(p, l, l.items, st);
+    if (err != cudaSuccess) return err;
+    switch (pad_of(p.N)) {
+        case Pad::kNone: return fwd_launch<T, S, V, Pass::kMain, Pad::kNone>(p, l, l.items, st);
+        case Pad::kLanes: return fwd_launch<T, S, V, Pass::kMain, Pad::kLanes>(p, l, l.items, st);
+        default: return fwd_launch<T, S, V, Pass::kMain, Pad::kStates>(p, l, l.items, st);
+    }
 }
 
 template <typename T>
@@ -491,7 +501,7 @@ constexpr int kStepWarps = 4;
 // and 16 states: 12.7 us, 71 MB at 5.6 TB/s (10.5 us at a copy's rate); 15.5 us
 // with the states behind the deltas and the gates behind the sums.  Warps that
 // took several sequences one after another took 20 to 34 us.
-template <typename T, int NL>
+template <typename T, int NL, Pad PAD>
 __global__ void __launch_bounds__(32 * kStepWarps) scan_step_kernel(ScanProblem p, int tiles) {
     constexpr int CL = 32 / NL, K = NL < 4 ? NL : 4, STEPS = NL;
     const int lane = threadIdx.x & 31;
@@ -503,7 +513,7 @@ __global__ void __launch_bounds__(32 * kStepWarps) scan_step_kernel(ScanProblem 
     const int d0 = g * Dg + c0;
     const long s = blockIdx.y;
     const int nl = lane % NL, cl = lane / NL, n0 = nl * kStates;
-    const bool whole = p.N % kStates == 0;
+    constexpr bool whole = PAD != Pad::kStates;
     const T *up = static_cast<const T *>(p.u) + s * p.ld_u + d0;
     const T *zp = static_cast<const T *>(p.z) + s * p.ld_z + d0;
     const float *hp = p.h0 + (s * p.D + d0) * p.N, *ap = p.A + (long)d0 * p.N;
@@ -568,8 +578,9 @@ __global__ void __launch_bounds__(32 * kStepWarps) scan_step_kernel(ScanProblem 
 #pragma unroll
             for (int i = 0; i < kStates; ++i) {
                 h[k][i] = fmaf(ex2(fmaf(dk, decay_rate(a[k][i]), kDecayBias)), h[k][i], duk * b[i]);
-                acc[k] = fmaf(h[k][i], c[i], acc[k]);
+                if (PAD != Pad::kStates || n0 + i < p.N) acc[k] = fmaf(h[k][i], c[i], acc[k]);
             }
+            if (PAD == Pad::kLanes && n0 >= p.N) acc[k] = 0.f;
             if (c0 + ch >= Dg || n0 >= p.N) continue;
             if (whole) __stcs(reinterpret_cast<float4 *>(ho + ch * p.N + n0), make_float4(h[k][0], h[k][1], h[k][2], h[k][3]));
             else store_states(ho, ch, n0, p.N, h[k]);
@@ -604,7 +615,11 @@ cudaError_t step_t(const ScanProblem &p, cudaStream_t st) {
         q.h0 = p.h0 + s0 * p.D * p.N;
         q.h_T = p.h_T + s0 * p.D * p.N;
         const dim3 grid(blocks, (unsigned)std::min(65535L, p.n_seq - s0));
-        scan_step_kernel<T, NL><<<grid, 32 * kStepWarps, 0, st>>>(q, tiles);
+        switch (pad_of(p.N)) {
+            case Pad::kNone: scan_step_kernel<T, NL, Pad::kNone><<<grid, 32 * kStepWarps, 0, st>>>(q, tiles); break;
+            case Pad::kLanes: scan_step_kernel<T, NL, Pad::kLanes><<<grid, 32 * kStepWarps, 0, st>>>(q, tiles); break;
+            default: scan_step_kernel<T, NL, Pad::kStates><<<grid, 32 * kStepWarps, 0, st>>>(q, tiles);
+        }
         const cudaError_t err = cudaGetLastError();
         if (err != cudaSuccess) return err;
     }

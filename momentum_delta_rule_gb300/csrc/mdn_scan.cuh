@@ -32,6 +32,16 @@ inline int lanes_of_states(int N) {
     return nl;
 }
 
+// Which of a channel's padded states a kernel meets: none, whole lanes of them,
+// or some beside others in a lane.  An infinite delta u makes NaN of a padded
+// state (inf times B = 0), which must not reach a sum over states.  The first
+// kind needs no instruction for that, the second one a channel and token of the
+// forward, the third one a state.
+enum class Pad { kNone, kLanes, kStates };
+inline Pad pad_of(int N) {
+    return N % kStates ? Pad::kStates : lanes_of_states(N) * kStates > N ? Pad::kLanes : Pad::kNone;
+}
+
 // A stretch of one sequence's tokens that a block runs on its own: the whole
 // sequence, or one of the segments a long sequence is cut into.
 struct Item {
@@ -136,6 +146,13 @@ __device__ __forceinline__ void store_states(float *base, long d, int n, int N, 
 #pragma unroll
     for (int i = 0; i < kStates; ++i)
         if (n + i < N) base[d * N + n + i] = f[i];
+}
+
+// A pair of states without the padded ones.
+__device__ __forceinline__ Pair real_states(Pair v, bool lo, bool hi) {
+    float x, y;
+    split_pair(v, x, y);
+    return make_pair(lo ? x : 0.f, hi ? y : 0.f);
 }
 
 // Stages B (and C) rows of tokens t0 .. t0 + n, group g, as fp32 [token][NP]

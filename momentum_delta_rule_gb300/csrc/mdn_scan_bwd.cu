@@ -98,7 +98,7 @@ __device__ __forceinline__ int reduce_triples(float *v, int nl) {
 // One block takes CB channels of one group through its items, each item's
 // chunks last first.  A lane's two channels are held as two pairs of states
 // each: pair i has channel i / 2, states 2 (i % 2) and the next.
-template <typename T, typename S, int V>
+template <typename T, typename S, int V, Pad PAD>
 __global__ void __launch_bounds__(S::NT, S::NT <= 128 ? 2 : 1)
 scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
     using Sm = BwdSmem<T, S, V>;
@@ -119,6 +119,12 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
     const int nl = lane % S::NL, n0 = nl * kStates;
     const int cw = warp * S::WC + lane / S::NL * 2;  // the lane's first channel in the block
     const bool live0 = c0 + cw < Dg && n0 < p.N, live1 = c0 + cw + 1 < Dg && n0 < p.N;
+    bool in[kStates];                                // of the lane's states, the real ones
+#pragma unroll
+    for (int i = 0; i < kStates; ++i) in[i] = n0 + i < p.N;
+    auto real = [&](Pair v, int i) {                 // pair i without padded states
+        return PAD == Pad::kStates ? real_states(v, in[i % 2 * 2], in[i % 2 * 2 + 1]) : v;
+    };
     const float skip0 = c0 + cw < Dg && p.D_skip ? p.D_skip[d0 + cw] : 0.f;
     const float skip1 = c0 + cw + 1 < Dg && p.D_skip ? p.D_skip[d0 + cw + 1] : 0.f;
     auto load_pairs = [&](const float *base, Pair *out) {
@@ -314,7 +320,7 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
                             const float d = dl.e[i / 2], x = i < 2 ? x0 : x1;
                             float e0, e1;
                             split_pair(fma2(make_pair(d, d), a2[i], make_pair(kDecayBias, kDecayBias)), e0, e1);
-                            h[i] = fma2(make_pair(ex2(e0), ex2(e1)), h[i], mul2(make_pair(x, x), state_pair(bv, i)));
+                            h[i] = real(fma2(make_pair(ex2(e0), ex2(e1)), h[i], mul2(make_pair(x, x), state_pair(bv, i))), i);
                         }
                     }
                     float x[kStates], y[kStates];
@@ -347,8 +353,8 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
                         const float d = dl.e[i / 2], x = i < 2 ? x0 : x1;
                         float e0, e1;
                         split_pair(fma2(make_pair(d, d), a2[i], make_pair(kDecayBias, kDecayBias)), e0, e1);
-                        a[j][i] = make_pair(ex2(e0), ex2(e1));
-                        h[j + 1][i] = fma2(a[j][i], h[j][i], mul2(make_pair(x, x), state_pair(bv, i)));
+                        a[j][i] = real(make_pair(ex2(e0), ex2(e1)), i);
+                        h[j + 1][i] = real(fma2(a[j][i], h[j][i], mul2(make_pair(x, x), state_pair(bv, i))), i);
                     }
                 }
                 float tri[kSub * 6], bc[kSub * 2 * kStates];
@@ -371,7 +377,7 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
                         for (int k = 0; k < 2; ++k) {
                             const int i = 2 * c + k;
                             const Pair b = state_pair(bv, i), cc = state_pair(cv, i), ht = h[j + 1][i];
-                            const Pair gt = fma2(cc, e, gc[i]);
+                            const Pair gt = real(fma2(cc, e, gc[i]), i);
                             db[k] = c ? fma2(gt, x, db[k]) : mul2(gt, x);
                             dc[k] = c ? fma2(ht, e, dc[k]) : mul2(ht, e);
                             y = k ? fma2(cc, ht, y) : mul2(cc, ht);
@@ -384,13 +390,14 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
                             // meet an infinite or NaN state
                             if (LAST && s * kSub + j >= n) dAc[i] = make_pair(0.f, 0.f);
                         }
-                        float lo, hi;
-                        split_pair(s1, lo, hi);
-                        tri[j * 6 + 3 * c] = lo + hi;
-                        split_pair(s2, lo, hi);
-                        tri[j * 6 + 3 * c + 1] = lo + hi;
-                        split_pair(y, lo, hi);
-                        tri[j * 6 + 3 * c + 2] = lo + hi;
+                        auto both = [&](Pair v) {
+                            float lo, hi;
+                            split_pair(v, lo, hi);
+                            return PAD != Pad::kLanes || in[0] ? lo + hi : 0.f;
+                        };
+                        tri[j * 6 + 3 * c] = both(s1);
+                        tri[j * 6 + 3 * c + 1] = both(s2);
+                        tri[j * 6 + 3 * c + 2] = both(y);
                     }
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
@@ -600,16 +607,25 @@ BwdPlan bwd_plan(int n_seq, int T_total, int D, int G, int N, bool packed) {
     return b;
 }
 
-template <typename T, typename S, int V>
-cudaError_t bwd_t(const ScanProblem &p, const Layout &l, const BwdPartials &w, const BwdPlan &b,
-                  cudaStream_t st) {
+template <typename T, typename S, int V, Pad PAD>
+cudaError_t bwd_launch(const ScanProblem &p, const Layout &l, const BwdPartials &w, const BwdPlan &b,
+                       cudaStream_t st) {
     const long blocks = b.tiles * w.slots;
     if (blocks > 0x7fffffffL) return cudaErrorInvalidConfiguration;
     constexpr int bytes = (int)sizeof(BwdSmem<T, S, V>);
-    const cudaError_t err = allow_shared<scan_bwd_kernel<T, S, V>>(bytes);
+    const cudaError_t err = allow_shared<scan_bwd_kernel<T, S, V, PAD>>(bytes);
     if (err != cudaSuccess) return err;
-    scan_bwd_kernel<T, S, V><<<(unsigned)blocks, S::NT, bytes, st>>>(p, l, w, (int)b.tiles);
+    scan_bwd_kernel<T, S, V, PAD><<<(unsigned)blocks, S::NT, bytes, st>>>(p, l, w, (int)b.tiles);
     return cudaGetLastError();
+}
+template <typename T, typename S, int V>
+cudaError_t bwd_t(const ScanProblem &p, const Layout &l, const BwdPartials &w, const BwdPlan &b,
+                  cudaStream_t st) {
+    switch (pad_of(p.N)) {
+        case Pad::kNone: return bwd_launch<T, S, V, Pad::kNone>(p, l, w, b, st);
+        case Pad::kLanes: return bwd_launch<T, S, V, Pad::kLanes>(p, l, w, b, st);
+        default: return bwd_launch<T, S, V, Pad::kStates>(p, l, w, b, st);
+    }
 }
 
 template <typename T>

@@ -12,7 +12,7 @@ from tests.test_gpu_ssm import _dev, _gen, _np, _scan_kw, _scan_ref, scan_case
 pytestmark = pytest.mark.gpu
 
 INF = float("inf")
-STATES = [8, 16, 32, 64, 128]
+STATES = [1, 2, 3, 4, 5, 8, 12, 16, 20, 24, 33, 64, 100, 128]
 
 
 def _same_kind(name, got, ref, mag, ulps):
@@ -75,6 +75,40 @@ def test_infinite_input(dtype, N):
 def test_infinite_adjoint_of_the_final_state(dtype, N):
     check_kind(positive_case(dtype, N, seed=N), dh_at=(0, 4, N - 1))
     check_kind(positive_case(dtype, N, seed=N), dh_at=(1, 9, 0))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("N", STATES)
+def test_infinite_step(dtype, N):
+    c = positive_case(dtype, N, seed=N)
+    c["dt"][0, 4, 1] = INF
+    c["dt"][0, 40, 7] = INF
+    check_kind(c)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("N", STATES)
+def test_infinite_adjoint(dtype, N):
+    check_kind(positive_case(dtype, N, seed=N), dy_at=(0, 30, 3))
+    check_kind(positive_case(dtype, N, G=2, D=14, seed=N), dy_at=(0, 6, 9))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("N", STATES)
+def test_infinite_step_of_one_token(dtype, N):
+    import momentum_delta_rule_gb300 as mdn
+    c = positive_case(dtype, N, lens=[1] * 3, D=40, seed=N)
+    c["u"][0, 0, 2] = INF
+    c["u"][0, 1, 35] = INF
+    c["dt"][0, 2, 17] = INF
+    d = _dev(c)
+    kw = {k: d[k] for k in ("D_skip", "dt_bias", "softplus")}
+    h = d["h0"].clone()
+    y = mdn.ssm_scan_step(d["u"][0], d["dt"][0], d["A"], d["Bm"][0], d["Cm"][0], h, z=d["z"][0], **kw)
+    with np.errstate(all="ignore"):
+        ref, mag = (_scan_ref(c, magnitude=m) for m in (False, True))
+    _same_kind("y", y, ref[0], mag[0], 80 + N)
+    _same_kind("h", h, ref[1], mag[1], 80)
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
