@@ -44,7 +44,12 @@ def _elsewhere(t, name, stream):
 
 
 def _on(t, stream):
-    return torch.cuda.stream(stream) if stream is not None else torch.cuda.device(t.device)
+    """Makes the call's device, and its stream where one is given, the current one."""
+    if stream is None:
+        return torch.cuda.device(t.device)
+    if stream.device != t.device:
+        raise ValueError("stream is on %s, the tensors on %s" % (stream.device, t.device))
+    return torch.cuda.stream(stream)
 
 
 def _row_stride(name, t, tail):
