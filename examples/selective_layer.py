@@ -80,10 +80,11 @@ class Layer:
         xz = h @ p["w_in"]
         u0, z = xz[..., :self.inner], xz[..., self.inner:]
         u, conv_T = mdn.short_conv_fwd(u0, p["conv_w"], bias=p["conv_b"], cu_seqlens=cu_seqlens,
-                                       state=state and state.get("conv"),
+                                       state=None if state is None else state.get("conv"),
                                        output_final_state=state is not None)
         px, dt, Bm, Cm = self._project(u)
-        out = mdn.ssm_scan_fwd(u, dt, p["A"], Bm, Cm, h0=state and state.get("ssm"), cu_seqlens=cu_seqlens,
+        out = mdn.ssm_scan_fwd(u, dt, p["A"], Bm, Cm, h0=None if state is None else state.get("ssm"),
+                               cu_seqlens=cu_seqlens,
                                output_final_state=state is not None, return_chunk_states=save is not None,
                                **self._scan_kw(z))
         y = out[0]

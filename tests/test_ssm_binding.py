@@ -1,4 +1,7 @@
-"""The state-space binding's handling of streams (no GPU needed)."""
+"""The state-space binding's handling of streams, and the example's of
+states (no GPU needed)."""
+import importlib.util
+import os
 import types
 
 import pytest
@@ -13,3 +16,33 @@ def test_a_stream_of_another_device_is_refused():
     other = types.SimpleNamespace(device=torch.device("cuda", 1))
     with pytest.raises(ValueError, match="stream"):
         ssm._on(t, other)
+
+
+def test_the_example_fills_an_empty_state(monkeypatch):
+    # a prompt from scratch: the caller's dict is empty until the prompt has run
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    spec = importlib.util.spec_from_file_location("selective_layer",
+                                                  os.path.join(root, "examples", "selective_layer.py"))
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    seen = {}
+
+    def conv(x, w, bias=None, state=None, cu_seqlens=None, output_final_state=False):
+        seen.update(conv=state)
+        return x, "conv" if output_final_state else None
+
+    def scan(u, *args, h0=None, output_final_state=True, **kw):
+        seen.update(ssm=h0)
+        return u, "ssm" if output_final_state else None
+
+    monkeypatch.setattr(ex.mdn, "short_conv_fwd", conv)
+    monkeypatch.setattr(ex.mdn, "ssm_scan_fwd", scan)
+    monkeypatch.setattr(ex.mdn, "norm_residual_fwd", lambda y, x, **kw: (x, y))
+    layer = ex.Layer(16, 32, dtype=torch.float32, device="cpu")
+    x, state = torch.zeros(1, 3, 16), {}
+    layer.prompt(x, x, state=state)
+    assert seen == dict(conv=None, ssm=None) and state == dict(conv="conv", ssm="ssm")
+    layer.prompt(x, x, state=state)                 # and goes on from there
+    assert seen == dict(conv="conv", ssm="ssm")
+    layer.prompt(x, x)
+    assert seen == dict(conv=None, ssm=None)
