@@ -79,12 +79,11 @@ class Layer:
         p = self.p
         xz = h @ p["w_in"]
         u0, z = xz[..., :self.inner], xz[..., self.inner:]
-        u, conv_T = mdn.short_conv_fwd(u0, p["conv_w"], bias=p["conv_b"], cu_seqlens=cu_seqlens,
-                                       state=None if state is None else state.get("conv"),
+        conv0, ssm0 = (None, None) if state is None else (state.get("conv"), state.get("ssm"))
+        u, conv_T = mdn.short_conv_fwd(u0, p["conv_w"], bias=p["conv_b"], state=conv0, cu_seqlens=cu_seqlens,
                                        output_final_state=state is not None)
         px, dt, Bm, Cm = self._project(u)
-        out = mdn.ssm_scan_fwd(u, dt, p["A"], Bm, Cm, h0=None if state is None else state.get("ssm"),
-                               cu_seqlens=cu_seqlens,
+        out = mdn.ssm_scan_fwd(u, dt, p["A"], Bm, Cm, h0=ssm0, cu_seqlens=cu_seqlens,
                                output_final_state=state is not None, return_chunk_states=save is not None,
                                **self._scan_kw(z))
         y = out[0]
@@ -94,7 +93,7 @@ class Layer:
             state.update(conv=conv_T, ssm=out[1])
         if save is not None:
             save.update(x=x, h=h, xz=xz, u=u, px=px, dt=dt, Bm=Bm, Cm=Cm, chunks=out[2], y=y, o=o, stats=new[2],
-                        cu=cu_seqlens)
+                        conv0=conv0, cu=cu_seqlens)
         return new[0], new[1]
 
     def token(self, x, h, state):
@@ -123,7 +122,8 @@ class Layer:
         dpx = torch.cat([k["ddt"] @ p["w_dt"].T, k["dB"].flatten(-2), k["dC"].flatten(-2)], -1)
         g["w_x"] = flat(s["u"]).T @ flat(dpx)
         du = k["du"] + dpx @ p["w_x"].T
-        c = mdn.short_conv_bwd(s["xz"][..., :self.inner], p["conv_w"], du, bias=p["conv_b"], cu_seqlens=s["cu"])
+        c = mdn.short_conv_bwd(s["xz"][..., :self.inner], p["conv_w"], du, bias=p["conv_b"], state=s["conv0"],
+                               need_dstate=False, cu_seqlens=s["cu"])
         g.update(conv_w=c["dw"], conv_b=c["dbias"])
         dxz = torch.cat([c["dx"], k["dz"]], -1)
         g["w_in"] = flat(s["h"]).T @ flat(dxz)
