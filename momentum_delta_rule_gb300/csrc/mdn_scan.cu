@@ -470,6 +470,10 @@ cudaError_t fwd_dispatch(const ScanProblem &p, const Layout &l, Pass pass, cudaS
                rows_aligned(p.z, p.ld_z, sizeof(T), bytes) &&
                rows_aligned(p.y, p.D, sizeof(T), bytes) && rows_aligned(p.dy, p.ld_dy, sizeof(T), bytes);
     });
+    // Four channels a lane above 32 states.  Forward in us with those and with
+    // two, bf16: 8192 tokens of 2048 channels, 64 states 292 and 335, 128 states
+    // 581 and 599 (fp32 661 and 739).  Where blocks are few, two are the better
+    // ones: 2048 tokens of 256 channels, 40 and 37, 93 and 63.
 #define MDN_SCAN_CASE(NL, CPT, NW, HW)                                \
     case NL:                                                          \
         if (V == MOST) return fwd_t<T, Shape<NL, CPT, NW, HW>, MOST>(p, l, pass, st); \
@@ -647,11 +651,12 @@ __global__ void states_copy_kernel(const float *from, float *to, long n) {
 }  // namespace
 
 // Warps of the recurrence that one item of `D` channels keeps busy, and the
-// warp schedulers of the device (152 SMs of four).  One warp alone takes a
-// token in about 1.3 times the issue time its work needs, so a sequence is
-// worth cutting, at the price of running its cut part twice, where it alone
-// would outlast twice the whole batch's work spread over the device; it is
-// then cut so that three warps meet on each scheduler.  Both passes in us, 2048
+// warp schedulers of the device (152 SMs of four).  A sequence is worth cutting,
+// at the price of running its cut part twice, where it is longer than 1.3 times
+// the tokens that each scheduler has of the whole batch's work; one warp alone
+// takes a token in about 1.3 times the issue time its work needs, so it alone
+// would outlast the batch spread over the device 1.7 times.  It is then cut so
+// that three warps meet on each scheduler.  Both passes in us, 2048
 // channels: one sequence of 16384 tokens 287, uncut 1063, with two warps a
 // scheduler 364, with four 287; one of 1024 tokens 31, uncut 69; four of 512,
 // which the rule leaves whole, 36, cut 45.

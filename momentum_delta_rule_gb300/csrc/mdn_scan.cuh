@@ -6,7 +6,7 @@
 namespace mdn {
 namespace scan {
 
-constexpr int kTokens = MDN_SSM_CHUNK;    // tokens per stage, and between saved states
+constexpr int kTokens = MDN_SSM_CHUNK;    // tokens between saved states, a chunk of the gradient
 constexpr int kStates = 4;                // states a lane holds of each of its channels
 
 // How a block covers channels and states.  A channel's (padded) states lie
@@ -153,32 +153,6 @@ __device__ __forceinline__ Pair real_states(Pair v, bool lo, bool hi) {
     float x, y;
     split_pair(v, x, y);
     return make_pair(lo ? x : 0.f, hi ? y : 0.f);
-}
-
-// Stages B (and C) rows of tokens t0 .. t0 + n, group g, as fp32 [token][NP]
-// by the `nt` threads tid = 0 .. nt - 1; rows n .. n_zero are zeroed.
-template <typename T, int NP, bool B_, bool C_>
-__device__ __forceinline__ void stage_bc(const ScanProblem &p, long t0, int n, int n_zero, int g,
-                                         int tid, int nt, float *Bs, float *Cs) {
-    for (int i = tid; i < n_zero * (NP / 4); i += nt) {
-        const int t = i / (NP / 4), k = i % (NP / 4) * 4;
-        const T *bp = static_cast<const T *>(p.Bm) + (t0 + t) * p.ld_B + (long)g * p.N + k;
-        const T *cp = static_cast<const T *>(p.Cm) + (t0 + t) * p.ld_C + (long)g * p.N + k;
-        float b[4], c[4];
-        if (p.bc_wide && t < n && k < p.N) {
-            if (B_) unpack<T, 4>(load_packet<T, 4>(bp), b);
-            if (C_) unpack<T, 4>(load_packet<T, 4>(cp), c);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const bool in = t < n && k + j < p.N;
-                b[j] = B_ && in ? to_f32(bp[j]) : 0.f;
-                c[j] = C_ && in ? to_f32(cp[j]) : 0.f;
-            }
-        }
-        if (B_) *reinterpret_cast<float4 *>(Bs + t * NP + k) = make_float4(b[0], b[1], b[2], b[3]);
-        if (C_) *reinterpret_cast<float4 *>(Cs + t * NP + k) = make_float4(c[0], c[1], c[2], c[3]);
-    }
 }
 
 // Sums v[0 .. M) over NL lanes, halving the values a lane carries at each
