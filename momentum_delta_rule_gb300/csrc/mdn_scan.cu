@@ -333,7 +333,7 @@ scan_fwd_kernel(ScanProblem p, Layout l, int tiles) {
                     load_states(l.pre_h + (long)(it.pre + k) * p.D * p.N, d0 + cw + c, n0, p.N, end);
                     const float s = l.pre_sum[(long)(it.pre + k) * p.D + d0 + cw + c];
 #pragma unroll
-                    for (int i = 0; i < kStates; ++i) s0[c][i] = fmaf(ex2(s * a[c][i]), s0[c][i], end[i]);
+                    for (int i = 0; i < kStates; ++i) s0[c][i] = through_segment(s * a[c][i], s0[c][i], end[i]);
                 }
             }
         }

@@ -133,6 +133,13 @@ __device__ __forceinline__ float decay_rate(float a) {
     return x;
 }
 
+// The state behind a segment, `end` where it began from zero, that began from x
+// and decayed by 2^e.  An infinite x stays: the segment's decay may be zero where
+// none of its tokens' is.
+__device__ __forceinline__ float through_segment(float e, float x, float end) {
+    return fabsf(x) == INFINITY ? x + end : fmaf(ex2(e), x, end);
+}
+
 // A lane's A, states or gradients of one channel (four of N): [D, N] row d.
 __device__ __forceinline__ void load_states(const float *base, long d, int n, int N, float *f) {
 #pragma unroll

@@ -241,10 +241,12 @@ scan_bwd_kernel(ScanProblem p, Layout l, BwdPartials w, int tiles) {
             const float s1 = live1 ? l.pre_sum[at * p.D + d0 + cw + 1] : 0.f;
 #pragma unroll
             for (int i = 0; i < kStates; ++i) {
-                float x, y;
+                float x, y, gx, gy, rx, ry;
                 const float sc = i < 2 ? s0 : s1;
                 split_pair(mul2(make_pair(sc, sc), a2[i]), x, y);
-                gc[i] = fma2(make_pair(ex2(x), ex2(y)), gc[i], r[i]);
+                split_pair(gc[i], gx, gy);
+                split_pair(r[i], rx, ry);
+                gc[i] = make_pair(through_segment(x, gx, rx), through_segment(y, gy, ry));
             }
         }
         for (int chunk = chunks - 1; chunk >= 0; --chunk) {

@@ -93,6 +93,22 @@ def test_infinite_adjoint(dtype, N):
     check_kind(positive_case(dtype, N, G=2, D=14, seed=N), dy_at=(0, 6, 9))
 
 
+@pytest.mark.parametrize("packed", [True, False])
+@pytest.mark.parametrize("N", [16, 20])
+def test_infinite_states_of_cut_sequences(N, packed):
+    # a segment's decay is zero in fp32 where none of its tokens' is
+    c = positive_case("fp32", N, lens=[700], seed=N)
+    c["packed"] = packed
+    c["A"] = c["A"].clamp(-2.0, 0.0) - 20.0
+    c["dt_bias"].zero_()
+    u = c["u"].clone()
+    c["u"][0, 100, 4] = INF
+    check_kind(c)
+    c["u"] = u
+    check_kind(c, dy_at=(0, 600, 7))
+    check_kind(c, dh_at=(0, 2, 1))
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("N", STATES)
 def test_infinite_step_of_one_token(dtype, N):
