@@ -579,6 +579,8 @@ size_t mdn_ssm_scan_bwd_workspace_size(int n_seq, int T_total, int D, int G, int
  * normal fp32 number, is taken as zero.  A is expected to be at most zero; larger values
  * are computed as written and may overflow.  A below -2.3e38, -inf too, counts
  * as that: a state that forgets everything at each step with delta > 0.
+ * Infinite and NaN inputs reach the outputs, here and in the gradient, that the
+ * formulas carry them to, and no others.
  * Errors: as mdn_short_conv_fwd; MDN_ERR_UNSUPPORTED for N above 128.
  */
 mdn_status mdn_ssm_scan_fwd(const void *u, const void *dt, const float *A,

@@ -15,14 +15,14 @@
 // memory, then each group of four tokens, last first, is run forward again
 // with its states and decays in registers and walked back.
 //
-// Measured, bf16, 16 states, 16384 tokens of 2048 channels: 647 us, and 26 us
-// for the adjoints of the cut parts and 19 us for the partial sums; the fp32
-// gradient of 8192 tokens of 2044 channels 414 us.  A token, channel and state
+// Measured, bf16, 16 states, 16384 tokens of 2048 channels: 641 to 651 us, and
+// 26 us for the adjoints of the cut parts and 19 us for the partial sums; in
+// fp32 785 us.  A token, channel and state
 // takes two exponentials and about 15 other operations with its share of the
 // exchanges, 537 M of them: the exponentials alone are 113 us, the bytes (u,
 // dt, B, C, z, dy and the saved states in, five gradients out) 80 us.  Bound
-// by the latency of dependent steps: 244 registers a thread and 100 KB of shared
-// memory hold an SM to eight warps, which fill 55 % of the issue slots and 61 %
+// by the latency of dependent steps: 230 registers a thread and 100 KB of shared
+// memory hold an SM to eight warps, which fill 55 % of the issue slots and 60 %
 // of the shared-memory pipe.  Tried: helper warps as in the
 // forward (987 us where this took 903), the same with registers moved from the
 // helpers to the rest (1215 us), channels instead of states in pairs (665 us).
