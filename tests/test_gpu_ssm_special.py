@@ -1,4 +1,4 @@
-"""Infinities in the selective scan's inputs: where the definition gives a
+"""Infinities and NaN in the operators' inputs: where the definition gives a
 finite number, an infinity or NaN, so do the kernels.  Numbers of states that
 fill no whole lanes, lengths that fill no whole batch of tokens and the places
 behind them must not turn an infinity into NaN, or a finite number into either.
@@ -7,7 +7,8 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_ssm import _dev, _gen, _np, _scan_kw, _scan_ref, scan_case
+from oracle import ssm
+from tests.test_gpu_ssm import TD, _dev, _gen, _np, _scan_kw, _scan_ref, conv_case, scan_case
 
 pytestmark = pytest.mark.gpu
 
@@ -157,3 +158,83 @@ def test_states_that_decay_at_once(dtype, N, lens):
     got = run()
     assert all(torch.isfinite(t).all() for t in want)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+NAN = float("nan")
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("N", [3, 16, 20])
+@pytest.mark.parametrize("key,at", [("u", (0, 3, 2)), ("u", (0, 40, 5)), ("dt", (0, 6, 0)), ("Bm", (0, 9, 0, 1)),
+                                    ("Cm", (0, 40, 0, 2)), ("z", (0, 20, 3)), ("h0", (1, 4, 0))])
+def test_nan_goes_no_further_than_in_the_formulas(dtype, N, key, at):
+    c = scan_case(dtype, [7, 34], D=12, N=N, strided=False, seed=N)
+    c[key][at] = NAN
+    check_kind(c)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("at", [6, 7, 40])
+def test_nan_adjoint_goes_no_further_than_in_the_formulas(dtype, at):
+    import momentum_delta_rule_gb300 as mdn
+    c = scan_case(dtype, [7, 34], D=12, N=20, strided=False, seed=at)
+    d = _dev(c)
+    args = (d["u"], d["dt"], d["A"], d["Bm"], d["Cm"])
+    dy = torch.randn(1, 41, 12, generator=_gen(at)).to(d["u"].dtype)
+    dy[0, at, 5] = NAN
+    hc = mdn.ssm_scan_fwd(*args, h0=d["h0"], return_chunk_states=True, **_scan_kw(d))[2]
+    g = mdn.ssm_scan_bwd(*args, hc, dy.cuda(), need_dh0=True, **_scan_kw(d))
+    ref, mag = (_scan_ref(c, dy=_np(dy).reshape(-1, 12), magnitude=m) for m in (False, True))
+    for k, v in g.items():
+        _same_kind(k, v, ref[3][k], mag[3][k], 2 * (64 + 16 * 34) + 41)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("D", [48, 46, 47])
+@pytest.mark.parametrize("value", [NAN, INF])
+def test_convolution_of_nan_and_infinities(dtype, D, value):
+    import momentum_delta_rule_gb300 as mdn
+    lens = [5, 1, 0, 30, 16]
+    cu = [0] + np.cumsum(lens).tolist()
+    c = conv_case(dtype, lens, D=D, W=4, strided=False, seed=D)
+    for t, ch in ((4, 3), (5, 7), (35, 9), (36, 11), (15, 2), (51, 20)):      # ends, starts, middles
+        c["x"][0, t, ch] = value
+    c["dy"][0, 35, 30] = c["dy"][0, 6, 31] = value
+    d = _dev(c)
+    kw = dict(bias=d["bias"], state=d["state"], cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda())
+    y, last = mdn.short_conv_fwd(d["x"], d["w"], output_final_state=True, **kw)
+    g = mdn.short_conv_bwd(d["x"], d["w"], d["dy"], dstate_T=d["dstate_T"], **kw)
+    with np.errstate(all="ignore"):
+        ref, mag = (ssm.conv(_np(c["x"])[0], _np(c["w"]), _np(c["bias"]), _np(c["state"]), cu, dy=_np(c["dy"])[0],
+                             dstate_T=_np(c["dstate_T"]), magnitude=m) for m in (False, True))
+    _same_kind("y", y, ref[0], mag[0], 64)
+    _same_kind("state_T", last, ref[1], np.abs(ref[1]), 0)
+    for k, v in g.items():
+        _same_kind(k, v, ref[2][k], mag[2][k], 64 + sum(lens))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("D", [64, 1001, 5000])
+@pytest.mark.parametrize("value", [NAN, INF])
+def test_norms_of_nan_and_infinities(dtype, D, value):
+    # a row has its own sums: the others', and the rows behind it, stay
+    import momentum_delta_rule_gb300 as mdn
+    R, bad = 400, 131
+    g = _gen(D)
+    y, x, gate, dX, dh = (torch.randn(R, D, generator=g).to(TD[dtype]).cuda() for _ in range(5))
+    w = torch.rand(D, generator=g).cuda() + 0.5
+    kw = dict(w_post=w, w_pre=w, scale=w, gate=gate)
+
+    def run():
+        X, h, st = mdn.norm_residual_fwd(y, x, return_stats=True, **kw)
+        b = mdn.norm_residual_bwd(y, x, st, dX, dh=dh, **kw)
+        return [X, h, st, b["dy"], b["dx"], b["dgate"]]
+
+    want = run()
+    for t in (y, x, gate, dX, dh):
+        keep = t[bad].clone()
+        t[bad, D // 2] = value
+        got = run()
+        t[bad] = keep
+        for a, b in zip(got, want):
+            assert torch.equal(a[:bad], b[:bad]) and torch.equal(a[bad + 1:], b[bad + 1:])
