@@ -23,7 +23,8 @@
  *    legacy default stream) and runs asynchronously; a call returns as soon as
  *    its kernels are enqueued.
  *  - The enqueueing calls (mdn_chunk_fwd and its variants, mdn_decode_step,
- *    mdn_prepare_inputs, and the state-space layer's operators) may be
+ *    mdn_prepare_inputs, the state-space layer's operators, linear attention and
+ *    the group norm) may be
  *    captured into a CUDA graph once one call has run on the device (the first
  *    call looks up the device's status word with cudaGetSymbolAddress); a replay reads the pointers given at capture.
  *    mdn_get_device_status synchronises and must not be captured.
@@ -676,6 +677,134 @@ mdn_status mdn_norm_residual_bwd(const void *y, const void *x, const void *gate,
                                  int64_t ld_gate, int64_t ld_dx_out, int64_t ld_dh,
                                  mdn_dtype dtype, void *workspace,
                                  size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Linear attention with a decay for each head, and the group norm with an
+ * activation that follows it.  The conventions on rows, alignment, malformed
+ * cu_seqlens and determinism are those of the state-space layer's operators
+ * above.  States [.., dk, dv] need 16 bytes where dv is a multiple of 4 (in
+ * the gradient: where dk or dv is).
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Bytes of device workspace mdn_linear_attn_fwd / _bwd need (a multiple of
+ * 256, possibly 0; 0 for invalid sizes).  T_total = B * T.
+ */
+size_t mdn_linear_attn_fwd_workspace_size(int n_seq, int T_total, int H, int Hkv, int dk,
+                                          int dv, mdn_dtype dtype);
+size_t mdn_linear_attn_bwd_workspace_size(int n_seq, int T_total, int H, int Hkv, int dk,
+                                          int dv, mdn_dtype dtype);
+
+/*
+ * mdn_linear_attn_fwd — causal linear attention over whole sequences.  Per
+ * head h, with lambda = exp(log_decay[h]) and the key and value head
+ * h / (H / Hkv):
+ *   S_t = lambda S_{t-1} + k_t v_t^T
+ *   o_t = scale S_t^T q_t
+ *
+ * Layout: q rows [B * T, H * dk] (dtype, ld_q), k rows [B * T, Hkv * dk]
+ *   (ld_k), v rows [B * T, Hkv * dv] (ld_v); log_decay [H] fp32; S0, S_T
+ *   [n_seq, H, dk, dv] fp32, NULL for zero / to skip; S_T may be S0; o
+ *   [B * T, H * dv] (dtype).  dk, dv in 1..128, Hkv divides H.  cu_seqlens,
+ *   n_seq, B, T as mdn_chunk_fwd.  workspace 256-byte aligned.
+ * log_decay is expected to be at most zero; larger values are computed as
+ * written and may overflow.  -inf is a decay of zero.
+ * States are fp32; bf16 rows meet in products of bf16 with fp32 sums, in
+ * which the states before each 64 tokens and the decayed q k^T within them are
+ * rounded to bf16 once.  Infinite and NaN rows reach what the formulas carry
+ * them to and, beyond that, the other tokens of their sequence's run of 64
+ * tokens; no other sequence and no other head.
+ * Errors: as mdn_short_conv_fwd; MDN_ERR_UNSUPPORTED for dk or dv above 128.
+ */
+mdn_status mdn_linear_attn_fwd(const void *q, const void *k, const void *v,
+                               const float *log_decay, const float *S0, void *o,
+                               float *S_T, const int32_t *cu_seqlens, int n_seq, int B,
+                               int T, int H, int Hkv, int dk, int dv, float scale,
+                               int64_t ld_q, int64_t ld_k, int64_t ld_v, mdn_dtype dtype,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * mdn_linear_attn_bwd — gradient of mdn_linear_attn_fwd from its inputs, the
+ * adjoint do rows [B * T, H * dv] (ld_do) of o and dS_T ([n_seq, H, dk, dv]
+ * fp32 or NULL for zero) of the final states:
+ *   dS_t = scale q_t do_t^T + lambda dS_{t+1}  (dS behind the last token: dS_T / lambda)
+ *   dq_t = scale S_t do_t,  dk_t = dS_t v_t,  dv_t = dS_t^T k_t,  dS0 = lambda dS_1
+ *   dq [B * T, H * dk], dk [B * T, Hkv * dk], dv [B * T, Hkv * dv] (dtype);
+ *   dS0 [n_seq, H, dk, dv] fp32 or NULL to skip.  A shared head's gradients
+ *   are summed over its query heads in fp32 and a fixed order.
+ * The decays are constants of the heads and get no gradient.
+ */
+mdn_status mdn_linear_attn_bwd(const void *q, const void *k, const void *v,
+                               const float *log_decay, const float *S0, const void *d_o,
+                               const float *dS_T, void *dq, void *dk_out, void *dv_out,
+                               float *dS0, const int32_t *cu_seqlens, int n_seq, int B,
+                               int T, int H, int Hkv, int dk, int dv, float scale,
+                               int64_t ld_q, int64_t ld_k, int64_t ld_v, int64_t ld_do,
+                               mdn_dtype dtype, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/*
+ * mdn_linear_attn_step — one token for each of n sequences: q rows
+ * [n, H * dk], k rows [n, Hkv * dk], v rows [n, Hkv * dv], o [n, H * dv]
+ * (dtype); S [n, H, dk, dv] fp32 is the state before the token and S_out
+ * receives the state after it (S_out may be S: in place).
+ */
+mdn_status mdn_linear_attn_step(const void *q, const void *k, const void *v,
+                                const float *log_decay, const float *S, float *S_out,
+                                void *o, int n, int H, int Hkv, int dk, int dv, float scale,
+                                int64_t ld_q, int64_t ld_k, int64_t ld_v, mdn_dtype dtype,
+                                void *stream);
+
+/* The activation of mdn_group_norm_fwd. */
+typedef enum mdn_norm_act {
+    MDN_ACT_NONE = 0,
+    MDN_ACT_SILU = 1,
+    MDN_ACT_SIGMOID = 2
+} mdn_norm_act;
+
+/* Bytes of device workspace mdn_group_norm_fwd / _bwd need (0 for invalid
+ * sizes and where none is needed).  rows = B * T. */
+size_t mdn_group_norm_fwd_workspace_size(int n_seq, int rows, int D, int G,
+                                         int over_sequence, mdn_dtype dtype);
+size_t mdn_group_norm_bwd_workspace_size(int n_seq, int rows, int D, int G,
+                                         int over_sequence, mdn_dtype dtype);
+
+/*
+ * mdn_group_norm_fwd — group norm with an activation, channels last.  Groups
+ * are D / G neighbouring channels, of each token by itself (over_sequence 0:
+ * the norm of each head's output), or of all tokens of a sequence:
+ *   n = (x - mean) rstd,  rstd = (mean((x - mean)^2) + eps)^(-1/2)
+ *   u = n weight + bias
+ *   y = act(u), or with a gate y = u act(gate)
+ * center 0: the mean is taken as zero (a root-mean-square norm).
+ *
+ * Layout: x, gate rows [B * T, D] (dtype; ld_x, ld_gate); weight, bias [D]
+ *   fp32 or NULL (1, 0); gate NULL: none; y [B * T, D] (dtype); stats: NULL, or
+ *   receives (mean, rstd), fp32, 8-byte aligned, [B * T, G, 2], or over
+ *   sequences [n_seq, G, 2] (zeros for an empty one).  cu_seqlens, n_seq, B, T
+ *   as mdn_chunk_fwd; cu_seqlens only over sequences.  D at most 16384, G
+ *   divides D.  workspace 256-byte aligned.
+ */
+mdn_status mdn_group_norm_fwd(const void *x, const void *gate, const float *weight,
+                              const float *bias, void *y, float *stats,
+                              const int32_t *cu_seqlens, int n_seq, int B, int T, int D,
+                              int G, int over_sequence, int center, mdn_norm_act act,
+                              float eps, int64_t ld_x, int64_t ld_gate, mdn_dtype dtype,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * mdn_group_norm_bwd — gradient of mdn_group_norm_fwd from its inputs, its
+ * stats and the adjoint dy rows [B * T, D] (ld_dy): dx, dgate [B * T, D]
+ * (dtype; dgate required with gate), dw, dbias [D] fp32 or NULL to skip.
+ */
+mdn_status mdn_group_norm_bwd(const void *x, const void *gate, const float *weight,
+                              const float *bias, const float *stats, const void *dy,
+                              void *dx, void *dgate, float *dw, float *dbias,
+                              const int32_t *cu_seqlens, int n_seq, int B, int T, int D,
+                              int G, int over_sequence, int center, mdn_norm_act act,
+                              int64_t ld_x, int64_t ld_gate, int64_t ld_dy,
+                              mdn_dtype dtype, void *workspace, size_t workspace_bytes,
+                              void *stream);
 
 /*
  * Synchronises `stream`, then reads and clears the device status word of the

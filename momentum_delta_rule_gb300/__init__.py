@@ -24,6 +24,10 @@ Entry points (same names as the C ABI):
 The state-space layer's operators (``momentum_delta_rule_gb300.ssm``, under
 the same names here): short_conv_fwd / _bwd / _step, ssm_scan_fwd / _bwd /
 _step, ssm_state_slots, norm_residual_fwd / _bwd.
+
+Linear attention with a decay for each head and the group norm behind it
+(``momentum_delta_rule_gb300.attn``): linear_attn_fwd / _bwd / _step,
+group_norm_fwd / _bwd.
 """
 import ctypes
 import os
@@ -35,7 +39,8 @@ __all__ = ["chunk_fwd", "chunk_fwd_kernel_count", "chunk_bwd", "block_fwd", "chu
            "abi_version", "status_string", "MdnError", "lib", "LIB_PATH",
            "EXPORTED_SYMBOLS",
            "short_conv_fwd", "short_conv_bwd", "short_conv_step", "ssm_scan_fwd", "ssm_scan_bwd",
-           "ssm_scan_step", "ssm_state_slots", "norm_residual_fwd", "norm_residual_bwd"]
+           "ssm_scan_step", "ssm_state_slots", "norm_residual_fwd", "norm_residual_bwd",
+           "linear_attn_fwd", "linear_attn_bwd", "linear_attn_step", "group_norm_fwd", "group_norm_bwd"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmdn.so")
@@ -63,7 +68,11 @@ EXPORTED_SYMBOLS = ["mdn_abi_version", "mdn_status_string",
                     "mdn_ssm_scan_fwd_workspace_size", "mdn_ssm_scan_bwd_workspace_size",
                     "mdn_ssm_scan_fwd", "mdn_ssm_scan_bwd", "mdn_ssm_scan_step",
                     "mdn_norm_residual_fwd", "mdn_norm_residual_bwd_workspace_size",
-                    "mdn_norm_residual_bwd"]
+                    "mdn_norm_residual_bwd",
+                    "mdn_linear_attn_fwd_workspace_size", "mdn_linear_attn_bwd_workspace_size",
+                    "mdn_linear_attn_fwd", "mdn_linear_attn_bwd", "mdn_linear_attn_step",
+                    "mdn_group_norm_fwd_workspace_size", "mdn_group_norm_bwd_workspace_size",
+                    "mdn_group_norm_fwd", "mdn_group_norm_bwd"]
 MDN_PATH_CUDA_CORE = 0
 MDN_PATH_TENSOR_CORE = 1
 
@@ -135,6 +144,7 @@ def lib():
     L.mdn_chunk_bwd.restype = c_int
     L.mdn_chunk_bwd.argtypes = [vp] * 23 + [c_int] * 8 + [vp, c_size, vp]
     ssm.declare(L)
+    attn.declare(L)
     _LIB = L
     return L
 
@@ -547,3 +557,6 @@ def device_status(stream=None, device=None):
 from . import ssm  # noqa: E402  (uses the helpers above)
 from .ssm import (norm_residual_bwd, norm_residual_fwd, short_conv_bwd, short_conv_fwd,  # noqa: E402
                   short_conv_step, ssm_scan_bwd, ssm_scan_fwd, ssm_scan_step, ssm_state_slots)
+from . import attn  # noqa: E402
+from .attn import (group_norm_bwd, group_norm_fwd, linear_attn_bwd, linear_attn_fwd,  # noqa: E402
+                   linear_attn_step)

@@ -1,0 +1,129 @@
+// Declarations shared by the translation units of linear attention with a
+// decay for each head and of the group norm.
+#pragma once
+
+#include "mdn_ssm.cuh"
+
+namespace mdn {
+
+// Everything here is one computation with different roles.  A pass takes rows
+// X, Y (kd wide) and W (vd wide) and a state Z [kd, vd], and computes along the
+// tokens, with the decay l of the head,
+//   out_i = out_scale (sum_{j <= i} l^(i-j) w_scale (X_i . Y_j) W_j + l^(i+1) Z^T X_i)
+//   Z    <- l^n Z + sum_j l^(n-1-j) w_scale Y_j W_j^T
+// or, reversed, with j >= i, l^(j-i), and the state that the last token sees:
+//   out_i = ... + l^(n-1-i) Z^T X_i,    Z <- l^n Z + sum_j l^(j+1) w_scale Y_j W_j^T.
+//   forward   X = q,  Y = k,  W = v,  Z = S
+//   dq        X = do, Y = v,  W = k,  Z = S^T
+//   dk        X = v,  Y = do, W = q,  Z = dS^T, reversed
+//   dv        X = k,  Y = q,  W = do, Z = dS,   reversed
+struct AttnPass {
+    const void *X, *Y, *W;
+    long ld_x, ld_y, ld_w;          // elements between tokens
+    int sx, sy, sw;                 // query heads that share a head of X, Y, W
+    int kd, vd;
+    bool reversed;
+    float out_scale, w_scale;
+    void *out;                      // [tokens, H, vd], dense; or nullptr (states only)
+    bool out_f32;                   // fp32 whatever the dtype
+    const float *init;              // [n_seq, H, ...] states the sequences start from, or nullptr
+    const float *seg_init;          // [slot, H, ...] states the segments start from, or nullptr
+    bool init_t;                    // those lie transposed, [vd, kd]
+    float *fin;                     // [n_seq, H, kd, vd] or nullptr
+    float *seg_out;                 // states only: [slot, H, kd, vd] of the segments alone
+};
+
+// A run of tokens of one sequence that one block takes.
+struct AttnItem {
+    int start, len, seq, slot, first, last, pad0, pad1;
+};
+
+struct AttnProblem {
+    AttnPass pass[3];
+    int n_pass;
+    const float *log_decay;
+    int H, n_seq, T, T_total;
+    int seg;                        // tokens of a segment (a multiple of 64), 0: whole sequences
+    int slots;                      // items, for packed sequences at most
+    const int32_t *cu;              // device, or nullptr for equal lengths
+    AttnItem *items;                // packed: slots items, longest first
+    int32_t *seg_off;               // packed: [n_seq + 1] slots of the sequences; [n_seq + 1] more: whether cu is well formed
+    mdn_dtype dtype;
+    int *status;
+};
+
+struct AttnStepProblem {
+    const void *q, *k, *v;
+    const float *log_decay, *S;
+    float *S_out;
+    void *o;
+    int n, H, shared, dk, dv;       // shared: query heads of a key and value head
+    float scale;
+    long ld_q, ld_k, ld_v;
+    mdn_dtype dtype;
+};
+
+struct GroupNormProblem {
+    const void *x, *gate, *dy;
+    const float *weight, *bias;
+    void *y, *dx, *dgate;
+    float *stats, *dw, *dbias;
+    const int32_t *cu;
+    int n_seq, T;                   // sequences (over_sequence) and their length when equal
+    long rows;
+    int D, G, act;
+    bool over_sequence, center;
+    float eps;
+    long ld_x, ld_gate, ld_dy;
+    mdn_dtype dtype;
+    unsigned char *ws;
+    int *status;
+};
+
+// Tokens of a segment for `lines` sequences times heads (0: none), and the most
+// slots they take.
+int attn_segment(int n_seq, long T_total, int H, int passes);
+long attn_slots(int n_seq, long T_total, int seg);
+
+cudaError_t launch_attn_layout(const AttnProblem &p, cudaStream_t st);
+cudaError_t launch_attn(const AttnProblem &p, cudaStream_t st);
+// Turns the segments' own states (seg [slot, H, kd, vd]) into the states they
+// start from.
+cudaError_t launch_attn_combine(const AttnProblem &p, float *seg, const float *init, int kd, int vd,
+                                bool reversed, cudaStream_t st);
+// out [tokens, H / shared, d] <- sums over the heads that share, of fp32 rows.
+cudaError_t launch_attn_reduce(const AttnProblem &p, const float *part, void *out, int d, int shared,
+                               cudaStream_t st);
+cudaError_t launch_attn_step(const AttnStepProblem &p, cudaStream_t st);
+
+cudaError_t launch_group_norm_fwd(const GroupNormProblem &p, cudaStream_t st);
+cudaError_t launch_group_norm_bwd(const GroupNormProblem &p, cudaStream_t st);
+size_t group_norm_fwd_workspace(int n_seq, long rows, int D, int G, bool over_sequence, mdn_dtype dtype);
+size_t group_norm_bwd_workspace(int n_seq, long rows, int D, int G, bool over_sequence, mdn_dtype dtype);
+
+// ---------------------------------------------------------------- device
+
+// The head's decay as a power of two: l^e = 2^(e * log2_decay).  A decay of
+// zero (-inf) becomes a finite number, so that l^0 is 1.
+__device__ __forceinline__ float log2_decay(const float *log_decay, int h) {
+    const float l = log_decay[h] * kLog2e;
+    return l < -1e30f ? -1e30f : l;
+}
+
+__device__ __forceinline__ bool attn_item(const AttnProblem &p, int i, AttnItem &it) {
+    if (p.cu) {
+        it = p.items[i];
+        return it.slot >= 0;
+    }
+    const int per = p.seg ? max(1, (p.T + p.seg - 1) / p.seg) : 1;
+    const int s = i / per, k = i - s * per;
+    it.seq = s;
+    it.slot = i;
+    it.start = s * p.T + k * p.seg;
+    it.len = p.seg ? min(p.seg, p.T - k * p.seg) : p.T;
+    it.first = k == 0;
+    it.last = k == per - 1;
+    return true;
+}
+
+}  // namespace mdn

@@ -1,0 +1,94 @@
+// Linear attention, one token for each of n sequences:
+//   S <- l S + k v^T,  o = scale S^T q.
+//
+// Memory bound: the fp32 states are read and written once, everything else is
+// small.  A block takes one state, a thread V neighbouring columns of every
+// RG-th row, all of which it asks for before it looks at q, k and v.
+#include "mdn_attn.cuh"
+
+namespace mdn {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <typename T, int V, int LPR>
+__global__ void __launch_bounds__(kThreads) attn_step_kernel(AttnStepProblem p) {
+    constexpr int RG = kThreads / LPR, ROWS = (128 + RG - 1) / RG;
+    __shared__ float qs[128], ks[128];
+    __shared__ __align__(16) float part[RG][LPR * V];
+    const int h = blockIdx.x % p.H, n = blockIdx.x / p.H;
+    const int lane = threadIdx.x % LPR, rg = threadIdx.x / LPR;
+    const int c = (blockIdx.y * LPR + lane) * V;
+    const bool in = c < p.dv;
+    const long at = (long)blockIdx.x * p.dk * p.dv + c;
+    Packet<float, V> s[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int r = rg + i * RG;
+        if (in && r < p.dk) s[i] = load_packet<float, V>(p.S + at + (long)r * p.dv);
+    }
+    const int hk = h / p.shared;
+    const T *q = static_cast<const T *>(p.q) + n * p.ld_q + (long)h * p.dk;
+    const T *k = static_cast<const T *>(p.k) + n * p.ld_k + (long)hk * p.dk;
+    const T *vp = static_cast<const T *>(p.v) + n * p.ld_v + (long)hk * p.dv;
+    if (threadIdx.x < p.dk) {
+        qs[threadIdx.x] = to_f32(q[threadIdx.x]);
+        ks[threadIdx.x] = to_f32(k[threadIdx.x]);
+    }
+    float v[V], o[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        v[j] = c + j < p.dv ? to_f32(vp[c + j]) : 0.f;
+        o[j] = 0.f;
+    }
+    const float f = exp2f(log2_decay(p.log_decay, h));
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int r = rg + i * RG;
+        if (in && r < p.dk) {
+            const float kr = ks[r], qr = qs[r];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                s[i].e[j] = fmaf(f, s[i].e[j], kr * v[j]);
+                o[j] = fmaf(qr, s[i].e[j], o[j]);
+            }
+            store_packet<float, V>(p.S_out + at + (long)r * p.dv, s[i]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) part[rg][lane * V + j] = o[j];
+    __syncthreads();
+    for (int j = threadIdx.x; j < LPR * V; j += kThreads) {
+        const int col = blockIdx.y * LPR * V + j;
+        if (col >= p.dv) continue;
+        float sum = 0.f;
+#pragma unroll
+        for (int g = 0; g < RG; ++g) sum += part[g][j];
+        static_cast<T *>(p.o)[(long)blockIdx.x * p.dv + col] = from_f32<T>(sum * p.scale);
+    }
+}
+
+template <typename T, int V, int LPR>
+cudaError_t launch(const AttnStepProblem &p, cudaStream_t st) {
+    const dim3 grid((unsigned)((long)p.n * p.H), (p.dv + LPR * V - 1) / (LPR * V));
+    attn_step_kernel<T, V, LPR><<<grid, kThreads, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t pick(const AttnStepProblem &p, cudaStream_t st) {
+    if (p.dv % 4) return launch<T, 1, 32>(p, st);
+    if (p.dv <= 32) return launch<T, 4, 8>(p, st);
+    if (p.dv <= 64) return launch<T, 4, 16>(p, st);
+    return launch<T, 4, 32>(p, st);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_step(const AttnStepProblem &p, cudaStream_t st) {
+    if (p.n == 0) return cudaSuccess;
+    return p.dtype == MDN_BF16 ? pick<__nv_bfloat16>(p, st) : pick<float>(p, st);
+}
+
+}  // namespace mdn
