@@ -1,6 +1,5 @@
 // Linear attention with a decay for each head, in chunks of 64 tokens, on the
-// CUDA cores in fp32: any head widths up to 128, any alignment, fp32 or bf16
-// rows.  (The passes and their roles: mdn_attn.cuh.)
+// CUDA cores: fp32 rows, any head widths up to 128, any alignment.  (The passes and their roles: mdn_attn.cuh.)
 //
 // Per chunk of n tokens with the state Z before it:
 //   A_ij  = l^(i-j) w_scale X_i . Y_j  (j <= i, else 0)
@@ -109,7 +108,6 @@ __global__ void __launch_bounds__(1024) attn_layout_kernel(AttnProblem p) {
     for (int i = base + tid; i < p.slots; i += 1024) p.items[i].slot = -1;
 }
 
-template <typename T>
 __global__ void __launch_bounds__(256) attn_kernel(AttnProblem p) {
     extern __shared__ __align__(16) float smem[];
     __shared__ float lam[kC + 1];
@@ -152,9 +150,9 @@ __global__ void __launch_bounds__(256) attn_kernel(AttnProblem p) {
     };
     put_state();
 
-    const T *X = static_cast<const T *>(a.X) + (long)(h / a.sx) * a.kd;
-    const T *Y = static_cast<const T *>(a.Y) + (long)(h / a.sy) * a.kd;
-    const T *W = static_cast<const T *>(a.W) + (long)(h / a.sw) * a.vd + c0;
+    const float *X = static_cast<const float *>(a.X) + (long)(h / a.sx) * a.kd;
+    const float *Y = static_cast<const float *>(a.Y) + (long)(h / a.sy) * a.kd;
+    const float *W = static_cast<const float *>(a.W) + (long)(h / a.sw) * a.vd + c0;
     const int chunks = (it.len + kC - 1) / kC;
     for (int c = 0; c < chunks; ++c) {
         const int at = (a.reversed ? chunks - 1 - c : c) * kC, n = min(kC, it.len - at);
@@ -163,12 +161,12 @@ __global__ void __launch_bounds__(256) attn_kernel(AttnProblem p) {
         for (int i = tid; i < kC * KR; i += 256) {
             const int r = i / KR, k = i - r * KR;
             const bool in = r < n && k < a.kd;
-            if (!states_only) Xs[r * KS + k] = in ? to_f32(X[(t0 + r) * a.ld_x + k]) : 0.f;
-            Ys[r * KS + k] = in ? to_f32(Y[(t0 + r) * a.ld_y + k]) : 0.f;
+            if (!states_only) Xs[r * KS + k] = in ? X[(t0 + r) * a.ld_x + k] : 0.f;
+            Ys[r * KS + k] = in ? Y[(t0 + r) * a.ld_y + k] : 0.f;
         }
         for (int i = tid; i < kC * kV; i += 256) {
             const int r = i / kV, k = i - r * kV;
-            Ws[r * kPitch + k] = r < n && k < cols ? to_f32(W[(t0 + r) * a.ld_w + k]) * a.w_scale : 0.f;
+            Ws[r * kPitch + k] = r < n && k < cols ? W[(t0 + r) * a.ld_w + k] * a.w_scale : 0.f;
         }
         __syncthreads();
         if (!states_only) {
@@ -253,9 +251,7 @@ __global__ void __launch_bounds__(256) attn_kernel(AttnProblem p) {
                 for (int q = 0; q < 4; ++q) {
                     const int col = tx * 4 + q;
                     if (col >= cols) continue;
-                    const float v = o[r][q] * a.out_scale;
-                    if (a.out_f32) static_cast<float *>(a.out)[row + col] = v;
-                    else static_cast<T *>(a.out)[row + col] = from_f32<T>(v);
+                    static_cast<float *>(a.out)[row + col] = o[r][q] * a.out_scale;
                 }
             }
         }
@@ -297,40 +293,61 @@ __global__ void __launch_bounds__(256) attn_kernel(AttnProblem p) {
         }
 }
 
-// One thread an element of a state, along the segments of its sequence.
-__global__ void __launch_bounds__(256) attn_combine_kernel(AttnProblem p, float *seg, const float *init, int size,
-                                                           bool reversed) {
-    const int s = blockIdx.x / p.H, h = blockIdx.x % p.H, e = blockIdx.y * 256 + threadIdx.x;
-    if (e >= size) return;
-    int off, n;
-    long len;
-    if (p.cu) {
-        off = p.seg_off[s];
-        n = p.seg_off[s + 1] - off;
-        len = p.seg_off[p.n_seq + 1] ? p.cu[s + 1] - p.cu[s] : 0;
-    } else {
-        n = max(1, (p.T + p.seg - 1) / p.seg);
-        off = s * n;
-        len = p.T;
+// Four neighbouring elements of a state a thread, along the segments of their
+// sequence, eight of which it asks for at a time.  One thread of a block works
+// out the decays: 64 x 64 blocks of which every warp reads the head's own make
+// the one sector that holds them the bottleneck (107 us instead of 8).
+template <int V>
+__global__ void __launch_bounds__(256) attn_combine_kernel(AttnProblem p, AttnCombine c) {
+    __shared__ float full, tail;
+    __shared__ int s_n, s_off;
+    const int s = blockIdx.x / p.H, h = blockIdx.x % p.H;
+    const bool reversed = blockIdx.z != 0;
+    if (threadIdx.x == 0) {
+        int off, n;
+        long len;
+        if (p.cu) {
+            off = p.seg_off[s];
+            n = p.seg_off[s + 1] - off;
+            len = p.seg_off[p.n_seq + 1] ? p.cu[s + 1] - p.cu[s] : 0;
+        } else {
+            n = max(1, (p.T + p.seg - 1) / p.seg);
+            off = s * n;
+            len = p.T;
+        }
+        const float l2 = log2_decay(p.log_decay, h);
+        full = exp2f((float)p.seg * l2);
+        tail = exp2f((float)(len - (long)(n - 1) * p.seg) * l2);
+        s_n = n;
+        s_off = off;
     }
-    const float l2 = log2_decay(p.log_decay, h);
-    const float full = exp2f((float)p.seg * l2), tail = exp2f((float)(len - (long)(n - 1) * p.seg) * l2);
-    const long step = (long)p.H * size;
-    float *at = seg + ((long)off * p.H + h) * size + e;
-    float z = init ? init[((long)s * p.H + h) * size + e] : 0.f;
-    if (!reversed) {
-        for (int k = 0; k < n; ++k, at += step) {
-            const float own = k < n - 1 ? *at : 0.f;
-            *at = z;
-            z = fmaf(full, z, own);
-        }
-    } else {
-        at += (n - 1) * step;
-        for (int k = n - 1; k >= 0; --k, at -= step) {
-            const float own = k > 0 ? *at : 0.f;
-            *at = z;
-            z = fmaf(k == n - 1 ? tail : full, z, own);
-        }
+    __syncthreads();
+    const int e = (blockIdx.y * 256 + threadIdx.x) * V, n = s_n;
+    if (e >= c.size) return;
+    const float f = full;
+    const float *init = c.init[reversed];
+    const long stride = (long)p.H * c.size, step = reversed ? -stride : stride;
+    float *at = c.seg[reversed] + ((long)s_off * p.H + h) * c.size + e + (reversed ? (n - 1) * stride : 0);
+    Packet<float, V> z;
+#pragma unroll
+    for (int v = 0; v < V; ++v) z.e[v] = 0.f;
+    if (init) z = load_packet<float, V>(init + ((long)s * p.H + h) * c.size + e);
+    for (int k0 = 0; k0 < n; k0 += 8) {
+        Packet<float, V> own[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k0 + k < n - 1) own[k] = load_packet<float, V>(at + k * step);    // the last one's leads nowhere
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k0 + k < n) {
+                store_packet<float, V>(at + k * step, z);
+                // (reversed, the sequence's short segment is the first)
+                const float g = reversed && k0 + k == 0 ? tail : f;
+                if (k0 + k < n - 1)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) z.e[v] = fmaf(g, z.e[v], own[k].e[v]);
+            }
+        at += 8 * step;
     }
 }
 
@@ -362,6 +379,7 @@ cudaError_t launch_attn_layout(const AttnProblem &p, cudaStream_t st) {
 
 cudaError_t launch_attn(const AttnProblem &p, cudaStream_t st) {
     if (p.slots == 0) return cudaSuccess;
+    if (p.dtype == MDN_BF16) return launch_attn_tc(p, st);
     int kd = 0, vd = 0;
     for (int i = 0; i < p.n_pass; ++i) {
         kd = kd > p.pass[i].kd ? kd : p.pass[i].kd;
@@ -369,24 +387,17 @@ cudaError_t launch_attn(const AttnProblem &p, cudaStream_t st) {
     }
     const dim3 grid((unsigned)(p.slots * (long)p.H), p.n_pass, (vd + kV - 1) / kV);
     const int smem = attn_smem(kd);
-    cudaError_t err;
-    if (p.dtype == MDN_BF16) {
-        err = allow_shared<attn_kernel<__nv_bfloat16>>(attn_smem(128));
-        if (err != cudaSuccess) return err;
-        attn_kernel<__nv_bfloat16><<<grid, 256, smem, st>>>(p);
-    } else {
-        err = allow_shared<attn_kernel<float>>(attn_smem(128));
-        if (err != cudaSuccess) return err;
-        attn_kernel<float><<<grid, 256, smem, st>>>(p);
-    }
+    const cudaError_t err = allow_shared<attn_kernel>(attn_smem(128));
+    if (err != cudaSuccess) return err;
+    attn_kernel<<<grid, 256, smem, st>>>(p);
     return cudaGetLastError();
 }
 
-cudaError_t launch_attn_combine(const AttnProblem &p, float *seg, const float *init, int kd, int vd, bool reversed,
-                                cudaStream_t st) {
-    const int size = kd * vd;
-    const dim3 grid((unsigned)((long)p.n_seq * p.H), (size + 255) / 256);
-    attn_combine_kernel<<<grid, 256, 0, st>>>(p, seg, init, size, reversed);
+cudaError_t launch_attn_combine(const AttnProblem &p, const AttnCombine &c, cudaStream_t st) {
+    const int V = c.size % 4 ? 1 : 4;
+    const dim3 grid((unsigned)((long)p.n_seq * p.H), (c.size / V + 255) / 256, c.seg[1] ? 2 : 1);
+    if (V == 4) attn_combine_kernel<4><<<grid, 256, 0, st>>>(p, c);
+    else attn_combine_kernel<1><<<grid, 256, 0, st>>>(p, c);
     return cudaGetLastError();
 }
 

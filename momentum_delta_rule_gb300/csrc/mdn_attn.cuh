@@ -52,6 +52,14 @@ struct AttnProblem {
     int *status;
 };
 
+// Segments' states [slot, H, size] in both directions ([1]: reversed, or
+// nullptr), and the states their sequences start from.
+struct AttnCombine {
+    float *seg[2];
+    const float *init[2];
+    int size;
+};
+
 struct AttnStepProblem {
     const void *q, *k, *v;
     const float *log_decay, *S;
@@ -86,11 +94,11 @@ int attn_segment(int n_seq, long T_total, int H, int passes);
 long attn_slots(int n_seq, long T_total, int seg);
 
 cudaError_t launch_attn_layout(const AttnProblem &p, cudaStream_t st);
+// fp32 rows on the CUDA cores, bf16 rows on the tensor cores.
 cudaError_t launch_attn(const AttnProblem &p, cudaStream_t st);
-// Turns the segments' own states (seg [slot, H, kd, vd]) into the states they
-// start from.
-cudaError_t launch_attn_combine(const AttnProblem &p, float *seg, const float *init, int kd, int vd,
-                                bool reversed, cudaStream_t st);
+cudaError_t launch_attn_tc(const AttnProblem &p, cudaStream_t st);
+// Turns the segments' own states into the states they start from.
+cudaError_t launch_attn_combine(const AttnProblem &p, const AttnCombine &c, cudaStream_t st);
 // out [tokens, H / shared, d] <- sums over the heads that share, of fp32 rows.
 cudaError_t launch_attn_reduce(const AttnProblem &p, const float *part, void *out, int d, int shared,
                                cudaStream_t st);

@@ -129,7 +129,7 @@ mdn_status mdn_linear_attn_fwd(const void *q, const void *k, const void *v, cons
         p.pass[0] = a;
         p.n_pass = 1;
         err = launch_attn(p, cs);
-        if (err == cudaSuccess) err = launch_attn_combine(p, a.seg_out, S0, dk, dv, false, cs);
+        if (err == cudaSuccess) err = launch_attn_combine(p, AttnCombine{{a.seg_out, nullptr}, {S0, nullptr}, dk * dv}, cs);
         a.seg_init = a.seg_out;
         a.seg_out = nullptr;
     }
@@ -193,8 +193,8 @@ mdn_status mdn_linear_attn_bwd(const void *q, const void *k, const void *v, cons
         p.pass[1] = rev;
         p.n_pass = 2;
         err = launch_attn(p, cs);
-        if (err == cudaSuccess) err = launch_attn_combine(p, fwd.seg_out, S0, dk, dv, false, cs);
-        if (err == cudaSuccess) err = launch_attn_combine(p, rev.seg_out, dS_T, dk, dv, true, cs);
+        if (err == cudaSuccess)
+            err = launch_attn_combine(p, AttnCombine{{fwd.seg_out, rev.seg_out}, {S0, dS_T}, dk * dv}, cs);
         seg_S = fwd.seg_out;
         seg_dS = rev.seg_out;
     }

@@ -1,0 +1,642 @@
+// Linear attention with a decay for each head on the 5th-generation tensor
+// cores: bf16 rows, head widths up to 128.  (The passes and their roles:
+// mdn_attn.cuh.)
+//
+// Per chunk of n <= 64 tokens, with the state Z before it and everything
+// transposed, so that every large product has 128 rows (columns of W) whatever
+// the chunk's length:
+//   MMA1  A    = X Y^T                    M 64 tokens, N 64, K kd
+//   MMA2  O1^T = Z^T X^T                  M vd, N 64, K kd; Z^T in bf16 from TMEM
+//   MMA3  O2^T = W^T P^T                  M vd, N 64, K 64;  P_ij = l^(i-j) w_scale A_ij in bf16
+//   MMA4  dZ^T = (D W)^T Y                M vd, N kd, K 64;  D_j = w_scale l^(n-1-j)
+//   out^T = out_scale (l^(i+1) O1^T + O2^T),   Z = l^n Z + dZ
+//
+// The decays l^(i+1) of O1 are applied to the fp32 result and the state is kept
+// in fp32 registers, so a term of out is rounded to bf16 once before it is
+// summed: with P or with Z.  D W is split into two bf16 parts, and Y is bf16 as
+// it comes.  With D = D1 + D2 in bf16 (to 2^-18),
+//   hi = D1 W rounded,  lo = D2 W + (D1 W - hi) rounded,
+// where D1 W - hi needs no more than bf16's eight bits and is exact: three
+// bf16x2 fmas for two elements, and 2^-18 more is left out.  (In fp32, with
+// conversions both ways, twelve instructions.)
+//
+// One CTA takes a run of a sequence's tokens and one head.  Warps: 0 and 1 copy
+// X, Y and W (cp.async into the 128-byte-swizzled operand layout: it takes rows
+// of any stride, and the tokens behind a sequence's end are zeros and not the
+// next sequence's); 2 issues MMA1 and MMA4, 3 owns TMEM and issues MMA2 and MMA3;
+// 4..7 split D W; 8..11 turn A into P; 12..15 write the outputs; 16..31 keep Z,
+// 32 columns each of their TMEM quadrant's 32 rows.  The only chain along the
+// tokens is MMA4 -> Z -> MMA2.  Loops are kept short rather than unrolled: with
+// eight warps of seven roles on a scheduler, straight code that each warp runs
+// once a chunk waits for its instructions (213 us with it, 161 us without, the
+// 32768 packed tokens of 16 heads).
+// Every wait is bounded (1 s); on expiry the CTA records MDN_ERR_DEVICE_TIMEOUT,
+// drains its copies and MMAs, frees TMEM and returns.
+#include "mdn_attn.cuh"
+#include "mdn_sm100.cuh"
+
+namespace mdn {
+namespace {
+
+using namespace sm100;
+
+constexpr int kC = 64;
+constexpr int kThreads = 1024;
+constexpr int kStages = 3;
+constexpr uint32_t kBlock = 8192;                 // 64 tokens x 64 columns, swizzled
+constexpr uint32_t kTile = 2 * kBlock;            // 64 tokens x 128 columns
+constexpr uint32_t kStage = 3 * kTile;            // X, Y, W
+constexpr uint32_t kOffParts = kStages * kStage;  // two buffers of D W in two parts
+constexpr uint32_t kOffP = kOffParts + 4 * kTile; // two buffers of P
+constexpr uint32_t kOffBars = kOffP + 2 * kBlock;
+constexpr uint32_t kBarsBytes = 2560;
+constexpr uint32_t kSmem = kOffBars + kBarsBytes;
+static_assert(kSmem <= 232448, "shared memory of one CTA");
+
+// TMEM columns
+constexpr uint32_t kColA = 0, kColO = 64 /* two of O1, O2: 64 each */, kColD = 320, kColZ = 448;
+constexpr uint32_t kTmemCols = 512;
+
+struct Bars {
+    uint64_t full[kStages], empty[kStages];
+    // What one side may do twice before the other looks has a barrier for each
+    // buffer: a wait sees no more than the last completion.
+    uint64_t a_ready, a_free, o1_done, d_ready, d_free, z_ready, drain[2];
+    uint64_t p_ready[2], parts_ready[2], parts_free[2], o_ready[2], o_free[2];
+    uint32_t tmem_base;
+    int abort;
+    float lam[kC + 1];                // l^e
+    float within[kC];                 // l^e w_scale out_scale: the decays of A
+    // what enters with the state decays by l^(i+1) out_scale, what leaves with it
+    // by l^(n-1-i) w_scale; reversed, the other way round.  The second kind is
+    // read from element 64 - n on and is zero behind its 64.
+    alignas(16) float enter[2 * kC];
+    uint2 leave[2 * kC];              // (two equal bf16 of its upper part, and of its lower one)
+};
+static_assert(sizeof(Bars) <= kBarsBytes, "barrier block");
+
+// mbar_wait for a whole warp that sleeps meanwhile, a millisecond at a time.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    const uint32_t at = smem_u32(bar);
+    uint64_t t0 = 0;
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(at), "r"(parity), "r"(1000000u)
+            : "memory");
+        if (__all_sync(0xffffffffu, ok)) return true;
+        if (t0 == 0) t0 = globaltimer();
+        bool over = *abort != 0;
+        if (!over && globaltimer() - t0 > kWaitLimitNs) {
+            *abort = 1;
+            over = true;
+        }
+        if (__any_sync(0xffffffffu, over)) return false;
+    }
+}
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], bf16 x bf16 -> fp32; A: two neighbouring K of
+// a row in each 32-bit column.
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Arrives on `bar` when all of this thread's cp.async so far have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// True in one lane of the warp.  Unlike a comparison of the lane's number it
+// tells the compiler so, which then issues an MMA's operands as they are and not
+// lane by lane: 43 to 106 cycles an MMA of the shapes here instead of 107.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&v);
+}
+
+// 16 (BYTES) or 4 bytes, or zeros.
+template <int BYTES>
+__device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const void *src, bool take) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(take ? 4 : 0) : "memory");
+}
+
+// A lane's part of that for rows r0, r0 + ROWS ..: 16 bytes of each.
+template <int ROWS>
+__device__ __forceinline__ void copy_rows(uint32_t tile, const __nv_bfloat16 *row, const __nv_bfloat16 *any, long step, int r0,
+                                          int to, int ch, int n) {
+    constexpr int kKinds = 8 / ROWS;
+    uint32_t at[kKinds];
+#pragma unroll
+    for (int k = 0; k < kKinds; ++k) at[k] = tile + sw128_offset(r0 + k * ROWS, ch);
+    if (n >= to) {
+#pragma unroll 1
+        for (int r = r0; r < to; r += 8) {
+#pragma unroll
+            for (int k = 0; k < kKinds; ++k, row += step) {
+                cp_async_or_zero<16>(at[k], row, true);
+                at[k] += 1024;
+            }
+        }
+        return;
+    }
+#pragma unroll 1
+    for (int r = r0; r < to; r += 8) {
+#pragma unroll
+        for (int k = 0; k < kKinds; ++k, row += step) {
+            const bool in = r + k * ROWS < n;
+            cp_async_or_zero<16>(at[k], in ? row : any, in);
+            at[k] += 1024;
+        }
+    }
+}
+
+// One warp copies rows [from, to) of `width` columns into a tile (zeros from the
+// n-th on), V elements at a time.
+template <int V>
+__device__ __forceinline__ void copy_tile(uint32_t tile, const __nv_bfloat16 *src, long ld, int width, int n, int from,
+                                          int to) {
+    const int lane = threadIdx.x & 31;
+    const int per = width / V;
+    if constexpr (V == 1) {
+        const int total = to * per;
+        for (int base = from * per; base < total; base += 32 * 8) {
+            unsigned short v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int i = base + u * 32 + lane, r = i / per;
+                v[u] = i < total && r < n ? *reinterpret_cast<const unsigned short *>(src + r * ld + (i - r * per)) : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int i = base + u * 32 + lane, r = i / per, c = i - r * per;
+                if (i < total)
+                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(tile + (c >> 6) * kBlock + sw128_offset(r, (c & 63) >> 3) +
+                                                                 (c & 7) * 2),
+                                 "h"(v[u])
+                                 : "memory");
+            }
+        }
+    } else if (V == 8 && (per == 16 || per == 8)) {
+        // 2 or 4 rows at a time: their places repeat every 8 rows
+        const int lpr = per == 16 ? 4 : 3, rows = 32 >> lpr;
+        const int ch = lane & (per - 1), r0 = from + (lane >> lpr);
+        const __nv_bfloat16 *row = src + r0 * ld + ch * 8;
+        const long step = rows * ld;
+        if (per == 16) copy_rows<2>(tile + (ch >> 3) * kBlock, row, src, step, r0, to, ch & 7, n);
+        else copy_rows<4>(tile, row, src, step, r0, to, ch, n);
+    } else {
+        const int total = to * per;
+        for (int i = from * per + lane; i < total; i += 32) {
+            const int r = i / per, c = (i - r * per) * V;
+            cp_async_or_zero<V * 2>(tile + (c >> 6) * kBlock + sw128_offset(r, (c & 63) >> 3) + (c & 7) * 2,
+                                    r < n ? src + r * ld + c : src, r < n);
+        }
+    }
+}
+
+// V: elements that X, Y and W move at a time.
+template <int V>
+__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnProblem p) {
+    extern __shared__ __align__(1024) unsigned char smem_raw[];    // (the only shared memory: at its start)
+    unsigned char *smem = smem_raw;
+    Bars *bars = reinterpret_cast<Bars *>(smem + kOffBars);
+    volatile int *abort = &bars->abort;
+    const AttnPass &a = p.pass[blockIdx.y];
+    const int h = blockIdx.x % p.H;
+    AttnItem it;
+    if (!attn_item(p, blockIdx.x / p.H, it)) return;
+    const bool states_only = a.out == nullptr;
+    const bool closes = a.reversed ? it.first : it.last;      // the sequence's last run in the pass's order
+    if (states_only && closes) return;                        // no run starts from that state
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const int kd = a.kd, vd = a.vd, ksteps = (kd + 15) / 16;
+    const int chunks = (it.len + kC - 1) / kC;
+    const bool rev = a.reversed;
+    auto chunk_at = [&](int c) { return (rev ? chunks - 1 - c : c) * kC; };
+    auto chunk_len = [&](int c) { return min(kC, it.len - chunk_at(c)); };
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&bars->full[i], 64);
+            mbar_init(&bars->empty[i], states_only ? 1 : 2);   // one commit of each issuer
+        }
+        mbar_init(&bars->a_ready, 1);
+        mbar_init(&bars->a_free, 4);
+        mbar_init(&bars->o1_done, 1);
+        mbar_init(&bars->d_ready, 1);
+        mbar_init(&bars->d_free, 16);
+        mbar_init(&bars->z_ready, 16);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->drain[i], 1);
+            mbar_init(&bars->p_ready[i], 4);
+            mbar_init(&bars->parts_ready[i], 4);
+            mbar_init(&bars->parts_free[i], 1);
+            mbar_init(&bars->o_ready[i], 1);
+            mbar_init(&bars->o_free[i], 4);
+        }
+        bars->abort = 0;
+        fence_mbar_init();
+    }
+    if (tid < 2 * kC) {
+        const float l2 = log2_decay(p.log_decay, h);
+        const float up = tid < kC ? exp2f((float)(tid + 1) * l2) : 0.f, down = tid < kC ? exp2f((float)(kC - 1 - tid) * l2) : 0.f;
+        bars->enter[tid] = (rev ? down : up) * a.out_scale;
+        const float f = (rev ? up : down) * a.w_scale;
+        const uint32_t hi = pack2(f, f);
+        const float rest = f - __uint_as_float(hi << 16);
+        bars->leave[tid] = make_uint2(hi, pack2(rest, rest));
+        if (tid < kC) {
+            bars->lam[kC - 1 - tid] = down;
+            bars->within[kC - 1 - tid] = down * (a.w_scale * a.out_scale);
+        }
+        if (tid == kC - 1) bars->lam[kC] = up;
+    }
+    // P's masked halves stay zero
+    *reinterpret_cast<uint4 *>(smem + kOffP + tid * 16) = make_uint4(0, 0, 0, 0);
+    static_assert(2 * kBlock == kThreads * 16, "one store a thread");
+    if (kd & 15)    // the products' last step reads up to the next 16 columns of X and Y
+        for (uint32_t i = tid; i < kOffParts / 16; i += kThreads)
+            *reinterpret_cast<uint4 *>(smem + i * 16) = make_uint4(0, 0, 0, 0);
+    if (warp == 3) {
+        tmem_alloc(&bars->tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    fence_proxy_async();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    const float *lam = bars->lam;      // [0 .. 64]
+
+    if (warp < 2) {
+        // ------------------------------------------------ copies: warp 0 X and
+        // half of Y, warp 1 the other half and W
+        const __nv_bfloat16 *X = static_cast<const __nv_bfloat16 *>(a.X) + (long)(h / a.sx) * kd;
+        const __nv_bfloat16 *Y = static_cast<const __nv_bfloat16 *>(a.Y) + (long)(h / a.sy) * kd;
+        const __nv_bfloat16 *W = static_cast<const __nv_bfloat16 *>(a.W) + (long)(h / a.sw) * vd;
+        for (int c = 0; c < chunks; ++c) {
+            const int st = c % kStages, n = chunk_len(c);
+            if (c >= kStages && !warp_wait(&bars->empty[st], (c / kStages - 1) & 1, abort)) break;
+            const uint32_t tile = smem_u32(smem + st * kStage);
+            const long t0 = it.start + (long)chunk_at(c);
+            copy_tile<V>(tile + kTile, Y + t0 * a.ld_y, a.ld_y, kd, n, warp * (kC / 2), (warp + 1) * (kC / 2));
+            if (warp == 1) copy_tile<V>(tile + 2 * kTile, W + t0 * a.ld_w, a.ld_w, vd, n, 0, kC);
+            else if (!states_only) copy_tile<V>(tile, X + t0 * a.ld_x, a.ld_x, kd, n, 0, kC);
+            // every lane arrives when its own copies have landed
+            if (V == 1) mbar_arrive(&bars->full[st]);
+            else copies_arrive(&bars->full[st]);
+        }
+        commit_copies();
+        wait_copies<0>();
+    } else if (warp < 4) {
+        // ------------------------------------------------ MMA issuers (the
+        // whole warp waits, one lane issues and commits).  The copies wrote
+        // through the generic proxy: hence the proxy fence on this side.
+        const uint32_t base = smem_u32(smem);
+        // Descriptors of the first stage; another stage, K step or part is an
+        // addition to the address field (units of 16 bytes).
+        auto along_k = [](int k) { return (uint32_t)((k >> 2) * (kBlock / 16) + (k & 3) * 2); };
+        const uint64_t x0 = sdesc_sw128(base, 16, 1024);
+        bool fine = true;
+        auto wait = [&](uint64_t *bar, uint32_t parity) { return fine = fine && warp_wait(bar, parity, abort); };
+        if (warp == 2) {
+            const uint32_t idesc_a = idesc_bf16(64, 64, false, false), idesc_d = idesc_bf16(128, ksteps * 16, true, true);
+            const uint64_t y0 = sdesc_sw128(base + kTile, 16, 1024), yt0 = sdesc_sw128(base + kTile, kBlock, 1024);
+            const uint64_t part0 = sdesc_sw128(base + kOffParts, kBlock, 1024);
+            for (int c = 0; c < chunks; ++c) {
+                const int st = c % kStages;
+                const uint32_t stage = (uint32_t)st * (kStage / 16);
+                if (!wait(&bars->full[st], (c / kStages) & 1)) break;
+                if (!states_only) {
+                    if (c >= 1 && !wait(&bars->a_free, (c - 1) & 1)) break;
+                    fence_proxy_async();
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t x = x0 + stage, y = y0 + stage;
+#pragma unroll 1
+                        for (int k = 0; k < ksteps; ++k)
+                            mma_bf16(tmem + kColA, x + along_k(k), y + along_k(k), idesc_a, k != 0);
+                        mma_commit(&bars->a_ready);
+                    }
+                    __syncwarp();
+                }
+                // the state's increment
+                if (!wait(&bars->parts_ready[c & 1], (c >> 1) & 1)) break;
+                if (c >= 1 && !wait(&bars->d_free, (c - 1) & 1)) break;
+                fence_proxy_async();
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t y = yt0 + stage, part = part0 + (uint32_t)((c & 1) * (2 * kTile / 16));
+#pragma unroll 1
+                    for (int k = 0; k < 8; ++k)      // (k / 4: the part)
+                        mma_bf16(tmem + kColD, part + (uint32_t)((k >> 2) * (kTile / 16) + (k & 3) * 128),
+                                 y + (uint32_t)((k & 3) * 128), idesc_d, k != 0);
+                    mma_commit(&bars->d_ready);
+                    mma_commit(&bars->parts_free[c & 1]);
+                    mma_commit(&bars->empty[st]);
+                }
+                __syncwarp();
+            }
+        } else if (!states_only) {
+            const uint32_t idesc_o1 = idesc_bf16(128, 64, false, false), idesc_o2 = idesc_bf16(128, 64, true, false);
+            const uint64_t wt0 = sdesc_sw128(base + 2 * kTile, kBlock, 1024), p0 = sdesc_sw128(base + kOffP, 16, 1024);
+            for (int c = 0; c < chunks; ++c) {
+                const int st = c % kStages;
+                const uint32_t stage = (uint32_t)st * (kStage / 16), o = tmem + kColO + (c & 1) * 128;
+                // what the state before the chunk gives
+                if (!wait(&bars->full[st], (c / kStages) & 1)) break;
+                if (c >= 2 && !wait(&bars->o_free[c & 1], ((c >> 1) - 1) & 1)) break;
+                if (!wait(&bars->z_ready, c & 1)) break;
+                fence_proxy_async();
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t x = x0 + stage;
+#pragma unroll 1
+                    for (int k = 0; k < ksteps; ++k) mma_bf16_ta(o, tmem + kColZ + k * 8, x + along_k(k), idesc_o1, k != 0);
+                    mma_commit(&bars->o1_done);
+                }
+                __syncwarp();
+                if (!wait(&bars->p_ready[c & 1], (c >> 1) & 1)) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t w = wt0 + stage, pp = p0 + (uint32_t)((c & 1) * (kBlock / 16));
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16(o + 64, w + (uint32_t)(k * 128), pp + (uint32_t)(k * 2), idesc_o2, k != 0);
+                    mma_commit(&bars->o_ready[c & 1]);
+                    mma_commit(&bars->empty[st]);
+                }
+                __syncwarp();
+            }
+        }
+        // all issued MMAs complete before TMEM is freed
+        if (elect_one()) {
+            mma_commit(&bars->drain[warp & 1]);
+            int dummy = 0;
+            mbar_wait(&bars->drain[warp & 1], 0, &dummy);
+        }
+        __syncwarp();
+    } else if (warp < 8) {
+        // ------------------------------------------------ D W in two parts
+        const int t = tid - 128, per = (vd + 7) / 8, total = kC * per;
+        for (int c = 0; c < chunks; ++c) {
+            const int st = c % kStages, n = chunk_len(c);
+            if (!warp_wait(&bars->full[st], (c / kStages) & 1, abort)) break;
+            if (c >= 2 && !warp_wait(&bars->parts_free[c & 1], ((c >> 1) - 1) & 1, abort)) break;
+            const unsigned char *w = smem + st * kStage + 2 * kTile;
+            unsigned char *out = smem + kOffParts + (c & 1) * 2 * kTile;
+            const uint2 *leave = bars->leave + (rev ? 0 : kC - n);
+#pragma unroll 2
+            for (int i = t; i < total; i += 128) {
+                const int r = per == 16 ? i >> 4 : i / per, ch = i - r * per;
+                const uint32_t at = (ch >> 3) * kBlock + sw128_offset(r, ch & 7);
+                const uint4 raw = *reinterpret_cast<const uint4 *>(w + at);
+                const uint2 d = *reinterpret_cast<const uint2 *>(leave + r);
+                const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    hi[q] = fma_bf16x2(in[q], d.x, 0x80008000u);
+                    lo[q] = fma_bf16x2(in[q], d.y, fma_bf16x2(in[q], d.x, hi[q] ^ 0x80008000u));
+                }
+                *reinterpret_cast<uint4 *>(out + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(out + kTile + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+            fence_proxy_async();
+            warp_arrive(&bars->parts_ready[c & 1]);
+        }
+    } else if (warp < 12) {
+        // ------------------------------------------------ A -> P.  Row i of the
+        // M = 64 product sits in lane 32 (i / 16) + i % 16; threads t and t + 16
+        // of a warp take eight columns each of every 16.  A warp's rows see the
+        // 16 columns of their own number with the mask, those on one side of it
+        // whole and those on the other not at all.
+        const int quad = warp & 3, i = quad * 16 + (lane & 15), j8 = (lane >> 4) * 8;
+        if (!states_only) {
+            const uint32_t from = tmem + kColA + ((uint32_t)(quad * 32) << 16);
+            float power[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) power[q] = lam[rev ? q : 7 - q];
+            for (int c = 0; c < chunks; ++c) {
+                if (!warp_wait(&bars->a_ready, c & 1, abort)) break;
+                // (P's buffer: the products with the last P in it are done)
+                if (c >= 2 && !warp_wait(&bars->o_ready[c & 1], ((c >> 1) - 1) & 1, abort)) break;
+                tc_fence_after();
+                unsigned char *out = smem + kOffP + (c & 1) * kBlock;
+                float s[8] = {};
+                auto put = [&](int m) {
+                    *reinterpret_cast<uint4 *>(out + sw128_offset(i, m * 2 + (lane >> 4))) =
+                        make_uint4(pack2(s[0], s[1]), pack2(s[2], s[3]), pack2(s[4], s[5]), pack2(s[6], s[7]));
+                };
+#pragma unroll 1
+                for (int m = rev ? quad + 1 : 0; m < (rev ? 4 : quad); ++m) {
+                    tmem_ld_16x2x8(from + m * 16, s);
+                    const int j0 = m * 16 + j8;
+                    const float f = bars->within[rev ? j0 - i : i - j0 - 7];
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int q = 0; q < 8; q += 2)
+                        split_pair(mul2(make_pair(s[q], s[q + 1]), mul2(make_pair(power[q], power[q + 1]), make_pair(f, f))), s[q],
+                                   s[q + 1]);
+                    put(m);
+                }
+                tmem_ld_16x2x8(from + quad * 16, s);
+                tmem_ld_wait();
+                tc_fence_before();
+                warp_arrive(&bars->a_free);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int j = quad * 16 + j8 + q, e = rev ? j - i : i - j;
+                    s[q] = e < 0 ? 0.f : s[q] * bars->within[max(e, 0)];
+                }
+                put(quad);
+                fence_proxy_async();
+                warp_arrive(&bars->p_ready[c & 1]);
+            }
+        }
+    } else if (warp < 16) {
+        // ------------------------------------------------ outputs
+        const int quad = warp & 3, col = quad * 32 + lane;
+        const uint32_t at = tmem + kColO + ((uint32_t)(quad * 32) << 16);
+        const long step = (long)p.H * vd;
+        const bool pairs = !(vd & 1) && !((uintptr_t)a.out & 3);
+        if (!states_only)
+            for (int c = 0; c < chunks; ++c) {
+                const int n = chunk_len(c);
+                if (!warp_wait(&bars->o_ready[c & 1], (c >> 1) & 1, abort)) break;
+                tc_fence_after();
+                const long row = ((it.start + (long)chunk_at(c)) * p.H + h) * vd + col;
+                const float *enter = bars->enter + (rev ? kC - n : 0);
+#pragma unroll 1
+                for (int m = 0; m < 4; ++m) {
+                    float o1[16], o2[16];
+                    tmem_ld16(at + (c & 1) * 128 + m * 16, o1);
+                    tmem_ld16(at + (c & 1) * 128 + 64 + m * 16, o2);
+                    tmem_ld_wait();
+                    if (m == 3) {
+                        tc_fence_before();
+                        warp_arrive(&bars->o_free[c & 1]);
+                    }
+                    const long first = row + m * 16 * step;
+                    const float *f = enter + m * 16;
+                    if (a.out_f32) {
+                        float *out = static_cast<float *>(a.out) + first;
+#pragma unroll
+                        for (int q = 0; q < 16; ++q, out += step)
+                            if (col < vd && m * 16 + q < n) *out = fmaf(f[q], o1[q], o2[q]);
+                        continue;
+                    }
+                    if (pairs && n == kC) {
+                        // neighbouring lanes trade halves: the even one writes
+                        // two columns of token q, the odd one of token q + 1
+                        uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<unsigned short *>(a.out) + first +
+                                                                     (lane & 1 ? step - 1 : 0));
+#pragma unroll
+                        for (int q = 0; q < 16; q += 2, out += step) {
+                            const float2 f2 = *reinterpret_cast<const float2 *>(bars->enter + m * 16 + q);
+                            float v0, v1;
+                            split_pair(fma2(make_pair(f2.x, f2.y), make_pair(o1[q], o1[q + 1]), make_pair(o2[q], o2[q + 1])), v0,
+                                       v1);
+                            const uint32_t mine = pack2(v0, v1), other = __shfl_xor_sync(0xffffffffu, mine, 1);
+                            if (col < vd) *out = __byte_perm(mine, other, lane & 1 ? 0x3276 : 0x5410);
+                        }
+                        continue;
+                    }
+                    if (col >= vd) continue;
+                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + first;
+#pragma unroll 1
+                    for (int q = 0; q < 16; ++q, out += step) {
+                        float v = 0.f;
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            if (k == q) v = fmaf(f[k], o1[k], o2[k]);
+                        if (m * 16 + q < n) *out = __float2bfloat16_rn(v);
+                    }
+                }
+            }
+    } else {
+        // ------------------------------------------------ the state: row `col`
+        // of Z^T, columns k0 .. k0 + 31
+        const int quad = warp & 3, col = quad * 32 + lane, k0 = ((warp - 16) >> 2) * 32;
+        const bool mine = k0 < kd;
+        const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16);
+        float z[32];
+        {
+            const bool opens = rev ? it.last : it.first;
+            const float *src = nullptr;
+            if (!states_only) {
+                if (a.seg_init) src = a.seg_init + ((long)it.slot * p.H + h) * kd * vd;
+                else if (a.init && opens) src = a.init + ((long)it.seq * p.H + h) * kd * vd;
+            }
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+                z[k] = src && k0 + k < kd && col < vd ? src[a.init_t ? col * kd + k0 + k : (k0 + k) * vd + col] : 0.f;
+        }
+        auto put = [&]() {
+            if (mine) {
+                float v[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(pack2(z[2 * k], z[2 * k + 1]));
+                tmem_st16(at + kColZ + k0 / 2, v);
+                tmem_st_wait();
+            }
+            tc_fence_before();
+            warp_arrive(&bars->z_ready);
+        };
+        if (!states_only && chunks) put();
+        bool fine = true;
+        for (int c = 0; c < chunks; ++c) {
+            if (!(fine = warp_wait(&bars->d_ready, c & 1, abort))) break;
+            tc_fence_after();
+            const float f = lam[chunk_len(c)];
+            if (mine)
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    float d[16];
+                    tmem_ld16(at + kColD + k0 + m * 16, d);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int q = 0; q < 16; q += 2) {
+                        float &z0 = z[m * 16 + q], &z1 = z[m * 16 + q + 1];
+                        split_pair(fma2(make_pair(f, f), make_pair(z0, z1), make_pair(d[q], d[q + 1])), z0, z1);
+                    }
+                }
+            tc_fence_before();
+            warp_arrive(&bars->d_free);
+            if (states_only || c + 1 == chunks) continue;
+            if (!(fine = warp_wait(&bars->o1_done, c & 1, abort))) break;
+            tc_fence_after();
+            put();
+        }
+        float *dst = nullptr;
+        if (states_only) dst = a.seg_out + ((long)it.slot * p.H + h) * kd * vd;
+        else if (a.fin && closes) dst = a.fin + ((long)it.seq * p.H + h) * kd * vd;
+        if (dst && fine && col < vd)
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+                if (k0 + k < kd) dst[(k0 + k) * vd + col] = z[k];
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid == 0 && bars->abort) atomicExch(p.status, MDN_ERR_DEVICE_TIMEOUT);
+    if (warp == 3) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int V>
+cudaError_t launch(const AttnProblem &p, cudaStream_t st) {
+    const cudaError_t err = allow_shared<attn_tc_kernel<V>>(kSmem);
+    if (err != cudaSuccess) return err;
+    attn_tc_kernel<V><<<dim3((unsigned)(p.slots * (long)p.H), p.n_pass), kThreads, kSmem, st>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tc(const AttnProblem &p, cudaStream_t st) {
+    const int V = packet_width(8, 2, [&](int V, int bytes) {
+        for (int i = 0; i < p.n_pass; ++i) {
+            const AttnPass &a = p.pass[i];
+            if (a.kd % V || a.vd % V || !rows_aligned(a.X, a.ld_x, 2, bytes) || !rows_aligned(a.Y, a.ld_y, 2, bytes) ||
+                !rows_aligned(a.W, a.ld_w, 2, bytes))
+                return false;
+        }
+        return true;
+    });
+    return V == 8 ? launch<8>(p, st) : V == 2 ? launch<2>(p, st) : launch<1>(p, st);
+}
+
+}  // namespace mdn
