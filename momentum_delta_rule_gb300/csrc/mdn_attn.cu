@@ -13,16 +13,26 @@
 namespace mdn {
 
 // A segment's states cost a second reading of Y and W and their own products,
-// so sequences are cut only where whole ones leave multiprocessors idle.
+// so sequences are cut only where whole ones leave multiprocessors idle.  In
+// units of the time a block takes for a chunk: the blocks of a launch run in
+// waves of 152, each of which fills its pipeline once (2.5); a chunk's states
+// alone take 0.45, and the two launches more that segments need 5.
 int attn_segment(int n_seq, long T_total, int H, int passes) {
-    const long lines = (long)n_seq * H * passes;
-    if (n_seq == 0 || lines >= 96) return 0;
-    const long mean = T_total / n_seq;
-    if (mean < 1024) return 0;
-    const long parts = (152 + lines - 1) / lines;
-    long seg = (mean + parts - 1) / parts;
-    seg = (seg + 63) / 64 * 64;
-    return (int)(seg < 256 ? 256 : seg);
+    if (n_seq == 0 || T_total == 0) return 0;
+    const long lines = (long)n_seq * H, mean = (T_total + n_seq - 1) / n_seq, chunks = (mean + 63) / 64;
+    auto waves = [](long blocks) { return (blocks + 151) / 152; };
+    const int states = passes > 1 ? 2 : 1;
+    double best = waves(lines * passes) * (chunks + 2.5);
+    long best_chunks = 0;
+    for (long parts = 2; parts <= 64 && parts * 4 <= chunks; ++parts) {
+        const long per = (chunks + parts - 1) / parts, n = (chunks + per - 1) / per;
+        const double t = waves(lines * states * (n - 1)) * (per * 0.45 + 2.5) + 5 + waves(lines * passes * n) * (per + 2.5);
+        if (t < best) {
+            best = t;
+            best_chunks = per;
+        }
+    }
+    return (int)(best_chunks * 64);
 }
 
 long attn_slots(int n_seq, long T_total, int seg) {
@@ -114,7 +124,7 @@ __global__ void __launch_bounds__(256) attn_kernel(AttnProblem p) {
     const AttnPass &a = p.pass[blockIdx.y];
     const int h = blockIdx.x % p.H, c0 = blockIdx.z * kV;
     AttnItem it;
-    if (!attn_item(p, blockIdx.x / p.H, it) || c0 >= a.vd) return;
+    if (!attn_item(p, blockIdx.x / p.H, it, reinterpret_cast<int *>(smem)) || c0 >= a.vd) return;
     const bool states_only = a.out == nullptr;
     const bool closes = a.reversed ? it.first : it.last;      // the sequence's last run in the pass's order
     if (states_only && closes) return;                        // no run starts from that state

@@ -46,7 +46,7 @@ struct AttnProblem {
     int seg;                        // tokens of a segment (a multiple of 64), 0: whole sequences
     int slots;                      // items, for packed sequences at most
     const int32_t *cu;              // device, or nullptr for equal lengths
-    AttnItem *items;                // packed: slots items, longest first
+    AttnItem *items;                // packed: slots items, longest first, or nullptr (attn_item)
     int32_t *seg_off;               // packed: [n_seq + 1] slots of the sequences; [n_seq + 1] more: whether cu is well formed
     mdn_dtype dtype;
     int *status;
@@ -118,10 +118,48 @@ __device__ __forceinline__ float log2_decay(const float *log_decay, int h) {
     return l < -1e30f ? -1e30f : l;
 }
 
-__device__ __forceinline__ bool attn_item(const AttnProblem &p, int i, AttnItem &it) {
-    if (p.cu) {
+// The item of block i (whole CTA; uniform result).  Few packed sequences that
+// are not cut order themselves, longest first: a kernel that does it costs 5 us
+// and its launch.  scratch: kAttnOrdered + 8 ints of shared memory.
+constexpr int kAttnOrdered = 256;
+__device__ __forceinline__ bool attn_item(const AttnProblem &p, int i, AttnItem &it, int *scratch) {
+    if (p.cu && p.items) {
         it = p.items[i];
         return it.slot >= 0;
+    }
+    if (p.cu) {
+        const int tid = threadIdx.x;
+        const bool ok = cu_well_formed(p.cu, p.n_seq, p.T_total);
+        if (tid == 0 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
+            if (!ok) atomicExch(p.status, MDN_ERR_INVALID_ARG);
+            p.seg_off[p.n_seq + 1] = ok;
+        }
+        int *lens = scratch + 8;
+        int start = 0, len = 0;
+        if (tid < p.n_seq) {
+            if (ok) {
+                start = p.cu[tid];
+                len = p.cu[tid + 1] - start;
+            }
+            lens[tid] = len;
+        }
+        __syncthreads();
+        if (tid < p.n_seq) {
+            int place = 0;
+            for (int j = 0; j < p.n_seq; ++j) place += lens[j] > len || (lens[j] == len && j < tid);
+            if (place == i) {
+                scratch[0] = start;
+                scratch[1] = len;
+                scratch[2] = tid;
+            }
+        }
+        __syncthreads();
+        it.start = scratch[0];
+        it.len = scratch[1];
+        it.seq = it.slot = scratch[2];
+        it.first = it.last = 1;
+        __syncthreads();
+        return true;
     }
     const int per = p.seg ? max(1, (p.T + p.seg - 1) / p.seg) : 1;
     const int s = i / per, k = i - s * per;

@@ -63,7 +63,8 @@ AttnProblem problem(const Heads &s, const Space &w, const float *log_decay, cons
     p.status = status;
     if (p.cu) {
         p.slots = (int)w.slots;
-        p.items = reinterpret_cast<AttnItem *>(ws + w.items);
+        // (few whole sequences order themselves)
+        if (w.seg || s.n_seq > kAttnOrdered) p.items = reinterpret_cast<AttnItem *>(ws + w.items);
         p.seg_off = reinterpret_cast<int32_t *>(ws + w.offs);
     } else {
         p.slots = s.n_seq * (w.seg ? (T + w.seg - 1) / w.seg : 1);
@@ -123,7 +124,7 @@ mdn_status mdn_linear_attn_fwd(const void *q, const void *k, const void *v, cons
     a.kd = dk; a.vd = dv;
     a.out_scale = scale; a.w_scale = 1.f;
     cudaError_t err = cudaSuccess;
-    if (p.cu) err = launch_attn_layout(p, cs);
+    if (p.items) err = launch_attn_layout(p, cs);
     if (w.seg && err == cudaSuccess) {
         a.seg_out = reinterpret_cast<float *>(ws + w.states);
         p.pass[0] = a;
@@ -184,7 +185,7 @@ mdn_status mdn_linear_attn_bwd(const void *q, const void *k, const void *v, cons
     rev.reversed = true;
     rev.w_scale = scale;
     cudaError_t err = cudaSuccess;
-    if (p.cu) err = launch_attn_layout(p, cs);
+    if (p.items) err = launch_attn_layout(p, cs);
     const float *seg_S = nullptr, *seg_dS = nullptr;
     if (w.seg && err == cudaSuccess) {
         fwd.seg_out = reinterpret_cast<float *>(ws + w.states);

@@ -21,15 +21,24 @@
 // conversions both ways, twelve instructions.)
 //
 // One CTA takes a run of a sequence's tokens and one head.  Warps: 0 and 1 copy
-// X, Y and W (cp.async into the 128-byte-swizzled operand layout: it takes rows
-// of any stride, and the tokens behind a sequence's end are zeros and not the
-// next sequence's); 2 issues MMA1 and MMA4, 3 owns TMEM and issues MMA2 and MMA3;
-// 4..7 split D W; 8..11 turn A into P; 12..15 write the outputs; 16..31 keep Z,
-// 32 columns each of their TMEM quadrant's 32 rows.  The only chain along the
-// tokens is MMA4 -> Z -> MMA2.  Loops are kept short rather than unrolled: with
-// eight warps of seven roles on a scheduler, straight code that each warp runs
-// once a chunk waits for its instructions (213 us with it, 161 us without, the
-// 32768 packed tokens of 16 heads).
+// X, Y and W into the 128-byte-swizzled operand layout; 2 issues MMA1 and MMA4,
+// 3 owns TMEM and issues MMA2 and MMA3; 4..7 split D W; 8..11 turn A into P;
+// 12..15 write the outputs; 16..31 keep Z, 32 columns each of their TMEM
+// quadrant's 32 rows.  The only chain along the tokens is MMA4 -> Z -> MMA2.
+//
+// Rows on 16-byte boundaries come by TMA, others with cp.async or plain loads.
+// In a sequence's last, partial chunk the tokens behind its end are zeros and
+// not the next sequence's.  (Outputs staged in the chunk's X tile by stmatrix
+// and stored by TMA took fewer instructions, but kept the tile from the next
+// load: 145 us for the prompts below.)
+//
+// What it is made for is few instructions: 32 warps of seven roles share four
+// schedulers and an instruction cache, so that every instruction saved shortens
+// all the handovers, and loops are kept short rather than unrolled (straight
+// code that each warp runs once a chunk waits for its instructions).  Packed
+// prompts of 32768 tokens, 16 heads of 128: 488 us at first, 213 with lane 0's
+// branch replaced by elect.sync and O's registers freed early, 161 with short
+// loops, 127 with two issuers, bf16x2 splitting and waits that only count.
 // Every wait is bounded (1 s); on expiry the CTA records MDN_ERR_DEVICE_TIMEOUT,
 // drains its copies and MMAs, frees TMEM and returns.
 #include "mdn_attn.cuh"
@@ -61,29 +70,40 @@ struct Bars {
     uint64_t full[kStages], empty[kStages];
     // What one side may do twice before the other looks has a barrier for each
     // buffer: a wait sees no more than the last completion.
-    uint64_t a_ready, a_free, o1_done, d_ready, d_free, z_ready, drain[2];
+    uint64_t a_ready, a_free, o1_done, d_ready, d_free, z_ready, partial, drain[2];
     uint64_t p_ready[2], parts_ready[2], parts_free[2], o_ready[2], o_free[2];
     uint32_t tmem_base;
     int abort;
     float lam[kC + 1];                // l^e
     float within[kC];                 // l^e w_scale out_scale: the decays of A
     // what enters with the state decays by l^(i+1) out_scale, what leaves with it
-    // by l^(n-1-i) w_scale; reversed, the other way round.  The second kind is
-    // read from element 64 - n on and is zero behind its 64.
-    alignas(16) float enter[2 * kC];
-    uint2 leave[2 * kC];              // (two equal bf16 of its upper part, and of its lower one)
+    // by l^(n-1-i) w_scale; reversed, the other way round.  [0]: whole chunks,
+    // [1]: the run's partial one.
+    alignas(16) float enter[2][kC];
+    uint2 leave[2][kC];               // (two equal bf16 of its upper part, and of its lower one)
 };
 static_assert(sizeof(Bars) <= kBarsBytes, "barrier block");
 
-// mbar_wait for a whole warp that sleeps meanwhile, a millisecond at a time.
+// mbar_wait for a whole warp.  Most of a CTA's warps wait at any time, and a try
+// ends unsuccessful after some 270 cycles whatever its time limit, so what is
+// done between tries counts: nothing but counting to 1024 here.  (With the look
+// at the flag and the clock each time, the kernel issued 8600 instructions a
+// chunk.)
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
     const uint32_t at = smem_u32(bar);
     uint64_t t0 = 0;
     for (;;) {
         uint32_t ok;
         asm volatile(
-            "{\n\t.reg .pred p;\n\t"
+            "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\t"
+            "mov.u32 n, 1024;\n"
+            "again:\n\t"
             "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "@p bra done;\n\t"
+            "sub.u32 n, n, 1;\n\t"
+            "setp.ne.u32 p, n, 0;\n\t"
+            "@p bra again;\n"
+            "done:\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(ok)
             : "r"(at), "r"(parity), "r"(1000000u)
@@ -139,6 +159,11 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
     return d;
 }
 
+__device__ __forceinline__ uint32_t neg_bf16x2(uint32_t a) {
+    uint32_t d;
+    asm("neg.bf16x2 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<uint32_t *>(&v);
@@ -153,37 +178,7 @@ __device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const void *src, 
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(take ? 4 : 0) : "memory");
 }
 
-// A lane's part of that for rows r0, r0 + ROWS ..: 16 bytes of each.
-template <int ROWS>
-__device__ __forceinline__ void copy_rows(uint32_t tile, const __nv_bfloat16 *row, const __nv_bfloat16 *any, long step, int r0,
-                                          int to, int ch, int n) {
-    constexpr int kKinds = 8 / ROWS;
-    uint32_t at[kKinds];
-#pragma unroll
-    for (int k = 0; k < kKinds; ++k) at[k] = tile + sw128_offset(r0 + k * ROWS, ch);
-    if (n >= to) {
-#pragma unroll 1
-        for (int r = r0; r < to; r += 8) {
-#pragma unroll
-            for (int k = 0; k < kKinds; ++k, row += step) {
-                cp_async_or_zero<16>(at[k], row, true);
-                at[k] += 1024;
-            }
-        }
-        return;
-    }
-#pragma unroll 1
-    for (int r = r0; r < to; r += 8) {
-#pragma unroll
-        for (int k = 0; k < kKinds; ++k, row += step) {
-            const bool in = r + k * ROWS < n;
-            cp_async_or_zero<16>(at[k], in ? row : any, in);
-            at[k] += 1024;
-        }
-    }
-}
-
-// One warp copies rows [from, to) of `width` columns into a tile (zeros from the
+// Without TMA: one warp copies rows [from, to) of `width` columns into a tile (zeros from the
 // n-th on), V elements at a time.
 template <int V>
 __device__ __forceinline__ void copy_tile(uint32_t tile, const __nv_bfloat16 *src, long ld, int width, int n, int from,
@@ -209,14 +204,6 @@ __device__ __forceinline__ void copy_tile(uint32_t tile, const __nv_bfloat16 *sr
                                  : "memory");
             }
         }
-    } else if (V == 8 && (per == 16 || per == 8)) {
-        // 2 or 4 rows at a time: their places repeat every 8 rows
-        const int lpr = per == 16 ? 4 : 3, rows = 32 >> lpr;
-        const int ch = lane & (per - 1), r0 = from + (lane >> lpr);
-        const __nv_bfloat16 *row = src + r0 * ld + ch * 8;
-        const long step = rows * ld;
-        if (per == 16) copy_rows<2>(tile + (ch >> 3) * kBlock, row, src, step, r0, to, ch & 7, n);
-        else copy_rows<4>(tile, row, src, step, r0, to, ch, n);
     } else {
         const int total = to * per;
         for (int i = from * per + lane; i < total; i += 32) {
@@ -227,9 +214,18 @@ __device__ __forceinline__ void copy_tile(uint32_t tile, const __nv_bfloat16 *sr
     }
 }
 
-// V: elements that X, Y and W move at a time.
+// V: elements that X, Y and W move at a time; 8: by TMA.
+struct Maps {
+    CUtensorMap x, y, w;
+};
+struct AllMaps {
+    Maps pass[3];
+};
+
 template <int V>
-__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnProblem p) {
+__global__ void __launch_bounds__(kThreads, 1)
+attn_tc_kernel(const __grid_constant__ AttnProblem p, const __grid_constant__ AllMaps maps) {
+    constexpr bool kTma = V == 8;
     extern __shared__ __align__(1024) unsigned char smem_raw[];    // (the only shared memory: at its start)
     unsigned char *smem = smem_raw;
     Bars *bars = reinterpret_cast<Bars *>(smem + kOffBars);
@@ -237,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     const AttnPass &a = p.pass[blockIdx.y];
     const int h = blockIdx.x % p.H;
     AttnItem it;
-    if (!attn_item(p, blockIdx.x / p.H, it)) return;
+    if (!attn_item(p, blockIdx.x / p.H, it, reinterpret_cast<int *>(smem))) return;
     const bool states_only = a.out == nullptr;
     const bool closes = a.reversed ? it.first : it.last;      // the sequence's last run in the pass's order
     if (states_only && closes) return;                        // no run starts from that state
@@ -250,8 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&bars->full[i], 64);
-            mbar_init(&bars->empty[i], states_only ? 1 : 2);   // one commit of each issuer
+            mbar_init(&bars->full[i], kTma ? 1 : 64);
+            mbar_init(&bars->empty[i], states_only ? 1 : 2);   // issuer of MMA4, outputs
         }
         mbar_init(&bars->a_ready, 1);
         mbar_init(&bars->a_free, 4);
@@ -259,6 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         mbar_init(&bars->d_ready, 1);
         mbar_init(&bars->d_free, 16);
         mbar_init(&bars->z_ready, 16);
+        mbar_init(&bars->partial, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->drain[i], 1);
             mbar_init(&bars->p_ready[i], 4);
@@ -272,22 +269,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     }
     if (tid < 2 * kC) {
         const float l2 = log2_decay(p.log_decay, h);
-        const float up = tid < kC ? exp2f((float)(tid + 1) * l2) : 0.f, down = tid < kC ? exp2f((float)(kC - 1 - tid) * l2) : 0.f;
-        bars->enter[tid] = (rev ? down : up) * a.out_scale;
+        const int i = tid & (kC - 1), n = tid < kC ? kC : it.len & (kC - 1);
+        const float up = exp2f((float)(i + 1) * l2), down = i < n ? exp2f((float)(n - 1 - i) * l2) : 0.f;
+        bars->enter[tid >> 6][i] = (rev ? down : up) * a.out_scale;
         const float f = (rev ? up : down) * a.w_scale;
         const uint32_t hi = pack2(f, f);
         const float rest = f - __uint_as_float(hi << 16);
-        bars->leave[tid] = make_uint2(hi, pack2(rest, rest));
+        bars->leave[tid >> 6][i] = make_uint2(hi, pack2(rest, rest));
         if (tid < kC) {
-            bars->lam[kC - 1 - tid] = down;
-            bars->within[kC - 1 - tid] = down * (a.w_scale * a.out_scale);
+            bars->lam[kC - 1 - i] = down;
+            bars->within[kC - 1 - i] = down * (a.w_scale * a.out_scale);
+            if (i == kC - 1) bars->lam[kC] = up;
         }
-        if (tid == kC - 1) bars->lam[kC] = up;
     }
     // P's masked halves stay zero
     *reinterpret_cast<uint4 *>(smem + kOffP + tid * 16) = make_uint4(0, 0, 0, 0);
     static_assert(2 * kBlock == kThreads * 16, "one store a thread");
-    if (kd & 15)    // the products' last step reads up to the next 16 columns of X and Y
+    if (!kTma && (kd & 15))    // the products' last step reads up to the next 16 columns of X and Y
         for (uint32_t i = tid; i < kOffParts / 16; i += kThreads)
             *reinterpret_cast<uint4 *>(smem + i * 16) = make_uint4(0, 0, 0, 0);
     if (warp == 3) {
@@ -302,25 +300,64 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     const float *lam = bars->lam;      // [0 .. 64]
 
     if (warp < 2) {
-        // ------------------------------------------------ copies: warp 0 X and
-        // half of Y, warp 1 the other half and W
+        // ------------------------------------------------ copies (without TMA:
+        // warp 0 X and half of Y, warp 1 the other half and W)
         const __nv_bfloat16 *X = static_cast<const __nv_bfloat16 *>(a.X) + (long)(h / a.sx) * kd;
         const __nv_bfloat16 *Y = static_cast<const __nv_bfloat16 *>(a.Y) + (long)(h / a.sy) * kd;
         const __nv_bfloat16 *W = static_cast<const __nv_bfloat16 *>(a.W) + (long)(h / a.sw) * vd;
-        for (int c = 0; c < chunks; ++c) {
+        const Maps &m = maps.pass[blockIdx.y];
+        int issued = 0;
+        for (int c = 0; c < chunks && !(kTma && warp); ++c, ++issued) {
             const int st = c % kStages, n = chunk_len(c);
             if (c >= kStages && !warp_wait(&bars->empty[st], (c / kStages - 1) & 1, abort)) break;
-            const uint32_t tile = smem_u32(smem + st * kStage);
+            unsigned char *stage = smem + st * kStage;
+            const uint32_t tile = smem_u32(stage);
             const long t0 = it.start + (long)chunk_at(c);
-            copy_tile<V>(tile + kTile, Y + t0 * a.ld_y, a.ld_y, kd, n, warp * (kC / 2), (warp + 1) * (kC / 2));
+            if (kTma) {
+                // (boxes of whole chunks: behind the last sequence's end they
+                // are filled with zeros, behind another's the rows are replaced)
+                uint64_t *landed = n == kC ? &bars->full[st] : &bars->partial;
+                const int blocks = (kd + 63) / 64, wblocks = (vd + 63) / 64;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(landed, kBlock * ((states_only ? 1 : 2) * blocks + wblocks));
+                    for (int i = 0; i < blocks; ++i) {
+                        if (!states_only) tma_load_3d(stage + i * kBlock, &m.x, landed, i * 64, h / a.sx, (int)t0);
+                        tma_load_3d(stage + kTile + i * kBlock, &m.y, landed, i * 64, h / a.sy, (int)t0);
+                    }
+                    for (int i = 0; i < wblocks; ++i)
+                        tma_load_3d(stage + 2 * kTile + i * kBlock, &m.w, landed, i * 64, h / a.sw, (int)t0);
+                }
+                __syncwarp();
+                if (n < kC) {
+                    if (!warp_wait(&bars->partial, 0, abort)) break;      // a run has one such chunk
+                    for (int i = n * 8 + lane; i < kC * 8; i += 32)
+#pragma unroll
+                        for (int k = 0; k < 6; ++k)
+                            *reinterpret_cast<uint4 *>(stage + k * kBlock + i * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async();
+                    warp_arrive(&bars->full[st]);
+                }
+                continue;
+            }
+            const int from = warp * (kC / 2), to = (warp + 1) * (kC / 2);
+            copy_tile<V>(tile + kTile, Y + t0 * a.ld_y, a.ld_y, kd, n, from, to);
             if (warp == 1) copy_tile<V>(tile + 2 * kTile, W + t0 * a.ld_w, a.ld_w, vd, n, 0, kC);
             else if (!states_only) copy_tile<V>(tile, X + t0 * a.ld_x, a.ld_x, kd, n, 0, kC);
-            // every lane arrives when its own copies have landed
             if (V == 1) mbar_arrive(&bars->full[st]);
-            else copies_arrive(&bars->full[st]);
+            else copies_arrive(&bars->full[st]);      // every lane, when its own copies have landed
         }
-        commit_copies();
-        wait_copies<0>();
+        if (kTma) {
+            // every issued copy must land before the CTA may exit (a partial
+            // chunk's has, or its wait ran out)
+            if (warp == 0 && lane < kStages && lane < issued) {
+                int dummy = 0;
+                mbar_wait(&bars->full[lane], ((issued - 1 - lane) / kStages) & 1, &dummy);
+            }
+            __syncwarp();
+        } else {
+            commit_copies();
+            wait_copies<0>();
+        }
     } else if (warp < 4) {
         // ------------------------------------------------ MMA issuers (the
         // whole warp waits, one lane issues and commits).  The copies wrote
@@ -412,28 +449,38 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     } else if (warp < 8) {
         // ------------------------------------------------ D W in two parts
         const int t = tid - 128, per = (vd + 7) / 8, total = kC * per;
+        const bool whole = per == 16 || per == 8;
+        const int r0 = t / per, apart = 128 / per;           // (128 / 16 or 128 / 8 rows)
+        const uint32_t at0 = ((t - r0 * per) >> 3) * kBlock + sw128_offset(r0, (t - r0 * per) & 7);
         for (int c = 0; c < chunks; ++c) {
             const int st = c % kStages, n = chunk_len(c);
             if (!warp_wait(&bars->full[st], (c / kStages) & 1, abort)) break;
             if (c >= 2 && !warp_wait(&bars->parts_free[c & 1], ((c >> 1) - 1) & 1, abort)) break;
             const unsigned char *w = smem + st * kStage + 2 * kTile;
             unsigned char *out = smem + kOffParts + (c & 1) * 2 * kTile;
-            const uint2 *leave = bars->leave + (rev ? 0 : kC - n);
-#pragma unroll 2
-            for (int i = t; i < total; i += 128) {
-                const int r = per == 16 ? i >> 4 : i / per, ch = i - r * per;
-                const uint32_t at = (ch >> 3) * kBlock + sw128_offset(r, ch & 7);
+            const uint2 *leave = bars->leave[n < kC];
+            auto split = [&](uint32_t at, uint2 d) {
                 const uint4 raw = *reinterpret_cast<const uint4 *>(w + at);
-                const uint2 d = *reinterpret_cast<const uint2 *>(leave + r);
                 const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     hi[q] = fma_bf16x2(in[q], d.x, 0x80008000u);
-                    lo[q] = fma_bf16x2(in[q], d.y, fma_bf16x2(in[q], d.x, hi[q] ^ 0x80008000u));
+                    lo[q] = fma_bf16x2(in[q], d.y, fma_bf16x2(in[q], d.x, neg_bf16x2(hi[q])));
                 }
                 *reinterpret_cast<uint4 *>(out + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 *reinterpret_cast<uint4 *>(out + kTile + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            };
+            if (whole) {
+                // the rows of a thread's packets lie whole swizzle periods apart
+#pragma unroll 1
+                for (int i = 0; i < total / 128; ++i)
+                    split(at0 + i * (apart * 128), leave[i * apart + r0]);
+            } else {
+                for (int i = t; i < total; i += 128) {
+                    const int r = i / per, ch = i - r * per;
+                    split((ch >> 3) * kBlock + sw128_offset(r, ch & 7), leave[r]);
+                }
             }
             fence_proxy_async();
             warp_arrive(&bars->parts_ready[c & 1]);
@@ -492,61 +539,61 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const int quad = warp & 3, col = quad * 32 + lane;
         const uint32_t at = tmem + kColO + ((uint32_t)(quad * 32) << 16);
         const long step = (long)p.H * vd;
-        const bool pairs = !(vd & 1) && !((uintptr_t)a.out & 3);
-        if (!states_only)
-            for (int c = 0; c < chunks; ++c) {
-                const int n = chunk_len(c);
-                if (!warp_wait(&bars->o_ready[c & 1], (c >> 1) & 1, abort)) break;
-                tc_fence_after();
-                const long row = ((it.start + (long)chunk_at(c)) * p.H + h) * vd + col;
-                const float *enter = bars->enter + (rev ? kC - n : 0);
+        const bool pairs = !(vd & 1) && !((uintptr_t)a.out & 3) && !a.out_f32;
+        for (int c = 0; c < chunks && !states_only; ++c) {
+            const int n = chunk_len(c);
+            if (!warp_wait(&bars->o_ready[c & 1], (c >> 1) & 1, abort)) break;
+            tc_fence_after();
+            const uint32_t from = at + (c & 1) * 128;
+            const long t0 = it.start + (long)chunk_at(c), row = (t0 * p.H + h) * vd + col;
+            const float *enter = bars->enter[n < kC];
+            if (pairs) {
+                // neighbouring lanes trade halves: the even one writes two
+                // columns of a token, the odd one of the next token
+                uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<unsigned short *>(a.out) + row + (lane & 1 ? step - 1 : 0));
+                const uint32_t order = lane & 1 ? 0x3276 : 0x5410;
+                int left = col < vd ? n - (lane & 1) : 0;             // of this lane's tokens 0, 2 ..
 #pragma unroll 1
-                for (int m = 0; m < 4; ++m) {
+                for (int m = 0; m < 4; ++m, enter += 16, left -= 16) {
                     float o1[16], o2[16];
-                    tmem_ld16(at + (c & 1) * 128 + m * 16, o1);
-                    tmem_ld16(at + (c & 1) * 128 + 64 + m * 16, o2);
+                    tmem_ld16(from + m * 16, o1);
+                    tmem_ld16(from + 64 + m * 16, o2);
                     tmem_ld_wait();
                     if (m == 3) {
                         tc_fence_before();
                         warp_arrive(&bars->o_free[c & 1]);
                     }
-                    const long first = row + m * 16 * step;
-                    const float *f = enter + m * 16;
-                    if (a.out_f32) {
-                        float *out = static_cast<float *>(a.out) + first;
 #pragma unroll
-                        for (int q = 0; q < 16; ++q, out += step)
-                            if (col < vd && m * 16 + q < n) *out = fmaf(f[q], o1[q], o2[q]);
-                        continue;
-                    }
-                    if (pairs && n == kC) {
-                        // neighbouring lanes trade halves: the even one writes
-                        // two columns of token q, the odd one of token q + 1
-                        uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<unsigned short *>(a.out) + first +
-                                                                     (lane & 1 ? step - 1 : 0));
-#pragma unroll
-                        for (int q = 0; q < 16; q += 2, out += step) {
-                            const float2 f2 = *reinterpret_cast<const float2 *>(bars->enter + m * 16 + q);
-                            float v0, v1;
-                            split_pair(fma2(make_pair(f2.x, f2.y), make_pair(o1[q], o1[q + 1]), make_pair(o2[q], o2[q + 1])), v0,
-                                       v1);
-                            const uint32_t mine = pack2(v0, v1), other = __shfl_xor_sync(0xffffffffu, mine, 1);
-                            if (col < vd) *out = __byte_perm(mine, other, lane & 1 ? 0x3276 : 0x5410);
-                        }
-                        continue;
-                    }
-                    if (col >= vd) continue;
-                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + first;
-#pragma unroll 1
-                    for (int q = 0; q < 16; ++q, out += step) {
-                        float v = 0.f;
-#pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            if (k == q) v = fmaf(f[k], o1[k], o2[k]);
-                        if (m * 16 + q < n) *out = __float2bfloat16_rn(v);
+                    for (int q = 0; q < 16; q += 2, out += step) {
+                        const float2 f = *reinterpret_cast<const float2 *>(enter + q);
+                        float v0, v1;
+                        split_pair(fma2(make_pair(f.x, f.y), make_pair(o1[q], o1[q + 1]), make_pair(o2[q], o2[q + 1])), v0, v1);
+                        const uint32_t mine = pack2(v0, v1), other = __shfl_xor_sync(0xffffffffu, mine, 1);
+                        if (q < left) *out = __byte_perm(mine, other, order);
                     }
                 }
+                continue;
             }
+#pragma unroll 1
+            for (int m8 = 0; m8 < 8; ++m8) {
+                float o1[8], o2[8];
+                tmem_ld8(from + m8 * 8, o1);
+                tmem_ld8(from + 64 + m8 * 8, o2);
+                tmem_ld_wait();
+                if (m8 == 7) {
+                    tc_fence_before();
+                    warp_arrive(&bars->o_free[c & 1]);
+                }
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int i = m8 * 8 + q;
+                    if (col >= vd || i >= n) continue;
+                    const float v = fmaf(enter[i], o1[q], o2[q]);
+                    if (a.out_f32) static_cast<float *>(a.out)[row + i * step] = v;
+                    else static_cast<__nv_bfloat16 *>(a.out)[row + i * step] = __float2bfloat16_rn(v);
+                }
+            }
+        }
     } else {
         // ------------------------------------------------ the state: row `col`
         // of Z^T, columns k0 .. k0 + 31
@@ -617,17 +664,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 }
 
 template <int V>
-cudaError_t launch(const AttnProblem &p, cudaStream_t st) {
+cudaError_t launch(const AttnProblem &p, const AllMaps &maps, cudaStream_t st) {
     const cudaError_t err = allow_shared<attn_tc_kernel<V>>(kSmem);
     if (err != cudaSuccess) return err;
-    attn_tc_kernel<V><<<dim3((unsigned)(p.slots * (long)p.H), p.n_pass), kThreads, kSmem, st>>>(p);
+    attn_tc_kernel<V><<<dim3((unsigned)(p.slots * (long)p.H), p.n_pass), kThreads, kSmem, st>>>(p, maps);
     return cudaGetLastError();
+}
+
+// [tokens, heads, width] rows as boxes of 64 tokens of 64 columns of a head.
+bool map_rows(CUtensorMap *map, const void *base, long tokens, int heads, int width, long ld) {
+    const uint64_t dims[3] = {(uint64_t)width, (uint64_t)heads, (uint64_t)tokens};
+    const uint64_t strides[2] = {(uint64_t)width * 2, (uint64_t)ld * 2};
+    const uint32_t box[3] = {64, 1, kC};
+    return make_map_3d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, dims, strides, box);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_tc(const AttnProblem &p, cudaStream_t st) {
-    const int V = packet_width(8, 2, [&](int V, int bytes) {
+    int V = packet_width(8, 2, [&](int V, int bytes) {
         for (int i = 0; i < p.n_pass; ++i) {
             const AttnPass &a = p.pass[i];
             if (a.kd % V || a.vd % V || !rows_aligned(a.X, a.ld_x, 2, bytes) || !rows_aligned(a.Y, a.ld_y, 2, bytes) ||
@@ -636,7 +691,16 @@ cudaError_t launch_attn_tc(const AttnProblem &p, cudaStream_t st) {
         }
         return true;
     });
-    return V == 8 ? launch<8>(p, st) : V == 2 ? launch<2>(p, st) : launch<1>(p, st);
+    AllMaps maps;
+    for (int i = 0; i < p.n_pass && V == 8 && p.T_total > 0; ++i) {
+        const AttnPass &a = p.pass[i];
+        Maps &m = maps.pass[i];
+        bool ok = map_rows(&m.y, a.Y, p.T_total, p.H / a.sy, a.kd, a.ld_y) &&
+                  map_rows(&m.w, a.W, p.T_total, p.H / a.sw, a.vd, a.ld_w);
+        if (a.out) ok = ok && map_rows(&m.x, a.X, p.T_total, p.H / a.sx, a.kd, a.ld_x);
+        if (!ok) return cudaErrorInvalidValue;
+    }
+    return V == 8 ? launch<8>(p, maps, st) : V == 2 ? launch<2>(p, maps, st) : launch<1>(p, maps, st);
 }
 
 }  // namespace mdn
