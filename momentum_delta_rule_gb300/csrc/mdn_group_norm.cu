@@ -23,91 +23,158 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Sum over the threads of a group: tpg threads (a power of two).  The halves of
+// A call's kernels follow one another by programmatic dependent launch: each lets
+// the next one be set up once its own blocks run, and waits for the one before
+// it, every thread of it, before it reads.
+__device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t follow(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+// Sums over the threads of a group: tpg threads (a power of two).  The halves of
 // `red` alternate, as one barrier a call then is enough.
-__device__ __forceinline__ float2 group_sum(float2 v, int tpg, float2 *red, int &turn) {
-    for (int o = min(tpg, 32) >> 1; o > 0; o >>= 1) {
-        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-    }
-    if (tpg <= 32) return v;
-    float2 *r = red + turn;
+template <int N>
+struct Sums {
+    float v[N];
+};
+template <int N>
+__device__ __forceinline__ Sums<N> group_sum(Sums<N> s, int tpg, Sums<N> *red, int &turn) {
+    for (int o = min(tpg, 32) >> 1; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) s.v[i] += __shfl_xor_sync(0xffffffffu, s.v[i], o);
+    if (tpg <= 32) return s;
+    Sums<N> *r = red + turn;
     turn ^= 32;
-    if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = v;
+    if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = s;
     __syncthreads();
     const int wpg = tpg >> 5;
-    v = r[((threadIdx.x >> 5) & ~(wpg - 1)) + (threadIdx.x & (wpg - 1))];
-    for (int o = wpg >> 1; o > 0; o >>= 1) {
-        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-    }
-    return v;
+    s = r[((threadIdx.x >> 5) & ~(wpg - 1)) + (threadIdx.x & (wpg - 1))];
+    for (int o = wpg >> 1; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) s.v[i] += __shfl_xor_sync(0xffffffffu, s.v[i], o);
+    return s;
 }
 
+// V values as pairs of fp32, two to an instruction (a single one beside a zero
+// that no sum takes).
 template <int V>
-__device__ __forceinline__ void activate(const float *x, int act, float *a) {
-    if (act == MDN_ACT_NONE) {
+struct Vals {
+    static constexpr int N = (V + 1) / 2;
+    Pair p[N];
+};
+__device__ __forceinline__ Pair both(float x) { return make_pair(x, x); }
+template <typename T, int V>
+__device__ __forceinline__ Vals<V> values(const Packet<T, V> &p) {
+    Vals<V> r;
+    if constexpr (V == 1) {
+        r.p[0] = make_pair(to_f32(p.e[0]), 0.f);
+    } else if constexpr (sizeof(T) == 2) {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(&p);
 #pragma unroll
-        for (int v = 0; v < V; ++v) a[v] = x[v];
+        for (int i = 0; i < V / 2; ++i) r.p[i] = make_pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) r.p[i] = make_pair(p.e[2 * i], p.e[2 * i + 1]);
+    }
+    return r;
+}
+template <typename T, int V>
+__device__ __forceinline__ Packet<T, V> packet(const Vals<V> &r) {
+    float f[2 * Vals<V>::N];
+#pragma unroll
+    for (int i = 0; i < Vals<V>::N; ++i) split_pair(r.p[i], f[2 * i], f[2 * i + 1]);
+    return pack<T, V>(f);
+}
+template <int V>
+__device__ __forceinline__ float sum_of(const Vals<V> &r) {
+    Pair s = r.p[0];
+#pragma unroll
+    for (int i = 1; i < Vals<V>::N; ++i) s = add2(s, r.p[i]);
+    float x, y;
+    split_pair(s, x, y);
+    return V == 1 ? x : x + y;
+}
+template <int V>
+__device__ __forceinline__ Vals<V> zeros() {
+    Vals<V> r;
+#pragma unroll
+    for (int i = 0; i < Vals<V>::N; ++i) r.p[i] = both(0.f);
+    return r;
+}
+template <int V>
+__device__ __forceinline__ Vals<V> load_weights(const float *w, long c, float none) {
+    Vals<V> r;
+#pragma unroll
+    for (int i = 0; i < Vals<V>::N; ++i)
+        r.p[i] = w ? make_pair(__ldg(w + c + 2 * i), V == 1 ? none : __ldg(w + c + 2 * i + 1)) : both(none);
+    return r;
+}
+
+__device__ __forceinline__ Pair sigmoid2(Pair x) {
+    float a, b;
+    split_pair(mul2(x, both(-kLog2e)), a, b);
+    split_pair(add2(make_pair(ex2(a), ex2(b)), both(1.f)), a, b);
+    return make_pair(rcp(a), rcp(b));
+}
+__device__ __forceinline__ Pair act2(Pair x, int act) {
+    if (act == MDN_ACT_NONE) return x;
+    const Pair s = sigmoid2(x);
+    return act == MDN_ACT_SILU ? mul2(x, s) : s;
+}
+// a <- act(x), d <- act'(x)
+__device__ __forceinline__ void act2_d(Pair x, int act, Pair &a, Pair &d) {
+    if (act == MDN_ACT_NONE) {
+        a = x;
+        d = both(1.f);
         return;
     }
-    sigmoids<V>(x, a);
-    if (act == MDN_ACT_SILU)
-#pragma unroll
-        for (int v = 0; v < V; ++v) a[v] *= x[v];
-}
-template <int V>
-__device__ __forceinline__ void activate_d(const float *x, int act, float *a, float *d) {
-    if (act == MDN_ACT_NONE) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            a[v] = x[v];
-            d[v] = 1.f;
-        }
-        return;
-    }
-    float s[V];
-    sigmoids<V>(x, s);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const bool silu = act == MDN_ACT_SILU;
-        a[v] = silu ? x[v] * s[v] : s[v];
-        d[v] = silu ? s[v] * fmaf(x[v], 1.f - s[v], 1.f) : s[v] * (1.f - s[v]);
+    const Pair s = sigmoid2(x), rest = fma2(s, both(-1.f), both(1.f));
+    if (act == MDN_ACT_SILU) {
+        a = mul2(x, s);
+        d = mul2(s, fma2(x, rest, both(1.f)));
+    } else {
+        a = s;
+        d = mul2(s, rest);
     }
 }
 
-template <int V>
-__device__ __forceinline__ void load_weights(const float *w, long c, float none, float *f) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) f[v] = w ? __ldg(w + c + v) : none;
-}
-
-// What a group's elements become, and their gradient.
+// What centered elements d = x - mean become.
 template <int V, bool GATE>
-__device__ __forceinline__ void forward_packet(float *x, const float *g, float mean, float rstd, const float *w,
-                                               const float *b, int act) {
+__device__ __forceinline__ Vals<V> forward_vals(const Vals<V> &d, const Vals<V> &g, float rstd, const Vals<V> &w,
+                                                const Vals<V> &b, int act) {
+    Vals<V> y;
+    const Pair r = both(rstd);
 #pragma unroll
-    for (int v = 0; v < V; ++v) x[v] = fmaf((x[v] - mean) * rstd, w[v], b[v]);
-    float a[V];
-    activate<V>(GATE ? g : x, act, a);
-#pragma unroll
-    for (int v = 0; v < V; ++v) x[v] = GATE ? x[v] * a[v] : a[v];
+    for (int i = 0; i < Vals<V>::N; ++i) {
+        const Pair u = fma2(mul2(d.p[i], r), w.p[i], b.p[i]);
+        y.p[i] = GATE ? mul2(u, act2(g.p[i], act)) : act2(u, act);
+    }
+    return y;
 }
 // x <- n, dy <- du, g <- dgate
 template <int V, bool GATE>
-__device__ __forceinline__ void backward_packet(float *x, float *g, float *dy, float mean, float rstd, const float *w,
-                                                const float *b, int act) {
-    float u[V], a[V], d[V];
+__device__ __forceinline__ void backward_vals(Vals<V> &x, Vals<V> &g, Vals<V> &dy, float mean, float rstd, const Vals<V> &w,
+                                              const Vals<V> &b, int act) {
+    const Pair m = both(-mean), r = both(rstd);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        x[v] = (x[v] - mean) * rstd;
-        u[v] = fmaf(x[v], w[v], b[v]);
-    }
-    activate_d<V>(GATE ? g : u, act, a, d);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        if (GATE) g[v] = dy[v] * u[v] * d[v];
-        dy[v] *= GATE ? a[v] : d[v];
+    for (int i = 0; i < Vals<V>::N; ++i) {
+        x.p[i] = mul2(add2(x.p[i], m), r);
+        const Pair u = fma2(x.p[i], w.p[i], b.p[i]);
+        Pair a, d;
+        act2_d(GATE ? g.p[i] : u, act, a, d);
+        if (GATE) g.p[i] = mul2(mul2(dy.p[i], u), d);
+        dy.p[i] = mul2(dy.p[i], GATE ? a : d);
     }
 }
 
@@ -136,20 +203,36 @@ __device__ __forceinline__ TokenPlace token_place(const GroupNormProblem &p, int
 // thread, as many as the widest group (16384 columns) needs.
 __host__ __device__ constexpr int most_threads(int NI, int V) { return NI <= 4 || V >= 8 ? 256 : V == 4 ? 512 : 1024; }
 
+// Q values from the first-th on, as fp32.
+template <int Q, int V>
+__device__ __forceinline__ Packet<float, Q> packet_of(const Vals<V> &r, int first) {
+    float f[2 * Vals<V>::N];
+#pragma unroll
+    for (int i = 0; i < Vals<V>::N; ++i) split_pair(r.p[i], f[2 * i], f[2 * i + 1]);
+    Packet<float, Q> q;
+#pragma unroll
+    for (int i = 0; i < Q; ++i) q.e[i] = f[first + i];
+    return q;
+}
+
+// Whether a thread keeps weights, and asks for the next token's packets before it
+// looks at this one's.
+__host__ __device__ constexpr bool held(int NI, int V) { return NI * V <= 16; }
+
 template <typename T, int V, int NI, bool GATE>
 __global__ void __launch_bounds__(most_threads(NI, V)) token_fwd_kernel(GroupNormProblem p, int tpg) {
-    __shared__ float2 red[64];
-    constexpr bool HOLD = NI * V <= 16;
+    __shared__ Sums<1> red[64];
+    constexpr bool HOLD = held(NI, V);
     int turn = 0;
     const TokenPlace t = token_place(p, tpg);
     const int w = p.D / p.G;
     const long c0 = t.g * w;
     const T *x = static_cast<const T *>(p.x) + c0, *gate = static_cast<const T *>(p.gate) + c0;
     T *y = static_cast<T *>(p.y) + c0;
-    float wt[HOLD ? NI : 1][V], bs[HOLD ? NI : 1][V];
+    Vals<V> wt[HOLD ? NI : 1], bs[HOLD ? NI : 1];
     auto weights = [&](int i, int c) {
-        load_weights<V>(p.weight, c0 + c, 1.f, wt[HOLD ? i : 0]);
-        load_weights<V>(p.bias, c0 + c, 0.f, bs[HOLD ? i : 0]);
+        wt[HOLD ? i : 0] = load_weights<V>(p.weight, c0 + c, 1.f);
+        bs[HOLD ? i : 0] = load_weights<V>(p.bias, c0 + c, 0.f);
     };
     if (HOLD)
 #pragma unroll
@@ -157,54 +240,61 @@ __global__ void __launch_bounds__(most_threads(NI, V)) token_fwd_kernel(GroupNor
             const int c = (i * tpg + t.tid) * V;
             if (c < w) weights(i, c);
         }
-    const float inv = 1.f / (float)w;
-    long row = t.row;
-    for (int k = 0; k < t.rounds; ++k, row += t.step) {
-        const bool live = row < p.rows;
-        Packet<T, V> px[NI], pg[GATE ? NI : 1];
+    Packet<T, V> px[NI], pg[GATE ? NI : 1];
+    auto load = [&](long row) {
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const int c = (i * tpg + t.tid) * V;
-            if (live && c < w) {
+            if (row < p.rows && c < w) {
                 px[i] = load_packet<T, V>(x + row * p.ld_x + c);
                 if (GATE) pg[i] = load_packet<T, V>(gate + row * p.ld_gate + c);
             }
         }
-        float mean = 0.f;
-        if (p.center) {
-            float s = 0.f;
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                float f[V];
-                if (live && (i * tpg + t.tid) * V < w) {
-                    unpack<T, V>(px[i], f);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) s += f[v];
-                }
-            }
-            mean = group_sum(make_float2(s, 0.f), tpg, red, turn).x * inv;
-        }
-        float s = 0.f;
+    };
+    const float inv = 1.f / (float)w;
+    long row = t.row;
+    if (HOLD) load(row);
+    for (int k = 0; k < t.rounds; ++k, row += t.step) {
+        const bool live = row < p.rows;
+        if (!HOLD) load(row);
+        Vals<V> d[NI], g[GATE ? NI : 1];
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            float f[V];
-            if (live && (i * tpg + t.tid) * V < w) {
-                unpack<T, V>(px[i], f);
-#pragma unroll
-                for (int v = 0; v < V; ++v) s = fmaf(f[v] - mean, f[v] - mean, s);
-            }
+            const bool in = live && (i * tpg + t.tid) * V < w;
+            d[i] = in ? values<T, V>(px[i]) : zeros<V>();
+            if (GATE && HOLD) g[i] = values<T, V>(pg[i]);
         }
-        const float rstd = rsqrtf(fmaf(group_sum(make_float2(s, 0.f), tpg, red, turn).x, inv, p.eps));
+        if (HOLD) load(row + t.step);
+        float mean = 0.f;
+        Sums<1> s;
+        if (p.center) {
+            s.v[0] = 0.f;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) s.v[0] += sum_of<V>(d[i]);
+            mean = group_sum(s, tpg, red, turn).v[0] * inv;
+        }
+        s.v[0] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const bool in = (i * tpg + t.tid) * V < w;
+            Vals<V> q;
+#pragma unroll
+            for (int j = 0; j < Vals<V>::N; ++j) {
+                d[i].p[j] = add2(d[i].p[j], both(-mean));
+                q.p[j] = mul2(d[i].p[j], d[i].p[j]);
+            }
+            if (in) s.v[0] += sum_of<V>(q);
+        }
+        const float rstd = rsqrtf(fmaf(group_sum(s, tpg, red, turn).v[0], inv, p.eps));
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const int c = (i * tpg + t.tid) * V;
             if (live && c < w) {
-                float f[V], g[V];
                 if (!HOLD) weights(i, c);
-                unpack<T, V>(px[i], f);
-                if (GATE) unpack<T, V>(pg[i], g);
-                forward_packet<V, GATE>(f, g, mean, rstd, wt[HOLD ? i : 0], bs[HOLD ? i : 0], p.act);
-                store_packet<T, V>(y + row * p.D + c, pack<T, V>(f));
+                if (GATE && !HOLD) g[i] = values<T, V>(pg[i]);
+                store_packet<T, V>(y + row * p.D + c,
+                                   packet<T, V>(forward_vals<V, GATE>(d[i], g[GATE ? i : 0], rstd, wt[HOLD ? i : 0],
+                                                                      bs[HOLD ? i : 0], p.act)));
             }
         }
         if (p.stats && live && t.tid == 0)
@@ -214,9 +304,9 @@ __global__ void __launch_bounds__(most_threads(NI, V)) token_fwd_kernel(GroupNor
 
 // part: [row lanes][2][D], one lane for every t.row of the first round.
 template <typename T, int V, int NI, bool GATE>
-__global__ void __launch_bounds__(most_threads(NI, V))
-token_bwd_kernel(GroupNormProblem p, int tpg, float *part) {
-    __shared__ float2 red[64];
+__global__ void __launch_bounds__(most_threads(NI, V)) token_bwd_kernel(GroupNormProblem p, int tpg, float *part) {
+    __shared__ Sums<2> red[64];
+    grid_trigger();
     int turn = 0;
     const TokenPlace t = token_place(p, tpg);
     const int w = p.D / p.G;
@@ -224,72 +314,91 @@ token_bwd_kernel(GroupNormProblem p, int tpg, float *part) {
     const T *x = static_cast<const T *>(p.x) + c0, *gate = static_cast<const T *>(p.gate) + c0;
     const T *dyp = static_cast<const T *>(p.dy) + c0;
     T *dx = static_cast<T *>(p.dx) + c0, *dgate = static_cast<T *>(p.dgate) + c0;
-    constexpr bool HOLD = NI * V <= 16;
-    float wt[HOLD ? NI : 1][V], bs[HOLD ? NI : 1][V], dw[NI][V], db[NI][V];
+    constexpr bool HOLD = held(NI, V);
+    Vals<V> wt[HOLD ? NI : 1], bs[HOLD ? NI : 1], dw[NI], db[NI];
     auto weights = [&](int i, int c) {
-        load_weights<V>(p.weight, c0 + c, 1.f, wt[HOLD ? i : 0]);
-        load_weights<V>(p.bias, c0 + c, 0.f, bs[HOLD ? i : 0]);
+        wt[HOLD ? i : 0] = load_weights<V>(p.weight, c0 + c, 1.f);
+        bs[HOLD ? i : 0] = load_weights<V>(p.bias, c0 + c, 0.f);
     };
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
         const int c = (i * tpg + t.tid) * V;
         if (HOLD && c < w) weights(i, c);
-#pragma unroll
-        for (int v = 0; v < V; ++v) dw[i][v] = db[i][v] = 0.f;
+        dw[i] = db[i] = zeros<V>();
     }
-    const float inv = 1.f / (float)w;
-    long row = t.row;
-    for (int k = 0; k < t.rounds; ++k, row += t.step) {
-        const bool live = row < p.rows;
-        Packet<T, V> px[NI], pd[NI], pg[GATE ? NI : 1];
-        float2 st = make_float2(0.f, 0.f), s = make_float2(0.f, 0.f);
-        if (live) st = reinterpret_cast<const float2 *>(p.stats)[row * p.G + t.g];
+    Packet<T, V> px[NI], pd[NI], pg[GATE ? NI : 1];
+    float2 st, next = make_float2(0.f, 0.f);
+    auto load = [&](long row) {
+        if (row >= p.rows) return;
+        next = reinterpret_cast<const float2 *>(p.stats)[row * p.G + t.g];
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const int c = (i * tpg + t.tid) * V;
-            if (live && c < w) {
+            if (c < w) {
                 px[i] = load_packet<T, V>(x + row * p.ld_x + c);
                 pd[i] = load_packet<T, V>(dyp + row * p.ld_dy + c);
                 if (GATE) pg[i] = load_packet<T, V>(gate + row * p.ld_gate + c);
             }
         }
-        // the elements are taken apart twice, as keeping n and dn of all of
-        // them takes twice the registers
-        auto element = [&](int i, int c, float *n, float *d, float *g) {
+    };
+    const float inv = 1.f / (float)w;
+    long row = t.row;
+    if (HOLD) load(row);
+    for (int k = 0; k < t.rounds; ++k, row += t.step) {
+        const bool live = row < p.rows;
+        if (!HOLD) load(row);
+        st = next;
+        // n and du of the thread's elements, kept where they are few and
+        // worked out twice where they are many
+        Vals<V> n[HOLD ? NI : 1], d[HOLD ? NI : 1], g[HOLD ? NI : 1];
+        auto element = [&](int i, int c, int to) {
             if (!HOLD) weights(i, c);
-            unpack<T, V>(px[i], n);
-            unpack<T, V>(pd[i], d);
-            if (GATE) unpack<T, V>(pg[i], g);
-            backward_packet<V, GATE>(n, g, d, st.x, st.y, wt[HOLD ? i : 0], bs[HOLD ? i : 0], p.act);
+            n[to] = values<T, V>(px[i]);
+            d[to] = values<T, V>(pd[i]);
+            if (GATE) g[to] = values<T, V>(pg[i]);
         };
+        auto finish = [&](int to) { backward_vals<V, GATE>(n[to], g[to], d[to], st.x, st.y, wt[to], bs[to], p.act); };
+        if (HOLD) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) element(i, 0, HOLD ? i : 0);
+            load(row + t.step);
+        }
+        Sums<2> s;
+        s.v[0] = s.v[1] = 0.f;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int c = (i * tpg + t.tid) * V;
+            const int c = (i * tpg + t.tid) * V, to = HOLD ? i : 0;
             if (live && c < w) {
-                float n[V], d[V], g[V];
-                element(i, c, n, d, g);
-                if (GATE) store_packet<T, V>(dgate + row * p.D + c, pack<T, V>(g));
+                if (!HOLD) element(i, c, to);
+                finish(to);
+                if (GATE) store_packet<T, V>(dgate + row * p.D + c, packet<T, V>(g[to]));
+                Vals<V> dn, dnn;
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    dw[i][v] = fmaf(d[v], n[v], dw[i][v]);
-                    db[i][v] += d[v];
-                    const float dn = d[v] * wt[HOLD ? i : 0][v];
-                    s.x += dn;
-                    s.y = fmaf(dn, n[v], s.y);
+                for (int j = 0; j < Vals<V>::N; ++j) {
+                    dw[i].p[j] = fma2(d[to].p[j], n[to].p[j], dw[i].p[j]);
+                    db[i].p[j] = add2(d[to].p[j], db[i].p[j]);
+                    dn.p[j] = mul2(d[to].p[j], wt[to].p[j]);
+                    dnn.p[j] = mul2(dn.p[j], n[to].p[j]);
                 }
+                s.v[0] += sum_of<V>(dn);
+                s.v[1] += sum_of<V>(dnn);
             }
         }
         s = group_sum(s, tpg, red, turn);
-        const float m1 = p.center ? s.x * inv : 0.f, m2 = s.y * inv;
+        const Pair m1 = both(p.center ? -s.v[0] * inv : 0.f), m2 = both(-s.v[1] * inv), r = both(st.y);
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int c = (i * tpg + t.tid) * V;
+            const int c = (i * tpg + t.tid) * V, to = HOLD ? i : 0;
             if (live && c < w) {
-                float n[V], d[V], g[V];
-                element(i, c, n, d, g);
+                if (!HOLD) {
+                    element(i, c, to);
+                    finish(to);
+                }
+                Vals<V> out;
 #pragma unroll
-                for (int v = 0; v < V; ++v) n[v] = st.y * (fmaf(d[v], wt[HOLD ? i : 0][v], -m1) - n[v] * m2);
-                store_packet<T, V>(dx + row * p.D + c, pack<T, V>(n));
+                for (int j = 0; j < Vals<V>::N; ++j)
+                    out.p[j] = mul2(r, fma2(n[to].p[j], m2, fma2(d[to].p[j], wt[to].p[j], m1)));
+                store_packet<T, V>(dx + row * p.D + c, packet<T, V>(out));
             }
         }
     }
@@ -298,34 +407,41 @@ token_bwd_kernel(GroupNormProblem p, int tpg, float *part) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
         const int c = (i * tpg + t.tid) * V;
-        if (c < w)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                out[c + v] = dw[i][v];
-                out[p.D + c + v] = db[i][v];
+        if (c < w) {
+            store_packet<float, V < 4 ? V : 4>(out + c, packet_of<V < 4 ? V : 4>(dw[i], 0));
+            store_packet<float, V < 4 ? V : 4>(out + p.D + c, packet_of<V < 4 ? V : 4>(db[i], 0));
+            if constexpr (V > 4) {
+                store_packet<float, 4>(out + c + 4, packet_of<4>(dw[i], 4));
+                store_packet<float, 4>(out + p.D + c + 4, packet_of<4>(db[i], 4));
             }
+        }
     }
 }
 
-// dw, dbias <- sums over the lanes of part, in their order.
-__global__ void __launch_bounds__(kThreads) param_kernel(const float *part, int lanes, int D, float *dw, float *dbias) {
-    __shared__ float sums[8][32];
+// dw, dbias <- sums over the lanes of part, in a fixed order.
+__global__ void __launch_bounds__(1024) param_kernel(const float *part, int lanes, int D, float *dw, float *dbias) {
+    __shared__ float sums[32][33];
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
     const long c = blockIdx.x * 32L + x;
+    grid_wait();
     float s = 0.f;
     if (c < 2L * D) {
         const float *src = part + c;
 #pragma unroll 8
-        for (int l = y; l < lanes; l += 8) s += src[(long)l * 2 * D];
+        for (int l = y; l < lanes; l += 32) s += src[(long)l * 2 * D];
     }
     sums[y][x] = s;
     __syncthreads();
-    if (y || c >= 2L * D) return;
-    for (int k = 1; k < 8; ++k) s += sums[k][x];
-    if (c < D) {
-        if (dw) dw[c] = s;
+    // warp y adds up column y
+    s = sums[x][y];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const long out = blockIdx.x * 32L + y;
+    if (x || out >= 2L * D) return;
+    if (out < D) {
+        if (dw) dw[out] = s;
     } else if (dbias) {
-        dbias[c - D] = s;
+        dbias[out - D] = s;
     }
 }
 
@@ -363,32 +479,6 @@ __device__ __forceinline__ long first_slot(const GroupNormProblem &p, int rows, 
     return p.cu ? p.cu[s] / rows + s : (long)s * ((p.T + rows - 1) / rows);
 }
 
-// Count, mean and sum of squared distances from it, of two parts together.
-struct Moments {
-    float n, mean, m2;
-};
-__device__ __forceinline__ Moments join(const Moments &a, const Moments &b) {
-    Moments r;
-    r.n = a.n + b.n;
-    const float f = r.n > 0.f ? b.n / r.n : 0.f, d = b.mean - a.mean;
-    r.mean = b.n > 0.f ? fmaf(d, f, a.mean) : a.mean;
-    r.m2 = b.n > 0.f ? a.m2 + b.m2 + (a.n > 0.f ? d * d * a.n * f : 0.f) : a.m2;
-    if (a.n <= 0.f) r = b;
-    return r;
-}
-__device__ __forceinline__ Moments join_warp(Moments a) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        Moments b;
-        b.n = __shfl_xor_sync(0xffffffffu, a.n, o);
-        b.mean = __shfl_xor_sync(0xffffffffu, a.mean, o);
-        b.m2 = __shfl_xor_sync(0xffffffffu, a.m2, o);
-        // the same order of the two in both lanes
-        a = (threadIdx.x & o) ? join(b, a) : join(a, b);
-    }
-    return a;
-}
-
 // Which columns a block takes: whole groups, their packets over its threads and
 // as many tokens at a time as fit.
 struct Columns {
@@ -417,9 +507,36 @@ __device__ __forceinline__ void by_group(const GroupNormProblem &p, const Column
     for (int g = warp; g < c.groups; g += kThreads / 32) take(g, ppg);
 }
 
+// Mean and sum of squared distances from it of parts with a mean, such a sum and
+// a count each: sums of the means' distances c and of their squares, from a
+// value that is near all of them (the first part's mean).
+struct Join {
+    float n, s1, s2;
+};
+__device__ __forceinline__ void join_part(Join &j, float center, float n, float mean, float m2) {
+    const float d = mean - center;
+    j.n += n;
+    j.s1 = fmaf(n, d, j.s1);
+    j.s2 += fmaf(n * d, d, m2);
+}
+__device__ __forceinline__ void join_warp(Join &j) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        j.n += __shfl_xor_sync(0xffffffffu, j.n, o);
+        j.s1 += __shfl_xor_sync(0xffffffffu, j.s1, o);
+        j.s2 += __shfl_xor_sync(0xffffffffu, j.s2, o);
+    }
+}
+// (mean, sum of squared distances)
+__device__ __forceinline__ float2 joined(const Join &j, float center) {
+    const float d = j.s1 / j.n, m2 = j.s2 - j.s1 * d;
+    return make_float2(center + d, m2 < 0.f ? 0.f : m2);      // (a NaN stays one)
+}
+
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) seq_stats_kernel(GroupNormProblem p, int rows, int per_block, float2 *part) {
-    __shared__ Moments mom[kThreads];
+    __shared__ float mom[3][kThreads];
+    grid_trigger();
     if (p.cu && !cu_well_formed(p.cu, p.n_seq, (int)p.rows)) {
         if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicExch(p.status, MDN_ERR_INVALID_ARG);
         return;
@@ -428,50 +545,53 @@ __global__ void __launch_bounds__(kThreads) seq_stats_kernel(GroupNormProblem p,
     if (!tile_of(p, rows, blockIdx.x, t)) return;
     const Columns c = columns_of(p, per_block, V);
     const int w = p.D / p.G;
-    Moments m = {0.f, 0.f, 0.f};
-    if (c.lane < c.lanes)
+    float n = 0.f, mean = 0.f, m2 = 0.f;
+    if (c.lane < c.lanes && c.lane < t.n)
         for (int pc = c.pc; pc < c.packets; pc += kThreads) {
-            const T *x = static_cast<const T *>(p.x) + t.start * p.ld_x + (long)c.g0 * w + pc * V;
+            const T *x = static_cast<const T *>(p.x) + (t.start + c.lane) * p.ld_x + (long)c.g0 * w + pc * V;
+            const long step = (long)c.lanes * p.ld_x;
+            const int count = (t.n - c.lane + c.lanes - 1) / c.lanes;
             // sums about the mean of the first packet, so that they do not cancel
-            float shift = 0.f, s1 = 0.f, s2 = 0.f;
-            int count = 0;
+            const float shift = p.center ? sum_of<V>(values<T, V>(load_packet<T, V>(x))) * (1.f / V) : 0.f;
+            Vals<V> s1 = zeros<V>(), s2 = zeros<V>();
+            const Pair minus = both(-shift);
 #pragma unroll 8
-            for (int r = c.lane; r < t.n; r += c.lanes, ++count) {
-                float f[V];
-                unpack<T, V>(load_packet<T, V>(x + r * p.ld_x), f);
-                if (r == c.lane && p.center) {
+            for (int r = 0; r < count; ++r) {
+                const Vals<V> f = values<T, V>(load_packet<T, V>(x + r * step));
 #pragma unroll
-                    for (int v = 0; v < V; ++v) shift += f[v] * (1.f / V);
-                }
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float d = f[v] - shift;
-                    s1 += d;
-                    s2 = fmaf(d, d, s2);
+                for (int j = 0; j < Vals<V>::N; ++j) {
+                    const Pair d = add2(f.p[j], minus);
+                    s1.p[j] = add2(s1.p[j], d);
+                    s2.p[j] = fma2(d, d, s2.p[j]);
                 }
             }
-            const float n = (float)count * V, mean = count ? s1 / n : 0.f;
-            Moments one;
-            one.n = n;
-            one.mean = p.center ? shift + mean : 0.f;
-            one.m2 = p.center ? fmaxf(s2 - s1 * mean, 0.f) : s2;
-            if (s2 != s2) one.m2 = s2;                   // fmaxf drops a NaN
-            m = join(m, one);
+            Join j = {0.f, 0.f, 0.f};
+            const float a = sum_of<V>(s1), b = sum_of<V>(s2), k = (float)count * V;
+            const float mine = p.center ? shift + a / k : 0.f, m = p.center ? b - a * (a / k) : b;
+            // (groups wider than the block: a thread's packets together)
+            if (n > 0.f) join_part(j, mean, n, mean, m2);
+            const float center = n > 0.f ? mean : mine;
+            join_part(j, center, k, mine, m < 0.f ? 0.f : m);
+            const float2 both_parts = joined(j, center);
+            n = j.n;
+            mean = p.center ? both_parts.x : 0.f;
+            m2 = p.center ? both_parts.y : j.s2;
         }
-    mom[threadIdx.x] = m;
+    mom[0][threadIdx.x] = n;
+    mom[1][threadIdx.x] = mean;
+    mom[2][threadIdx.x] = m2;
     __syncthreads();
     by_group(p, c, V, [&](int g, int ppg) {
-        Moments a = {0.f, 0.f, 0.f};
-        if (c.packets >= kThreads && c.groups == 1) {
-            for (int i = threadIdx.x & 31; i < kThreads; i += 32) a = join(a, mom[i]);
-        } else {
-            for (int i = threadIdx.x & 31; i < ppg * c.lanes; i += 32) {
-                const int lane = i / ppg;
-                a = join(a, mom[lane * c.packets + g * ppg + (i - lane * ppg)]);
-            }
+        const bool whole = c.packets >= kThreads && c.groups == 1;
+        const int count = whole ? kThreads : ppg * c.lanes;
+        const float center = mom[1][whole ? 0 : g * ppg];
+        Join j = {0.f, 0.f, 0.f};
+        for (int i = threadIdx.x & 31; i < count; i += 32) {
+            const int lane = whole ? 0 : i / ppg, at = whole ? i : lane * c.packets + g * ppg + (i - lane * ppg);
+            join_part(j, center, mom[0][at], mom[0][at] > 0.f ? mom[1][at] : center, mom[2][at]);
         }
-        a = join_warp(a);
-        if ((threadIdx.x & 31) == 0) part[(long)blockIdx.x * p.G + c.g0 + g] = make_float2(a.mean, a.m2);
+        join_warp(j);
+        if ((threadIdx.x & 31) == 0) part[(long)blockIdx.x * p.G + c.g0 + g] = p.center ? joined(j, center) : make_float2(0.f, j.s2);
     });
 }
 
@@ -479,46 +599,52 @@ __global__ void __launch_bounds__(kThreads) seq_stats_kernel(GroupNormProblem p,
 __global__ void __launch_bounds__(kThreads) seq_join_kernel(GroupNormProblem p, int rows, const float2 *part, float2 *stats) {
     const long i = blockIdx.x * (long)(kThreads / 32) + (threadIdx.x >> 5);
     const bool ok = !p.cu || cu_well_formed(p.cu, p.n_seq, (int)p.rows);
+    grid_trigger();
+    grid_wait();
     if (i >= (long)p.n_seq * p.G) return;
     const int s = (int)(i / p.G), g = (int)(i - (long)s * p.G), w = p.D / p.G;
     const int len = !ok ? 0 : p.cu ? p.cu[s + 1] - p.cu[s] : p.T;
     const int tiles = (len + rows - 1) / rows;
-    const long slot = ok ? first_slot(p, rows, s) : 0;
-    Moments a = {0.f, 0.f, 0.f};
+    const float2 *src = part + (ok ? first_slot(p, rows, s) : 0) * p.G + g;
+    const float center = tiles ? src[0].x : 0.f;
+    Join j = {0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int k = threadIdx.x & 31; k < tiles; k += 32) {
-        const float2 v = part[(slot + k) * p.G + g];
-        Moments one = {(float)min(rows, len - k * rows) * w, v.x, v.y};
-        a = join(a, one);
+        const float2 v = src[(long)k * p.G];
+        join_part(j, center, (float)min(rows, len - k * rows) * w, v.x, v.y);
     }
-    a = join_warp(a);
-    if ((threadIdx.x & 31) == 0)
-        stats[i] = len ? make_float2(a.mean, rsqrtf(a.m2 / a.n + p.eps)) : make_float2(0.f, 0.f);
+    join_warp(j);
+    if ((threadIdx.x & 31) == 0) {
+        const float2 v = joined(j, center);
+        stats[i] = len ? make_float2(p.center ? v.x : 0.f, rsqrtf((p.center ? v.y : j.s2) / j.n + p.eps)) : make_float2(0.f, 0.f);
+    }
 }
 
 template <typename T, int V, bool GATE>
 __global__ void __launch_bounds__(kThreads) seq_apply_kernel(GroupNormProblem p, int rows, int per_block, const float2 *stats) {
-    if (p.cu && !cu_well_formed(p.cu, p.n_seq, (int)p.rows)) return;
+    const bool ok = !p.cu || cu_well_formed(p.cu, p.n_seq, (int)p.rows);
+    grid_trigger();
+    grid_wait();
     Tile t;
-    if (!tile_of(p, rows, blockIdx.x, t)) return;
+    if (!ok || !tile_of(p, rows, blockIdx.x, t)) return;
     const Columns c = columns_of(p, per_block, V);
     if (c.lane >= c.lanes) return;
     const int w = p.D / p.G;
     for (int pc = c.pc; pc < c.packets; pc += kThreads) {
         const long col = (long)c.g0 * w + pc * V;
         const float2 st = stats[(long)t.seq * p.G + col / w];
-        float wt[V], bs[V];
-        load_weights<V>(p.weight, col, 1.f, wt);
-        load_weights<V>(p.bias, col, 0.f, bs);
+        const Vals<V> wt = load_weights<V>(p.weight, col, 1.f), bs = load_weights<V>(p.bias, col, 0.f);
         const T *x = static_cast<const T *>(p.x) + t.start * p.ld_x + col;
         const T *gate = static_cast<const T *>(p.gate) + t.start * p.ld_gate + col;
         T *y = static_cast<T *>(p.y) + t.start * p.D + col;
+        const Pair minus = both(-st.x);
 #pragma unroll 4
         for (int r = c.lane; r < t.n; r += c.lanes) {
-            float f[V], g[V];
-            unpack<T, V>(load_packet<T, V>(x + r * p.ld_x), f);
-            if (GATE) unpack<T, V>(load_packet<T, V>(gate + r * p.ld_gate), g);
-            forward_packet<V, GATE>(f, g, st.x, st.y, wt, bs, p.act);
-            store_packet<T, V>(y + (long)r * p.D, pack<T, V>(f));
+            Vals<V> f = values<T, V>(load_packet<T, V>(x + r * p.ld_x)), g;
+            if (GATE) g = values<T, V>(load_packet<T, V>(gate + r * p.ld_gate));
+#pragma unroll
+            for (int j = 0; j < Vals<V>::N; ++j) f.p[j] = add2(f.p[j], minus);
+            store_packet<T, V>(y + (long)r * p.D, packet<T, V>(forward_vals<V, GATE>(f, g, st.y, wt, bs, p.act)));
         }
     }
 }
@@ -529,6 +655,7 @@ __global__ void __launch_bounds__(kThreads)
 seq_sums_kernel(GroupNormProblem p, int rows, int per_block, float2 *part, float *params) {
     __shared__ float2 red[kThreads];
     __shared__ float cols[2][kThreads * V];
+    grid_trigger();
     const bool ok = !p.cu || cu_well_formed(p.cu, p.n_seq, (int)p.rows);
     if (!ok && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicExch(p.status, MDN_ERR_INVALID_ARG);
     Tile t;
@@ -540,52 +667,56 @@ seq_sums_kernel(GroupNormProblem p, int rows, int per_block, float2 *part, float
     // whole rounds of packets, for the barriers; one round where lanes > 1
     for (int base = 0; base < c.packets; base += kThreads) {
         const int pc = base + c.pc;
-        float dw[V], db[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) dw[v] = db[v] = 0.f;
+        Vals<V> dw = zeros<V>(), db = zeros<V>();
         if (some && c.lane < c.lanes && pc < c.packets) {
             const long col = (long)c.g0 * w + pc * V;
             const float2 st = reinterpret_cast<const float2 *>(p.stats)[(long)t.seq * p.G + col / w];
-            float wt[V], bs[V];
-            load_weights<V>(p.weight, col, 1.f, wt);
-            load_weights<V>(p.bias, col, 0.f, bs);
+            const Vals<V> wt = load_weights<V>(p.weight, col, 1.f), bs = load_weights<V>(p.bias, col, 0.f);
             const T *x = static_cast<const T *>(p.x) + t.start * p.ld_x + col;
             const T *gate = static_cast<const T *>(p.gate) + t.start * p.ld_gate + col;
             const T *dy = static_cast<const T *>(p.dy) + t.start * p.ld_dy + col;
 #pragma unroll 4
             for (int r = c.lane; r < t.n; r += c.lanes) {
-                float n[V], d[V], g[V];
-                unpack<T, V>(load_packet<T, V>(x + r * p.ld_x), n);
-                unpack<T, V>(load_packet<T, V>(dy + r * p.ld_dy), d);
-                if (GATE) unpack<T, V>(load_packet<T, V>(gate + r * p.ld_gate), g);
-                backward_packet<V, GATE>(n, g, d, st.x, st.y, wt, bs, p.act);
+                Vals<V> n = values<T, V>(load_packet<T, V>(x + r * p.ld_x)), g;
+                Vals<V> d = values<T, V>(load_packet<T, V>(dy + r * p.ld_dy));
+                if (GATE) g = values<T, V>(load_packet<T, V>(gate + r * p.ld_gate));
+                backward_vals<V, GATE>(n, g, d, st.x, st.y, wt, bs, p.act);
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    dw[v] = fmaf(d[v], n[v], dw[v]);
-                    db[v] += d[v];
+                for (int j = 0; j < Vals<V>::N; ++j) {
+                    dw.p[j] = fma2(d.p[j], n.p[j], dw.p[j]);
+                    db.p[j] = add2(db.p[j], d.p[j]);
                 }
             }
             // the groups' sums follow from the columns'
+            Vals<V> a, b;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                s.x = fmaf(db[v], wt[v], s.x);
-                s.y = fmaf(dw[v], wt[v], s.y);
+            for (int j = 0; j < Vals<V>::N; ++j) {
+                a.p[j] = mul2(db.p[j], wt.p[j]);
+                b.p[j] = mul2(dw.p[j], wt.p[j]);
             }
+            s.x += sum_of<V>(a);
+            s.y += sum_of<V>(b);
         }
         if (!out) continue;
+        float fw[2 * Vals<V>::N], fb[2 * Vals<V>::N];
+#pragma unroll
+        for (int j = 0; j < Vals<V>::N; ++j) {
+            split_pair(dw.p[j], fw[2 * j], fw[2 * j + 1]);
+            split_pair(db.p[j], fb[2 * j], fb[2 * j + 1]);
+        }
         if (c.lanes == 1) {
             if (c.lane == 0 && pc < c.packets)
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    out[pc * V + v] = dw[v];
-                    out[p.D + pc * V + v] = db[v];
+                    out[pc * V + v] = fw[v];
+                    out[p.D + pc * V + v] = fb[v];
                 }
             continue;
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            cols[0][threadIdx.x * V + v] = dw[v];
-            cols[1][threadIdx.x * V + v] = db[v];
+            cols[0][threadIdx.x * V + v] = fw[v];
+            cols[1][threadIdx.x * V + v] = fb[v];
         }
         __syncthreads();
         const int n = c.packets * V;
@@ -622,13 +753,16 @@ seq_sums_kernel(GroupNormProblem p, int rows, int per_block, float2 *part, float
 __global__ void __launch_bounds__(kThreads) seq_means_kernel(GroupNormProblem p, int rows, const float2 *part, float2 *means) {
     const long i = blockIdx.x * (long)(kThreads / 32) + (threadIdx.x >> 5);
     const bool ok = !p.cu || cu_well_formed(p.cu, p.n_seq, (int)p.rows);
+    grid_trigger();
+    grid_wait();
     if (!ok || i >= (long)p.n_seq * p.G) return;
     const int s = (int)(i / p.G), g = (int)(i - (long)s * p.G);
     const int len = p.cu ? p.cu[s + 1] - p.cu[s] : p.T, tiles = (len + rows - 1) / rows;
-    const long slot = first_slot(p, rows, s);
+    const float2 *src = part + first_slot(p, rows, s) * p.G + g;
     float2 a = make_float2(0.f, 0.f);
+#pragma unroll 4
     for (int k = threadIdx.x & 31; k < tiles; k += 32) {
-        const float2 v = part[(slot + k) * p.G + g];
+        const float2 v = src[(long)k * p.G];
         a.x += v.x;
         a.y += v.y;
     }
@@ -645,9 +779,11 @@ __global__ void __launch_bounds__(kThreads) seq_means_kernel(GroupNormProblem p,
 
 template <typename T, int V, bool GATE>
 __global__ void __launch_bounds__(kThreads) seq_dx_kernel(GroupNormProblem p, int rows, int per_block, const float2 *means) {
-    if (p.cu && !cu_well_formed(p.cu, p.n_seq, (int)p.rows)) return;
+    const bool ok = !p.cu || cu_well_formed(p.cu, p.n_seq, (int)p.rows);
+    grid_trigger();
+    grid_wait();
     Tile t;
-    if (!tile_of(p, rows, blockIdx.x, t)) return;
+    if (!ok || !tile_of(p, rows, blockIdx.x, t)) return;
     const Columns c = columns_of(p, per_block, V);
     if (c.lane >= c.lanes) return;
     const int w = p.D / p.G;
@@ -655,24 +791,23 @@ __global__ void __launch_bounds__(kThreads) seq_dx_kernel(GroupNormProblem p, in
         const long col = (long)c.g0 * w + pc * V;
         const float2 st = reinterpret_cast<const float2 *>(p.stats)[(long)t.seq * p.G + col / w];
         const float2 m = means[(long)t.seq * p.G + col / w];
-        float wt[V], bs[V];
-        load_weights<V>(p.weight, col, 1.f, wt);
-        load_weights<V>(p.bias, col, 0.f, bs);
+        const Vals<V> wt = load_weights<V>(p.weight, col, 1.f), bs = load_weights<V>(p.bias, col, 0.f);
         const T *x = static_cast<const T *>(p.x) + t.start * p.ld_x + col;
         const T *gate = static_cast<const T *>(p.gate) + t.start * p.ld_gate + col;
         const T *dy = static_cast<const T *>(p.dy) + t.start * p.ld_dy + col;
         T *dx = static_cast<T *>(p.dx) + t.start * p.D + col, *dgate = static_cast<T *>(p.dgate) + t.start * p.D + col;
+        const Pair m1 = both(-m.x), m2 = both(-m.y), rstd = both(st.y);
 #pragma unroll 4
         for (int r = c.lane; r < t.n; r += c.lanes) {
-            float n[V], d[V], g[V];
-            unpack<T, V>(load_packet<T, V>(x + r * p.ld_x), n);
-            unpack<T, V>(load_packet<T, V>(dy + r * p.ld_dy), d);
-            if (GATE) unpack<T, V>(load_packet<T, V>(gate + r * p.ld_gate), g);
-            backward_packet<V, GATE>(n, g, d, st.x, st.y, wt, bs, p.act);
-            if (GATE) store_packet<T, V>(dgate + (long)r * p.D, pack<T, V>(g));
+            Vals<V> n = values<T, V>(load_packet<T, V>(x + r * p.ld_x)), g;
+            Vals<V> d = values<T, V>(load_packet<T, V>(dy + r * p.ld_dy));
+            if (GATE) g = values<T, V>(load_packet<T, V>(gate + r * p.ld_gate));
+            backward_vals<V, GATE>(n, g, d, st.x, st.y, wt, bs, p.act);
+            if (GATE) store_packet<T, V>(dgate + (long)r * p.D, packet<T, V>(g));
 #pragma unroll
-            for (int v = 0; v < V; ++v) n[v] = st.y * (fmaf(d[v], wt[v], -m.x) - n[v] * m.y);
-            store_packet<T, V>(dx + (long)r * p.D, pack<T, V>(n));
+            for (int j = 0; j < Vals<V>::N; ++j)
+                n.p[j] = mul2(rstd, fma2(n.p[j], m2, fma2(d.p[j], wt.p[j], m1)));
+            store_packet<T, V>(dx + (long)r * p.D, packet<T, V>(n));
         }
     }
 }
@@ -728,9 +863,8 @@ TokenShape token_shape(const GroupNormProblem &p, int V, int per_sm) {
 
 // The gradient's blocks: each lane of tokens leaves a row of the parameters'
 // sums behind, which are read again.
-constexpr int kFwdPerSM = 8, kBwdPerSM = 4;
+constexpr int kFwdPerSM = 8, kBwdPerSM = 3;
 long token_lanes_most(long rows, int D, int G) {
-    // for any packet width: at most 152 * 4 * 256 threads, and one unit more
     const long w = D / G;
     long most = 0;
     for (int V : {8, 4, 2, 1}) {
@@ -777,8 +911,7 @@ cudaError_t token_pick(const GroupNormProblem &p, const TokenShape &t, float *pa
 
 cudaError_t params(const GroupNormProblem &p, const float *part, long lanes, cudaStream_t st) {
     if (!p.dw && !p.dbias) return cudaSuccess;
-    param_kernel<<<(2 * p.D + 31) / 32, kThreads, 0, st>>>(part, (int)lanes, p.D, p.dw, p.dbias);
-    return cudaGetLastError();
+    return follow(param_kernel, dim3((2 * p.D + 31) / 32), 1024, st, part, (int)lanes, p.D, p.dw, p.dbias);
 }
 
 template <typename T, int V, bool GATE>
@@ -804,15 +937,15 @@ cudaError_t run(const GroupNormProblem &p, bool bwd, cudaStream_t st) {
     if (!bwd) {
         float2 *stats = p.stats ? reinterpret_cast<float2 *>(p.stats) : second;
         seq_stats_kernel<T, V><<<grid, kThreads, 0, st>>>(p, rows, gpb, part);
-        seq_join_kernel<<<joins, kThreads, 0, st>>>(p, rows, part, stats);
-        seq_apply_kernel<T, V, GATE><<<grid, kThreads, 0, st>>>(p, rows, gpb, stats);
-        return cudaGetLastError();
+        if ((err = cudaGetLastError()) != cudaSuccess) return err;
+        if ((err = follow(seq_join_kernel, dim3(joins), kThreads, st, p, rows, part, stats)) != cudaSuccess) return err;
+        return follow(seq_apply_kernel<T, V, GATE>, grid, kThreads, st, p, rows, gpb, stats);
     }
     float *prm = p.dw || p.dbias ? reinterpret_cast<float *>(ws) : nullptr;
     seq_sums_kernel<T, V, GATE><<<grid, kThreads, 0, st>>>(p, rows, gpb, part, prm);
-    seq_means_kernel<<<joins, kThreads, 0, st>>>(p, rows, part, second);
-    seq_dx_kernel<T, V, GATE><<<grid, kThreads, 0, st>>>(p, rows, gpb, second);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    if ((err = follow(seq_means_kernel, dim3(joins), kThreads, st, p, rows, part, second)) != cudaSuccess) return err;
+    if ((err = follow(seq_dx_kernel<T, V, GATE>, grid, kThreads, st, p, rows, gpb, second)) != cudaSuccess) return err;
     return params(p, prm, slots, st);
 }
 
