@@ -1,13 +1,6 @@
-// Linear attention with a decay for each head, in chunks of 64 tokens, on the
-// CUDA cores: fp32 rows, any head widths up to 128, any alignment.  (The passes and their roles: mdn_attn.cuh.)
-//
-// Per chunk of n tokens with the state Z before it:
-//   A_ij  = l^(i-j) w_scale X_i . Y_j  (j <= i, else 0)
-//   out   = out_scale (A W + diag(l^(i+1)) X Z)
-//   Z     = l^n Z + (diag(w_scale l^(n-1-j)) Y)^T W
-// One block takes a run of a sequence's tokens, one head and 64 columns of W;
-// every matrix is staged in shared memory in fp32 and multiplied in 4 x 4
-// register tiles.
+// Linear attention with a decay for each head: how sequences are cut and laid
+// out, the segments' states joined, shared heads' gradients summed.  (The passes
+// and their roles: mdn_attn.cuh; their kernels: mdn_attn_tc.cu, mdn_attn_tc32.cu.)
 #include "mdn_attn.cuh"
 
 namespace mdn {
@@ -40,10 +33,6 @@ long attn_slots(int n_seq, long T_total, int seg) {
 }
 
 namespace {
-
-constexpr int kC = 64;              // tokens of a chunk
-constexpr int kV = 64;              // columns of W a block takes
-constexpr int kPitch = kV + 4;
 
 // Packed sequences: every sequence's slots, and the items, longest first.
 __global__ void __launch_bounds__(1024) attn_layout_kernel(AttnProblem p) {
@@ -118,191 +107,6 @@ __global__ void __launch_bounds__(1024) attn_layout_kernel(AttnProblem p) {
     for (int i = base + tid; i < p.slots; i += 1024) p.items[i].slot = -1;
 }
 
-__global__ void __launch_bounds__(256) attn_kernel(AttnProblem p) {
-    extern __shared__ __align__(16) float smem[];
-    __shared__ float lam[kC + 1];
-    const AttnPass &a = p.pass[blockIdx.y];
-    const int h = blockIdx.x % p.H, c0 = blockIdx.z * kV;
-    AttnItem it;
-    if (!attn_item(p, blockIdx.x / p.H, it, reinterpret_cast<int *>(smem)) || c0 >= a.vd) return;
-    const bool states_only = a.out == nullptr;
-    const bool closes = a.reversed ? it.first : it.last;      // the sequence's last run in the pass's order
-    if (states_only && closes) return;                        // no run starts from that state
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int KR = (a.kd + 7) & ~7, KS = KR + 4, cols = min(kV, a.vd - c0);
-    float *Xs = smem, *Ys = Xs + kC * KS, *Ws = Ys + kC * KS, *As = Ws + kC * kPitch, *Zs = As + kC * kPitch;
-    const float l2 = log2_decay(p.log_decay, h);
-    if (tid <= kC) lam[tid] = exp2f((float)tid * l2);
-
-    // the state: rows 8 ty .., columns 4 tx ..
-    float z[8][4];
-    {
-        const bool opens = a.reversed ? it.last : it.first;
-        const float *src = nullptr;
-        if (!states_only) {
-            if (a.seg_init) src = a.seg_init + ((long)it.slot * p.H + h) * a.kd * a.vd;
-            else if (a.init && opens) src = a.init + ((long)it.seq * p.H + h) * a.kd * a.vd;
-        }
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int k = ty * 8 + r, col = c0 + tx * 4 + c;
-                z[r][c] = src && k < a.kd && col < a.vd
-                              ? src[a.init_t ? (long)col * a.kd + k : (long)k * a.vd + col] : 0.f;
-            }
-    }
-    auto put_state = [&]() {
-        if (ty * 8 < KR)
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-                *reinterpret_cast<float4 *>(Zs + (ty * 8 + r) * kPitch + tx * 4) = make_float4(z[r][0], z[r][1], z[r][2], z[r][3]);
-    };
-    put_state();
-
-    const float *X = static_cast<const float *>(a.X) + (long)(h / a.sx) * a.kd;
-    const float *Y = static_cast<const float *>(a.Y) + (long)(h / a.sy) * a.kd;
-    const float *W = static_cast<const float *>(a.W) + (long)(h / a.sw) * a.vd + c0;
-    const int chunks = (it.len + kC - 1) / kC;
-    for (int c = 0; c < chunks; ++c) {
-        const int at = (a.reversed ? chunks - 1 - c : c) * kC, n = min(kC, it.len - at);
-        const long t0 = it.start + at;
-        __syncthreads();                                      // the last chunk's readers are done
-        for (int i = tid; i < kC * KR; i += 256) {
-            const int r = i / KR, k = i - r * KR;
-            const bool in = r < n && k < a.kd;
-            if (!states_only) Xs[r * KS + k] = in ? X[(t0 + r) * a.ld_x + k] : 0.f;
-            Ys[r * KS + k] = in ? Y[(t0 + r) * a.ld_y + k] : 0.f;
-        }
-        for (int i = tid; i < kC * kV; i += 256) {
-            const int r = i / kV, k = i - r * kV;
-            Ws[r * kPitch + k] = r < n && k < cols ? W[(t0 + r) * a.ld_w + k] * a.w_scale : 0.f;
-        }
-        __syncthreads();
-        if (!states_only) {
-            float s[4][4] = {};
-            for (int k = 0; k < KR; k += 4) {
-                float4 x[4], y[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    x[r] = *reinterpret_cast<const float4 *>(Xs + (ty + 16 * r) * KS + k);
-                    y[r] = *reinterpret_cast<const float4 *>(Ys + (tx + 16 * r) * KS + k);
-                }
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        s[r][q] = fmaf(x[r].x, y[q].x, s[r][q]);
-                        s[r][q] = fmaf(x[r].y, y[q].y, s[r][q]);
-                        s[r][q] = fmaf(x[r].z, y[q].z, s[r][q]);
-                        s[r][q] = fmaf(x[r].w, y[q].w, s[r][q]);
-                    }
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int i = ty + 16 * r, j = tx + 16 * q, e = a.reversed ? j - i : i - j;
-                    As[i * kPitch + j] = e < 0 ? 0.f : s[r][q] * lam[e];
-                }
-            __syncthreads();
-            float o[4][4] = {};
-            for (int k = 0; k < KR; k += 4) {
-                float4 x[4], zr[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    x[r] = *reinterpret_cast<const float4 *>(Xs + (ty + 16 * r) * KS + k);
-                    zr[r] = *reinterpret_cast<const float4 *>(Zs + (k + r) * kPitch + tx * 4);
-                }
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float xs[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        o[r][0] = fmaf(xs[q], zr[q].x, o[r][0]);
-                        o[r][1] = fmaf(xs[q], zr[q].y, o[r][1]);
-                        o[r][2] = fmaf(xs[q], zr[q].z, o[r][2]);
-                        o[r][3] = fmaf(xs[q], zr[q].w, o[r][3]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = ty + 16 * r;
-                const float f = i < n ? lam[a.reversed ? n - 1 - i : i + 1] : 0.f;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) o[r][q] *= f;
-            }
-            for (int j = 0; j < n; j += 4) {
-                float4 s4[4], w[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    s4[r] = *reinterpret_cast<const float4 *>(As + (ty + 16 * r) * kPitch + j);
-                    w[r] = *reinterpret_cast<const float4 *>(Ws + (j + r) * kPitch + tx * 4);
-                }
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float sr[4] = {s4[r].x, s4[r].y, s4[r].z, s4[r].w};
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        o[r][0] = fmaf(sr[q], w[q].x, o[r][0]);
-                        o[r][1] = fmaf(sr[q], w[q].y, o[r][1]);
-                        o[r][2] = fmaf(sr[q], w[q].z, o[r][2]);
-                        o[r][3] = fmaf(sr[q], w[q].w, o[r][3]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = ty + 16 * r;
-                if (i >= n) continue;
-                const long row = ((t0 + i) * p.H + h) * a.vd + c0;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int col = tx * 4 + q;
-                    if (col >= cols) continue;
-                    static_cast<float *>(a.out)[row + col] = o[r][q] * a.out_scale;
-                }
-            }
-        }
-        if (ty * 8 < KR) {
-            const float f = lam[n];
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) z[r][q] *= f;
-            for (int j = 0; j < n; ++j) {
-                const float d = lam[a.reversed ? j + 1 : n - 1 - j];
-                float4 w = *reinterpret_cast<const float4 *>(Ws + j * kPitch + tx * 4);
-                w.x *= d; w.y *= d; w.z *= d; w.w *= d;
-                const float4 y0 = *reinterpret_cast<const float4 *>(Ys + j * KS + ty * 8);
-                const float4 y1 = *reinterpret_cast<const float4 *>(Ys + j * KS + ty * 8 + 4);
-                const float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
-#pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    z[r][0] = fmaf(y[r], w.x, z[r][0]);
-                    z[r][1] = fmaf(y[r], w.y, z[r][1]);
-                    z[r][2] = fmaf(y[r], w.z, z[r][2]);
-                    z[r][3] = fmaf(y[r], w.w, z[r][3]);
-                }
-            }
-        }
-        __syncthreads();                                      // Zs has been read
-        put_state();
-    }
-    float *dst = nullptr;
-    if (states_only) dst = a.seg_out + ((long)it.slot * p.H + h) * a.kd * a.vd;
-    else if (a.fin && closes) dst = a.fin + ((long)it.seq * p.H + h) * a.kd * a.vd;
-    if (!dst) return;
-#pragma unroll
-    for (int r = 0; r < 8; ++r)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int k = ty * 8 + r, col = c0 + tx * 4 + c;
-            if (k < a.kd && col < a.vd) dst[(long)k * a.vd + col] = z[r][c];
-        }
-}
-
 // Four neighbouring elements of a state a thread, along the segments of their
 // sequence, eight of which it asks for at a time.  One thread of a block works
 // out the decays: 64 x 64 blocks of which every warp reads the head's own make
@@ -375,11 +179,6 @@ __global__ void __launch_bounds__(256) attn_reduce_kernel(const float *part, T *
     }
 }
 
-int attn_smem(int kd) {
-    const int KR = (kd + 7) & ~7, KS = KR + 4;
-    return (2 * kC * KS + 2 * kC * kPitch + KR * kPitch) * (int)sizeof(float);
-}
-
 }  // namespace
 
 cudaError_t launch_attn_layout(const AttnProblem &p, cudaStream_t st) {
@@ -389,18 +188,7 @@ cudaError_t launch_attn_layout(const AttnProblem &p, cudaStream_t st) {
 
 cudaError_t launch_attn(const AttnProblem &p, cudaStream_t st) {
     if (p.slots == 0) return cudaSuccess;
-    if (p.dtype == MDN_BF16) return launch_attn_tc(p, st);
-    int kd = 0, vd = 0;
-    for (int i = 0; i < p.n_pass; ++i) {
-        kd = kd > p.pass[i].kd ? kd : p.pass[i].kd;
-        vd = vd > p.pass[i].vd ? vd : p.pass[i].vd;
-    }
-    const dim3 grid((unsigned)(p.slots * (long)p.H), p.n_pass, (vd + kV - 1) / kV);
-    const int smem = attn_smem(kd);
-    const cudaError_t err = allow_shared<attn_kernel>(attn_smem(128));
-    if (err != cudaSuccess) return err;
-    attn_kernel<<<grid, 256, smem, st>>>(p);
-    return cudaGetLastError();
+    return p.dtype == MDN_BF16 ? launch_attn_tc(p, st) : launch_attn_tc32(p, st);
 }
 
 cudaError_t launch_attn_combine(const AttnProblem &p, const AttnCombine &c, cudaStream_t st) {

@@ -94,9 +94,9 @@ int attn_segment(int n_seq, long T_total, int H, int passes);
 long attn_slots(int n_seq, long T_total, int seg);
 
 cudaError_t launch_attn_layout(const AttnProblem &p, cudaStream_t st);
-// fp32 rows on the CUDA cores, bf16 rows on the tensor cores.
 cudaError_t launch_attn(const AttnProblem &p, cudaStream_t st);
-cudaError_t launch_attn_tc(const AttnProblem &p, cudaStream_t st);
+cudaError_t launch_attn_tc(const AttnProblem &p, cudaStream_t st);      // bf16 rows
+cudaError_t launch_attn_tc32(const AttnProblem &p, cudaStream_t st);    // fp32 rows
 // Turns the segments' own states into the states they start from.
 cudaError_t launch_attn_combine(const AttnProblem &p, const AttnCombine &c, cudaStream_t st);
 // out [tokens, H / shared, d] <- sums over the heads that share, of fp32 rows.

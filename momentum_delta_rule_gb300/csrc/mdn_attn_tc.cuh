@@ -1,0 +1,87 @@
+// What the tensor-core kernels of linear attention share (mdn_attn_tc.cu: bf16
+// rows, mdn_attn_tc32.cu: fp32 rows).
+#pragma once
+
+#include "mdn_attn.cuh"
+#include "mdn_sm100.cuh"
+
+namespace mdn {
+namespace attn_tc {
+
+using namespace sm100;
+
+constexpr int kC = 64;                            // tokens of a chunk
+constexpr uint32_t kBlock = 8192;                 // 64 tokens x 64 columns, swizzled
+constexpr uint32_t kTile = 2 * kBlock;            // 64 tokens x 128 columns
+
+// mbar_wait for a whole warp.  Most of a CTA's warps wait at any time, and a try
+// ends unsuccessful after some 270 cycles whatever its time limit, so what is
+// done between tries counts: nothing but counting to 1024 here.  (With the look
+// at the flag and the clock each time, the kernel issued 8600 instructions a
+// chunk.)
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    const uint32_t at = smem_u32(bar);
+    uint64_t t0 = 0;
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\t"
+            "mov.u32 n, 1024;\n"
+            "again:\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "@p bra done;\n\t"
+            "sub.u32 n, n, 1;\n\t"
+            "setp.ne.u32 p, n, 0;\n\t"
+            "@p bra again;\n"
+            "done:\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(at), "r"(parity), "r"(1000000u)
+            : "memory");
+        if (__all_sync(0xffffffffu, ok)) return true;
+        if (t0 == 0) t0 = globaltimer();
+        bool over = *abort != 0;
+        if (!over && globaltimer() - t0 > kWaitLimitNs) {
+            *abort = 1;
+            over = true;
+        }
+        if (__any_sync(0xffffffffu, over)) return false;
+    }
+}
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], bf16 x bf16 -> fp32; A: two neighbouring K of
+// a row in each 32-bit column.
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// True in one lane of the warp.  Unlike a comparison of the lane's number it
+// tells the compiler so, which then issues an MMA's operands as they are and not
+// lane by lane: 43 to 106 cycles an MMA of the shapes here instead of 107.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&v);
+}
+
+}  // namespace attn_tc
+}  // namespace mdn

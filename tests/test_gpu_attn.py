@@ -14,7 +14,8 @@ evaluation's own error.  That is
   * operands that are not fp32: bf16 rows round q k^T with its decay to bf16, or
     the state, of which each term passes one: half a step, 2^-8 m.  The states
     themselves are sums of products with v (or do) times a decay, as two bf16
-    parts: 2^-17 m.
+    parts: 2^-17 m.  (fp32 rows are products of three bf16 parts each, which
+    leave out less than a rounding in fp32.)
 """
 import numpy as np
 import pytest
