@@ -7,19 +7,23 @@ namespace mdn {
 
 // A segment's states cost a second reading of Y and W and their own products,
 // so sequences are cut only where whole ones leave multiprocessors idle.  In
-// units of the time a block takes for a chunk: the blocks of a launch run in
-// waves of 152, each of which fills its pipeline once (2.5); a chunk's states
-// alone take 0.45, and the two launches more that segments need 5.
-int attn_segment(int n_seq, long T_total, int H, int passes) {
+// units of the time a block takes for a chunk (1.7 us for bf16 rows, 6 for fp32):
+// the blocks of a launch run in waves of 152, each of which fills its pipeline
+// once; a chunk's states alone take 0.55, a segment reads the states of those
+// before it, and the launch more costs what it costs.
+int attn_segment(int n_seq, long T_total, int H, int passes, mdn_dtype dtype) {
     if (n_seq == 0 || T_total == 0) return 0;
+    const bool wide = dtype == MDN_F32;
+    const double fill = wide ? 0.5 : 2.5, more = wide ? 1.0 : 3.0, read = wide ? 0.1 : 0.3;
     const long lines = (long)n_seq * H, mean = (T_total + n_seq - 1) / n_seq, chunks = (mean + 63) / 64;
     auto waves = [](long blocks) { return (blocks + 151) / 152; };
     const int states = passes > 1 ? 2 : 1;
-    double best = waves(lines * passes) * (chunks + 2.5);
+    double best = waves(lines * passes) * (chunks + fill);
     long best_chunks = 0;
-    for (long parts = 2; parts <= 64 && parts * 4 <= chunks; ++parts) {
+    for (long parts = 2; parts <= 64 && parts <= chunks; ++parts) {
         const long per = (chunks + parts - 1) / parts, n = (chunks + per - 1) / per;
-        const double t = waves(lines * states * (n - 1)) * (per * 0.45 + 2.5) + 5 + waves(lines * passes * n) * (per + 2.5);
+        const double t = waves(lines * states * (n - 1)) * (per * 0.55 + fill) + more +
+                         waves(lines * passes * n) * (per + fill + read * n);
         if (t < best) {
             best = t;
             best_chunks = per;
@@ -93,9 +97,10 @@ __global__ void __launch_bounds__(1024) attn_layout_kernel(AttnProblem p) {
                 it.len = p.seg ? min(p.seg, len - k * p.seg) : len;
                 it.seq = s;
                 it.slot = at + k;
-                it.first = k == 0;
-                it.last = k == n - 1;
-                it.pad0 = it.pad1 = 0;
+                it.k = k;
+                it.n = n;
+                it.tail = len - (n - 1) * p.seg;
+                it.pad = 0;
                 p.items[place + k] = it;
             }
         }
@@ -107,16 +112,19 @@ __global__ void __launch_bounds__(1024) attn_layout_kernel(AttnProblem p) {
     for (int i = base + tid; i < p.slots; i += 1024) p.items[i].slot = -1;
 }
 
-// Four neighbouring elements of a state a thread, along the segments of their
-// sequence, eight of which it asks for at a time.  One thread of a block works
-// out the decays: 64 x 64 blocks of which every warp reads the head's own make
-// the one sector that holds them the bottleneck (107 us instead of 8).
+// Turns the segments' own states into the states they start from: V neighbouring
+// elements of a state a thread, eight segments asked for at a time.  One thread
+// of a block works out the decays: thousands of blocks of which every warp reads
+// the head's own make the one sector that holds them the bottleneck (107 us
+// instead of 8).
 template <int V>
-__global__ void __launch_bounds__(256) attn_combine_kernel(AttnProblem p, AttnCombine c) {
+__global__ void __launch_bounds__(256) attn_combine_kernel(AttnProblem p, float *seg0, float *seg1, int size) {
     __shared__ float full, tail;
     __shared__ int s_n, s_off;
     const int s = blockIdx.x / p.H, h = blockIdx.x % p.H;
     const bool reversed = blockIdx.z != 0;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (threadIdx.x == 0) {
         int off, n;
         long len;
@@ -137,20 +145,16 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(AttnProblem p, AttnCo
     }
     __syncthreads();
     const int e = (blockIdx.y * 256 + threadIdx.x) * V, n = s_n;
-    if (e >= c.size) return;
+    if (e >= size) return;
     const float f = full;
-    const float *init = c.init[reversed];
-    const long stride = (long)p.H * c.size, step = reversed ? -stride : stride;
-    float *at = c.seg[reversed] + ((long)s_off * p.H + h) * c.size + e + (reversed ? (n - 1) * stride : 0);
-    Packet<float, V> z;
-#pragma unroll
-    for (int v = 0; v < V; ++v) z.e[v] = 0.f;
-    if (init) z = load_packet<float, V>(init + ((long)s * p.H + h) * c.size + e);
+    const long stride = (long)p.H * size, step = reversed ? -stride : stride;
+    float *at = (reversed ? seg1 : seg0) + ((long)s_off * p.H + h) * size + e + (reversed ? (n - 1) * stride : 0);
+    Packet<float, V> z = load_packet<float, V>(at + (n - 1) * step);       // (attn_keep_initial)
     for (int k0 = 0; k0 < n; k0 += 8) {
         Packet<float, V> own[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            if (k0 + k < n - 1) own[k] = load_packet<float, V>(at + k * step);    // the last one's leads nowhere
+            if (k0 + k < n - 1) own[k] = load_packet<float, V>(at + k * step);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             if (k0 + k < n) {
@@ -191,12 +195,19 @@ cudaError_t launch_attn(const AttnProblem &p, cudaStream_t st) {
     return p.dtype == MDN_BF16 ? launch_attn_tc(p, st) : launch_attn_tc32(p, st);
 }
 
-cudaError_t launch_attn_combine(const AttnProblem &p, const AttnCombine &c, cudaStream_t st) {
-    const int V = c.size % 4 ? 1 : 4;
-    const dim3 grid((unsigned)((long)p.n_seq * p.H), (c.size / V + 255) / 256, c.seg[1] ? 2 : 1);
-    if (V == 4) attn_combine_kernel<4><<<grid, 256, 0, st>>>(p, c);
-    else attn_combine_kernel<1><<<grid, 256, 0, st>>>(p, c);
-    return cudaGetLastError();
+cudaError_t launch_attn_combine(const AttnProblem &p, float *seg, float *seg_reversed, int size, cudaStream_t st) {
+    const int V = size % 4 ? 1 : 4;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((long)p.n_seq * p.H), (size / V + 255) / 256, seg_reversed ? 2 : 1);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return V == 4 ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<4>, p, seg, seg_reversed, size)
+                  : cudaLaunchKernelEx(&cfg, attn_combine_kernel<1>, p, seg, seg_reversed, size);
 }
 
 cudaError_t launch_attn_reduce(const AttnProblem &p, const float *part, void *out, int d, int shared, cudaStream_t st) {

@@ -27,7 +27,8 @@ struct AttnPass {
     void *out;                      // [tokens, H, vd], dense; or nullptr (states only)
     bool out_f32;                   // fp32 whatever the dtype
     const float *init;              // [n_seq, H, ...] states the sequences start from, or nullptr
-    const float *seg_init;          // [slot, H, ...] states the segments start from, or nullptr
+    const float *seg_init;          // [slot, H, ...] the segments' own states, or nullptr
+    bool combined;                  // ... or already the states they start from
     bool init_t;                    // those lie transposed, [vd, kd]
     float *fin;                     // [n_seq, H, kd, vd] or nullptr
     float *seg_out;                 // states only: [slot, H, kd, vd] of the segments alone
@@ -35,7 +36,13 @@ struct AttnPass {
 
 // A run of tokens of one sequence that one block takes.
 struct AttnItem {
-    int start, len, seq, slot, first, last, pad0, pad1;
+    int start, len, seq, slot;
+    int k, n;                       // which segment of the sequence, of how many
+    int tail;                       // tokens of the last one
+    int pad;
+
+    __host__ __device__ bool first() const { return k == 0; }
+    __host__ __device__ bool last() const { return k == n - 1; }
 };
 
 struct AttnProblem {
@@ -50,14 +57,6 @@ struct AttnProblem {
     int32_t *seg_off;               // packed: [n_seq + 1] slots of the sequences; [n_seq + 1] more: whether cu is well formed
     mdn_dtype dtype;
     int *status;
-};
-
-// Segments' states [slot, H, size] in both directions ([1]: reversed, or
-// nullptr), and the states their sequences start from.
-struct AttnCombine {
-    float *seg[2];
-    const float *init[2];
-    int size;
 };
 
 struct AttnStepProblem {
@@ -88,17 +87,17 @@ struct GroupNormProblem {
     int *status;
 };
 
-// Tokens of a segment for `lines` sequences times heads (0: none), and the most
-// slots they take.
-int attn_segment(int n_seq, long T_total, int H, int passes);
+// Tokens of a segment (0: none), and the most slots they take.
+int attn_segment(int n_seq, long T_total, int H, int passes, mdn_dtype dtype);
 long attn_slots(int n_seq, long T_total, int seg);
 
 cudaError_t launch_attn_layout(const AttnProblem &p, cudaStream_t st);
 cudaError_t launch_attn(const AttnProblem &p, cudaStream_t st);
 cudaError_t launch_attn_tc(const AttnProblem &p, cudaStream_t st);      // bf16 rows
 cudaError_t launch_attn_tc32(const AttnProblem &p, cudaStream_t st);    // fp32 rows
-// Turns the segments' own states into the states they start from.
-cudaError_t launch_attn_combine(const AttnProblem &p, const AttnCombine &c, cudaStream_t st);
+// Segments' own states [slot, H, size] (the second: reversed, or nullptr) -> the
+// states they start from.
+cudaError_t launch_attn_combine(const AttnProblem &p, float *seg, float *seg_reversed, int size, cudaStream_t st);
 // out [tokens, H / shared, d] <- sums over the heads that share, of fp32 rows.
 cudaError_t launch_attn_reduce(const AttnProblem &p, const float *part, void *out, int d, int shared,
                                cudaStream_t st);
@@ -157,7 +156,9 @@ __device__ __forceinline__ bool attn_item(const AttnProblem &p, int i, AttnItem 
         it.start = scratch[0];
         it.len = scratch[1];
         it.seq = it.slot = scratch[2];
-        it.first = it.last = 1;
+        it.k = 0;
+        it.n = 1;
+        it.tail = it.len;
         __syncthreads();
         return true;
     }
@@ -167,9 +168,49 @@ __device__ __forceinline__ bool attn_item(const AttnProblem &p, int i, AttnItem 
     it.slot = i;
     it.start = s * p.T + k * p.seg;
     it.len = p.seg ? min(p.seg, p.T - k * p.seg) : p.T;
-    it.first = k == 0;
-    it.last = k == per - 1;
+    it.k = k;
+    it.n = per;
+    it.tail = p.T - (per - 1) * p.seg;
     return true;
+}
+
+// Where sequences are cut, the last segment of a pass's order leaves no state to
+// another: its place keeps the state that its sequence starts from, which may
+// be overwritten by the time a later block asks for it (final states may replace
+// the initial ones).
+__device__ __forceinline__ void attn_keep_initial(const AttnProblem &p, const AttnPass &a, const AttnItem &it, int h) {
+    const long size = (long)a.kd * a.vd;
+    const float *src = a.init ? a.init + ((long)it.seq * p.H + h) * size : nullptr;
+    float *dst = a.seg_out + ((long)it.slot * p.H + h) * size;
+    for (int i = threadIdx.x; i < size; i += blockDim.x) dst[i] = src ? src[i] : 0.f;
+}
+
+// The state a run of tokens starts from: elements [0, N) of a thread, `step`
+// apart from element `at` of a state [kd, vd] or its transpose on, of which `take`
+// are there.  Where sequences are cut: the sequence's initial state and the
+// segments' own ones before this run's (behind it, reversed), in their order,
+// unless a kernel of its own has joined them.
+template <int N>
+__device__ __forceinline__ void attn_initial(const AttnProblem &p, const AttnPass &a, const AttnItem &it, int h, long at, long step,
+                                             int take, float *z) {
+    const long size = (long)a.kd * a.vd, next = (a.reversed ? -1 : 1) * (long)p.H * size;
+    const int before = a.reversed ? it.n - 1 - it.k : it.k;      // segments of the sequence
+    const float *src = nullptr;
+    if (a.out != nullptr && a.seg_init)
+        src = a.seg_init + ((long)(a.combined ? it.slot : a.reversed ? it.slot - it.k : it.slot + (it.n - 1 - it.k)) * p.H + h) * size + at;
+    else if (a.out != nullptr && a.init)
+        src = a.init + ((long)it.seq * p.H + h) * size + at;
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = src && i < take ? src[i * step] : 0.f;
+    if (a.out == nullptr || !a.seg_init || a.combined) return;
+    const float l2 = log2_decay(p.log_decay, h), full = exp2f((float)p.seg * l2), tail = exp2f((float)it.tail * l2);
+    src = a.seg_init + ((long)(a.reversed ? it.slot + before : it.slot - before) * p.H + h) * size + at;
+    for (int j = 0; j < before; ++j, src += next) {
+        const float f = a.reversed && j == 0 ? tail : full;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < take) z[i] = fmaf(f, z[i], src[i * step]);
+    }
 }
 
 }  // namespace mdn

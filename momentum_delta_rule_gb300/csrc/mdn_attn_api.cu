@@ -26,10 +26,10 @@ struct Space {
     int seg = 0;
     long slots = 0;
 };
-Space space(const Heads &s, bool bwd) {
+Space space(const Heads &s, mdn_dtype dtype, bool bwd) {
     Space w;
     if (s.L == 0) return w;
-    w.seg = attn_segment(s.n_seq, s.L, s.H, bwd ? 3 : 1);
+    w.seg = attn_segment(s.n_seq, s.L, s.H, bwd ? 3 : 1, dtype);
     w.slots = attn_slots(s.n_seq, s.L, w.seg);
     auto take = [&](size_t bytes) {
         const size_t at = w.total;
@@ -48,6 +48,12 @@ Space space(const Heads &s, bool bwd) {
     }
     return w;
 }
+
+// Whether a kernel of its own joins the segments' states, rather than each block
+// those before its own: blocks read a state in 2.5 us, the kernel takes 8 and its
+// launch 2.  (16 heads of 128 over 16384 tokens in 9 segments: 102 us and 92; 64
+// over 2048 tokens in 2: 151 and 163.)
+bool many_segments(const Space &w, int n_seq, long L) { return L / n_seq > 3L * w.seg; }
 
 AttnProblem problem(const Heads &s, const Space &w, const float *log_decay, const int32_t *cu, int T, mdn_dtype dtype,
                     int *status, unsigned char *ws) {
@@ -83,7 +89,7 @@ static size_t attn_workspace(int n_seq, int T_total, int H, int Hkv, int dk, int
     if (n_seq < 0 || T_total < 0 || !heads_ok(H, Hkv, dk, dv) || !valid_dtype(dtype) ||
         !heads_small(n_seq, T_total, H, dk, dv))
         return 0;
-    return space(Heads{n_seq, T_total, H, Hkv, dk, dv}, bwd).total;
+    return space(Heads{n_seq, T_total, H, Hkv, dk, dv}, dtype, bwd).total;
 }
 size_t mdn_linear_attn_fwd_workspace_size(int n_seq, int T_total, int H, int Hkv, int dk, int dv, mdn_dtype dtype) {
     return attn_workspace(n_seq, T_total, H, Hkv, dk, dv, dtype, false);
@@ -108,7 +114,7 @@ mdn_status mdn_linear_attn_fwd(const void *q, const void *k, const void *v, cons
              .out(o, el, some).out(S_T, sa, false, S0).ok())
         return MDN_ERR_INVALID_ARG;
     const Heads s{n_seq, L, H, Hkv, dk, dv};
-    const Space w = space(s, false);
+    const Space w = space(s, dtype, false);
     if (!workspace_ok(workspace, workspace_bytes, w.total)) return MDN_ERR_INVALID_ARG;
     int *status = nullptr;
     const mdn_status st = current_device_status(&status);
@@ -127,10 +133,12 @@ mdn_status mdn_linear_attn_fwd(const void *q, const void *k, const void *v, cons
     if (p.items) err = launch_attn_layout(p, cs);
     if (w.seg && err == cudaSuccess) {
         a.seg_out = reinterpret_cast<float *>(ws + w.states);
+        a.init = S0;
         p.pass[0] = a;
         p.n_pass = 1;
         err = launch_attn(p, cs);
-        if (err == cudaSuccess) err = launch_attn_combine(p, AttnCombine{{a.seg_out, nullptr}, {S0, nullptr}, dk * dv}, cs);
+        a.combined = many_segments(w, n_seq, L);
+        if (a.combined && err == cudaSuccess) err = launch_attn_combine(p, a.seg_out, nullptr, dk * dv, cs);
         a.seg_init = a.seg_out;
         a.seg_out = nullptr;
     }
@@ -161,7 +169,7 @@ mdn_status mdn_linear_attn_bwd(const void *q, const void *k, const void *v, cons
              .out(dS0, sa, false).ok())
         return MDN_ERR_INVALID_ARG;
     const Heads s{n_seq, L, H, Hkv, dk, dv};
-    const Space w = space(s, true);
+    const Space w = space(s, dtype, true);
     if (!workspace_ok(workspace, workspace_bytes, w.total)) return MDN_ERR_INVALID_ARG;
     int *status = nullptr;
     const mdn_status st = current_device_status(&status);
@@ -171,7 +179,7 @@ mdn_status mdn_linear_attn_bwd(const void *q, const void *k, const void *v, cons
     if (!some && !dS0) return MDN_OK;
     AttnProblem p = problem(s, w, log_decay, cu_seqlens, T, dtype, status, ws);
     const int shared = H / Hkv;
-    // the states that segments start from: S, and dS at their ends
+    // the segments' own states: S, and dS at their ends
     AttnPass fwd = {}, rev = {};
     fwd.Y = k; fwd.W = v;
     fwd.ld_y = ld_k; fwd.ld_w = ld_v;
@@ -187,15 +195,18 @@ mdn_status mdn_linear_attn_bwd(const void *q, const void *k, const void *v, cons
     cudaError_t err = cudaSuccess;
     if (p.items) err = launch_attn_layout(p, cs);
     const float *seg_S = nullptr, *seg_dS = nullptr;
+    bool combined = false;
     if (w.seg && err == cudaSuccess) {
         fwd.seg_out = reinterpret_cast<float *>(ws + w.states);
+        fwd.init = S0;
+        rev.init = dS_T;
         rev.seg_out = reinterpret_cast<float *>(ws + w.states2);
         p.pass[0] = fwd;
         p.pass[1] = rev;
         p.n_pass = 2;
         err = launch_attn(p, cs);
-        if (err == cudaSuccess)
-            err = launch_attn_combine(p, AttnCombine{{fwd.seg_out, rev.seg_out}, {S0, dS_T}, dk * dv}, cs);
+        combined = many_segments(w, n_seq, L);
+        if (combined && err == cudaSuccess) err = launch_attn_combine(p, fwd.seg_out, rev.seg_out, dk * dv, cs);
         seg_S = fwd.seg_out;
         seg_dS = rev.seg_out;
     }
@@ -218,7 +229,9 @@ mdn_status mdn_linear_attn_bwd(const void *q, const void *k, const void *v, cons
     b.out_scale = 1.f; b.w_scale = scale;
     b.out = to_dk; b.out_f32 = shared > 1;
     b.init = dS_T; b.seg_init = seg_dS; b.init_t = true;
+    a.combined = b.combined = combined;
     AttnPass c = rev;
+    c.combined = combined;
     c.seg_out = nullptr;
     c.X = k; c.ld_x = ld_k; c.sx = shared;
     c.out_scale = 1.f;

@@ -160,10 +160,15 @@ attn_tc_kernel(const __grid_constant__ AttnProblem p, const __grid_constant__ Al
     const AttnPass &a = p.pass[blockIdx.y];
     const int h = blockIdx.x % p.H;
     AttnItem it;
+    grid_launch_dependents();
+    grid_dependency_wait();
     if (!attn_item(p, blockIdx.x / p.H, it, reinterpret_cast<int *>(smem))) return;
     const bool states_only = a.out == nullptr;
-    const bool closes = a.reversed ? it.first : it.last;      // the sequence's last run in the pass's order
-    if (states_only && closes) return;                        // no run starts from that state
+    const bool closes = a.reversed ? it.first() : it.last();  // the sequence's last run in the pass's order
+    if (states_only && closes) {
+        attn_keep_initial(p, a, it, h);
+        return;
+    }
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int kd = a.kd, vd = a.vd, ksteps = (kd + 15) / 16;
     const int chunks = (it.len + kC - 1) / kC;
@@ -186,7 +191,7 @@ attn_tc_kernel(const __grid_constant__ AttnProblem p, const __grid_constant__ Al
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->drain[i], 1);
             mbar_init(&bars->p_ready[i], 4);
-            mbar_init(&bars->parts_ready[i], 4);
+            mbar_init(&bars->parts_ready[i], states_only ? 12 : 4);
             mbar_init(&bars->parts_free[i], 1);
             mbar_init(&bars->o_ready[i], 1);
             mbar_init(&bars->o_free[i], 4);
@@ -373,9 +378,10 @@ attn_tc_kernel(const __grid_constant__ AttnProblem p, const __grid_constant__ Al
             mbar_wait(&bars->drain[warp & 1], 0, &dummy);
         }
         __syncwarp();
-    } else if (warp < 8) {
-        // ------------------------------------------------ D W in two parts
-        const int t = tid - 128, per = (vd + 7) / 8, total = kC * per;
+    } else if (warp < 8 || (states_only && warp < 16)) {
+        // ------------------------------------------------ D W in two parts (for
+        // states alone by three times the warps, which would be idle)
+        const int t = tid & 127, third = (warp - 4) >> 2, thirds = states_only ? 3 : 1, per = (vd + 7) / 8, total = kC * per;
         const bool whole = per == 16 || per == 8;
         const int r0 = t / per, apart = 128 / per;           // (128 / 16 or 128 / 8 rows)
         const uint32_t at0 = ((t - r0 * per) >> 3) * kBlock + sw128_offset(r0, (t - r0 * per) & 7);
@@ -400,11 +406,11 @@ attn_tc_kernel(const __grid_constant__ AttnProblem p, const __grid_constant__ Al
             };
             if (whole) {
                 // the rows of a thread's packets lie whole swizzle periods apart
-#pragma unroll 1
-                for (int i = 0; i < total / 128; ++i)
+#pragma unroll 2
+                for (int i = third; i < total / 128; i += thirds)
                     split(at0 + i * (apart * 128), leave[i * apart + r0]);
             } else {
-                for (int i = t; i < total; i += 128) {
+                for (int i = t + third * 128; i < total; i += thirds * 128) {
                     const int r = i / per, ch = i - r * per;
                     split((ch >> 3) * kBlock + sw128_offset(r, ch & 7), leave[r]);
                 }
@@ -528,17 +534,8 @@ attn_tc_kernel(const __grid_constant__ AttnProblem p, const __grid_constant__ Al
         const bool mine = k0 < kd;
         const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16);
         float z[32];
-        {
-            const bool opens = rev ? it.last : it.first;
-            const float *src = nullptr;
-            if (!states_only) {
-                if (a.seg_init) src = a.seg_init + ((long)it.slot * p.H + h) * kd * vd;
-                else if (a.init && opens) src = a.init + ((long)it.seq * p.H + h) * kd * vd;
-            }
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-                z[k] = src && k0 + k < kd && col < vd ? src[a.init_t ? col * kd + k0 + k : (k0 + k) * vd + col] : 0.f;
-        }
+        attn_initial<32>(p, a, it, h, a.init_t ? (long)col * kd + k0 : (long)k0 * vd + col, a.init_t ? 1 : vd,
+                         col < vd ? kd - k0 : 0, z);
         auto put = [&]() {
             if (mine) {
                 float v[16];
@@ -594,8 +591,7 @@ template <int V>
 cudaError_t launch(const AttnProblem &p, const AllMaps &maps, cudaStream_t st) {
     const cudaError_t err = allow_shared<attn_tc_kernel<V>>(kSmem);
     if (err != cudaSuccess) return err;
-    attn_tc_kernel<V><<<dim3((unsigned)(p.slots * (long)p.H), p.n_pass), kThreads, kSmem, st>>>(p, maps);
-    return cudaGetLastError();
+    return launch_after(attn_tc_kernel<V>, p, kThreads, kSmem, st, p, maps);
 }
 
 // [tokens, heads, width] rows as boxes of 64 tokens of 64 columns of a head.

@@ -83,5 +83,22 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<uint32_t *>(&v);
 }
 
+// Launches a pass's kernel: set up while the kernel before it ends, which it
+// waits for (grid_dependency_wait) before it reads anything.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), const AttnProblem &p, int threads, int smem, cudaStream_t st, const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.slots * (long)p.H), p.n_pass);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace attn_tc
 }  // namespace mdn

@@ -103,10 +103,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc32_kernel(const __grid_con
     const AttnPass &a = p.pass[blockIdx.y];
     const int h = blockIdx.x % p.H;
     AttnItem it;
+    grid_launch_dependents();
+    grid_dependency_wait();
     if (!attn_item(p, blockIdx.x / p.H, it, reinterpret_cast<int *>(smem))) return;
     const bool states_only = a.out == nullptr;
-    const bool closes = a.reversed ? it.first : it.last;      // the sequence's last run in the pass's order
-    if (states_only && closes) return;                        // no run starts from that state
+    const bool closes = a.reversed ? it.first() : it.last();  // the sequence's last run in the pass's order
+    if (states_only && closes) {
+        attn_keep_initial(p, a, it, h);
+        return;
+    }
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int kd = a.kd, vd = a.vd, ksteps = (kd + 15) / 16;
     const int chunks = (it.len + kC - 1) / kC;
@@ -145,17 +150,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc32_kernel(const __grid_con
     const int col = quad * 32 + lane, k0 = group * 32;
     const bool mine = k0 < kd;
     float z[32];
-    {
-        const bool opens = rev ? it.last : it.first;
-        const float *src = nullptr;
-        if (!states_only) {
-            if (a.seg_init) src = a.seg_init + ((long)it.slot * p.H + h) * kd * vd;
-            else if (a.init && opens) src = a.init + ((long)it.seq * p.H + h) * kd * vd;
-        }
-#pragma unroll
-        for (int k = 0; k < 32; ++k)
-            z[k] = src && k0 + k < kd && col < vd ? src[a.init_t ? col * kd + k0 + k : (k0 + k) * vd + col] : 0.f;
-    }
+    attn_initial<32>(p, a, it, h, a.init_t ? (long)col * kd + k0 : (long)k0 * vd + col, a.init_t ? 1 : vd,
+                     col < vd ? kd - k0 : 0, z);
     auto put_state = [&]() {
         if (!mine) return;
         float part[3][16];
@@ -367,8 +363,7 @@ template <int V>
 cudaError_t launch(const AttnProblem &p, cudaStream_t st) {
     const cudaError_t err = allow_shared<attn_tc32_kernel<V>>(kSmem);
     if (err != cudaSuccess) return err;
-    attn_tc32_kernel<V><<<dim3((unsigned)(p.slots * (long)p.H), p.n_pass), kThreads, kSmem, st>>>(p);
-    return cudaGetLastError();
+    return launch_after(attn_tc32_kernel<V>, p, kThreads, kSmem, st, p);
 }
 
 }  // namespace
