@@ -14,6 +14,8 @@
 // groups of a sequence take two readings, the second one after the sums of
 // tiles of its tokens have been joined; a sequence batch that fits the L2 cache
 // is read from memory once.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "mdn_attn.cuh"
@@ -227,8 +229,11 @@ __global__ void __launch_bounds__(most_threads(NI, V)) token_fwd_kernel(GroupNor
     const TokenPlace t = token_place(p, tpg);
     const int w = p.D / p.G;
     const long c0 = t.g * w;
-    const T *x = static_cast<const T *>(p.x) + c0, *gate = static_cast<const T *>(p.gate) + c0;
-    T *y = static_cast<T *>(p.y) + c0;
+    // this thread's packets of the next token to load, and of the one to store
+    const T *x = static_cast<const T *>(p.x) + t.row * p.ld_x + c0 + t.tid * V;
+    const T *gate = static_cast<const T *>(p.gate) + t.row * p.ld_gate + c0 + t.tid * V;
+    T *y = static_cast<T *>(p.y) + t.row * p.D + c0 + t.tid * V;
+    const long x_step = t.step * p.ld_x, gate_step = t.step * p.ld_gate, y_step = t.step * p.D;
     Vals<V> wt[HOLD ? NI : 1], bs[HOLD ? NI : 1];
     auto weights = [&](int i, int c) {
         wt[HOLD ? i : 0] = load_weights<V>(p.weight, c0 + c, 1.f);
@@ -244,12 +249,13 @@ __global__ void __launch_bounds__(most_threads(NI, V)) token_fwd_kernel(GroupNor
     auto load = [&](long row) {
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int c = (i * tpg + t.tid) * V;
-            if (row < p.rows && c < w) {
-                px[i] = load_packet<T, V>(x + row * p.ld_x + c);
-                if (GATE) pg[i] = load_packet<T, V>(gate + row * p.ld_gate + c);
+            if (row < p.rows && (i * tpg + t.tid) * V < w) {
+                px[i] = load_packet<T, V>(x + i * tpg * V);
+                if (GATE) pg[i] = load_packet<T, V>(gate + i * tpg * V);
             }
         }
+        x += x_step;
+        if (GATE) gate += gate_step;
     };
     const float inv = 1.f / (float)w;
     long row = t.row;
@@ -292,13 +298,14 @@ __global__ void __launch_bounds__(most_threads(NI, V)) token_fwd_kernel(GroupNor
             if (live && c < w) {
                 if (!HOLD) weights(i, c);
                 if (GATE && !HOLD) g[i] = values<T, V>(pg[i]);
-                store_packet<T, V>(y + row * p.D + c,
+                store_packet<T, V>(y + i * tpg * V,
                                    packet<T, V>(forward_vals<V, GATE>(d[i], g[GATE ? i : 0], rstd, wt[HOLD ? i : 0],
                                                                       bs[HOLD ? i : 0], p.act)));
             }
         }
         if (p.stats && live && t.tid == 0)
             reinterpret_cast<float2 *>(p.stats)[row * p.G + t.g] = make_float2(mean, rstd);
+        y += y_step;
     }
 }
 
@@ -311,9 +318,12 @@ __global__ void __launch_bounds__(most_threads(NI, V)) token_bwd_kernel(GroupNor
     const TokenPlace t = token_place(p, tpg);
     const int w = p.D / p.G;
     const long c0 = t.g * w;
-    const T *x = static_cast<const T *>(p.x) + c0, *gate = static_cast<const T *>(p.gate) + c0;
-    const T *dyp = static_cast<const T *>(p.dy) + c0;
-    T *dx = static_cast<T *>(p.dx) + c0, *dgate = static_cast<T *>(p.dgate) + c0;
+    const T *x = static_cast<const T *>(p.x) + t.row * p.ld_x + c0 + t.tid * V;
+    const T *gate = static_cast<const T *>(p.gate) + t.row * p.ld_gate + c0 + t.tid * V;
+    const T *dyp = static_cast<const T *>(p.dy) + t.row * p.ld_dy + c0 + t.tid * V;
+    T *dx = static_cast<T *>(p.dx) + t.row * p.D + c0 + t.tid * V, *dgate = static_cast<T *>(p.dgate) + t.row * p.D + c0 + t.tid * V;
+    const float2 *stats = reinterpret_cast<const float2 *>(p.stats) + t.row * p.G + t.g;
+    const long x_step = t.step * p.ld_x, gate_step = t.step * p.ld_gate, dy_step = t.step * p.ld_dy, out_step = t.step * p.D;
     constexpr bool HOLD = held(NI, V);
     Vals<V> wt[HOLD ? NI : 1], bs[HOLD ? NI : 1], dw[NI], db[NI];
     auto weights = [&](int i, int c) {
@@ -330,16 +340,18 @@ __global__ void __launch_bounds__(most_threads(NI, V)) token_bwd_kernel(GroupNor
     float2 st, next = make_float2(0.f, 0.f);
     auto load = [&](long row) {
         if (row >= p.rows) return;
-        next = reinterpret_cast<const float2 *>(p.stats)[row * p.G + t.g];
+        next = *stats;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int c = (i * tpg + t.tid) * V;
-            if (c < w) {
-                px[i] = load_packet<T, V>(x + row * p.ld_x + c);
-                pd[i] = load_packet<T, V>(dyp + row * p.ld_dy + c);
-                if (GATE) pg[i] = load_packet<T, V>(gate + row * p.ld_gate + c);
+        for (int i = 0; i < NI; ++i)
+            if ((i * tpg + t.tid) * V < w) {
+                px[i] = load_packet<T, V>(x + i * tpg * V);
+                pd[i] = load_packet<T, V>(dyp + i * tpg * V);
+                if (GATE) pg[i] = load_packet<T, V>(gate + i * tpg * V);
             }
-        }
+        stats += t.step * p.G;
+        x += x_step;
+        dyp += dy_step;
+        if (GATE) gate += gate_step;
     };
     const float inv = 1.f / (float)w;
     long row = t.row;
@@ -371,7 +383,7 @@ __global__ void __launch_bounds__(most_threads(NI, V)) token_bwd_kernel(GroupNor
             if (live && c < w) {
                 if (!HOLD) element(i, c, to);
                 finish(to);
-                if (GATE) store_packet<T, V>(dgate + row * p.D + c, packet<T, V>(g[to]));
+                if (GATE) store_packet<T, V>(dgate + i * tpg * V, packet<T, V>(g[to]));
                 Vals<V> dn, dnn;
 #pragma unroll
                 for (int j = 0; j < Vals<V>::N; ++j) {
@@ -398,9 +410,11 @@ __global__ void __launch_bounds__(most_threads(NI, V)) token_bwd_kernel(GroupNor
 #pragma unroll
                 for (int j = 0; j < Vals<V>::N; ++j)
                     out.p[j] = mul2(r, fma2(n[to].p[j], m2, fma2(d[to].p[j], wt[to].p[j], m1)));
-                store_packet<T, V>(dx + row * p.D + c, packet<T, V>(out));
+                store_packet<T, V>(dx + i * tpg * V, packet<T, V>(out));
             }
         }
+        dx += out_step;
+        if (GATE) dgate += out_step;
     }
     if (!part) return;
     float *out = part + t.row * 2 * p.D + c0;
@@ -812,6 +826,202 @@ __global__ void __launch_bounds__(kThreads) seq_dx_kernel(GroupNormProblem p, in
     }
 }
 
+// ------------------------------------------------ ... in a cluster's shared memory
+//
+// A cluster of blocks takes neighbouring groups of one sequence, each block a run
+// of its tokens.  Their packets are copied into shared memory at once, every
+// thread its own (one column's, of every lanes-th token), and read from there
+// for the sums and again for the results; the blocks' sums meet through the
+// cluster's shared memory.  One launch and one reading instead of three and two.
+
+// Tokens of a block, for a sequence of len.
+__device__ __forceinline__ int cluster_rows(int len, int blocks) { return (len + blocks - 1) / blocks; }
+
+template <typename T, int V, bool GATE, bool BWD>
+__global__ void __launch_bounds__(kThreads) seq_cluster_kernel(GroupNormProblem p, int per_block, int blocks, float *params) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ float mom[3][kThreads];
+    __shared__ float cols[BWD ? 2 * kThreads * V : 1];
+    __shared__ float3 own[kThreads], all[kThreads];     // of the block's groups
+    if (BWD) grid_trigger();
+    const int column_blocks = (p.G + per_block - 1) / per_block;
+    const int rank = blockIdx.x % blocks, which = blockIdx.x / blocks, cb = which % column_blocks, seq = which / column_blocks;
+    const bool ok = !p.cu || cu_well_formed(p.cu, p.n_seq, (int)p.rows);
+    if (!ok && blockIdx.x == 0 && threadIdx.x == 0) atomicExch(p.status, MDN_ERR_INVALID_ARG);
+    const int len = !ok ? 0 : p.cu ? p.cu[seq + 1] - p.cu[seq] : p.T;
+    const long first = !ok ? 0 : p.cu ? p.cu[seq] : (long)seq * p.T;
+    const int rows = cluster_rows(len, blocks), n = max(0, min(rows, len - rank * rows));
+    const long start = first + (long)rank * rows;
+    const int w = p.D / p.G, g0 = cb * per_block, groups = min(per_block, p.G - g0), ppg = w / V, packets = groups * ppg;
+    const int lanes = kThreads / packets, lane = threadIdx.x / packets, pc = threadIdx.x - lane * packets;
+    const int count = lane < lanes && lane < n ? (n - lane + lanes - 1) / lanes : 0;      // this thread's tokens
+    const long col = (long)g0 * w + pc * V;
+    constexpr int kArrays = BWD ? (GATE ? 3 : 2) : 1;
+    using P = Packet<T, V>;
+    P *tile = reinterpret_cast<P *>(smem) + threadIdx.x;        // [array][token of the thread][thread]
+    const int depth = (rows + lanes - 1) / lanes;
+    auto at = [&](int array, int r) -> P & { return tile[(array * depth + r) * kThreads]; };
+    {
+        const T *src[3] = {static_cast<const T *>(p.x), static_cast<const T *>(p.dy), static_cast<const T *>(p.gate)};
+        const long ld[3] = {p.ld_x, p.ld_dy, p.ld_gate};
+#pragma unroll
+        for (int a = 0; a < kArrays; ++a) {
+            const T *from = src[a] + (start + lane) * ld[a] + col;
+            for (int r = 0; r < count; ++r) copy_packet<T, V>(&at(a, r), from + r * (lanes * ld[a]));
+        }
+        commit_copies();
+    }
+    const Vals<V> wt = count ? load_weights<V>(p.weight, col, 1.f) : zeros<V>();
+    const Vals<V> bs = count ? load_weights<V>(p.bias, col, 0.f) : zeros<V>();
+    float2 st = make_float2(0.f, 0.f);
+    if (BWD && count) st = reinterpret_cast<const float2 *>(p.stats)[(long)seq * p.G + col / w];
+    wait_copies<0>();
+    float3 mine = make_float3(0.f, 0.f, 0.f);
+    if constexpr (!BWD) {
+        if (count) {
+            // sums about the mean of the first packet, so that they do not cancel
+            const float shift = p.center ? sum_of<V>(values<T, V>(at(0, 0))) * (1.f / V) : 0.f;
+            Vals<V> s1 = zeros<V>(), s2 = zeros<V>();
+            const Pair minus = both(-shift);
+#pragma unroll 4
+            for (int r = 0; r < count; ++r) {
+                const Vals<V> f = values<T, V>(at(0, r));
+#pragma unroll
+                for (int j = 0; j < Vals<V>::N; ++j) {
+                    const Pair d = add2(f.p[j], minus);
+                    s1.p[j] = add2(s1.p[j], d);
+                    s2.p[j] = fma2(d, d, s2.p[j]);
+                }
+            }
+            const float a = sum_of<V>(s1), b = sum_of<V>(s2), k = (float)count * V, m2 = p.center ? b - a * (a / k) : b;
+            mine = make_float3(k, p.center ? shift + a / k : 0.f, m2 < 0.f ? 0.f : m2);
+        }
+    } else {
+        Vals<V> dw = zeros<V>(), db = zeros<V>();
+#pragma unroll 2
+        for (int r = 0; r < count; ++r) {
+            Vals<V> x = values<T, V>(at(0, r)), d = values<T, V>(at(1, r)), g;
+            if (GATE) g = values<T, V>(at(kArrays - 1, r));
+            backward_vals<V, GATE>(x, g, d, st.x, st.y, wt, bs, p.act);
+#pragma unroll
+            for (int j = 0; j < Vals<V>::N; ++j) {
+                dw.p[j] = fma2(d.p[j], x.p[j], dw.p[j]);
+                db.p[j] = add2(db.p[j], d.p[j]);
+            }
+        }
+        Vals<V> a, b;
+#pragma unroll
+        for (int j = 0; j < Vals<V>::N; ++j) {
+            a.p[j] = mul2(db.p[j], wt.p[j]);
+            b.p[j] = mul2(dw.p[j], wt.p[j]);
+        }
+        mine = make_float3(0.f, sum_of<V>(a), sum_of<V>(b));
+        if (params) {
+            float fw[2 * Vals<V>::N], fb[2 * Vals<V>::N];
+#pragma unroll
+            for (int j = 0; j < Vals<V>::N; ++j) {
+                split_pair(dw.p[j], fw[2 * j], fw[2 * j + 1]);
+                split_pair(db.p[j], fb[2 * j], fb[2 * j + 1]);
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                cols[threadIdx.x * V + v] = fw[v];
+                cols[(kThreads + threadIdx.x) * V + v] = fb[v];
+            }
+            __syncthreads();
+            const int c = packets * V;
+            float *out = params + ((long)seq * blocks + rank) * 2 * p.D + (long)g0 * w;
+            for (int i = threadIdx.x; i < 2 * c; i += kThreads) {
+                const int k = i >= c, at_col = i - k * c;
+                float sum = 0.f;
+                for (int l = 0; l < lanes; ++l) sum += cols[k * kThreads * V + l * c + at_col];
+                out[k * p.D + at_col] = sum;
+            }
+        }
+    }
+    mom[0][threadIdx.x] = mine.x;
+    mom[1][threadIdx.x] = mine.y;
+    mom[2][threadIdx.x] = mine.z;
+    __syncthreads();
+    for (int g = threadIdx.x >> 5; g < groups; g += kThreads / 32) {
+        const float center = BWD ? 0.f : mom[1][g * ppg];
+        Join j = {0.f, 0.f, 0.f};
+        for (int i = threadIdx.x & 31; i < ppg * lanes; i += 32) {
+            const int l = i / ppg, k = l * packets + g * ppg + (i - l * ppg);
+            if (BWD) {
+                j.s1 += mom[1][k];
+                j.s2 += mom[2][k];
+            } else {
+                join_part(j, center, mom[0][k], mom[0][k] > 0.f ? mom[1][k] : center, mom[2][k]);
+            }
+        }
+        join_warp(j);
+        if ((threadIdx.x & 31) == 0) {
+            float2 v = make_float2(j.s1, j.s2);
+            if (!BWD) v = j.n > 0.f && p.center ? joined(j, center) : make_float2(0.f, j.s2);
+            own[g] = make_float3(j.n, v.x, v.y);
+        }
+    }
+    cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+    cluster.sync();
+    // every block joins all blocks' sums, in their order
+    for (int g = threadIdx.x; g < groups; g += kThreads) {
+        const float center = BWD ? 0.f : cluster.map_shared_rank(own, 0)[g].y;      // (the first block has tokens)
+        Join j = {0.f, 0.f, 0.f};
+        for (int k = 0; k < blocks; ++k) {
+            const float3 v = cluster.map_shared_rank(own, k)[g];
+            if (BWD) {
+                j.s1 += v.y;
+                j.s2 += v.z;
+            } else if (v.x > 0.f) {
+                join_part(j, center, v.x, v.y, v.z);
+            }
+        }
+        if (BWD) {
+            const float inv = len ? 1.f / ((float)len * (float)w) : 0.f;
+            all[g] = make_float3(p.center ? j.s1 * inv : 0.f, j.s2 * inv, 0.f);
+        } else {
+            float2 v = make_float2(0.f, 0.f);
+            if (len) {
+                const float2 m = joined(j, center);
+                v = make_float2(p.center ? m.x : 0.f, rsqrtf((p.center ? m.y : j.s2) / j.n + p.eps));
+            }
+            all[g] = make_float3(v.x, v.y, 0.f);
+            if (p.stats && rank == 0) reinterpret_cast<float2 *>(p.stats)[(long)seq * p.G + g0 + g] = v;
+        }
+    }
+    // (a block's sums stay until all have read them)
+    cluster.sync();
+    if (!count) return;
+    const float3 got = all[pc / ppg];
+    if constexpr (!BWD) {
+        const T *gate = static_cast<const T *>(p.gate) + (start + lane) * p.ld_gate + col;
+        T *y = static_cast<T *>(p.y) + (start + lane) * p.D + col;
+        const Pair minus = both(-got.x);
+#pragma unroll 4
+        for (int r = 0; r < count; ++r) {
+            Vals<V> f = values<T, V>(at(0, r)), g;
+            if (GATE) g = values<T, V>(load_packet<T, V>(gate + r * (lanes * p.ld_gate)));
+#pragma unroll
+            for (int j = 0; j < Vals<V>::N; ++j) f.p[j] = add2(f.p[j], minus);
+            store_packet<T, V>(y + (long)r * lanes * p.D, packet<T, V>(forward_vals<V, GATE>(f, g, got.y, wt, bs, p.act)));
+        }
+    } else {
+        T *dx = static_cast<T *>(p.dx) + (start + lane) * p.D + col, *dgate = static_cast<T *>(p.dgate) + (start + lane) * p.D + col;
+        const Pair m1 = both(-got.x), m2 = both(-got.y), rstd = both(st.y);
+#pragma unroll 2
+        for (int r = 0; r < count; ++r) {
+            Vals<V> x = values<T, V>(at(0, r)), d = values<T, V>(at(1, r)), g;
+            if (GATE) g = values<T, V>(at(kArrays - 1, r));
+            backward_vals<V, GATE>(x, g, d, st.x, st.y, wt, bs, p.act);
+            if (GATE) store_packet<T, V>(dgate + (long)r * lanes * p.D, packet<T, V>(g));
+#pragma unroll
+            for (int j = 0; j < Vals<V>::N; ++j) x.p[j] = mul2(rstd, fma2(x.p[j], m2, fma2(d.p[j], wt.p[j], m1)));
+            store_packet<T, V>(dx + (long)r * lanes * p.D, packet<T, V>(x));
+        }
+    }
+}
+
 // ------------------------------------------------------------------- host
 
 int pow2_at_least(long x) {
@@ -830,6 +1040,30 @@ int tile_rows(long rows, int D) {
 }
 long tile_slots(int n_seq, long rows, int D) { return rows / tile_rows(rows, D) + n_seq; }
 
+// How sequences are taken by clusters, if they are: neighbouring groups of 128
+// bytes a token, and so many blocks that a thread's packets of the longest
+// sequence there can be fit shared memory, three blocks to a multiprocessor where
+// that goes.  (8 sequences of 2048 tokens of 2048 bf16 columns in 32 groups:
+// CLUSTERNOW us, and 65 in tiles.)
+struct ClusterShape {
+    int per_block, blocks, smem;
+};
+ClusterShape cluster_shape(const GroupNormProblem &p, int V, int el, bool bwd) {
+    const int w = p.D / p.G, arrays = bwd ? (p.gate ? 3 : 2) : 1;
+    ClusterShape c = {std::min(p.G, std::max(1, 128 / (w * el))), 0, 0};
+    const long packets = (long)c.per_block * (w / V);
+    if (packets > kThreads) return c;
+    const long lanes = kThreads / packets, longest = p.cu ? p.rows : p.T;
+    for (int blocks = 1; blocks <= 8; blocks *= 2) {
+        const long rows = (longest + blocks - 1) / blocks, bytes = (rows + lanes - 1) / lanes * kThreads * V * el * arrays;
+        if (bytes > (blocks < 8 ? 56 : 176) * 1024) continue;
+        c.blocks = blocks;
+        c.smem = (int)bytes;
+        break;
+    }
+    return c;
+}
+
 // Groups of a block that takes parts of sequences.
 int groups_per_block(int D, int G, int V) { return std::max(1, std::min(G, kThreads * V / (D / G))); }
 
@@ -843,8 +1077,10 @@ long gcd(long a, long b) { return b ? gcd(b, a % b) : a; }
 TokenShape token_shape(const GroupNormProblem &p, int V, int per_sm) {
     TokenShape t;
     const long P = (p.D / p.G) / V;
-    // up to eight packets a thread before a group takes several warps
-    t.tpg = P <= 32 ? pow2_at_least(P) : std::max(32, pow2_at_least((P + 7) / 8));
+    // up to four packets a thread before a group takes several warps, and more
+    // where that would take more than a block of 256
+    const int each = P <= 4 * kThreads ? 4 : 8;
+    t.tpg = P <= 32 ? pow2_at_least(P) : std::max(32, pow2_at_least((P + each - 1) / each));
     t.NI = (int)((P + t.tpg - 1) / t.tpg);
     if (t.tpg > 1024) {
         t.tpg = 1024;
@@ -863,7 +1099,7 @@ TokenShape token_shape(const GroupNormProblem &p, int V, int per_sm) {
 
 // The gradient's blocks: each lane of tokens leaves a row of the parameters'
 // sums behind, which are read again.
-constexpr int kFwdPerSM = 8, kBwdPerSM = 3;
+constexpr int kFwdPerSM = 8, kBwdPerSM = 2;
 long token_lanes_most(long rows, int D, int G) {
     const long w = D / G;
     long most = 0;
@@ -914,6 +1150,26 @@ cudaError_t params(const GroupNormProblem &p, const float *part, long lanes, cud
     return follow(param_kernel, dim3((2 * p.D + 31) / 32), 1024, st, part, (int)lanes, p.D, p.dw, p.dbias);
 }
 
+template <typename T, int V, bool GATE, bool BWD>
+cudaError_t cluster_launch(const GroupNormProblem &p, const ClusterShape &c, float *prm, cudaStream_t st) {
+    const auto kernel = seq_cluster_kernel<T, V, GATE, BWD>;
+    // (the largest of the shapes; below 48 KiB with the static arrays nothing need be asked)
+    const cudaError_t err = allow_shared<seq_cluster_kernel<T, V, GATE, BWD>>(176 * 1024);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((long)p.n_seq * ((p.G + c.per_block - 1) / c.per_block) * c.blocks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = c.smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = c.blocks;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p, c.per_block, c.blocks, prm);
+}
+
 template <typename T, int V, bool GATE>
 cudaError_t run(const GroupNormProblem &p, bool bwd, cudaStream_t st) {
     cudaError_t err;
@@ -922,6 +1178,12 @@ cudaError_t run(const GroupNormProblem &p, bool bwd, cudaStream_t st) {
         float *part = bwd && (p.dw || p.dbias) ? reinterpret_cast<float *>(p.ws) : nullptr;
         if ((err = token_pick<T, V, GATE>(p, t, part, bwd, st)) != cudaSuccess) return err;
         return bwd ? params(p, part, t.lanes, st) : cudaSuccess;
+    }
+    const ClusterShape c = cluster_shape(p, V, (int)sizeof(T), bwd);
+    if (c.blocks) {
+        float *prm = bwd && (p.dw || p.dbias) ? reinterpret_cast<float *>(p.ws) : nullptr;
+        err = bwd ? cluster_launch<T, V, GATE, true>(p, c, prm, st) : cluster_launch<T, V, GATE, false>(p, c, prm, st);
+        return bwd && err == cudaSuccess ? params(p, prm, (long)p.n_seq * c.blocks, st) : err;
     }
     const int rows = tile_rows(p.rows, p.D), gpb = groups_per_block(p.D, p.G, V);
     const long slots = p.cu ? tile_slots(p.n_seq, p.rows, p.D) : (long)p.n_seq * ((p.T + rows - 1) / rows);
@@ -985,8 +1247,9 @@ size_t group_norm_fwd_workspace(int n_seq, long rows, int D, int G, bool over_se
 size_t group_norm_bwd_workspace(int n_seq, long rows, int D, int G, bool over_sequence, mdn_dtype dtype) {
     if (rows == 0) return 0;
     if (!over_sequence) return round256(token_lanes_most(rows, D, G) * 2 * D * sizeof(float));
+    // (clusters leave a row of sums for each of their blocks, eight at most)
     return group_norm_fwd_workspace(n_seq, rows, D, G, true, dtype) +
-           round256(tile_slots(n_seq, rows, D) * 2 * D * sizeof(float));
+           round256(std::max(tile_slots(n_seq, rows, D), 8L * n_seq) * 2 * D * sizeof(float));
 }
 
 }  // namespace mdn
