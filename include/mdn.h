@@ -688,12 +688,13 @@ mdn_status mdn_norm_residual_bwd(const void *y, const void *x, const void *gate,
 
 /*
  * Bytes of device workspace mdn_linear_attn_fwd / _bwd need (a multiple of
- * 256, possibly 0; 0 for invalid sizes).  T_total = B * T.
+ * 256, possibly 0; 0 for invalid sizes).  T_total = B * T; packed: nonzero with
+ * cu_seqlens.
  */
 size_t mdn_linear_attn_fwd_workspace_size(int n_seq, int T_total, int H, int Hkv, int dk,
-                                          int dv, mdn_dtype dtype);
+                                          int dv, int packed, mdn_dtype dtype);
 size_t mdn_linear_attn_bwd_workspace_size(int n_seq, int T_total, int H, int Hkv, int dk,
-                                          int dv, mdn_dtype dtype);
+                                          int dv, int packed, mdn_dtype dtype);
 
 /*
  * mdn_linear_attn_fwd — causal linear attention over whole sequences.  Per

@@ -26,7 +26,7 @@ struct Space {
     int seg = 0;
     long slots = 0;
 };
-Space space(const Heads &s, mdn_dtype dtype, bool bwd) {
+Space space(const Heads &s, bool packed, mdn_dtype dtype, bool bwd) {
     Space w;
     if (s.L == 0) return w;
     w.seg = attn_segment(s.n_seq, s.L, s.H, bwd ? 3 : 1, dtype);
@@ -36,8 +36,8 @@ Space space(const Heads &s, mdn_dtype dtype, bool bwd) {
         w.total += round256(bytes);
         return at;
     };
-    w.items = take(w.slots * sizeof(AttnItem));
-    w.offs = take((s.n_seq + 2) * sizeof(int32_t));
+    w.items = take(packed ? w.slots * sizeof(AttnItem) : 0);
+    w.offs = take(packed ? (s.n_seq + 2) * sizeof(int32_t) : 0);
     const size_t states = w.seg ? (size_t)w.slots * s.H * s.dk * s.dv * sizeof(float) : 0;
     w.states = take(states);
     if (bwd) {
@@ -85,17 +85,19 @@ using namespace mdn;
 
 extern "C" {
 
-static size_t attn_workspace(int n_seq, int T_total, int H, int Hkv, int dk, int dv, mdn_dtype dtype, bool bwd) {
+static size_t attn_workspace(int n_seq, int T_total, int H, int Hkv, int dk, int dv, int packed, mdn_dtype dtype, bool bwd) {
     if (n_seq < 0 || T_total < 0 || !heads_ok(H, Hkv, dk, dv) || !valid_dtype(dtype) ||
         !heads_small(n_seq, T_total, H, dk, dv))
         return 0;
-    return space(Heads{n_seq, T_total, H, Hkv, dk, dv}, dtype, bwd).total;
+    return space(Heads{n_seq, T_total, H, Hkv, dk, dv}, packed != 0, dtype, bwd).total;
 }
-size_t mdn_linear_attn_fwd_workspace_size(int n_seq, int T_total, int H, int Hkv, int dk, int dv, mdn_dtype dtype) {
-    return attn_workspace(n_seq, T_total, H, Hkv, dk, dv, dtype, false);
+size_t mdn_linear_attn_fwd_workspace_size(int n_seq, int T_total, int H, int Hkv, int dk, int dv, int packed,
+                                          mdn_dtype dtype) {
+    return attn_workspace(n_seq, T_total, H, Hkv, dk, dv, packed, dtype, false);
 }
-size_t mdn_linear_attn_bwd_workspace_size(int n_seq, int T_total, int H, int Hkv, int dk, int dv, mdn_dtype dtype) {
-    return attn_workspace(n_seq, T_total, H, Hkv, dk, dv, dtype, true);
+size_t mdn_linear_attn_bwd_workspace_size(int n_seq, int T_total, int H, int Hkv, int dk, int dv, int packed,
+                                          mdn_dtype dtype) {
+    return attn_workspace(n_seq, T_total, H, Hkv, dk, dv, packed, dtype, true);
 }
 
 mdn_status mdn_linear_attn_fwd(const void *q, const void *k, const void *v, const float *log_decay, const float *S0,
@@ -114,7 +116,7 @@ mdn_status mdn_linear_attn_fwd(const void *q, const void *k, const void *v, cons
              .out(o, el, some).out(S_T, sa, false, S0).ok())
         return MDN_ERR_INVALID_ARG;
     const Heads s{n_seq, L, H, Hkv, dk, dv};
-    const Space w = space(s, dtype, false);
+    const Space w = space(s, cu_seqlens != nullptr, dtype, false);
     if (!workspace_ok(workspace, workspace_bytes, w.total)) return MDN_ERR_INVALID_ARG;
     int *status = nullptr;
     const mdn_status st = current_device_status(&status);
@@ -169,7 +171,7 @@ mdn_status mdn_linear_attn_bwd(const void *q, const void *k, const void *v, cons
              .out(dS0, sa, false).ok())
         return MDN_ERR_INVALID_ARG;
     const Heads s{n_seq, L, H, Hkv, dk, dv};
-    const Space w = space(s, dtype, true);
+    const Space w = space(s, cu_seqlens != nullptr, dtype, true);
     if (!workspace_ok(workspace, workspace_bytes, w.total)) return MDN_ERR_INVALID_ARG;
     int *status = nullptr;
     const mdn_status st = current_device_status(&status);

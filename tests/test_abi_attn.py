@@ -87,11 +87,13 @@ def test_group_norm_bwd_rejects(L, over, code):
 def test_sizes(L):
     f, b = L.mdn_linear_attn_fwd_workspace_size, L.mdn_linear_attn_bwd_workspace_size
     for g in (f, b):
-        assert g(2, 5000, 4, 2, 16, 8, 1) > 0 and g(2, 5000, 4, 2, 16, 8, 1) % 256 == 0
-        assert g(2, 5000, 3, 2, 16, 8, 1) == 0 and g(2, 5000, 4, 2, 129, 8, 1) == 0 and g(-1, 50, 4, 2, 16, 8, 1) == 0
-        assert g(2, 0, 4, 2, 16, 8, 1) == 0
+        assert g(2, 5000, 4, 2, 16, 8, 1, 1) > 0 and g(2, 5000, 4, 2, 16, 8, 1, 1) % 256 == 0
+        assert g(2, 5000, 3, 2, 16, 8, 1, 1) == 0 and g(2, 5000, 4, 2, 129, 8, 1, 1) == 0 and g(-1, 50, 4, 2, 16, 8, 1, 1) == 0
+        assert g(2, 0, 4, 2, 16, 8, 1, 1) == 0
+    # equal lengths that are not cut need none
+    assert f(4, 400, 4, 2, 16, 8, 0, 1) == 0 and f(4, 400, 4, 2, 16, 8, 1, 1) > 0
     # shared heads' gradients by query head
-    assert b(2, 5000, 4, 2, 16, 8, 1) >= b(2, 5000, 4, 4, 16, 8, 1) + 5000 * 4 * 24 * 4
+    assert b(2, 5000, 4, 2, 16, 8, 1, 1) >= b(2, 5000, 4, 4, 16, 8, 1, 1) + 5000 * 4 * 24 * 4
     n = L.mdn_group_norm_fwd_workspace_size
     assert n(2, 100, 64, 4, 0, 1) == 0 and n(2, 100, 64, 4, 1, 1) > 0 and n(2, 100, 64, 5, 1, 1) == 0
     assert L.mdn_group_norm_bwd_workspace_size(2, 100, 64, 4, 0, 1) > 0
