@@ -710,11 +710,14 @@ size_t mdn_linear_attn_bwd_workspace_size(int n_seq, int T_total, int H, int Hkv
  *   n_seq, B, T as mdn_chunk_fwd.  workspace 256-byte aligned.
  * log_decay is expected to be at most zero; larger values are computed as
  * written and may overflow.  -inf is a decay of zero.
- * States are fp32; bf16 rows meet in products of bf16 with fp32 sums, in
- * which the states before each 64 tokens and the decayed q k^T within them are
- * rounded to bf16 once.  Infinite and NaN rows reach what the formulas carry
- * them to and, beyond that, the other tokens of their sequence's run of 64
- * tokens; no other sequence and no other head.
+ * States are fp32.  bf16 rows meet in products of bf16 with fp32 sums, in which
+ * the states before each 64 tokens and the decayed q k^T within them are rounded
+ * to bf16 once, and the decayed v that states gather is taken as two bf16 parts
+ * (a state is off by some 4e-6 of its size).  fp32 rows are multiplied as three
+ * bf16 parts each, as exactly as in fp32; their values are expected below 3e38.
+ * Infinite and NaN rows reach what the formulas carry them to and, beyond that,
+ * the other tokens of their sequence's run of 64 tokens, where they may appear
+ * as NaN; no other sequence and no other head.
  * Errors: as mdn_short_conv_fwd; MDN_ERR_UNSUPPORTED for dk or dv above 128.
  */
 mdn_status mdn_linear_attn_fwd(const void *q, const void *k, const void *v,

@@ -84,6 +84,7 @@ struct GroupNormProblem {
     long ld_x, ld_gate, ld_dy;
     mdn_dtype dtype;
     unsigned char *ws;
+    int *ok;                        // whether cu is well formed, or nullptr
     int *status;
 };
 

@@ -461,6 +461,21 @@ __global__ void __launch_bounds__(1024) param_kernel(const float *part, int lane
 
 // -------------------------------------------------------- a sequence's groups
 
+// Whether cu_seqlens is well formed (whole CTA; uniform result): looked at by
+// every block, or of many sequences once, by check_kernel.
+constexpr int kManySequences = 1024;
+__device__ __forceinline__ bool sequences_ok(const GroupNormProblem &p) {
+    if (!p.cu) return true;
+    if (p.ok) return *p.ok != 0;
+    return cu_well_formed(p.cu, p.n_seq, (int)p.rows);
+}
+__global__ void __launch_bounds__(1024) check_kernel(GroupNormProblem p) {
+    const bool ok = cu_well_formed(p.cu, p.n_seq, (int)p.rows);
+    if (threadIdx.x) return;
+    *p.ok = ok;
+    if (!ok) atomicExch(p.status, MDN_ERR_INVALID_ARG);
+}
+
 // A tile of a sequence's tokens: `rows` of them at a time.  Tiles of sequence s
 // begin at slot cu[s] / rows + s, which leaves room for the last, partial one.
 struct Tile {
@@ -551,7 +566,7 @@ template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) seq_stats_kernel(GroupNormProblem p, int rows, int per_block, float2 *part) {
     __shared__ float mom[3][kThreads];
     grid_trigger();
-    if (p.cu && !cu_well_formed(p.cu, p.n_seq, (int)p.rows)) {
+    if (!sequences_ok(p)) {
         if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicExch(p.status, MDN_ERR_INVALID_ARG);
         return;
     }
@@ -612,7 +627,7 @@ __global__ void __launch_bounds__(kThreads) seq_stats_kernel(GroupNormProblem p,
 // One warp a group of a sequence: the statistics from the tiles'.
 __global__ void __launch_bounds__(kThreads) seq_join_kernel(GroupNormProblem p, int rows, const float2 *part, float2 *stats) {
     const long i = blockIdx.x * (long)(kThreads / 32) + (threadIdx.x >> 5);
-    const bool ok = !p.cu || cu_well_formed(p.cu, p.n_seq, (int)p.rows);
+    const bool ok = sequences_ok(p);
     grid_trigger();
     grid_wait();
     if (i >= (long)p.n_seq * p.G) return;
@@ -636,7 +651,7 @@ __global__ void __launch_bounds__(kThreads) seq_join_kernel(GroupNormProblem p, 
 
 template <typename T, int V, bool GATE>
 __global__ void __launch_bounds__(kThreads) seq_apply_kernel(GroupNormProblem p, int rows, int per_block, const float2 *stats) {
-    const bool ok = !p.cu || cu_well_formed(p.cu, p.n_seq, (int)p.rows);
+    const bool ok = sequences_ok(p);
     grid_trigger();
     grid_wait();
     Tile t;
@@ -670,7 +685,7 @@ seq_sums_kernel(GroupNormProblem p, int rows, int per_block, float2 *part, float
     __shared__ float2 red[kThreads];
     __shared__ float cols[2][kThreads * V];
     grid_trigger();
-    const bool ok = !p.cu || cu_well_formed(p.cu, p.n_seq, (int)p.rows);
+    const bool ok = sequences_ok(p);
     if (!ok && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicExch(p.status, MDN_ERR_INVALID_ARG);
     Tile t;
     const bool some = ok && tile_of(p, rows, blockIdx.x, t);
@@ -766,7 +781,7 @@ seq_sums_kernel(GroupNormProblem p, int rows, int per_block, float2 *part, float
 // One warp a group of a sequence: its means of dn and dn n.
 __global__ void __launch_bounds__(kThreads) seq_means_kernel(GroupNormProblem p, int rows, const float2 *part, float2 *means) {
     const long i = blockIdx.x * (long)(kThreads / 32) + (threadIdx.x >> 5);
-    const bool ok = !p.cu || cu_well_formed(p.cu, p.n_seq, (int)p.rows);
+    const bool ok = sequences_ok(p);
     grid_trigger();
     grid_wait();
     if (!ok || i >= (long)p.n_seq * p.G) return;
@@ -793,7 +808,7 @@ __global__ void __launch_bounds__(kThreads) seq_means_kernel(GroupNormProblem p,
 
 template <typename T, int V, bool GATE>
 __global__ void __launch_bounds__(kThreads) seq_dx_kernel(GroupNormProblem p, int rows, int per_block, const float2 *means) {
-    const bool ok = !p.cu || cu_well_formed(p.cu, p.n_seq, (int)p.rows);
+    const bool ok = sequences_ok(p);
     grid_trigger();
     grid_wait();
     Tile t;
@@ -846,7 +861,7 @@ __global__ void __launch_bounds__(kThreads) seq_cluster_kernel(GroupNormProblem 
     if (BWD) grid_trigger();
     const int column_blocks = (p.G + per_block - 1) / per_block;
     const int rank = blockIdx.x % blocks, which = blockIdx.x / blocks, cb = which % column_blocks, seq = which / column_blocks;
-    const bool ok = !p.cu || cu_well_formed(p.cu, p.n_seq, (int)p.rows);
+    const bool ok = sequences_ok(p);
     if (!ok && blockIdx.x == 0 && threadIdx.x == 0) atomicExch(p.status, MDN_ERR_INVALID_ARG);
     const int len = !ok ? 0 : p.cu ? p.cu[seq + 1] - p.cu[seq] : p.T;
     const long first = !ok ? 0 : p.cu ? p.cu[seq] : (long)seq * p.T;
@@ -1051,8 +1066,8 @@ struct ClusterShape {
 ClusterShape cluster_shape(const GroupNormProblem &p, int V, int el, bool bwd) {
     const int w = p.D / p.G, arrays = bwd ? (p.gate ? 3 : 2) : 1;
     ClusterShape c = {std::min(p.G, std::max(1, 128 / (w * el))), 0, 0};
-    const long packets = (long)c.per_block * (w / V);
-    if (packets > kThreads) return c;
+    const long packets = (long)c.per_block * (w / V), column_blocks = (p.G + c.per_block - 1) / c.per_block;
+    if (packets > kThreads || p.n_seq * column_blocks * 8 > 0x7fffffffL) return c;
     const long lanes = kThreads / packets, longest = p.cu ? p.rows : p.T;
     for (int blocks = 1; blocks <= 8; blocks *= 2) {
         const long rows = (longest + blocks - 1) / blocks, bytes = (rows + lanes - 1) / lanes * kThreads * V * el * arrays;
@@ -1179,6 +1194,10 @@ cudaError_t run(const GroupNormProblem &p, bool bwd, cudaStream_t st) {
         if ((err = token_pick<T, V, GATE>(p, t, part, bwd, st)) != cudaSuccess) return err;
         return bwd ? params(p, part, t.lanes, st) : cudaSuccess;
     }
+    if (p.ok) {
+        check_kernel<<<1, 1024, 0, st>>>(p);
+        if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    }
     const ClusterShape c = cluster_shape(p, V, (int)sizeof(T), bwd);
     if (c.blocks) {
         float *prm = bwd && (p.dw || p.dbias) ? reinterpret_cast<float *>(p.ws) : nullptr;
@@ -1216,7 +1235,12 @@ cudaError_t gated(const GroupNormProblem &p, bool bwd, cudaStream_t st) {
     return p.gate ? run<T, V, true>(p, bwd, st) : run<T, V, false>(p, bwd, st);
 }
 
-cudaError_t launch(const GroupNormProblem &p, bool bwd, cudaStream_t st) {
+cudaError_t launch(const GroupNormProblem &given, bool bwd, cudaStream_t st) {
+    GroupNormProblem p = given;
+    if (p.cu && p.n_seq > kManySequences) {
+        p.ok = reinterpret_cast<int *>(p.ws);
+        p.ws += 256;
+    }
     if (p.rows == 0) {
         cudaError_t err = cudaSuccess;
         if (!bwd && p.stats && p.over_sequence && p.n_seq)
@@ -1242,7 +1266,8 @@ cudaError_t launch_group_norm_bwd(const GroupNormProblem &p, cudaStream_t st) { 
 
 size_t group_norm_fwd_workspace(int n_seq, long rows, int D, int G, bool over_sequence, mdn_dtype) {
     if (!over_sequence || rows == 0) return 0;
-    return round256(tile_slots(n_seq, rows, D) * G * sizeof(float2)) + round256((long)n_seq * G * sizeof(float2));
+    // (256: check_kernel's flag)
+    return 256 + round256(tile_slots(n_seq, rows, D) * G * sizeof(float2)) + round256((long)n_seq * G * sizeof(float2));
 }
 size_t group_norm_bwd_workspace(int n_seq, long rows, int D, int G, bool over_sequence, mdn_dtype dtype) {
     if (rows == 0) return 0;

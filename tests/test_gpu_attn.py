@@ -281,13 +281,13 @@ def test_prompt_then_tokens():
     check(c, dict(o=torch.cat(outs, 1), S_T=S))
 
 
-def test_nan_and_infinities_stay_with_their_sequence_and_run():
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_nan_and_infinities_stay_with_their_sequence_and_run(dtype):
     """A bad token reaches its own run of 64 tokens, later ones of its sequence
     and the state, and nothing else."""
-    import momentum_delta_rule_gb300 as mdn
     for bad in (float("nan"), float("inf")):
         for name in ("q", "k", "v"):
-            c = case("bf16", [200, 130], 2, 2, 64, 64, True)
+            c = case(dtype, [200, 130], 2, 2, 64, 64, True)
             d = dev(c)
             want = run(d, train=False)
             d[name][0, 70, 0] = bad                   # sequence 0, its second run, head 0
@@ -365,3 +365,75 @@ def test_rows_far_apart():
     torch.cuda.synchronize()
     for name in want:
         assert torch.equal(got[name], want[name]), name
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_many_sequences(dtype):
+    """More than a block orders by itself, some of them empty."""
+    lens = [(7 * i) % 5 for i in range(700)]
+    check_case(case(dtype, lens, 2, 1, 16, 24, True, seed=13))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_what_lies_behind_a_sequence_is_not_read(dtype):
+    """Neighbours' rows come with a run's last tokens and are left out, whatever
+    they hold."""
+    c = case(dtype, [70, 58], 2, 2, 64, 64, True)
+    d = dev(c)
+    want = run(d)
+    for name in ("q", "k", "v", "do"):
+        d[name][0, 70:] = float("nan")
+    got = run(d)
+    torch.cuda.synchronize()
+    for name in ("o", "dq", "dk", "dv"):
+        assert torch.equal(got[name][:, :70], want[name][:, :70]), name
+    assert torch.equal(got["S_T"][0], want["S_T"][0]) and torch.equal(got["dS0"][0], want["dS0"][0])
+
+
+def test_two_streams_at_once():
+    import momentum_delta_rule_gb300 as mdn
+    a, b = (dev(case(dt, [900, 33], 4, 2, 64, 64, True, seed=i)) for i, dt in enumerate(("bf16", "fp32")))
+    want = [run(a), run(b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(10):
+        for i, (d, s) in enumerate(zip((a, b), streams)):
+            with torch.cuda.stream(s):
+                got[i].append(run(d))
+    torch.cuda.synchronize()
+    assert mdn.device_status() == mdn.MDN_OK
+    for w, gs in zip(want, got):
+        for g in gs:
+            for name in w:
+                assert torch.equal(g[name], w[name]), name
+
+
+def test_calls_one_behind_another():
+    """Each call's kernels are set up while the one before it ends: what one call
+    writes the next one reads whole."""
+    import momentum_delta_rule_gb300 as mdn
+    c = case("bf16", [1500, 1500], 2, 2, 64, 64, False)
+    d = dev(c)
+    args = (d["k"], d["v"], d["log_decay"])
+    o, S = mdn.linear_attn_fwd(d["q"], *args, scale=d["scale"], S0=d["S0"])
+    o2, S2 = mdn.linear_attn_fwd(o, *args, scale=d["scale"], S0=S)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        p, P = mdn.linear_attn_fwd(d["q"], *args, scale=d["scale"], S0=d["S0"])
+        p2, P2 = mdn.linear_attn_fwd(p, *args, scale=d["scale"], S0=P)
+        assert torch.equal(p2, o2) and torch.equal(P2, S2)
+
+
+def test_outputs_of_any_alignment():
+    import momentum_delta_rule_gb300 as mdn
+    c = case("bf16", [100, 100], 2, 2, 64, 64, False)
+    d = dev(c)
+    want = run(d, train=False)["o"]
+    buf = torch.zeros(want.numel() + 8, dtype=torch.bfloat16, device="cuda")
+    for off in (1, 2, 3, 8):
+        o = buf[off:off + want.numel()].view(want.shape)
+        mdn.linear_attn_fwd(d["q"], d["k"], d["v"], d["log_decay"], scale=d["scale"], S0=d["S0"], o=o)
+        assert torch.equal(o, want)
+        assert (buf[:off] == 0).all() and (buf[off + want.numel():] == 0).all()
+        buf.zero_()

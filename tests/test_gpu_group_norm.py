@@ -280,3 +280,27 @@ def test_workspaces_hold_what_is_written():
                 g = mdn.group_norm_bwd(d["x"], G, want["stats"], d["dy"], workspace=ws[:need], **kw)
                 assert torch.equal(g["dw"], want["dw"]) and torch.equal(g["dx"], want["dx"])
             assert (ws[need:] == 0x55).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_many_sequences(dtype):
+    check_case(case(dtype, [(7 * i) % 4 for i in range(1500)], 48, 3, over="sequence", seed=17))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("lens,D,G,packed", [([9000], 64, 1, True), ([4001, 3000], 96, 2, True), ([5000, 5000], 40, 1, False),
+                                             ([40000], 16, 2, False)])
+def test_long_sequences(dtype, lens, D, G, packed):
+    """Beyond what a cluster's shared memory holds, and just within."""
+    check_case(case(dtype, lens, D, G, over="sequence", packed=packed, seed=19))
+
+
+def test_a_malformed_end_of_many_sequences():
+    import momentum_delta_rule_gb300 as mdn
+    x = torch.randn(1, 3000, 32, device="cuda")
+    cu = torch.arange(0, 3001, 2, dtype=torch.int32, device="cuda")
+    cu[700] = 5
+    y = torch.full_like(x, 7.0)
+    _, stats = mdn.group_norm_fwd(x, 4, over="sequence", cu_seqlens=cu, y=y, return_stats=True)
+    assert mdn.device_status() == mdn.MDN_ERR_INVALID_ARG
+    assert (y == 7).all() and (stats == 0).all()
