@@ -10,10 +10,14 @@
 //
 // Memory bound.  A token's group is read once: its elements stay in the
 // registers of a few threads, which take the same group of every so-manieth
-// token, so that weights and the parameters' sums stay in registers too.  The
-// groups of a sequence take two readings, the second one after the sums of
-// tiles of its tokens have been joined; a sequence batch that fits the L2 cache
-// is read from memory once.
+// token, so that weights and the parameters' sums stay in registers too.  With 16
+// groups of 128 bf16 columns and a gate, 32768 tokens take 85 us (403 MB: 0.70 of
+// the copy rate), forward and gradient of 16384 tokens 118 (0.50): the activation
+// and its derivative on the CUDA cores, at 24 and 16 warps a multiprocessor.
+// Groups too wide for that are read again from the caches, in loops.
+// The groups of a sequence are read once where a cluster's shared memory holds
+// them, twice otherwise: the second time after the sums of tiles of its tokens
+// have been joined (from the L2 cache, if the batch fits it).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -201,9 +205,15 @@ __device__ __forceinline__ TokenPlace token_place(const GroupNormProblem &p, int
     return t;
 }
 
-// Threads of a block at most: of groups that take more than four packets a
-// thread, as many as the widest group (16384 columns) needs.
-__host__ __device__ constexpr int most_threads(int NI, int V) { return NI <= 4 || V >= 8 ? 256 : V == 4 ? 512 : 1024; }
+// Threads of a block at most where each has NI packets of a group, as many as the
+// registers leave.  Wider groups are taken by blocks of kThreadsWide in loops.
+// (16384 tokens of one group of 2049 fp32 columns, gate: the forward 182 us, in
+// loops 226; with the gradient 461 in loops, 945 with eight packets a thread.)
+__host__ __device__ constexpr int most_threads(int NI, int V, bool bwd) {
+    const int most = (V == 8 ? 2 : V == 4 ? 4 : 8) / (bwd && V < 8 ? 2 : 1);
+    return NI > most ? 0 : bwd && V == 8 ? 256 : 512;
+}
+constexpr int kThreadsWide = 512;
 
 // Q values from the first-th on, as fp32.
 template <int Q, int V>
@@ -217,14 +227,11 @@ __device__ __forceinline__ Packet<float, Q> packet_of(const Vals<V> &r, int firs
     return q;
 }
 
-// Whether a thread keeps weights, and asks for the next token's packets before it
+// A thread keeps its weights, and asks for the next token's packets before it
 // looks at this one's.
-__host__ __device__ constexpr bool held(int NI, int V) { return NI * V <= 16; }
-
 template <typename T, int V, int NI, bool GATE>
-__global__ void __launch_bounds__(most_threads(NI, V)) token_fwd_kernel(GroupNormProblem p, int tpg) {
+__global__ void __launch_bounds__(most_threads(NI, V, false)) token_fwd_kernel(GroupNormProblem p, int tpg) {
     __shared__ Sums<1> red[64];
-    constexpr bool HOLD = held(NI, V);
     int turn = 0;
     const TokenPlace t = token_place(p, tpg);
     const int w = p.D / p.G;
@@ -234,17 +241,15 @@ __global__ void __launch_bounds__(most_threads(NI, V)) token_fwd_kernel(GroupNor
     const T *gate = static_cast<const T *>(p.gate) + t.row * p.ld_gate + c0 + t.tid * V;
     T *y = static_cast<T *>(p.y) + t.row * p.D + c0 + t.tid * V;
     const long x_step = t.step * p.ld_x, gate_step = t.step * p.ld_gate, y_step = t.step * p.D;
-    Vals<V> wt[HOLD ? NI : 1], bs[HOLD ? NI : 1];
-    auto weights = [&](int i, int c) {
-        wt[HOLD ? i : 0] = load_weights<V>(p.weight, c0 + c, 1.f);
-        bs[HOLD ? i : 0] = load_weights<V>(p.bias, c0 + c, 0.f);
-    };
-    if (HOLD)
+    Vals<V> wt[NI], bs[NI];
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int c = (i * tpg + t.tid) * V;
-            if (c < w) weights(i, c);
+    for (int i = 0; i < NI; ++i) {
+        const int c = (i * tpg + t.tid) * V;
+        if (c < w) {
+            wt[i] = load_weights<V>(p.weight, c0 + c, 1.f);
+            bs[i] = load_weights<V>(p.bias, c0 + c, 0.f);
         }
+    }
     Packet<T, V> px[NI], pg[GATE ? NI : 1];
     auto load = [&](long row) {
 #pragma unroll
@@ -259,18 +264,17 @@ __global__ void __launch_bounds__(most_threads(NI, V)) token_fwd_kernel(GroupNor
     };
     const float inv = 1.f / (float)w;
     long row = t.row;
-    if (HOLD) load(row);
+    load(row);
     for (int k = 0; k < t.rounds; ++k, row += t.step) {
         const bool live = row < p.rows;
-        if (!HOLD) load(row);
         Vals<V> d[NI], g[GATE ? NI : 1];
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const bool in = live && (i * tpg + t.tid) * V < w;
             d[i] = in ? values<T, V>(px[i]) : zeros<V>();
-            if (GATE && HOLD) g[i] = values<T, V>(pg[i]);
+            if (GATE) g[i] = values<T, V>(pg[i]);
         }
-        if (HOLD) load(row + t.step);
+        load(row + t.step);
         float mean = 0.f;
         Sums<1> s;
         if (p.center) {
@@ -296,11 +300,8 @@ __global__ void __launch_bounds__(most_threads(NI, V)) token_fwd_kernel(GroupNor
         for (int i = 0; i < NI; ++i) {
             const int c = (i * tpg + t.tid) * V;
             if (live && c < w) {
-                if (!HOLD) weights(i, c);
-                if (GATE && !HOLD) g[i] = values<T, V>(pg[i]);
                 store_packet<T, V>(y + i * tpg * V,
-                                   packet<T, V>(forward_vals<V, GATE>(d[i], g[GATE ? i : 0], rstd, wt[HOLD ? i : 0],
-                                                                      bs[HOLD ? i : 0], p.act)));
+                                   packet<T, V>(forward_vals<V, GATE>(d[i], g[GATE ? i : 0], rstd, wt[i], bs[i], p.act)));
             }
         }
         if (p.stats && live && t.tid == 0)
@@ -309,9 +310,56 @@ __global__ void __launch_bounds__(most_threads(NI, V)) token_fwd_kernel(GroupNor
     }
 }
 
+// The same for groups too wide for that: a block takes one at a time, in loops,
+// and reads it again from the L1 cache for each of the sums and the result.
+template <typename T, int V, bool GATE>
+__global__ void __launch_bounds__(kThreadsWide, 2) wide_fwd_kernel(GroupNormProblem p) {
+    __shared__ Sums<1> red[64];
+    int turn = 0;
+    const TokenPlace t = token_place(p, kThreadsWide);
+    const int w = p.D / p.G;
+    const long c0 = t.g * w;
+    const float inv = 1.f / (float)w;
+    for (long row = t.row; row < p.rows; row += t.step) {
+        const T *x = static_cast<const T *>(p.x) + row * p.ld_x + c0, *gate = static_cast<const T *>(p.gate) + row * p.ld_gate + c0;
+        T *y = static_cast<T *>(p.y) + row * p.D + c0;
+        float mean = 0.f;
+        Sums<1> s;
+        if (p.center) {
+            s.v[0] = 0.f;
+#pragma unroll 4
+            for (int c = t.tid * V; c < w; c += kThreadsWide * V) s.v[0] += sum_of<V>(values<T, V>(load_packet<T, V>(x + c)));
+            mean = group_sum(s, kThreadsWide, red, turn).v[0] * inv;
+        }
+        auto centered = [&](int c) {
+            Vals<V> d = values<T, V>(load_packet<T, V>(x + c));
+#pragma unroll
+            for (int j = 0; j < Vals<V>::N; ++j) d.p[j] = add2(d.p[j], both(-mean));
+            return d;
+        };
+        s.v[0] = 0.f;
+#pragma unroll 4
+        for (int c = t.tid * V; c < w; c += kThreadsWide * V) {
+            Vals<V> d = centered(c);
+#pragma unroll
+            for (int j = 0; j < Vals<V>::N; ++j) d.p[j] = mul2(d.p[j], d.p[j]);
+            s.v[0] += sum_of<V>(d);
+        }
+        const float rstd = rsqrtf(fmaf(group_sum(s, kThreadsWide, red, turn).v[0], inv, p.eps));
+#pragma unroll 2
+        for (int c = t.tid * V; c < w; c += kThreadsWide * V) {
+            Vals<V> g;
+            if (GATE) g = values<T, V>(load_packet<T, V>(gate + c));
+            store_packet<T, V>(y + c, packet<T, V>(forward_vals<V, GATE>(centered(c), g, rstd, load_weights<V>(p.weight, c0 + c, 1.f),
+                                                                         load_weights<V>(p.bias, c0 + c, 0.f), p.act)));
+        }
+        if (p.stats && t.tid == 0) reinterpret_cast<float2 *>(p.stats)[row * p.G + t.g] = make_float2(mean, rstd);
+    }
+}
+
 // part: [row lanes][2][D], one lane for every t.row of the first round.
 template <typename T, int V, int NI, bool GATE>
-__global__ void __launch_bounds__(most_threads(NI, V)) token_bwd_kernel(GroupNormProblem p, int tpg, float *part) {
+__global__ void __launch_bounds__(most_threads(NI, V, true)) token_bwd_kernel(GroupNormProblem p, int tpg, float *part) {
     __shared__ Sums<2> red[64];
     grid_trigger();
     int turn = 0;
@@ -324,16 +372,14 @@ __global__ void __launch_bounds__(most_threads(NI, V)) token_bwd_kernel(GroupNor
     T *dx = static_cast<T *>(p.dx) + t.row * p.D + c0 + t.tid * V, *dgate = static_cast<T *>(p.dgate) + t.row * p.D + c0 + t.tid * V;
     const float2 *stats = reinterpret_cast<const float2 *>(p.stats) + t.row * p.G + t.g;
     const long x_step = t.step * p.ld_x, gate_step = t.step * p.ld_gate, dy_step = t.step * p.ld_dy, out_step = t.step * p.D;
-    constexpr bool HOLD = held(NI, V);
-    Vals<V> wt[HOLD ? NI : 1], bs[HOLD ? NI : 1], dw[NI], db[NI];
-    auto weights = [&](int i, int c) {
-        wt[HOLD ? i : 0] = load_weights<V>(p.weight, c0 + c, 1.f);
-        bs[HOLD ? i : 0] = load_weights<V>(p.bias, c0 + c, 0.f);
-    };
+    Vals<V> wt[NI], bs[NI], dw[NI], db[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
         const int c = (i * tpg + t.tid) * V;
-        if (HOLD && c < w) weights(i, c);
+        if (c < w) {
+            wt[i] = load_weights<V>(p.weight, c0 + c, 1.f);
+            bs[i] = load_weights<V>(p.bias, c0 + c, 0.f);
+        }
         dw[i] = db[i] = zeros<V>();
     }
     Packet<T, V> px[NI], pd[NI], pg[GATE ? NI : 1];
@@ -355,42 +401,33 @@ __global__ void __launch_bounds__(most_threads(NI, V)) token_bwd_kernel(GroupNor
     };
     const float inv = 1.f / (float)w;
     long row = t.row;
-    if (HOLD) load(row);
+    load(row);
     for (int k = 0; k < t.rounds; ++k, row += t.step) {
         const bool live = row < p.rows;
-        if (!HOLD) load(row);
         st = next;
-        // n and du of the thread's elements, kept where they are few and
-        // worked out twice where they are many
-        Vals<V> n[HOLD ? NI : 1], d[HOLD ? NI : 1], g[HOLD ? NI : 1];
-        auto element = [&](int i, int c, int to) {
-            if (!HOLD) weights(i, c);
-            n[to] = values<T, V>(px[i]);
-            d[to] = values<T, V>(pd[i]);
-            if (GATE) g[to] = values<T, V>(pg[i]);
-        };
-        auto finish = [&](int to) { backward_vals<V, GATE>(n[to], g[to], d[to], st.x, st.y, wt[to], bs[to], p.act); };
-        if (HOLD) {
+        Vals<V> n[NI], d[NI], g[NI];
 #pragma unroll
-            for (int i = 0; i < NI; ++i) element(i, 0, HOLD ? i : 0);
-            load(row + t.step);
+        for (int i = 0; i < NI; ++i) {
+            n[i] = values<T, V>(px[i]);
+            d[i] = values<T, V>(pd[i]);
+            if (GATE) g[i] = values<T, V>(pg[i]);
         }
+        load(row + t.step);
         Sums<2> s;
         s.v[0] = s.v[1] = 0.f;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int c = (i * tpg + t.tid) * V, to = HOLD ? i : 0;
+            const int c = (i * tpg + t.tid) * V;
             if (live && c < w) {
-                if (!HOLD) element(i, c, to);
-                finish(to);
-                if (GATE) store_packet<T, V>(dgate + i * tpg * V, packet<T, V>(g[to]));
+                backward_vals<V, GATE>(n[i], g[i], d[i], st.x, st.y, wt[i], bs[i], p.act);
+                if (GATE) store_packet<T, V>(dgate + i * tpg * V, packet<T, V>(g[i]));
                 Vals<V> dn, dnn;
 #pragma unroll
                 for (int j = 0; j < Vals<V>::N; ++j) {
-                    dw[i].p[j] = fma2(d[to].p[j], n[to].p[j], dw[i].p[j]);
-                    db[i].p[j] = add2(d[to].p[j], db[i].p[j]);
-                    dn.p[j] = mul2(d[to].p[j], wt[to].p[j]);
-                    dnn.p[j] = mul2(dn.p[j], n[to].p[j]);
+                    dw[i].p[j] = fma2(d[i].p[j], n[i].p[j], dw[i].p[j]);
+                    db[i].p[j] = add2(d[i].p[j], db[i].p[j]);
+                    dn.p[j] = mul2(d[i].p[j], wt[i].p[j]);
+                    dnn.p[j] = mul2(dn.p[j], n[i].p[j]);
                 }
                 s.v[0] += sum_of<V>(dn);
                 s.v[1] += sum_of<V>(dnn);
@@ -400,16 +437,12 @@ __global__ void __launch_bounds__(most_threads(NI, V)) token_bwd_kernel(GroupNor
         const Pair m1 = both(p.center ? -s.v[0] * inv : 0.f), m2 = both(-s.v[1] * inv), r = both(st.y);
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int c = (i * tpg + t.tid) * V, to = HOLD ? i : 0;
+            const int c = (i * tpg + t.tid) * V;
             if (live && c < w) {
-                if (!HOLD) {
-                    element(i, c, to);
-                    finish(to);
-                }
                 Vals<V> out;
 #pragma unroll
                 for (int j = 0; j < Vals<V>::N; ++j)
-                    out.p[j] = mul2(r, fma2(n[to].p[j], m2, fma2(d[to].p[j], wt[to].p[j], m1)));
+                    out.p[j] = mul2(r, fma2(n[i].p[j], m2, fma2(d[i].p[j], wt[i].p[j], m1)));
                 store_packet<T, V>(dx + i * tpg * V, packet<T, V>(out));
             }
         }
@@ -430,6 +463,90 @@ __global__ void __launch_bounds__(most_threads(NI, V)) token_bwd_kernel(GroupNor
             }
         }
     }
+}
+
+// The same for groups too wide for that, as wide_fwd_kernel: what the sums take
+// is worked out again for dx; the parameters' sums are in shared memory, every
+// thread its own columns'.
+template <typename T, int V, bool GATE>
+__global__ void __launch_bounds__(kThreadsWide, 2) wide_bwd_kernel(GroupNormProblem p, float *part) {
+    __shared__ Sums<2> red[64];
+    extern __shared__ __align__(16) unsigned char acc_raw[];
+    grid_trigger();
+    int turn = 0;
+    const TokenPlace t = token_place(p, kThreadsWide);
+    const int w = p.D / p.G;
+    const long c0 = t.g * w;
+    const float inv = 1.f / (float)w;
+    using Acc = Packet<float, V < 4 ? V : 4>;
+    constexpr int Q = V < 4 ? V : 4;
+    float *dw = reinterpret_cast<float *>(acc_raw), *db = dw + w;
+    if (part)
+        for (int c = t.tid * V; c < w; c += kThreadsWide * V)
+#pragma unroll
+            for (int j = 0; j < V; ++j) dw[c + j] = db[c + j] = 0.f;
+    for (long row = t.row; row < p.rows; row += t.step) {
+        const T *x = static_cast<const T *>(p.x) + row * p.ld_x + c0, *gate = static_cast<const T *>(p.gate) + row * p.ld_gate + c0,
+                *dy = static_cast<const T *>(p.dy) + row * p.ld_dy + c0;
+        T *dx = static_cast<T *>(p.dx) + row * p.D + c0, *dgate = static_cast<T *>(p.dgate) + row * p.D + c0;
+        const float2 st = reinterpret_cast<const float2 *>(p.stats)[row * p.G + t.g];
+        Vals<V> n, d, g, wt;
+        auto element = [&](int c) {
+            n = values<T, V>(load_packet<T, V>(x + c));
+            d = values<T, V>(load_packet<T, V>(dy + c));
+            if (GATE) g = values<T, V>(load_packet<T, V>(gate + c));
+            wt = load_weights<V>(p.weight, c0 + c, 1.f);
+            backward_vals<V, GATE>(n, g, d, st.x, st.y, wt, load_weights<V>(p.bias, c0 + c, 0.f), p.act);
+        };
+        Sums<2> s;
+        s.v[0] = s.v[1] = 0.f;
+#pragma unroll 2
+        for (int c = t.tid * V; c < w; c += kThreadsWide * V) {
+            element(c);
+            Vals<V> dn, dnn, du_n;
+#pragma unroll
+            for (int j = 0; j < Vals<V>::N; ++j) {
+                du_n.p[j] = mul2(d.p[j], n.p[j]);
+                dn.p[j] = mul2(d.p[j], wt.p[j]);
+                dnn.p[j] = mul2(dn.p[j], n.p[j]);
+            }
+            s.v[0] += sum_of<V>(dn);
+            s.v[1] += sum_of<V>(dnn);
+            if (part)
+#pragma unroll
+                for (int q = 0; q < V; q += Q) {
+                    Acc a = load_packet<float, Q>(dw + c + q), b = load_packet<float, Q>(db + c + q);
+                    const Acc da = packet_of<Q>(du_n, q), dbb = packet_of<Q>(d, q);
+#pragma unroll
+                    for (int j = 0; j < Q; ++j) {
+                        a.e[j] += da.e[j];
+                        b.e[j] += dbb.e[j];
+                    }
+                    store_packet<float, Q>(dw + c + q, a);
+                    store_packet<float, Q>(db + c + q, b);
+                }
+        }
+        s = group_sum(s, kThreadsWide, red, turn);
+        const Pair m1 = both(p.center ? -s.v[0] * inv : 0.f), m2 = both(-s.v[1] * inv), r = both(st.y);
+#pragma unroll 2
+        for (int c = t.tid * V; c < w; c += kThreadsWide * V) {
+            element(c);
+            Vals<V> out;
+#pragma unroll
+            for (int j = 0; j < Vals<V>::N; ++j)
+                out.p[j] = mul2(r, fma2(n.p[j], m2, fma2(d.p[j], wt.p[j], m1)));
+            if (GATE) store_packet<T, V>(dgate + c, packet<T, V>(g));
+            store_packet<T, V>(dx + c, packet<T, V>(out));
+        }
+    }
+    if (!part) return;
+    float *out = part + t.row * 2 * p.D + c0;
+    for (int c = t.tid * V; c < w; c += kThreadsWide * V)
+#pragma unroll
+        for (int q = 0; q < V; q += Q) {
+            store_packet<float, Q>(out + c + q, load_packet<float, Q>(dw + c + q));
+            store_packet<float, Q>(out + p.D + c + q, load_packet<float, Q>(db + c + q));
+        }
 }
 
 // dw, dbias <- sums over the lanes of part, in a fixed order.
@@ -1059,7 +1176,9 @@ long tile_slots(int n_seq, long rows, int D) { return rows / tile_rows(rows, D) 
 // bytes a token, and so many blocks that a thread's packets of the longest
 // sequence there can be fit shared memory, three blocks to a multiprocessor where
 // that goes.  (8 sequences of 2048 tokens of 2048 bf16 columns in 32 groups:
-// CLUSTERNOW us, and 65 in tiles.)
+// 47 us; with two blocks to a multiprocessor 52, in tiles 64.  Forward and
+// gradient of 1531 fp32 tokens of 330 columns in 6 groups and 5 sequences: 64,
+// and 84 in tiles.)
 struct ClusterShape {
     int per_block, blocks, smem;
 };
@@ -1089,32 +1208,41 @@ struct TokenShape {
 };
 long gcd(long a, long b) { return b ? gcd(b, a % b) : a; }
 
-TokenShape token_shape(const GroupNormProblem &p, int V, int per_sm) {
-    TokenShape t;
-    const long P = (p.D / p.G) / V;
-    // up to four packets a thread before a group takes several warps, and more
-    // where that would take more than a block of 256
-    const int each = P <= 4 * kThreads ? 4 : 8;
-    t.tpg = P <= 32 ? pow2_at_least(P) : std::max(32, pow2_at_least((P + each - 1) / each));
-    t.NI = (int)((P + t.tpg - 1) / t.tpg);
-    if (t.tpg > 1024) {
-        t.tpg = 1024;
-        t.NI = (int)((P + 1023) / 1024);
-    }
-    t.NI = pow2_at_least(t.NI);
-    t.threads = std::max(kThreads, t.tpg);
+// Over `most` blocks at most.
+void spread(const GroupNormProblem &p, TokenShape &t, long most) {
     const long ipb = t.threads / t.tpg, unit = p.G / gcd(ipb, p.G);
-    const long need = (p.rows * p.G + ipb - 1) / ipb, most = 152L * std::max(1, per_sm * kThreads / t.threads);
-    long blocks = std::min(need, most);
-    blocks = blocks / unit * unit;
+    const long blocks = std::min((p.rows * p.G + ipb - 1) / ipb, most) / unit * unit;
     t.blocks = std::max(blocks, unit);
     t.lanes = t.blocks * ipb / p.G;
+}
+// The gradient's blocks: two of 256 threads to a multiprocessor, as many as are
+// there at once, since each lane of tokens leaves a row of the parameters' sums
+// behind.  (16384 tokens of 16 groups of 128 bf16 columns, gate: forward and
+// gradient 124 us; with one block 154, three 141, four 123.)
+TokenShape token_shape(const GroupNormProblem &p, int V, bool bwd) {
+    TokenShape t;
+    const long P = (p.D / p.G) / V;
+    // Two packets a thread, of small ones four, and more only where a block has no
+    // more threads: more of them leave no registers for weights and the next token.
+    // (32768 tokens of one group of 2048 bf16 columns, gate: one 110 us, two 86,
+    // four 230; of four groups: 101, 79, 78.  16384 tokens of 1023 fp32 columns:
+    // two 84, four 67.)
+    for (int each = V < 4 ? 4 : 2;; each *= 2) {
+        t.tpg = P <= 32 ? pow2_at_least(P) : std::max(32, pow2_at_least((P + each - 1) / each));
+        t.NI = pow2_at_least((P + t.tpg - 1) / t.tpg);
+        const int most = most_threads(t.NI, V, bwd);
+        if (t.tpg <= most) break;
+        if (most == 0) {
+            t.tpg = t.threads = kThreadsWide;
+            t.NI = 0;
+            spread(p, t, 152L * 2);
+            return t;
+        }
+    }
+    t.threads = std::max(kThreads, t.tpg);
+    spread(p, t, 152L * std::max(1, 2 * kThreads / t.threads));
     return t;
 }
-
-// The gradient's blocks: each lane of tokens leaves a row of the parameters'
-// sums behind, which are read again.
-constexpr int kFwdPerSM = 8, kBwdPerSM = 2;
 long token_lanes_most(long rows, int D, int G) {
     const long w = D / G;
     long most = 0;
@@ -1124,7 +1252,7 @@ long token_lanes_most(long rows, int D, int G) {
         p.rows = rows;
         p.D = D;
         p.G = G;
-        most = std::max(most, token_shape(p, V, kBwdPerSM).lanes);
+        most = std::max(most, token_shape(p, V, true).lanes);
     }
     return most;
 }
@@ -1144,20 +1272,53 @@ int width_of(const GroupNormProblem &p, bool bwd) {
 }
 
 template <typename T, int V, int NI, bool GATE>
-cudaError_t token_launch(const GroupNormProblem &p, const TokenShape &t, float *part, bool bwd, cudaStream_t st) {
-    if (bwd) token_bwd_kernel<T, V, NI, GATE><<<(unsigned)t.blocks, t.threads, 0, st>>>(p, t.tpg, part);
-    else token_fwd_kernel<T, V, NI, GATE><<<(unsigned)t.blocks, t.threads, 0, st>>>(p, t.tpg);
+cudaError_t token_launch(const GroupNormProblem &p, TokenShape t, float *part, bool bwd, cudaStream_t st) {
+    if (bwd) {
+        if constexpr (most_threads(NI, V, true) > 0)
+            token_bwd_kernel<T, V, NI, GATE><<<(unsigned)t.blocks, t.threads, 0, st>>>(p, t.tpg, part);
+        return cudaGetLastError();
+    }
+    // The forward takes two whole waves: blocks end at different times, and the
+    // second one's fill the gaps.  (32768 tokens of 16 groups of 128 columns,
+    // gate.  bf16, three blocks to a multiprocessor at once: in all 5 96 us, 6 85,
+    // 7 98, 8 92, 12 90; fp32, four: 5 171, 6 150, 7 141, 8 134, 12 135.)
+    spread(p, t, 1L << 30);
+    if (t.blocks > 152) {
+        int resident = 1;
+        const cudaError_t err =
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, token_fwd_kernel<T, V, NI, GATE>, t.threads, 0);
+        if (err != cudaSuccess) return err;
+        spread(p, t, 152L * 2 * std::max(1, resident));
+    }
+    token_fwd_kernel<T, V, NI, GATE><<<(unsigned)t.blocks, t.threads, 0, st>>>(p, t.tpg);
+    return cudaGetLastError();
+}
+template <typename T, int V, bool GATE>
+cudaError_t wide_launch(const GroupNormProblem &p, const TokenShape &t, float *part, bool bwd, cudaStream_t st) {
+    if (bwd) {
+        const int smem = part ? 2 * (p.D / p.G) * (int)sizeof(float) : 0;
+        // (the widest group's)
+        const cudaError_t err = smem > 47 * 1024 ? allow_shared<wide_bwd_kernel<T, V, GATE>>(2 * 16384 * (int)sizeof(float)) : cudaSuccess;
+        if (err != cudaSuccess) return err;
+        wide_bwd_kernel<T, V, GATE><<<(unsigned)t.blocks, kThreadsWide, smem, st>>>(p, part);
+    } else {
+        wide_fwd_kernel<T, V, GATE><<<(unsigned)t.blocks, kThreadsWide, 0, st>>>(p);
+    }
     return cudaGetLastError();
 }
 template <typename T, int V, bool GATE>
 cudaError_t token_pick(const GroupNormProblem &p, const TokenShape &t, float *part, bool bwd, cudaStream_t st) {
     switch (t.NI) {
+        case 0: return wide_launch<T, V, GATE>(p, t, part, bwd, st);
         case 1: return token_launch<T, V, 1, GATE>(p, t, part, bwd, st);
         case 2: return token_launch<T, V, 2, GATE>(p, t, part, bwd, st);
-        case 4: return token_launch<T, V, 4, GATE>(p, t, part, bwd, st);
-        case 8: return token_launch<T, V, 8, GATE>(p, t, part, bwd, st);
-        default: return token_launch<T, V, 16, GATE>(p, t, part, bwd, st);
+        case 4:
+            if constexpr (V < 8) return token_launch<T, V, 4, GATE>(p, t, part, bwd, st);
+            break;
+        case 8:
+            if constexpr (V < 4) return token_launch<T, V, 8, GATE>(p, t, part, bwd, st);
     }
+    return cudaErrorInvalidValue;      // (token_shape gives no others)
 }
 
 cudaError_t params(const GroupNormProblem &p, const float *part, long lanes, cudaStream_t st) {
@@ -1189,7 +1350,7 @@ template <typename T, int V, bool GATE>
 cudaError_t run(const GroupNormProblem &p, bool bwd, cudaStream_t st) {
     cudaError_t err;
     if (!p.over_sequence) {
-        const TokenShape t = token_shape(p, V, bwd ? kBwdPerSM : kFwdPerSM);
+        const TokenShape t = token_shape(p, V, bwd);
         float *part = bwd && (p.dw || p.dbias) ? reinterpret_cast<float *>(p.ws) : nullptr;
         if ((err = token_pick<T, V, GATE>(p, t, part, bwd, st)) != cudaSuccess) return err;
         return bwd ? params(p, part, t.lanes, st) : cudaSuccess;

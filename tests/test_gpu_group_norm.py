@@ -154,6 +154,13 @@ def test_groups_of_a_token(dtype, rows, D, G):
     check_case(case(dtype, [rows], D, G, seed=rows))
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("rows,D,G", [(650, 2049, 1), (330, 4098, 2), (400, 4608, 1), (310, 2438, 1), (700, 1536, 1)])
+def test_wide_groups_of_more_tokens_than_blocks(dtype, gate, rows, D, G):
+    check_case(case(dtype, [rows], D, G, gate, seed=rows))
+
+
 SEQS = [([1], 4, 2, True), ([64, 64], 64, 4, False), ([5, 0, 130, 1], 330, 6, True), ([700], 96, 1, True),
         ([33, 33, 33], 2048, 32, False), ([40, 3], 1001, 7, True), ([300, 20], 16, 16, True), ([9, 2], 16384, 1, True),
         ([7], 8190, 2, True), ([2100, 900], 40, 5, True)]
