@@ -18,7 +18,10 @@
 //   hi = D1 W rounded,  lo = D2 W + (D1 W - hi) rounded,
 // where D1 W - hi needs no more than bf16's eight bits and is exact: three
 // bf16x2 fmas for two elements, and 2^-18 more is left out.  (In fp32, with
-// conversions both ways, twelve instructions.)
+// conversions both ways, twelve instructions.)  States are off by 4e-6 in all.  A
+// third part has no room beside three stages in shared memory; with the parts
+// in TMEM as MMA4's first operand there is room, states are as exact as fp32 has
+// them, and the prompts below take 145 us.
 //
 // One CTA takes a run of a sequence's tokens and one head.  Warps: 0 and 1 copy
 // X, Y and W into the 128-byte-swizzled operand layout; 2 issues MMA1 and MMA4,
@@ -36,9 +39,13 @@
 // schedulers and an instruction cache, so that every instruction saved shortens
 // all the handovers, and loops are kept short rather than unrolled (straight
 // code that each warp runs once a chunk waits for its instructions).  Packed
-// prompts of 32768 tokens, 16 heads of 128: 488 us at first, 213 with lane 0's
-// branch replaced by elect.sync and O's registers freed early, 161 with short
-// loops, 127 with two issuers, bf16x2 splitting and waits that only count.
+// prompts of 32768 tokens in 21 sequences, 16 heads of 128: 488 us at first, 213
+// with lane 0's branch replaced by elect.sync and O's registers freed early, 161
+// with short loops, 127 with two issuers, bf16x2 splitting and waits that only
+// count, 114 with TMA and sequences that order themselves (537 MB, 0.69 of the copy
+// rate).  A chunk is 1964 cycles of the tensor pipe (MMA1 58 a step, MMA2 43, MMA3
+// 77, MMA4 106) and takes some 3200: handovers along MMA4 -> Z -> MMA2, and issue
+// slots (54 %).  The state's warps splitting too, instead of warps 4..7: 119 us.
 // Every wait is bounded (1 s); on expiry the CTA records MDN_ERR_DEVICE_TIMEOUT,
 // drains its copies and MMAs, frees TMEM and returns.
 #include "mdn_attn_tc.cuh"
@@ -96,17 +103,14 @@ __device__ __forceinline__ uint32_t neg_bf16x2(uint32_t a) {
     asm("neg.bf16x2 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
-// 16 (BYTES) or 4 bytes, or zeros.
-template <int BYTES>
+
+// 4 bytes, or zeros.
 __device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const void *src, bool take) {
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(take ? 4 : 0) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(take ? 4 : 0) : "memory");
 }
 
-// Without TMA: one warp copies rows [from, to) of `width` columns into a tile (zeros from the
-// n-th on), V elements at a time.
+// Without TMA: one warp copies rows [from, to) of `width` columns into a tile
+// (zeros from the n-th on), V elements (one or two) at a time.
 template <int V>
 __device__ __forceinline__ void copy_tile(uint32_t tile, const __nv_bfloat16 *src, long ld, int width, int n, int from,
                                           int to) {
@@ -135,8 +139,8 @@ __device__ __forceinline__ void copy_tile(uint32_t tile, const __nv_bfloat16 *sr
         const int total = to * per;
         for (int i = from * per + lane; i < total; i += 32) {
             const int r = i / per, c = (i - r * per) * V;
-            cp_async_or_zero<V * 2>(tile + (c >> 6) * kBlock + sw128_offset(r, (c & 63) >> 3) + (c & 7) * 2,
-                                    r < n ? src + r * ld + c : src, r < n);
+            cp_async_or_zero(tile + (c >> 6) * kBlock + sw128_offset(r, (c & 63) >> 3) + (c & 7) * 2,
+                             r < n ? src + r * ld + c : src, r < n);
         }
     }
 }
@@ -243,9 +247,8 @@ attn_tc_kernel(const __grid_constant__ AttnProblem p, const __grid_constant__ Al
             const int st = c % kStages, n = chunk_len(c);
             if (c >= kStages && !warp_wait(&bars->empty[st], (c / kStages - 1) & 1, abort)) break;
             unsigned char *stage = smem + st * kStage;
-            const uint32_t tile = smem_u32(stage);
             const long t0 = it.start + (long)chunk_at(c);
-            if (kTma) {
+            if constexpr (kTma) {
                 // (boxes of whole chunks: behind the last sequence's end they
                 // are filled with zeros, behind another's the rows are replaced)
                 uint64_t *landed = n == kC ? &bars->full[st] : &bars->partial;
@@ -269,14 +272,15 @@ attn_tc_kernel(const __grid_constant__ AttnProblem p, const __grid_constant__ Al
                     fence_proxy_async();
                     warp_arrive(&bars->full[st]);
                 }
-                continue;
+            } else {
+                const uint32_t tile = smem_u32(stage);
+                const int from = warp * (kC / 2), to = (warp + 1) * (kC / 2);
+                copy_tile<V>(tile + kTile, Y + t0 * a.ld_y, a.ld_y, kd, n, from, to);
+                if (warp == 1) copy_tile<V>(tile + 2 * kTile, W + t0 * a.ld_w, a.ld_w, vd, n, 0, kC);
+                else if (!states_only) copy_tile<V>(tile, X + t0 * a.ld_x, a.ld_x, kd, n, 0, kC);
+                if (V == 1) mbar_arrive(&bars->full[st]);
+                else copies_arrive(&bars->full[st]);      // every lane, when its own copies have landed
             }
-            const int from = warp * (kC / 2), to = (warp + 1) * (kC / 2);
-            copy_tile<V>(tile + kTile, Y + t0 * a.ld_y, a.ld_y, kd, n, from, to);
-            if (warp == 1) copy_tile<V>(tile + 2 * kTile, W + t0 * a.ld_w, a.ld_w, vd, n, 0, kC);
-            else if (!states_only) copy_tile<V>(tile, X + t0 * a.ld_x, a.ld_x, kd, n, 0, kC);
-            if (V == 1) mbar_arrive(&bars->full[st]);
-            else copies_arrive(&bars->full[st]);      // every lane, when its own copies have landed
         }
         if (kTma) {
             // every issued copy must land before the CTA may exit (a partial
