@@ -83,6 +83,18 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<uint32_t *>(&v);
 }
 
+// a, b -> N bf16 parts, packed: each what the ones before it leave, rounded.
+template <int N>
+__device__ __forceinline__ void split_parts(float a, float b, uint32_t *part) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        part[i] = pack2(a, b);
+        if (i == N - 1) break;
+        a -= __uint_as_float(part[i] << 16);
+        b -= __uint_as_float(part[i] & 0xffff0000u);
+    }
+}
+
 // Launches a pass's kernel: set up while the kernel before it ends, which it
 // waits for (grid_dependency_wait) before it reads anything.
 template <typename... P, typename... A>

@@ -47,21 +47,11 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= kBarsBytes, "barrier block");
 
-// a, b -> their three parts, packed.
-__device__ __forceinline__ void split3(float a, float b, uint32_t *part) {
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        part[i] = pack2(a, b);
-        if (i == 2) break;
-        a -= __uint_as_float(part[i] << 16);
-        b -= __uint_as_float(part[i] & 0xffff0000u);
-    }
-}
 // Eight columns of a row as the operand's 16-byte packets.
 __device__ __forceinline__ void put_parts(unsigned char *operand, uint32_t part_bytes, uint32_t at, const float *f) {
     uint32_t r[4][3];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) split3(f[2 * q], f[2 * q + 1], r[q]);
+    for (int q = 0; q < 4; ++q) split_parts<3>(f[2 * q], f[2 * q + 1], r[q]);
 #pragma unroll
     for (int i = 0; i < 3; ++i)
         *reinterpret_cast<uint4 *>(operand + i * part_bytes + at) = make_uint4(r[0][i], r[1][i], r[2][i], r[3][i]);
@@ -158,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc32_kernel(const __grid_con
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
             uint32_t r[3];
-            split3(z[2 * k], z[2 * k + 1], r);
+            split_parts<3>(z[2 * k], z[2 * k + 1], r);
 #pragma unroll
             for (int i = 0; i < 3; ++i) part[i][k] = __uint_as_float(r[i]);
         }
