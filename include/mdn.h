@@ -711,9 +711,9 @@ size_t mdn_linear_attn_bwd_workspace_size(int n_seq, int T_total, int H, int Hkv
  * log_decay is expected to be at most zero; larger values are computed as
  * written and may overflow.  -inf is a decay of zero.
  * States are fp32.  bf16 rows meet in products of bf16 with fp32 sums, in which
- * the states before each 64 tokens, the decayed q k^T within them and the decayed
- * v that states gather are taken as two bf16 parts each: outputs are the formulas'
- * rounded to bf16 once, a state is off by some 4e-6 of its size.  fp32 rows are multiplied as three
+ * the states before each 64 tokens and the decayed q k^T within them are taken as
+ * two bf16 parts each and the decayed v that states gather as three: outputs are
+ * the formulas' rounded to bf16 once, states as exact as in fp32.  fp32 rows are multiplied as three
  * bf16 parts each, as exactly as in fp32; their values are expected below 3e38.
  * Infinite and NaN rows reach what the formulas carry them to and, beyond that,
  * the other tokens of their sequence's run of 64 tokens, where they may appear

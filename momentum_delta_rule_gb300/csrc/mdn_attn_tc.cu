@@ -13,41 +13,40 @@
 //
 // The decays l^(i+1) of O1 are applied to the fp32 result and the state is kept
 // in fp32 registers.  A term of out passes one operand that is not bf16 as it
-// comes, P or Z: in two parts (2^-17 of it), so that out is rounded once.  (With
-// one part each outputs are off by 2.3e-3 instead of 1.7e-3, and the prompts below
-// take 104 us instead of 123.)  D W is split into two bf16 parts, and Y is bf16 as
-// it comes.  With D = D1 + D2 in bf16 (to 2^-18),
-//   hi = D1 W rounded,  lo = D2 W + (D1 W - hi) rounded,
-// where D1 W - hi needs no more than bf16's eight bits and is exact: three
-// bf16x2 fmas for two elements, and 2^-18 more is left out.  (In fp32, with
-// conversions both ways, twelve instructions.)  States are off by 4e-6 in all.  A
-// third part has no room beside three stages in shared memory; with the parts
-// in TMEM as MMA4's first operand there is room, states are as exact as fp32 has
-// them, and the prompts below take 145 us.
+// comes, P or Z: in two parts (2^-17 of it), so that out is rounded once, to its
+// type.  D W comes in three parts, all 24 bits of an fp32 product, and Y is bf16, so
+// that states are as exact as fp32 has them: off by 2e-7.  (One part of P and Z
+// and two of D W: outputs off by 2.3e-3 instead of 1.7e-3, states by 4e-6, and
+// the prompts below take 104 us instead of 134.)
 //
 // One CTA takes a run of a sequence's tokens and one head.  Warps: 0 and 1 copy
 // X, Y and W into the 128-byte-swizzled operand layout; 2 issues MMA1 and MMA4,
-// 3 owns TMEM and issues MMA2 and MMA3; 4..7 split D W; 8..11 turn A into P;
-// 12..15 write the outputs; 16..31 keep Z, 32 columns each of their TMEM
-// quadrant's 32 rows.  The only chain along the tokens is MMA4 -> Z -> MMA2.
+// 3 owns TMEM and issues MMA2 and MMA3; 4..7 turn A into P; 8..11 write the
+// outputs; 12..27 keep Z, 32 columns each of their TMEM quadrant's 32 rows, and
+// split the next chunk's D W (for states alone warps 4..11 do).  The only chain
+// along the tokens is MMA4 -> Z -> MMA2.  TMEM is full: A lies in the buffer of the
+// O2 that it leads to, which is written when A has been read.
 //
 // Rows on 16-byte boundaries come by TMA, others with cp.async or plain loads.
 // In a sequence's last, partial chunk the tokens behind its end are zeros and
 // not the next sequence's.  (Outputs staged in the chunk's X tile by stmatrix
 // and stored by TMA took fewer instructions, but kept the tile from the next
-// load: 145 us for the prompts below.)
+// load.)
 //
-// What it is made for is few instructions: 32 warps of seven roles share four
+// What it is made for is few instructions: 28 warps of six roles share four
 // schedulers and an instruction cache, so that every instruction saved shortens
-// all the handovers, and loops are kept short rather than unrolled (straight
-// code that each warp runs once a chunk waits for its instructions).  Packed
-// prompts of 32768 tokens in 21 sequences, 16 heads of 128: 488 us at first, 213
-// with lane 0's branch replaced by elect.sync and O's registers freed early, 161
-// with short loops, 127 with two issuers, bf16x2 splitting and waits that only
-// count, 114 with TMA and sequences that order themselves (537 MB, 0.69 of the copy
-// rate).  A chunk is 1964 cycles of the tensor pipe (MMA1 58 a step, MMA2 43, MMA3
-// 77, MMA4 106) and takes some 3200: handovers along MMA4 -> Z -> MMA2, and issue
-// slots (54 %).  The state's warps splitting too, instead of warps 4..7: 119 us.
+// all the handovers; the roles' loops are kept short (straight code that each
+// warp runs once a chunk waits for its instructions).  The issuers' are not: what
+// is added to a descriptor is known, two instructions an MMA (in loops the same
+// products took 154 us, up to 150 cycles an MMA).  Packed prompts of 32768 tokens in
+// 21 sequences, 16 heads of 128: 134 us (537 MB, 0.59 of the copy rate).  A chunk
+// takes some 3600 cycles.  Its products are 3040 cycles of the tensor pipe where
+// each runs by itself (MMA1 58 a step, MMA2 43, MMA3 77, MMA4 106), and its
+// operands, parts and rows 336 KB through shared memory, 2700 cycles at 128 bytes:
+// shared memory first, and with it every wait on a barrier.  Tried: four warps
+// that do nothing but split 133 (one long prompt 112 instead of 108, training 191
+// instead of 187); the split behind dZ, in one buffer, 145; one issuer in a fixed
+// order 159; MMA3 without the blocks that are zero 138.
 // Every wait is bounded (1 s); on expiry the CTA records MDN_ERR_DEVICE_TIMEOUT,
 // drains its copies and MMAs, frees TMEM and returns.
 #include "mdn_attn_tc.cuh"
@@ -57,11 +56,13 @@ namespace {
 
 using namespace attn_tc;
 
-constexpr int kThreads = 1024;
-constexpr int kStages = 3;
-constexpr uint32_t kStage = 3 * kTile;            // X, Y, W
-constexpr uint32_t kOffParts = kStages * kStage;  // two buffers of D W in two parts
-constexpr uint32_t kOffP = kOffParts + 4 * kTile; // two parts of P
+constexpr int kThreads = 896;
+// Places for chunks: two of X and Y, three of W, which is split a chunk ahead.
+constexpr int kStages = 2, kStagesW = 3;
+constexpr uint32_t kStage = 2 * kTile;                                // X, Y
+constexpr uint32_t kOffW = kStages * kStage;
+constexpr uint32_t kOffParts = kOffW + kStagesW * kTile;              // two buffers of D W in three parts
+constexpr uint32_t kOffP = kOffParts + 6 * kTile;                     // two parts of P
 constexpr uint32_t kOffBars = kOffP + 2 * kBlock;
 constexpr uint32_t kBarsBytes = 2560;
 constexpr uint32_t kSmem = kOffBars + kBarsBytes;
@@ -73,7 +74,7 @@ constexpr uint32_t kColD = 256, kColZ = 384 /* two parts of 64 */;
 constexpr uint32_t kTmemCols = 512;
 
 struct Bars {
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[kStages], empty[kStages], full_w[kStagesW], empty_w[kStagesW];
     // What one side may do twice before the other looks has a barrier for each
     // buffer: a wait sees no more than the last completion.
     uint64_t o1_done, d_ready, d_free, z_ready, p_ready, partial, drain[2];
@@ -85,26 +86,13 @@ struct Bars {
     // what enters with the state decays by l^(i+1) out_scale, what leaves with it
     // by l^(n-1-i) w_scale; reversed, the other way round.  [0]: whole chunks,
     // [1]: the run's partial one.
-    alignas(16) float enter[2][kC];
-    uint2 leave[2][kC];               // (two equal bf16 of its upper part, and of its lower one)
+    alignas(16) float enter[2][kC], leave[2][kC];
 };
 static_assert(sizeof(Bars) <= kBarsBytes, "barrier block");
 
 // Arrives on `bar` when all of this thread's cp.async so far have landed.
 __device__ __forceinline__ void copies_arrive(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
-    uint32_t d;
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-    return d;
-}
-
-__device__ __forceinline__ uint32_t neg_bf16x2(uint32_t a) {
-    uint32_t d;
-    asm("neg.bf16x2 %0, %1;" : "=r"(d) : "r"(a));
-    return d;
 }
 
 // 4 bytes, or zeros.
@@ -186,18 +174,22 @@ attn_tc_kernel(const __grid_constant__ AttnProblem p, const __grid_constant__ Al
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&bars->full[i], kTma ? 1 : 64);
-            mbar_init(&bars->empty[i], states_only ? 1 : 2);   // issuer of MMA4, outputs
+            mbar_init(&bars->empty[i], states_only ? 1 : 2);   // MMA4, MMA2
+        }
+        for (int i = 0; i < kStagesW; ++i) {
+            mbar_init(&bars->full_w[i], kTma ? 1 : 64);
+            mbar_init(&bars->empty_w[i], 1);                   // MMA3, or for states alone MMA4
         }
         mbar_init(&bars->o1_done, 1);
         mbar_init(&bars->d_ready, 1);
         mbar_init(&bars->d_free, 16);
         mbar_init(&bars->z_ready, 16);
         mbar_init(&bars->p_ready, 4);
-        mbar_init(&bars->partial, 1);
+        mbar_init(&bars->partial, 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->drain[i], 1);
             mbar_init(&bars->a_ready[i], 1);
-            mbar_init(&bars->parts_ready[i], states_only ? 12 : 4);
+            mbar_init(&bars->parts_ready[i], states_only ? 8 : 16);
             mbar_init(&bars->parts_free[i], 1);
             mbar_init(&bars->o_ready[i], 1);
             mbar_init(&bars->o_free[i], 4);
@@ -210,10 +202,7 @@ attn_tc_kernel(const __grid_constant__ AttnProblem p, const __grid_constant__ Al
         const int i = tid & (kC - 1), n = tid < kC ? kC : it.len & (kC - 1);
         const float up = exp2f((float)(i + 1) * l2), down = i < n ? exp2f((float)(n - 1 - i) * l2) : 0.f;
         bars->enter[tid >> 6][i] = (rev ? down : up) * a.out_scale;
-        const float f = (rev ? up : down) * a.w_scale;
-        const uint32_t hi = pack2(f, f);
-        const float rest = f - __uint_as_float(hi << 16);
-        bars->leave[tid >> 6][i] = make_uint2(hi, pack2(rest, rest));
+        bars->leave[tid >> 6][i] = (rev ? up : down) * a.w_scale;
         if (tid < kC) {
             bars->lam[kC - 1 - i] = down;
             bars->within[kC - 1 - i] = down * (a.w_scale * a.out_scale);
@@ -221,8 +210,8 @@ attn_tc_kernel(const __grid_constant__ AttnProblem p, const __grid_constant__ Al
         }
     }
     // P's masked halves stay zero
-    *reinterpret_cast<uint4 *>(smem + kOffP + tid * 16) = make_uint4(0, 0, 0, 0);
-    static_assert(2 * kBlock == kThreads * 16, "one store a thread");
+    for (uint32_t i = tid; i < 2 * kBlock / 16; i += kThreads)
+        *reinterpret_cast<uint4 *>(smem + kOffP + i * 16) = make_uint4(0, 0, 0, 0);
     if (!kTma && (kd & 15))    // the products' last step reads up to the next 16 columns of X and Y
         for (uint32_t i = tid; i < kOffParts / 16; i += kThreads)
             *reinterpret_cast<uint4 *>(smem + i * 16) = make_uint4(0, 0, 0, 0);
@@ -236,6 +225,41 @@ attn_tc_kernel(const __grid_constant__ AttnProblem p, const __grid_constant__ Al
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
     const float *lam = bars->lam;      // [0 .. 64]
+    // Thread t of `of` splits its share of chunk c's W.
+    auto split_chunk = [&](int c, int t, int of) {
+        const int per = (vd + 7) / 8, total = kC * per;
+        const bool whole = per == 16 || per == 8;
+        const unsigned char *w = smem + kOffW + c % kStagesW * kTile;
+        unsigned char *out = smem + kOffParts + (c & 1) * (3 * kTile);
+        const float *leave = bars->leave[chunk_len(c) < kC];
+        auto split = [&](uint32_t at, float d) {
+            const uint4 raw = *reinterpret_cast<const uint4 *>(w + at);
+            const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+            uint32_t r[4][3];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                split_parts<3>(__uint_as_float(in[q] << 16) * d, __uint_as_float(in[q] & 0xffff0000u) * d, r[q]);
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                *reinterpret_cast<uint4 *>(out + i * kTile + at) = make_uint4(r[0][i], r[1][i], r[2][i], r[3][i]);
+        };
+        if (whole) {
+            // the rows of a thread's packets lie whole swizzle periods apart
+            const int sh = per == 16 ? 4 : 3, apart = of >> sh;
+            int r = t >> sh;
+            uint32_t at = ((t & (per - 1)) >> 3) * kBlock + sw128_offset(r, t & 7);
+#pragma unroll 1
+            for (; r < kC; r += apart, at += apart * 128) split(at, leave[r]);
+        } else {
+#pragma unroll 1
+            for (int i = t; i < total; i += of) {
+                const int r = i / per, ch = i - r * per;
+                split((ch >> 3) * kBlock + sw128_offset(r, ch & 7), leave[r]);
+            }
+        }
+        fence_proxy_async();
+        warp_arrive(&bars->parts_ready[c & 1]);
+    };
 
     if (warp < 2) {
         // ------------------------------------------------ copies (without TMA:
@@ -244,53 +268,83 @@ attn_tc_kernel(const __grid_constant__ AttnProblem p, const __grid_constant__ Al
         const __nv_bfloat16 *Y = static_cast<const __nv_bfloat16 *>(a.Y) + (long)(h / a.sy) * kd;
         const __nv_bfloat16 *W = static_cast<const __nv_bfloat16 *>(a.W) + (long)(h / a.sw) * vd;
         const Maps &m = maps.pass[blockIdx.y];
-        int issued = 0;
-        for (int c = 0; c < chunks && !(kTma && warp); ++c, ++issued) {
+        // W of chunk c + 1 is asked for with X and Y of chunk c.
+        int issued = 0, issued_w = 0;
+        auto copy_w = [&](int c) {
+            const int st = c % kStagesW, n = chunk_len(c);
+            if (c >= kStagesW && !warp_wait(&bars->empty_w[st], (c / kStagesW - 1) & 1, abort)) return false;
+            unsigned char *tile = smem + kOffW + st * kTile;
+            const long t0 = it.start + (long)chunk_at(c);
+            if constexpr (kTma) {
+                uint64_t *landed = n == kC ? &bars->full_w[st] : &bars->partial;
+                const int blocks = (vd + 63) / 64;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(landed, kBlock * blocks);
+                    for (int i = 0; i < blocks; ++i)
+                        tma_load_3d(tile + i * kBlock, &m.w, landed, i * 64, h / a.sw, (int)t0);
+                }
+                __syncwarp();
+            } else {
+                copy_tile<V>(smem_u32(tile), W + t0 * a.ld_w, a.ld_w, vd, n, warp * (kC / 2), (warp + 1) * (kC / 2));
+                if (V == 1) mbar_arrive(&bars->full_w[st]);
+                else copies_arrive(&bars->full_w[st]);      // every lane, when its own copies have landed
+            }
+            ++issued_w;
+            return true;
+        };
+        const int mine = kTma && warp ? 0 : chunks;
+        bool fine = mine == 0 || copy_w(0);
+        for (int c = 0; c < mine && fine; ++c) {
             const int st = c % kStages, n = chunk_len(c);
-            if (c >= kStages && !warp_wait(&bars->empty[st], (c / kStages - 1) & 1, abort)) break;
+            if (c >= kStages && !(fine = warp_wait(&bars->empty[st], (c / kStages - 1) & 1, abort))) break;
             unsigned char *stage = smem + st * kStage;
             const long t0 = it.start + (long)chunk_at(c);
             if constexpr (kTma) {
                 // (boxes of whole chunks: behind the last sequence's end they
                 // are filled with zeros, behind another's the rows are replaced)
                 uint64_t *landed = n == kC ? &bars->full[st] : &bars->partial;
-                const int blocks = (kd + 63) / 64, wblocks = (vd + 63) / 64;
+                const int blocks = (kd + 63) / 64;
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(landed, kBlock * ((states_only ? 1 : 2) * blocks + wblocks));
+                    mbar_arrive_expect_tx(landed, kBlock * (states_only ? 1 : 2) * blocks);
                     for (int i = 0; i < blocks; ++i) {
                         if (!states_only) tma_load_3d(stage + i * kBlock, &m.x, landed, i * 64, h / a.sx, (int)t0);
                         tma_load_3d(stage + kTile + i * kBlock, &m.y, landed, i * 64, h / a.sy, (int)t0);
                     }
-                    for (int i = 0; i < wblocks; ++i)
-                        tma_load_3d(stage + 2 * kTile + i * kBlock, &m.w, landed, i * 64, h / a.sw, (int)t0);
                 }
                 __syncwarp();
+                ++issued;
                 if (n < kC) {
-                    if (!warp_wait(&bars->partial, 0, abort)) break;      // a run has one such chunk
-                    for (int i = n * 8 + lane; i < kC * 8; i += 32)
+                    if (!(fine = warp_wait(&bars->partial, 0, abort))) break;      // a run has one such chunk
+                    unsigned char *w = smem + kOffW + c % kStagesW * kTile;
+                    for (int i = n * 8 + lane; i < kC * 8; i += 32) {
 #pragma unroll
-                        for (int k = 0; k < 6; ++k)
+                        for (int k = 0; k < 4; ++k)
                             *reinterpret_cast<uint4 *>(stage + k * kBlock + i * 16) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            *reinterpret_cast<uint4 *>(w + k * kBlock + i * 16) = make_uint4(0, 0, 0, 0);
+                    }
                     fence_proxy_async();
                     warp_arrive(&bars->full[st]);
+                    warp_arrive(&bars->full_w[c % kStagesW]);
                 }
             } else {
                 const uint32_t tile = smem_u32(stage);
                 const int from = warp * (kC / 2), to = (warp + 1) * (kC / 2);
                 copy_tile<V>(tile + kTile, Y + t0 * a.ld_y, a.ld_y, kd, n, from, to);
-                if (warp == 1) copy_tile<V>(tile + 2 * kTile, W + t0 * a.ld_w, a.ld_w, vd, n, 0, kC);
-                else if (!states_only) copy_tile<V>(tile, X + t0 * a.ld_x, a.ld_x, kd, n, 0, kC);
+                if (!states_only) copy_tile<V>(tile, X + t0 * a.ld_x, a.ld_x, kd, n, from, to);
                 if (V == 1) mbar_arrive(&bars->full[st]);
-                else copies_arrive(&bars->full[st]);      // every lane, when its own copies have landed
+                else copies_arrive(&bars->full[st]);
             }
+            if (c + 1 < chunks) fine = copy_w(c + 1);
         }
         if (kTma) {
             // every issued copy must land before the CTA may exit (a partial
             // chunk's has, or its wait ran out)
-            if (warp == 0 && lane < kStages && lane < issued) {
-                int dummy = 0;
-                mbar_wait(&bars->full[lane], ((issued - 1 - lane) / kStages) & 1, &dummy);
-            }
+            int dummy = 0;
+            if (lane < kStages && lane < issued) mbar_wait(&bars->full[lane], ((issued - 1 - lane) / kStages) & 1, &dummy);
+            if (lane < kStagesW && lane < issued_w)
+                mbar_wait(&bars->full_w[lane], ((issued_w - 1 - lane) / kStagesW) & 1, &dummy);
             __syncwarp();
         } else {
             commit_copies();
@@ -301,16 +355,17 @@ attn_tc_kernel(const __grid_constant__ AttnProblem p, const __grid_constant__ Al
         // whole warp waits, one lane issues and commits).  The copies wrote
         // through the generic proxy: hence the proxy fence on this side.
         const uint32_t base = smem_u32(smem);
-        // Descriptors of the first stage; another stage, K step or part is an
-        // addition to the address field (units of 16 bytes).
+        // Lower words of the first stage's descriptors (the upper ones are alike);
+        // another stage, K step or part is an addition to the address field (units
+        // of 16 bytes).
         auto along_k = [](int k) { return (uint32_t)((k >> 2) * (kBlock / 16) + (k & 3) * 2); };
-        const uint64_t x0 = sdesc_sw128(base, 16, 1024);
+        const uint32_t hi = (uint32_t)(sdesc_sw128(base, 16, 1024) >> 32), x0 = (uint32_t)sdesc_sw128(base, 16, 1024);
         bool fine = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) { return fine = fine && warp_wait(bar, parity, abort); };
         if (warp == 2) {
             const uint32_t idesc_a = idesc_bf16(64, 64, false, false), idesc_d = idesc_bf16(128, ksteps * 16, true, true);
-            const uint64_t y0 = sdesc_sw128(base + kTile, 16, 1024), yt0 = sdesc_sw128(base + kTile, kBlock, 1024);
-            const uint64_t part0 = sdesc_sw128(base + kOffParts, kBlock, 1024);
+            const uint32_t y0 = (uint32_t)sdesc_sw128(base + kTile, 16, 1024), yt0 = (uint32_t)sdesc_sw128(base + kTile, kBlock, 1024);
+            const uint32_t part0 = (uint32_t)sdesc_sw128(base + kOffParts, kBlock, 1024);
             for (int c = 0; c < chunks; ++c) {
                 const int st = c % kStages;
                 const uint32_t stage = (uint32_t)st * (kStage / 16);
@@ -320,10 +375,10 @@ attn_tc_kernel(const __grid_constant__ AttnProblem p, const __grid_constant__ Al
                     fence_proxy_async();
                     tc_fence_after();
                     if (elect_one()) {
-                        const uint64_t x = x0 + stage, y = y0 + stage;
-#pragma unroll 1
-                        for (int k = 0; k < ksteps; ++k)
-                            mma_bf16(tmem + kColA + (c & 1) * 128, x + along_k(k), y + along_k(k), idesc_a, k != 0);
+                        const uint32_t x = x0 + stage, y = y0 + stage;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (k < ksteps) mma_lo(tmem + kColA + (c & 1) * 128, x + along_k(k), y + along_k(k), hi, idesc_a, k != 0);
                         mma_commit(&bars->a_ready[c & 1]);
                     }
                     __syncwarp();
@@ -334,20 +389,23 @@ attn_tc_kernel(const __grid_constant__ AttnProblem p, const __grid_constant__ Al
                 fence_proxy_async();
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint64_t y = yt0 + stage, part = part0 + (uint32_t)((c & 1) * (2 * kTile / 16));
-#pragma unroll 1
-                    for (int k = 0; k < 8; ++k)      // the lower part first: each MMA cuts the sum short
-                        mma_bf16(tmem + kColD, part + (uint32_t)((1 - (k >> 2)) * (kTile / 16) + (k & 3) * 128),
-                                 y + (uint32_t)((k & 3) * 128), idesc_d, k != 0);
+                    const uint32_t y = yt0 + stage, part = part0 + (uint32_t)((c & 1) * (3 * kTile / 16));
+#pragma unroll
+                    for (int k = 0; k < 12; ++k)      // the lowest part first: each MMA cuts the sum short
+                        mma_lo(tmem + kColD, part + (uint32_t)((2 - (k >> 2)) * (kTile / 16) + (k & 3) * 128),
+                               y + (uint32_t)((k & 3) * 128), hi, idesc_d, k != 0);
                     mma_commit(&bars->d_ready);
-                    mma_commit(&bars->parts_free[c & 1]);
                     mma_commit(&bars->empty[st]);
+                    if (states_only) {
+                        mma_commit(&bars->parts_free[c & 1]);
+                        mma_commit(&bars->empty_w[c % kStagesW]);
+                    }
                 }
                 __syncwarp();
             }
         } else if (!states_only) {
             const uint32_t idesc_o1 = idesc_bf16(128, 64, false, false), idesc_o2 = idesc_bf16(128, 64, true, false);
-            const uint64_t wt0 = sdesc_sw128(base + 2 * kTile, kBlock, 1024), p0 = sdesc_sw128(base + kOffP, 16, 1024);
+            const uint32_t wt0 = (uint32_t)sdesc_sw128(base + kOffW, kBlock, 1024), p0 = (uint32_t)sdesc_sw128(base + kOffP, 16, 1024);
             for (int c = 0; c < chunks; ++c) {
                 const int st = c % kStages;
                 const uint32_t stage = (uint32_t)st * (kStage / 16), o = tmem + kColO + (c & 1) * 128;
@@ -358,25 +416,29 @@ attn_tc_kernel(const __grid_constant__ AttnProblem p, const __grid_constant__ Al
                 fence_proxy_async();
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint64_t x = x0 + stage;
                     // (lower parts first, here and below)
-#pragma unroll 1
-                    for (int k = 0; k < ksteps; ++k) mma_bf16_ta(o, tmem + kColZ + 64 + k * 8, x + along_k(k), idesc_o1, k != 0);
-#pragma unroll 1
-                    for (int k = 0; k < ksteps; ++k) mma_bf16_ta(o, tmem + kColZ + k * 8, x + along_k(k), idesc_o1, 1);
+                    const uint32_t x = x0 + stage;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (k < ksteps) mma_ta_lo(o, tmem + kColZ + 64 + k * 8, x + along_k(k), hi, idesc_o1, k != 0);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (k < ksteps) mma_ta_lo(o, tmem + kColZ + k * 8, x + along_k(k), hi, idesc_o1, 1);
                     mma_commit(&bars->o1_done);
+                    mma_commit(&bars->empty[st]);
                 }
                 __syncwarp();
+                if (!wait(&bars->full_w[c % kStagesW], (c / kStagesW) & 1)) break;
                 if (!wait(&bars->p_ready, c & 1)) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint64_t w = wt0 + stage;
-#pragma unroll 1
+                    const uint32_t w = wt0 + (uint32_t)(c % kStagesW * (kTile / 16));
+#pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        mma_bf16(o + 64, w + (uint32_t)((k & 3) * 128),
-                                 p0 + (uint32_t)((1 - (k >> 2)) * (kBlock / 16) + (k & 3) * 2), idesc_o2, k != 0);
+                        mma_lo(o + 64, w + (uint32_t)((k & 3) * 128), p0 + (uint32_t)((1 - (k >> 2)) * (kBlock / 16) + (k & 3) * 2), hi,
+                               idesc_o2, k != 0);
                     mma_commit(&bars->o_ready[c & 1]);
-                    mma_commit(&bars->empty[st]);
+                    mma_commit(&bars->empty_w[c % kStagesW]);
                 }
                 __syncwarp();
             }
@@ -388,47 +450,14 @@ attn_tc_kernel(const __grid_constant__ AttnProblem p, const __grid_constant__ Al
             mbar_wait(&bars->drain[warp & 1], 0, &dummy);
         }
         __syncwarp();
-    } else if (warp < 8 || (states_only && warp < 16)) {
-        // ------------------------------------------------ D W in two parts (for
-        // states alone by three times the warps, which would be idle)
-        const int t = tid & 127, third = (warp - 4) >> 2, thirds = states_only ? 3 : 1, per = (vd + 7) / 8, total = kC * per;
-        const bool whole = per == 16 || per == 8;
-        const int r0 = t / per, apart = 128 / per;           // (128 / 16 or 128 / 8 rows)
-        const uint32_t at0 = ((t - r0 * per) >> 3) * kBlock + sw128_offset(r0, (t - r0 * per) & 7);
+    } else if (states_only && warp < 12) {
+        // ------------------------------------------------ D W for states alone
         for (int c = 0; c < chunks; ++c) {
-            const int st = c % kStages, n = chunk_len(c);
-            if (!warp_wait(&bars->full[st], (c / kStages) & 1, abort)) break;
+            if (!warp_wait(&bars->full_w[c % kStagesW], (c / kStagesW) & 1, abort)) break;
             if (c >= 2 && !warp_wait(&bars->parts_free[c & 1], ((c >> 1) - 1) & 1, abort)) break;
-            const unsigned char *w = smem + st * kStage + 2 * kTile;
-            unsigned char *out = smem + kOffParts + (c & 1) * 2 * kTile;
-            const uint2 *leave = bars->leave[n < kC];
-            auto split = [&](uint32_t at, uint2 d) {
-                const uint4 raw = *reinterpret_cast<const uint4 *>(w + at);
-                const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    hi[q] = fma_bf16x2(in[q], d.x, 0x80008000u);
-                    lo[q] = fma_bf16x2(in[q], d.y, fma_bf16x2(in[q], d.x, neg_bf16x2(hi[q])));
-                }
-                *reinterpret_cast<uint4 *>(out + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4 *>(out + kTile + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            };
-            if (whole) {
-                // the rows of a thread's packets lie whole swizzle periods apart
-#pragma unroll 2
-                for (int i = third; i < total / 128; i += thirds)
-                    split(at0 + i * (apart * 128), leave[i * apart + r0]);
-            } else {
-                for (int i = t + third * 128; i < total; i += thirds * 128) {
-                    const int r = i / per, ch = i - r * per;
-                    split((ch >> 3) * kBlock + sw128_offset(r, ch & 7), leave[r]);
-                }
-            }
-            fence_proxy_async();
-            warp_arrive(&bars->parts_ready[c & 1]);
+            split_chunk(c, tid - 128, 256);
         }
-    } else if (warp < 12) {
+    } else if (warp < 8) {
         // ------------------------------------------------ A -> P.  Row i of the
         // M = 64 product sits in lane 32 (i / 16) + i % 16; threads t and t + 16
         // of a warp take eight columns each of every 16.  A warp's rows see the
@@ -481,7 +510,7 @@ attn_tc_kernel(const __grid_constant__ AttnProblem p, const __grid_constant__ Al
                 warp_arrive(&bars->p_ready);
             }
         }
-    } else if (warp < 16) {
+    } else if (warp < 12) {
         // ------------------------------------------------ outputs
         const int quad = warp & 3, col = quad * 32 + lane;
         const uint32_t at = tmem + kColO + ((uint32_t)(quad * 32) << 16);
@@ -544,7 +573,7 @@ attn_tc_kernel(const __grid_constant__ AttnProblem p, const __grid_constant__ Al
     } else {
         // ------------------------------------------------ the state: row `col`
         // of Z^T, columns k0 .. k0 + 31
-        const int quad = warp & 3, col = quad * 32 + lane, k0 = ((warp - 16) >> 2) * 32;
+        const int quad = warp & 3, col = quad * 32 + lane, k0 = ((warp - 12) >> 2) * 32;
         const bool mine = k0 < kd;
         const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16);
         float z[32];
@@ -570,9 +599,20 @@ attn_tc_kernel(const __grid_constant__ AttnProblem p, const __grid_constant__ Al
             tc_fence_before();
             warp_arrive(&bars->z_ready);
         };
-        if (!states_only && chunks) put();
         bool fine = true;
-        for (int c = 0; c < chunks; ++c) {
+        auto split_next = [&](int c) {
+            if (!warp_wait(&bars->full_w[c % kStagesW], (c / kStagesW) & 1, abort)) return false;
+            split_chunk(c, tid - 384, 512);
+            return true;
+        };
+        if (!states_only && chunks) {
+            fine = split_next(0);
+            put();
+        }
+        for (int c = 0; c < chunks && fine; ++c) {
+            // the next chunk's D W, in a buffer whose products were done with dZ
+            // of the last chunk
+            if (!states_only && c + 1 < chunks && !(fine = split_next(c + 1))) break;
             if (!(fine = warp_wait(&bars->d_ready, c & 1, abort))) break;
             tc_fence_after();
             const float f = lam[chunk_len(c)];

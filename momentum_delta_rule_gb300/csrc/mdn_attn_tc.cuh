@@ -65,6 +65,31 @@ __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
+// The same two products with the descriptors' lower words (addresses and leading
+// offsets) apart from the upper ones, which an MMA's neighbours share: one addition
+// an operand.
+__device__ __forceinline__ void mma_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %3};\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ta_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // True in one lane of the warp.  Unlike a comparison of the lane's number it
 // tells the compiler so, which then issues an MMA's operands as they are and not
 // lane by lane: 43 to 106 cycles an MMA of the shapes here instead of 107.
@@ -90,8 +115,8 @@ __device__ __forceinline__ void split_parts(float a, float b, uint32_t *part) {
     for (int i = 0; i < N; ++i) {
         part[i] = pack2(a, b);
         if (i == N - 1) break;
-        a -= __uint_as_float(part[i] << 16);
-        b -= __uint_as_float(part[i] & 0xffff0000u);
+        split_pair(fma2(make_pair(__uint_as_float(part[i] << 16), __uint_as_float(part[i] & 0xffff0000u)), make_pair(-1.f, -1.f),
+                        make_pair(a, b)), a, b);
     }
 }
 

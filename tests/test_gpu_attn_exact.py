@@ -1,7 +1,8 @@
 """bf16 rows are a matter of the rows alone: outputs and gradients of linear
-attention on bf16 rows are the formulas' on those rows, rounded to bf16 once.
+attention on bf16 rows are the formulas' on those rows, rounded to bf16 once, and
+states, which are fp32, have fp32's errors.
 
-Let y be what a kernel rounds to x, E a bound of |y - ref|.  Where x is
+Outputs.  Let y be what a kernel rounds to x, E a bound of |y - ref|.  Where x is
 not the number that ref itself rounds to, r, the middle between the two lies
 between y and ref, so that |x - ref| is at most half a step and E more, and |r -
 ref| at least half a step less E.  In all cases |x - ref| <= |r - ref| + 2 E.  With
@@ -12,6 +13,12 @@ E is
   * 2^-16 m: a term passes one operand (the decayed q k^T or the state) that is
     taken as two bf16 parts, the first off by half a step, 2^-8, the second by
     half a step of that at most.
+
+States of at most 16 tokens, which a product of one step takes at once.  In
+steps of 2^-24: a decay's exp2, its products with the scale and a row and the scale
+itself 7, the sum of T products and the carried state T + 1, each addition cut
+short rather than rounded (twice as much), three parts of 8 bits each leave 1,
+the decayed initial state 5 and its sum 1: (2 T + 16) 2^-24 m, beside (late - m).
 """
 import numpy as np
 import pytest
@@ -70,3 +77,19 @@ def test_rounded_once_at_any_decay(decay):
     got = run(dev(c))
     torch.cuda.synchronize()
     check_rounded_once(c, got)
+
+
+@pytest.mark.parametrize("init", [False, True])
+@pytest.mark.parametrize("lens,H,Hkv,dk,dv", [([1, 2, 3, 5], 2, 1, 128, 128), ([2, 16, 2], 4, 4, 64, 40), ([2, 3], 1, 1, 33, 57)])
+def test_states_are_fp32(lens, H, Hkv, dk, dv, init):
+    c = case("bf16", lens, H, Hkv, dk, dv, True, init=init, seed=21)
+    if not init:
+        c["dS_T"] = torch.zeros_like(c["dS_T"])
+    got = run(dev(c))
+    torch.cuda.synchronize()
+    ref, E = bounds(c, 2 * max(lens) + 16, 0.0)
+    for name in ("S_T", "dS0"):
+        off = np.abs(got[name].double().cpu().numpy() - ref[name])
+        tol = 2.0 ** -24 * np.abs(ref[name]) + E[name]
+        assert (off <= tol).all(), "%s: %d of %d off, worst %.2f times the tolerance" % (
+            name, (off > tol).sum(), off.size, (off / tol).max())
