@@ -64,7 +64,7 @@ AttnProblem problem(const Heads &s, const Space &w, const float *log_decay, cons
     p.T = T;
     p.T_total = (int)s.L;
     p.seg = w.seg;
-    p.cu = s.L ? cu : nullptr;
+    p.cu = cu;
     p.dtype = dtype;
     p.status = status;
     if (p.cu) {
@@ -76,6 +76,14 @@ AttnProblem problem(const Heads &s, const Space &w, const float *log_decay, cons
         p.slots = s.n_seq * (w.seg ? (T + w.seg - 1) / w.seg : 1);
     }
     return p;
+}
+
+// Without tokens the states stay as they are: no kernel, which would read the
+// decays that such a call need not have.
+cudaError_t keep_states(const Heads &s, float *to, const float *from, cudaStream_t st) {
+    const size_t bytes = (size_t)s.n_seq * s.H * s.dk * s.dv * sizeof(float);
+    if (to == nullptr || to == from || bytes == 0) return cudaSuccess;
+    return from ? cudaMemcpyAsync(to, from, bytes, cudaMemcpyDeviceToDevice, st) : cudaMemsetAsync(to, 0, bytes, st);
 }
 
 }  // namespace
@@ -123,7 +131,7 @@ mdn_status mdn_linear_attn_fwd(const void *q, const void *k, const void *v, cons
     if (st != MDN_OK) return st;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    if (!some && !S_T) return MDN_OK;
+    if (!some) return finish(keep_states(s, S_T, S0, cs));
     AttnProblem p = problem(s, w, log_decay, cu_seqlens, T, dtype, status, ws);
     AttnPass a = {};
     a.X = q; a.Y = k; a.W = v;
@@ -146,7 +154,7 @@ mdn_status mdn_linear_attn_fwd(const void *q, const void *k, const void *v, cons
     }
     a.init = S0;
     a.fin = S_T;
-    a.out = some ? o : S_T;          // without tokens nothing is written there
+    a.out = o;
     p.pass[0] = a;
     p.n_pass = 1;
     if (err == cudaSuccess) err = launch_attn(p, cs);
@@ -178,7 +186,7 @@ mdn_status mdn_linear_attn_bwd(const void *q, const void *k, const void *v, cons
     if (st != MDN_OK) return st;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    if (!some && !dS0) return MDN_OK;
+    if (!some) return finish(keep_states(s, dS0, dS_T, cs));
     AttnProblem p = problem(s, w, log_decay, cu_seqlens, T, dtype, status, ws);
     const int shared = H / Hkv;
     // the segments' own states: S, and dS at their ends
@@ -212,8 +220,8 @@ mdn_status mdn_linear_attn_bwd(const void *q, const void *k, const void *v, cons
         seg_S = fwd.seg_out;
         seg_dS = rev.seg_out;
     }
-    void *to_dk = shared > 1 && some ? static_cast<void *>(ws + w.dk) : dk_out;
-    void *to_dv = shared > 1 && some ? static_cast<void *>(ws + w.dv) : dv_out;
+    void *to_dk = shared > 1 ? static_cast<void *>(ws + w.dk) : dk_out;
+    void *to_dv = shared > 1 ? static_cast<void *>(ws + w.dv) : dv_out;
     AttnPass a = {};
     a.X = d_o; a.Y = v; a.W = k;
     a.ld_x = ld_do; a.ld_y = ld_v; a.ld_w = ld_k;
@@ -237,20 +245,15 @@ mdn_status mdn_linear_attn_bwd(const void *q, const void *k, const void *v, cons
     c.seg_out = nullptr;
     c.X = k; c.ld_x = ld_k; c.sx = shared;
     c.out_scale = 1.f;
-    c.out = some ? to_dv : dS0; c.out_f32 = shared > 1;
+    c.out = to_dv; c.out_f32 = shared > 1;
     c.init = dS_T; c.seg_init = seg_dS;
     c.fin = dS0;
-    if (some) {
-        p.pass[0] = a;
-        p.pass[1] = b;
-        p.pass[2] = c;
-        p.n_pass = 3;
-    } else {
-        p.pass[0] = c;
-        p.n_pass = 1;
-    }
+    p.pass[0] = a;
+    p.pass[1] = b;
+    p.pass[2] = c;
+    p.n_pass = 3;
     if (err == cudaSuccess) err = launch_attn(p, cs);
-    if (shared > 1 && some) {
+    if (shared > 1) {
         if (err == cudaSuccess) err = launch_attn_reduce(p, reinterpret_cast<float *>(ws + w.dk), dk_out, dk, shared, cs);
         if (err == cudaSuccess) err = launch_attn_reduce(p, reinterpret_cast<float *>(ws + w.dv), dv_out, dv, shared, cs);
     }

@@ -678,7 +678,7 @@ cudaError_t launch_attn_tc(const AttnProblem &p, cudaStream_t st) {
         return true;
     });
     AllMaps maps;
-    for (int i = 0; i < p.n_pass && V == 8 && p.T_total > 0; ++i) {
+    for (int i = 0; i < p.n_pass && V == 8; ++i) {
         const AttnPass &a = p.pass[i];
         Maps &m = maps.pass[i];
         bool ok = map_rows(&m.y, a.Y, p.T_total, p.H / a.sy, a.kd, a.ld_y) &&
