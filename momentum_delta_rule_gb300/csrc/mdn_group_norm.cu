@@ -795,104 +795,113 @@ __global__ void __launch_bounds__(kThreads) seq_apply_kernel(GroupNormProblem p,
     }
 }
 
-// Sums of dn and dn n of a tile's groups, and of du n and du of its columns.
+// Sums of dn and dn n of a tile's groups, and of du n and du of its columns.  Where
+// there are more tiles than rows for the columns' sums, blocks take tiles in turn
+// and add them up.
 template <typename T, int V, bool GATE>
 __global__ void __launch_bounds__(kThreads)
-seq_sums_kernel(GroupNormProblem p, int rows, int per_block, float2 *part, float *params) {
+seq_sums_kernel(GroupNormProblem p, int rows, int per_block, int slots, float2 *part, float *params) {
     __shared__ float2 red[kThreads];
     __shared__ float cols[2][kThreads * V];
     grid_trigger();
     const bool ok = sequences_ok(p);
     if (!ok && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicExch(p.status, MDN_ERR_INVALID_ARG);
-    Tile t;
-    const bool some = ok && tile_of(p, rows, blockIdx.x, t);
     const Columns c = columns_of(p, per_block, V);
     const int w = p.D / p.G;
-    float2 s = make_float2(0.f, 0.f);
     float *out = params ? params + (long)blockIdx.x * 2 * p.D + (long)c.g0 * w : nullptr;
-    // whole rounds of packets, for the barriers; one round where lanes > 1
-    for (int base = 0; base < c.packets; base += kThreads) {
-        const int pc = base + c.pc;
-        Vals<V> dw = zeros<V>(), db = zeros<V>();
-        if (some && c.lane < c.lanes && pc < c.packets) {
-            const long col = (long)c.g0 * w + pc * V;
-            const float2 st = reinterpret_cast<const float2 *>(p.stats)[(long)t.seq * p.G + col / w];
-            const Vals<V> wt = load_weights<V>(p.weight, col, 1.f), bs = load_weights<V>(p.bias, col, 0.f);
-            const T *x = static_cast<const T *>(p.x) + t.start * p.ld_x + col;
-            const T *gate = static_cast<const T *>(p.gate) + t.start * p.ld_gate + col;
-            const T *dy = static_cast<const T *>(p.dy) + t.start * p.ld_dy + col;
+    for (int slot = blockIdx.x; slot < slots; slot += gridDim.x) {
+        const bool first = slot == blockIdx.x;
+        Tile t;
+        const bool some = ok && tile_of(p, rows, slot, t);
+        if (!some && !first) continue;
+        if (!first) __syncthreads();       // (the last tile's sums have been read)
+        float2 s = make_float2(0.f, 0.f);
+        // whole rounds of packets, for the barriers; one round where lanes > 1
+        for (int base = 0; base < c.packets; base += kThreads) {
+            const int pc = base + c.pc;
+            Vals<V> dw = zeros<V>(), db = zeros<V>();
+            if (some && c.lane < c.lanes && pc < c.packets) {
+                const long col = (long)c.g0 * w + pc * V;
+                const float2 st = reinterpret_cast<const float2 *>(p.stats)[(long)t.seq * p.G + col / w];
+                const Vals<V> wt = load_weights<V>(p.weight, col, 1.f), bs = load_weights<V>(p.bias, col, 0.f);
+                const T *x = static_cast<const T *>(p.x) + t.start * p.ld_x + col;
+                const T *gate = static_cast<const T *>(p.gate) + t.start * p.ld_gate + col;
+                const T *dy = static_cast<const T *>(p.dy) + t.start * p.ld_dy + col;
 #pragma unroll 4
-            for (int r = c.lane; r < t.n; r += c.lanes) {
-                Vals<V> n = values<T, V>(load_packet<T, V>(x + r * p.ld_x)), g;
-                Vals<V> d = values<T, V>(load_packet<T, V>(dy + r * p.ld_dy));
-                if (GATE) g = values<T, V>(load_packet<T, V>(gate + r * p.ld_gate));
-                backward_vals<V, GATE>(n, g, d, st.x, st.y, wt, bs, p.act);
+                for (int r = c.lane; r < t.n; r += c.lanes) {
+                    Vals<V> n = values<T, V>(load_packet<T, V>(x + r * p.ld_x)), g;
+                    Vals<V> d = values<T, V>(load_packet<T, V>(dy + r * p.ld_dy));
+                    if (GATE) g = values<T, V>(load_packet<T, V>(gate + r * p.ld_gate));
+                    backward_vals<V, GATE>(n, g, d, st.x, st.y, wt, bs, p.act);
+#pragma unroll
+                    for (int j = 0; j < Vals<V>::N; ++j) {
+                        dw.p[j] = fma2(d.p[j], n.p[j], dw.p[j]);
+                        db.p[j] = add2(db.p[j], d.p[j]);
+                    }
+                }
+                // the groups' sums follow from the columns'
+                Vals<V> a, b;
 #pragma unroll
                 for (int j = 0; j < Vals<V>::N; ++j) {
-                    dw.p[j] = fma2(d.p[j], n.p[j], dw.p[j]);
-                    db.p[j] = add2(db.p[j], d.p[j]);
+                    a.p[j] = mul2(db.p[j], wt.p[j]);
+                    b.p[j] = mul2(dw.p[j], wt.p[j]);
                 }
+                s.x += sum_of<V>(a);
+                s.y += sum_of<V>(b);
             }
-            // the groups' sums follow from the columns'
-            Vals<V> a, b;
+            if (!out) continue;
+            float fw[2 * Vals<V>::N], fb[2 * Vals<V>::N];
 #pragma unroll
             for (int j = 0; j < Vals<V>::N; ++j) {
-                a.p[j] = mul2(db.p[j], wt.p[j]);
-                b.p[j] = mul2(dw.p[j], wt.p[j]);
+                split_pair(dw.p[j], fw[2 * j], fw[2 * j + 1]);
+                split_pair(db.p[j], fb[2 * j], fb[2 * j + 1]);
             }
-            s.x += sum_of<V>(a);
-            s.y += sum_of<V>(b);
-        }
-        if (!out) continue;
-        float fw[2 * Vals<V>::N], fb[2 * Vals<V>::N];
+            if (c.lanes == 1) {
+                if (c.lane == 0 && pc < c.packets)
 #pragma unroll
-        for (int j = 0; j < Vals<V>::N; ++j) {
-            split_pair(dw.p[j], fw[2 * j], fw[2 * j + 1]);
-            split_pair(db.p[j], fb[2 * j], fb[2 * j + 1]);
-        }
-        if (c.lanes == 1) {
-            if (c.lane == 0 && pc < c.packets)
+                    for (int v = 0; v < V; ++v) {
+                        float *to = out + pc * V + v;
+                        to[0] = first ? fw[v] : to[0] + fw[v];
+                        to[p.D] = first ? fb[v] : to[p.D] + fb[v];
+                    }
+                continue;
+            }
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    out[pc * V + v] = fw[v];
-                    out[p.D + pc * V + v] = fb[v];
-                }
-            continue;
+            for (int v = 0; v < V; ++v) {
+                cols[0][threadIdx.x * V + v] = fw[v];
+                cols[1][threadIdx.x * V + v] = fb[v];
+            }
+            __syncthreads();
+            const int n = c.packets * V;
+            for (int i = threadIdx.x; i < 2 * n; i += kThreads) {
+                const int which = i >= n, col = i - which * n;
+                float sum = 0.f;
+                for (int l = 0; l < c.lanes; ++l) sum += cols[which][l * n + col];
+                float *to = out + which * p.D + col;
+                *to = first ? sum : *to + sum;
+            }
         }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            cols[0][threadIdx.x * V + v] = fw[v];
-            cols[1][threadIdx.x * V + v] = fb[v];
-        }
+        if (!some) continue;
+        red[threadIdx.x] = s;
         __syncthreads();
-        const int n = c.packets * V;
-        for (int i = threadIdx.x; i < 2 * n; i += kThreads) {
-            const int which = i >= n, col = i - which * n;
-            float sum = 0.f;
-            for (int l = 0; l < c.lanes; ++l) sum += cols[which][l * n + col];
-            out[which * p.D + col] = sum;
-        }
-    }
-    if (!some) return;
-    red[threadIdx.x] = s;
-    __syncthreads();
-    by_group(p, c, V, [&](int g, int ppg) {
-        float2 a = make_float2(0.f, 0.f);
-        const bool whole = c.packets >= kThreads && c.groups == 1;
-        const int count = whole ? kThreads : ppg * c.lanes;
-        for (int i = threadIdx.x & 31; i < count; i += 32) {
-            const int lane = whole ? 0 : i / ppg;
-            const float2 v = red[whole ? i : lane * c.packets + g * ppg + (i - lane * ppg)];
-            a.x += v.x;
-            a.y += v.y;
-        }
+        by_group(p, c, V, [&](int g, int ppg) {
+            float2 a = make_float2(0.f, 0.f);
+            const bool whole = c.packets >= kThreads && c.groups == 1;
+            const int count = whole ? kThreads : ppg * c.lanes;
+            for (int i = threadIdx.x & 31; i < count; i += 32) {
+                const int lane = whole ? 0 : i / ppg;
+                const float2 v = red[whole ? i : lane * c.packets + g * ppg + (i - lane * ppg)];
+                a.x += v.x;
+                a.y += v.y;
+            }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
-            a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
-        }
-        if ((threadIdx.x & 31) == 0) part[(long)blockIdx.x * p.G + c.g0 + g] = a;
-    });
+            for (int o = 16; o > 0; o >>= 1) {
+                a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
+                a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
+            }
+            if ((threadIdx.x & 31) == 0) part[(long)slot * p.G + c.g0 + g] = a;
+        });
+    }
 }
 
 // One warp a group of a sequence: its means of dn and dn n.
@@ -965,193 +974,201 @@ __global__ void __launch_bounds__(kThreads) seq_dx_kernel(GroupNormProblem p, in
 // thread its own (one column's, of every lanes-th token), and read from there
 // for the sums and again for the results; the blocks' sums meet through the
 // cluster's shared memory.  One launch and one reading instead of three and two.
+// The gradient's clusters take sequences in turn where there are many, and add
+// the columns' sums up: `walkers` of them to a column.
 
 // Tokens of a block, for a sequence of len.
 __device__ __forceinline__ int cluster_rows(int len, int blocks) { return (len + blocks - 1) / blocks; }
 
 template <typename T, int V, bool GATE, bool BWD>
-__global__ void __launch_bounds__(kThreads) seq_cluster_kernel(GroupNormProblem p, int per_block, int blocks, float *params) {
+__global__ void __launch_bounds__(kThreads) seq_cluster_kernel(GroupNormProblem p, int per_block, int blocks, int walkers, float *params) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float mom[3][kThreads];
     __shared__ float cols[BWD ? 2 * kThreads * V : 1];
     __shared__ float3 own[kThreads], all[kThreads];     // of the block's groups
     if (BWD) grid_trigger();
     const int column_blocks = (p.G + per_block - 1) / per_block;
-    const int rank = blockIdx.x % blocks, which = blockIdx.x / blocks, cb = which % column_blocks, seq = which / column_blocks;
+    const int rank = blockIdx.x % blocks, which = blockIdx.x / blocks, cb = which % column_blocks, walker = which / column_blocks;
     const bool ok = sequences_ok(p);
     if (!ok && blockIdx.x == 0 && threadIdx.x == 0) atomicExch(p.status, MDN_ERR_INVALID_ARG);
-    const int len = !ok ? 0 : p.cu ? p.cu[seq + 1] - p.cu[seq] : p.T;
-    const long first = !ok ? 0 : p.cu ? p.cu[seq] : (long)seq * p.T;
-    const int rows = cluster_rows(len, blocks), n = max(0, min(rows, len - rank * rows));
-    const long start = first + (long)rank * rows;
-    const int w = p.D / p.G, g0 = cb * per_block, groups = min(per_block, p.G - g0), ppg = w / V, packets = groups * ppg;
-    const int lanes = kThreads / packets, lane = threadIdx.x / packets, pc = threadIdx.x - lane * packets;
-    const int count = lane < lanes && lane < n ? (n - lane + lanes - 1) / lanes : 0;      // this thread's tokens
-    const long col = (long)g0 * w + pc * V;
-    constexpr int kArrays = BWD ? (GATE ? 3 : 2) : 1;
-    using P = Packet<T, V>;
-    P *tile = reinterpret_cast<P *>(smem) + threadIdx.x;        // [array][token of the thread][thread]
-    const int depth = (rows + lanes - 1) / lanes;
-    auto at = [&](int array, int r) -> P & { return tile[(array * depth + r) * kThreads]; };
-    {
-        const T *src[3] = {static_cast<const T *>(p.x), static_cast<const T *>(p.dy), static_cast<const T *>(p.gate)};
-        const long ld[3] = {p.ld_x, p.ld_dy, p.ld_gate};
+    int seq = walker;
+    do {
+        const int len = !ok ? 0 : p.cu ? p.cu[seq + 1] - p.cu[seq] : p.T;
+        const long first = !ok ? 0 : p.cu ? p.cu[seq] : (long)seq * p.T;
+        const int rows = cluster_rows(len, blocks), n = max(0, min(rows, len - rank * rows));
+        const long start = first + (long)rank * rows;
+        const int w = p.D / p.G, g0 = cb * per_block, groups = min(per_block, p.G - g0), ppg = w / V, packets = groups * ppg;
+        const int lanes = kThreads / packets, lane = threadIdx.x / packets, pc = threadIdx.x - lane * packets;
+        const int count = lane < lanes && lane < n ? (n - lane + lanes - 1) / lanes : 0;      // this thread's tokens
+        const long col = (long)g0 * w + pc * V;
+        constexpr int kArrays = BWD ? (GATE ? 3 : 2) : 1;
+        using P = Packet<T, V>;
+        P *tile = reinterpret_cast<P *>(smem) + threadIdx.x;        // [array][token of the thread][thread]
+        const int depth = (rows + lanes - 1) / lanes;
+        auto at = [&](int array, int r) -> P & { return tile[(array * depth + r) * kThreads]; };
+        {
+            const T *src[3] = {static_cast<const T *>(p.x), static_cast<const T *>(p.dy), static_cast<const T *>(p.gate)};
+            const long ld[3] = {p.ld_x, p.ld_dy, p.ld_gate};
 #pragma unroll
-        for (int a = 0; a < kArrays; ++a) {
-            const T *from = src[a] + (start + lane) * ld[a] + col;
-            for (int r = 0; r < count; ++r) copy_packet<T, V>(&at(a, r), from + r * (lanes * ld[a]));
+            for (int a = 0; a < kArrays; ++a) {
+                const T *from = src[a] + (start + lane) * ld[a] + col;
+                for (int r = 0; r < count; ++r) copy_packet<T, V>(&at(a, r), from + r * (lanes * ld[a]));
+            }
+            commit_copies();
         }
-        commit_copies();
-    }
-    const Vals<V> wt = count ? load_weights<V>(p.weight, col, 1.f) : zeros<V>();
-    const Vals<V> bs = count ? load_weights<V>(p.bias, col, 0.f) : zeros<V>();
-    float2 st = make_float2(0.f, 0.f);
-    if (BWD && count) st = reinterpret_cast<const float2 *>(p.stats)[(long)seq * p.G + col / w];
-    wait_copies<0>();
-    float3 mine = make_float3(0.f, 0.f, 0.f);
-    if constexpr (!BWD) {
-        if (count) {
-            // sums about the mean of the first packet, so that they do not cancel
-            const float shift = p.center ? sum_of<V>(values<T, V>(at(0, 0))) * (1.f / V) : 0.f;
-            Vals<V> s1 = zeros<V>(), s2 = zeros<V>();
-            const Pair minus = both(-shift);
+        const Vals<V> wt = count ? load_weights<V>(p.weight, col, 1.f) : zeros<V>();
+        const Vals<V> bs = count ? load_weights<V>(p.bias, col, 0.f) : zeros<V>();
+        float2 st = make_float2(0.f, 0.f);
+        if (BWD && count) st = reinterpret_cast<const float2 *>(p.stats)[(long)seq * p.G + col / w];
+        wait_copies<0>();
+        float3 mine = make_float3(0.f, 0.f, 0.f);
+        if constexpr (!BWD) {
+            if (count) {
+                // sums about the mean of the first packet, so that they do not cancel
+                const float shift = p.center ? sum_of<V>(values<T, V>(at(0, 0))) * (1.f / V) : 0.f;
+                Vals<V> s1 = zeros<V>(), s2 = zeros<V>();
+                const Pair minus = both(-shift);
 #pragma unroll 4
+                for (int r = 0; r < count; ++r) {
+                    const Vals<V> f = values<T, V>(at(0, r));
+#pragma unroll
+                    for (int j = 0; j < Vals<V>::N; ++j) {
+                        const Pair d = add2(f.p[j], minus);
+                        s1.p[j] = add2(s1.p[j], d);
+                        s2.p[j] = fma2(d, d, s2.p[j]);
+                    }
+                }
+                const float a = sum_of<V>(s1), b = sum_of<V>(s2), k = (float)count * V, m2 = p.center ? b - a * (a / k) : b;
+                mine = make_float3(k, p.center ? shift + a / k : 0.f, m2 < 0.f ? 0.f : m2);
+            }
+        } else {
+            Vals<V> dw = zeros<V>(), db = zeros<V>();
+#pragma unroll 2
             for (int r = 0; r < count; ++r) {
-                const Vals<V> f = values<T, V>(at(0, r));
+                Vals<V> x = values<T, V>(at(0, r)), d = values<T, V>(at(1, r)), g;
+                if (GATE) g = values<T, V>(at(kArrays - 1, r));
+                backward_vals<V, GATE>(x, g, d, st.x, st.y, wt, bs, p.act);
 #pragma unroll
                 for (int j = 0; j < Vals<V>::N; ++j) {
-                    const Pair d = add2(f.p[j], minus);
-                    s1.p[j] = add2(s1.p[j], d);
-                    s2.p[j] = fma2(d, d, s2.p[j]);
+                    dw.p[j] = fma2(d.p[j], x.p[j], dw.p[j]);
+                    db.p[j] = add2(db.p[j], d.p[j]);
                 }
             }
-            const float a = sum_of<V>(s1), b = sum_of<V>(s2), k = (float)count * V, m2 = p.center ? b - a * (a / k) : b;
-            mine = make_float3(k, p.center ? shift + a / k : 0.f, m2 < 0.f ? 0.f : m2);
-        }
-    } else {
-        Vals<V> dw = zeros<V>(), db = zeros<V>();
-#pragma unroll 2
-        for (int r = 0; r < count; ++r) {
-            Vals<V> x = values<T, V>(at(0, r)), d = values<T, V>(at(1, r)), g;
-            if (GATE) g = values<T, V>(at(kArrays - 1, r));
-            backward_vals<V, GATE>(x, g, d, st.x, st.y, wt, bs, p.act);
+            Vals<V> a, b;
 #pragma unroll
             for (int j = 0; j < Vals<V>::N; ++j) {
-                dw.p[j] = fma2(d.p[j], x.p[j], dw.p[j]);
-                db.p[j] = add2(db.p[j], d.p[j]);
+                a.p[j] = mul2(db.p[j], wt.p[j]);
+                b.p[j] = mul2(dw.p[j], wt.p[j]);
+            }
+            mine = make_float3(0.f, sum_of<V>(a), sum_of<V>(b));
+            if (params) {
+                float fw[2 * Vals<V>::N], fb[2 * Vals<V>::N];
+#pragma unroll
+                for (int j = 0; j < Vals<V>::N; ++j) {
+                    split_pair(dw.p[j], fw[2 * j], fw[2 * j + 1]);
+                    split_pair(db.p[j], fb[2 * j], fb[2 * j + 1]);
+                }
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    cols[threadIdx.x * V + v] = fw[v];
+                    cols[(kThreads + threadIdx.x) * V + v] = fb[v];
+                }
+                __syncthreads();
+                const int c = packets * V;
+                float *out = params + ((long)walker * blocks + rank) * 2 * p.D + (long)g0 * w;
+                for (int i = threadIdx.x; i < 2 * c; i += kThreads) {
+                    const int k = i >= c, at_col = i - k * c;
+                    float sum = 0.f;
+                    for (int l = 0; l < lanes; ++l) sum += cols[k * kThreads * V + l * c + at_col];
+                    float *to = out + k * p.D + at_col;
+                    *to = seq == walker ? sum : *to + sum;
+                }
             }
         }
-        Vals<V> a, b;
-#pragma unroll
-        for (int j = 0; j < Vals<V>::N; ++j) {
-            a.p[j] = mul2(db.p[j], wt.p[j]);
-            b.p[j] = mul2(dw.p[j], wt.p[j]);
-        }
-        mine = make_float3(0.f, sum_of<V>(a), sum_of<V>(b));
-        if (params) {
-            float fw[2 * Vals<V>::N], fb[2 * Vals<V>::N];
-#pragma unroll
-            for (int j = 0; j < Vals<V>::N; ++j) {
-                split_pair(dw.p[j], fw[2 * j], fw[2 * j + 1]);
-                split_pair(db.p[j], fb[2 * j], fb[2 * j + 1]);
+        mom[0][threadIdx.x] = mine.x;
+        mom[1][threadIdx.x] = mine.y;
+        mom[2][threadIdx.x] = mine.z;
+        __syncthreads();
+        for (int g = threadIdx.x >> 5; g < groups; g += kThreads / 32) {
+            const float center = BWD ? 0.f : mom[1][g * ppg];
+            Join j = {0.f, 0.f, 0.f};
+            for (int i = threadIdx.x & 31; i < ppg * lanes; i += 32) {
+                const int l = i / ppg, k = l * packets + g * ppg + (i - l * ppg);
+                if (BWD) {
+                    j.s1 += mom[1][k];
+                    j.s2 += mom[2][k];
+                } else {
+                    join_part(j, center, mom[0][k], mom[0][k] > 0.f ? mom[1][k] : center, mom[2][k]);
+                }
             }
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                cols[threadIdx.x * V + v] = fw[v];
-                cols[(kThreads + threadIdx.x) * V + v] = fb[v];
-            }
-            __syncthreads();
-            const int c = packets * V;
-            float *out = params + ((long)seq * blocks + rank) * 2 * p.D + (long)g0 * w;
-            for (int i = threadIdx.x; i < 2 * c; i += kThreads) {
-                const int k = i >= c, at_col = i - k * c;
-                float sum = 0.f;
-                for (int l = 0; l < lanes; ++l) sum += cols[k * kThreads * V + l * c + at_col];
-                out[k * p.D + at_col] = sum;
+            join_warp(j);
+            if ((threadIdx.x & 31) == 0) {
+                float2 v = make_float2(j.s1, j.s2);
+                if (!BWD) v = j.n > 0.f && p.center ? joined(j, center) : make_float2(0.f, j.s2);
+                own[g] = make_float3(j.n, v.x, v.y);
             }
         }
-    }
-    mom[0][threadIdx.x] = mine.x;
-    mom[1][threadIdx.x] = mine.y;
-    mom[2][threadIdx.x] = mine.z;
-    __syncthreads();
-    for (int g = threadIdx.x >> 5; g < groups; g += kThreads / 32) {
-        const float center = BWD ? 0.f : mom[1][g * ppg];
-        Join j = {0.f, 0.f, 0.f};
-        for (int i = threadIdx.x & 31; i < ppg * lanes; i += 32) {
-            const int l = i / ppg, k = l * packets + g * ppg + (i - l * ppg);
+        cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+        cluster.sync();
+        // every block joins all blocks' sums, in their order
+        for (int g = threadIdx.x; g < groups; g += kThreads) {
+            const float center = BWD ? 0.f : cluster.map_shared_rank(own, 0)[g].y;      // (the first block has tokens)
+            Join j = {0.f, 0.f, 0.f};
+            for (int k = 0; k < blocks; ++k) {
+                const float3 v = cluster.map_shared_rank(own, k)[g];
+                if (BWD) {
+                    j.s1 += v.y;
+                    j.s2 += v.z;
+                } else if (v.x > 0.f) {
+                    join_part(j, center, v.x, v.y, v.z);
+                }
+            }
             if (BWD) {
-                j.s1 += mom[1][k];
-                j.s2 += mom[2][k];
+                const float inv = len ? 1.f / ((float)len * (float)w) : 0.f;
+                all[g] = make_float3(p.center ? j.s1 * inv : 0.f, j.s2 * inv, 0.f);
             } else {
-                join_part(j, center, mom[0][k], mom[0][k] > 0.f ? mom[1][k] : center, mom[2][k]);
+                float2 v = make_float2(0.f, 0.f);
+                if (len) {
+                    const float2 m = joined(j, center);
+                    v = make_float2(p.center ? m.x : 0.f, rsqrtf((p.center ? m.y : j.s2) / j.n + p.eps));
+                }
+                all[g] = make_float3(v.x, v.y, 0.f);
+                if (p.stats && rank == 0) reinterpret_cast<float2 *>(p.stats)[(long)seq * p.G + g0 + g] = v;
             }
         }
-        join_warp(j);
-        if ((threadIdx.x & 31) == 0) {
-            float2 v = make_float2(j.s1, j.s2);
-            if (!BWD) v = j.n > 0.f && p.center ? joined(j, center) : make_float2(0.f, j.s2);
-            own[g] = make_float3(j.n, v.x, v.y);
-        }
-    }
-    cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
-    cluster.sync();
-    // every block joins all blocks' sums, in their order
-    for (int g = threadIdx.x; g < groups; g += kThreads) {
-        const float center = BWD ? 0.f : cluster.map_shared_rank(own, 0)[g].y;      // (the first block has tokens)
-        Join j = {0.f, 0.f, 0.f};
-        for (int k = 0; k < blocks; ++k) {
-            const float3 v = cluster.map_shared_rank(own, k)[g];
-            if (BWD) {
-                j.s1 += v.y;
-                j.s2 += v.z;
-            } else if (v.x > 0.f) {
-                join_part(j, center, v.x, v.y, v.z);
-            }
-        }
-        if (BWD) {
-            const float inv = len ? 1.f / ((float)len * (float)w) : 0.f;
-            all[g] = make_float3(p.center ? j.s1 * inv : 0.f, j.s2 * inv, 0.f);
-        } else {
-            float2 v = make_float2(0.f, 0.f);
-            if (len) {
-                const float2 m = joined(j, center);
-                v = make_float2(p.center ? m.x : 0.f, rsqrtf((p.center ? m.y : j.s2) / j.n + p.eps));
-            }
-            all[g] = make_float3(v.x, v.y, 0.f);
-            if (p.stats && rank == 0) reinterpret_cast<float2 *>(p.stats)[(long)seq * p.G + g0 + g] = v;
-        }
-    }
-    // (a block's sums stay until all have read them)
-    cluster.sync();
-    if (!count) return;
-    const float3 got = all[pc / ppg];
-    if constexpr (!BWD) {
-        const T *gate = static_cast<const T *>(p.gate) + (start + lane) * p.ld_gate + col;
-        T *y = static_cast<T *>(p.y) + (start + lane) * p.D + col;
-        const Pair minus = both(-got.x);
+        // (a block's sums stay until all have read them)
+        cluster.sync();
+        if (count) {
+            const float3 got = all[pc / ppg];
+            if constexpr (!BWD) {
+                const T *gate = static_cast<const T *>(p.gate) + (start + lane) * p.ld_gate + col;
+                T *y = static_cast<T *>(p.y) + (start + lane) * p.D + col;
+                const Pair minus = both(-got.x);
 #pragma unroll 4
-        for (int r = 0; r < count; ++r) {
-            Vals<V> f = values<T, V>(at(0, r)), g;
-            if (GATE) g = values<T, V>(load_packet<T, V>(gate + r * (lanes * p.ld_gate)));
+                for (int r = 0; r < count; ++r) {
+                    Vals<V> f = values<T, V>(at(0, r)), g;
+                    if (GATE) g = values<T, V>(load_packet<T, V>(gate + r * (lanes * p.ld_gate)));
 #pragma unroll
-            for (int j = 0; j < Vals<V>::N; ++j) f.p[j] = add2(f.p[j], minus);
-            store_packet<T, V>(y + (long)r * lanes * p.D, packet<T, V>(forward_vals<V, GATE>(f, g, got.y, wt, bs, p.act)));
-        }
-    } else {
-        T *dx = static_cast<T *>(p.dx) + (start + lane) * p.D + col, *dgate = static_cast<T *>(p.dgate) + (start + lane) * p.D + col;
-        const Pair m1 = both(-got.x), m2 = both(-got.y), rstd = both(st.y);
+                    for (int j = 0; j < Vals<V>::N; ++j) f.p[j] = add2(f.p[j], minus);
+                    store_packet<T, V>(y + (long)r * lanes * p.D, packet<T, V>(forward_vals<V, GATE>(f, g, got.y, wt, bs, p.act)));
+                }
+            } else {
+                T *dx = static_cast<T *>(p.dx) + (start + lane) * p.D + col, *dgate = static_cast<T *>(p.dgate) + (start + lane) * p.D + col;
+                const Pair m1 = both(-got.x), m2 = both(-got.y), rstd = both(st.y);
 #pragma unroll 2
-        for (int r = 0; r < count; ++r) {
-            Vals<V> x = values<T, V>(at(0, r)), d = values<T, V>(at(1, r)), g;
-            if (GATE) g = values<T, V>(at(kArrays - 1, r));
-            backward_vals<V, GATE>(x, g, d, st.x, st.y, wt, bs, p.act);
-            if (GATE) store_packet<T, V>(dgate + (long)r * lanes * p.D, packet<T, V>(g));
+                for (int r = 0; r < count; ++r) {
+                    Vals<V> x = values<T, V>(at(0, r)), d = values<T, V>(at(1, r)), g;
+                    if (GATE) g = values<T, V>(at(kArrays - 1, r));
+                    backward_vals<V, GATE>(x, g, d, st.x, st.y, wt, bs, p.act);
+                    if (GATE) store_packet<T, V>(dgate + (long)r * lanes * p.D, packet<T, V>(g));
 #pragma unroll
-            for (int j = 0; j < Vals<V>::N; ++j) x.p[j] = mul2(rstd, fma2(x.p[j], m2, fma2(d.p[j], wt.p[j], m1)));
-            store_packet<T, V>(dx + (long)r * lanes * p.D, packet<T, V>(x));
+                    for (int j = 0; j < Vals<V>::N; ++j) x.p[j] = mul2(rstd, fma2(x.p[j], m2, fma2(d.p[j], wt.p[j], m1)));
+                    store_packet<T, V>(dx + (long)r * lanes * p.D, packet<T, V>(x));
+                }
+            }
         }
-    }
+        seq += walkers;
+    } while (BWD && seq < p.n_seq);
 }
 
 // ------------------------------------------------------------------- host
@@ -1171,6 +1188,12 @@ int tile_rows(long rows, int D) {
     return r;
 }
 long tile_slots(int n_seq, long rows, int D) { return rows / tile_rows(rows, D) + n_seq; }
+// The gradient's rows of parameter sums: one for every block that takes tiles,
+// for every cluster's blocks that take sequences, and no more for more sequences
+// than leave no multiprocessor without work.  (Otherwise 32768 sequences of one
+// token of 2048 bf16 columns would take 4.3 GB for 134 MB.)
+long sum_blocks(int n_seq, long rows, int D) { return rows / tile_rows(rows, D) + std::min(n_seq, 512); }
+int cluster_walkers(int n_seq, long blocks) { return (int)std::min<long>(n_seq, std::max(64L, 152 * 8 / blocks)); }
 
 // How sequences are taken by clusters, if they are: neighbouring groups of 128
 // bytes a token, and so many blocks that a thread's packets of the longest
@@ -1182,9 +1205,10 @@ long tile_slots(int n_seq, long rows, int D) { return rows / tile_rows(rows, D) 
 struct ClusterShape {
     int per_block, blocks, smem;
 };
+int groups_per_cluster(int D, int G, int el) { return std::min(G, std::max(1, 128 / (D / G * el))); }
 ClusterShape cluster_shape(const GroupNormProblem &p, int V, int el, bool bwd) {
     const int w = p.D / p.G, arrays = bwd ? (p.gate ? 3 : 2) : 1;
-    ClusterShape c = {std::min(p.G, std::max(1, 128 / (w * el))), 0, 0};
+    ClusterShape c = {groups_per_cluster(p.D, p.G, el), 0, 0};
     const long packets = (long)c.per_block * (w / V), column_blocks = (p.G + c.per_block - 1) / c.per_block;
     if (packets > kThreads || p.n_seq * column_blocks * 8 > 0x7fffffffL) return c;
     const long lanes = kThreads / packets, longest = p.cu ? p.rows : p.T;
@@ -1327,13 +1351,13 @@ cudaError_t params(const GroupNormProblem &p, const float *part, long lanes, cud
 }
 
 template <typename T, int V, bool GATE, bool BWD>
-cudaError_t cluster_launch(const GroupNormProblem &p, const ClusterShape &c, float *prm, cudaStream_t st) {
+cudaError_t cluster_launch(const GroupNormProblem &p, const ClusterShape &c, int walkers, float *prm, cudaStream_t st) {
     const auto kernel = seq_cluster_kernel<T, V, GATE, BWD>;
     // (the largest of the shapes; below 48 KiB with the static arrays nothing need be asked)
     const cudaError_t err = allow_shared<seq_cluster_kernel<T, V, GATE, BWD>>(176 * 1024);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long)p.n_seq * ((p.G + c.per_block - 1) / c.per_block) * c.blocks));
+    cfg.gridDim = dim3((unsigned)((long)walkers * ((p.G + c.per_block - 1) / c.per_block) * c.blocks));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = c.smem;
     cfg.stream = st;
@@ -1343,7 +1367,7 @@ cudaError_t cluster_launch(const GroupNormProblem &p, const ClusterShape &c, flo
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p, c.per_block, c.blocks, prm);
+    return cudaLaunchKernelEx(&cfg, kernel, p, c.per_block, c.blocks, walkers, prm);
 }
 
 template <typename T, int V, bool GATE>
@@ -1362,8 +1386,10 @@ cudaError_t run(const GroupNormProblem &p, bool bwd, cudaStream_t st) {
     const ClusterShape c = cluster_shape(p, V, (int)sizeof(T), bwd);
     if (c.blocks) {
         float *prm = bwd && (p.dw || p.dbias) ? reinterpret_cast<float *>(p.ws) : nullptr;
-        err = bwd ? cluster_launch<T, V, GATE, true>(p, c, prm, st) : cluster_launch<T, V, GATE, false>(p, c, prm, st);
-        return bwd && err == cudaSuccess ? params(p, prm, (long)p.n_seq * c.blocks, st) : err;
+        if (!bwd) return cluster_launch<T, V, GATE, false>(p, c, p.n_seq, prm, st);
+        const int walkers = cluster_walkers(p.n_seq, (p.G + c.per_block - 1) / c.per_block * c.blocks);
+        err = cluster_launch<T, V, GATE, true>(p, c, walkers, prm, st);
+        return err == cudaSuccess ? params(p, prm, (long)walkers * c.blocks, st) : err;
     }
     const int rows = tile_rows(p.rows, p.D), gpb = groups_per_block(p.D, p.G, V);
     const long slots = p.cu ? tile_slots(p.n_seq, p.rows, p.D) : (long)p.n_seq * ((p.T + rows - 1) / rows);
@@ -1384,11 +1410,12 @@ cudaError_t run(const GroupNormProblem &p, bool bwd, cudaStream_t st) {
         return follow(seq_apply_kernel<T, V, GATE>, grid, kThreads, st, p, rows, gpb, stats);
     }
     float *prm = p.dw || p.dbias ? reinterpret_cast<float *>(ws) : nullptr;
-    seq_sums_kernel<T, V, GATE><<<grid, kThreads, 0, st>>>(p, rows, gpb, part, prm);
+    const long summed = std::min(slots, sum_blocks(p.n_seq, p.rows, p.D));
+    seq_sums_kernel<T, V, GATE><<<dim3((unsigned)summed, grid.y), kThreads, 0, st>>>(p, rows, gpb, (int)slots, part, prm);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
     if ((err = follow(seq_means_kernel, dim3(joins), kThreads, st, p, rows, part, second)) != cudaSuccess) return err;
     if ((err = follow(seq_dx_kernel<T, V, GATE>, grid, kThreads, st, p, rows, gpb, second)) != cudaSuccess) return err;
-    return params(p, prm, slots, st);
+    return params(p, prm, summed, st);
 }
 
 template <typename T, int V>
@@ -1433,9 +1460,12 @@ size_t group_norm_fwd_workspace(int n_seq, long rows, int D, int G, bool over_se
 size_t group_norm_bwd_workspace(int n_seq, long rows, int D, int G, bool over_sequence, mdn_dtype dtype) {
     if (rows == 0) return 0;
     if (!over_sequence) return round256(token_lanes_most(rows, D, G) * 2 * D * sizeof(float));
-    // (clusters leave a row of sums for each of their blocks, eight at most)
-    return group_norm_fwd_workspace(n_seq, rows, D, G, true, dtype) +
-           round256(std::max(tile_slots(n_seq, rows, D), 8L * n_seq) * 2 * D * sizeof(float));
+    // (a cluster has eight blocks at most)
+    const int per_block = groups_per_cluster(D, G, dtype == MDN_BF16 ? 2 : 4);
+    long most = sum_blocks(n_seq, rows, D);
+    for (long blocks = 1; blocks <= 8; blocks *= 2)
+        most = std::max(most, cluster_walkers(n_seq, (G + per_block - 1) / per_block * blocks) * blocks);
+    return group_norm_fwd_workspace(n_seq, rows, D, G, true, dtype) + round256(most * 2 * D * sizeof(float));
 }
 
 }  // namespace mdn

@@ -80,3 +80,12 @@ def test_without_sequences_nothing_happens(rec):
 def test_with_tokens_kernels_run(rec):
     launched, copies = rec.copies("mdn_linear_attn_fwd", *_args(FWD, S_T=P(0xb000)))
     assert len([e for e in launched if e.limit is None]) == 1 and copies == []
+
+
+@pytest.mark.parametrize("n_seq,rows,D,G", [(32768, 32768, 2048, 16), (16384, 32768, 4096, 32), (1 << 20, 1 << 20, 512, 4),
+                                            (4096, 4096, 16384, 8), (30000, 90000, 96, 3)])
+def test_the_norms_gradient_over_many_sequences_asks_for_less_than_its_rows(n_seq, rows, D, G):
+    """Each sequence leaves sums of weight and bias behind: however many there are,
+    they take less than the bf16 rows themselves."""
+    size = mdn.lib().mdn_group_norm_bwd_workspace_size(n_seq, rows, D, G, 1, 1)
+    assert 0 < size <= rows * D * 2, size
