@@ -10,6 +10,7 @@ import momentum_delta_rule_gb300 as mdn
 from momentum_delta_rule_gb300 import build
 from tests import _launches
 from tests.test_abi_attn import BWD, FWD, P
+from tests.test_gpu_attn_paths import COMBINED, JOINED
 
 UNITS = ("mdn_attn_api", "mdn_attn", "mdn_attn_tc", "mdn_attn_tc32", "mdn_attn_step", "mdn_group_norm")
 WRAPPED = _launches.WRAPPED + ("cudaLaunchKernelExC", "cudaOccupancyMaxActiveBlocksPerMultiprocessorWithFlags", "cudaMemcpyAsync")
@@ -89,3 +90,33 @@ def test_the_norms_gradient_over_many_sequences_asks_for_less_than_its_rows(n_se
     they take less than the bf16 rows themselves."""
     size = mdn.lib().mdn_group_norm_bwd_workspace_size(n_seq, rows, D, G, 1, 1)
     assert 0 < size <= rows * D * 2, size
+
+
+def _kernels(rec, bwd, dtype, lens, H, Hkv, dk, dv, packed):
+    """Launches of a call by what they do: laying packed sequences out and summing
+    shared heads' gradients left out."""
+    n = len(lens)
+    B, T = (1, sum(lens)) if packed else (n, lens[0])
+    kw = dict(cu=P(0x9000) if packed else None, n_seq=n, B=B, T=T, H=H, Hkv=Hkv, dk=dk, dv=dv, ld_q=H * dk, ld_k=Hkv * dk,
+              ld_v=Hkv * dv, dtype=dtype)
+    call = ("mdn_linear_attn_bwd", *_args(BWD, ld_do=H * dv, **kw)) if bwd else ("mdn_linear_attn_fwd", *_args(FWD, **kw))
+    out = [e for e in rec.calls(*call) if e.limit is None]
+    if packed and out[0].grid == 1 and out[0].block == 1024:
+        out = out[1:]
+    return out[:-2] if bwd and H != Hkv else out
+
+
+@pytest.mark.parametrize("lens,H,Hkv,dk,dv,packed,where", JOINED)
+def test_where_segments_join_the_states_themselves(rec, lens, H, Hkv, dk, dv, packed, where):
+    # the segments' own states, then the outputs: nothing between them
+    for w in where:
+        out = _kernels(rec, w.startswith("bwd"), w.endswith("bf16"), lens, H, Hkv, dk, dv, packed)
+        assert len(out) == 2, w
+
+
+@pytest.mark.parametrize("lens,H,Hkv,dk,dv,packed,offset", COMBINED)
+def test_where_a_kernel_joins_the_states(rec, lens, H, Hkv, dk, dv, packed, offset):
+    for bwd in (False, True):
+        for dtype in (0, 1):
+            out = _kernels(rec, bwd, dtype, lens, H, Hkv, dk, dv, packed)
+            assert len(out) == 3 and out[1].grid == len(lens) * H
