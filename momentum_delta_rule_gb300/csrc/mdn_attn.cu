@@ -11,8 +11,8 @@ namespace mdn {
 // the blocks of a launch run in waves of 152, each of which fills its pipeline
 // once; a chunk's states alone take 0.55, a segment reads the states of those
 // before it, and the launch more costs what it costs.  (16384 tokens of 16 heads of
-// 128 bf16 columns: 93 us cut in 9, 340 whole.  Forward and gradients of 1531 fp32
-// tokens in 5 sequences, 6 heads on 3, 40 and 72 columns: 119, 138 whole.)
+// 128 bf16 columns: 108 us cut in 9, 116 in 8, 446 whole.  Forward and gradients of
+// 1531 fp32 tokens in 5 sequences, 6 heads on 3, 40 and 72 columns: 114, 135 whole.)
 int attn_segment(int n_seq, long T_total, int H, int passes, mdn_dtype dtype) {
     if (n_seq == 0 || T_total == 0) return 0;
     const bool wide = dtype == MDN_F32;

@@ -51,8 +51,8 @@ Space space(const Heads &s, bool packed, mdn_dtype dtype, bool bwd) {
 
 // Whether a kernel of its own joins the segments' states, rather than each block
 // those before its own: blocks read a state in 2.5 us, the kernel takes 8 and its
-// launch 2.  (16 heads of 128 over 16384 tokens in 9 segments: 102 us and 92; 64
-// over 2048 tokens in 2: 151 and 163.)
+// launch 2.  (16 heads of 128 over 16384 tokens in 9 segments: 118 us and 108; 64
+// over 2048 tokens in 2: 64 and 69.)
 bool many_segments(const Space &w, int n_seq, long L) { return L / n_seq > 3L * w.seg; }
 
 AttnProblem problem(const Heads &s, const Space &w, const float *log_decay, const int32_t *cu, int T, mdn_dtype dtype,

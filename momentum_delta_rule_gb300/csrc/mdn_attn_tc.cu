@@ -39,14 +39,16 @@
 // warp runs once a chunk waits for its instructions).  The issuers' are not: what
 // is added to a descriptor is known, two instructions an MMA (in loops the same
 // products took 154 us, up to 150 cycles an MMA).  Packed prompts of 32768 tokens in
-// 21 sequences, 16 heads of 128: 134 us (537 MB, 0.59 of the copy rate).  A chunk
-// takes some 3600 cycles.  Its products are 3040 cycles of the tensor pipe where
-// each runs by itself (MMA1 58 a step, MMA2 43, MMA3 77, MMA4 106), and its
-// operands, parts and rows 336 KB through shared memory, 2700 cycles at 128 bytes:
-// shared memory first, and with it every wait on a barrier.  Tried: four warps
-// that do nothing but split 133 (one long prompt 112 instead of 108, training 191
-// instead of 187); the split behind dZ, in one buffer, 145; one issuer in a fixed
-// order 159; MMA3 without the blocks that are zero 138.
+// 21 sequences, 16 heads of 128: 134 us, calls one behind another (537 MB, 0.59 of
+// the copy rate).  A sixth of that is fill and uneven ends; in between a chunk takes
+// some 3600 cycles.  No unit is full then (tensor pipe 43 % of the cycles, issue slots
+// 63 %, DRAM 49 %): its products are 3040 cycles where each runs by itself (MMA1 58 a
+// step, MMA2 43, MMA3 77, MMA4 106) but two issuers' are in turns and slower, a
+// barrier that is already complete takes 200 to 400 cycles to see, and the state's
+// warps do one thing after another: split, dZ, Z.  Tried: four warps that do nothing
+// but split 133 (one long prompt 112 instead of 109, training 191 instead of 187);
+// the split behind dZ, in one buffer, 145; one issuer in a fixed order 159; MMA3
+// without the blocks that are zero 138.
 // Every wait is bounded (1 s); on expiry the CTA records MDN_ERR_DEVICE_TIMEOUT,
 // drains its copies and MMAs, frees TMEM and returns.
 #include "mdn_attn_tc.cuh"

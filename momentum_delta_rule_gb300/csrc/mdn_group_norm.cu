@@ -11,9 +11,10 @@
 // Memory bound.  A token's group is read once: its elements stay in the
 // registers of a few threads, which take the same group of every so-manieth
 // token, so that weights and the parameters' sums stay in registers too.  With 16
-// groups of 128 bf16 columns and a gate, 32768 tokens take 85 us (403 MB: 0.70 of
-// the copy rate), forward and gradient of 16384 tokens 118 (0.50): the activation
+// groups of 128 bf16 columns and a gate, 32768 tokens take 81 us (403 MB: 0.73 of
+// the copy rate), forward and gradient of 16384 tokens 114 (0.52): the activation
 // and its derivative on the CUDA cores, at 24 and 16 warps a multiprocessor.
+// (Times here and below: calls one behind another, through the binding.)
 // Groups too wide for that are read again from the caches, in loops.
 // The groups of a sequence are read once where a cluster's shared memory holds
 // them, twice otherwise: the second time after the sums of tiles of its tokens
@@ -645,10 +646,9 @@ __device__ __forceinline__ Columns columns_of(const GroupNormProblem &p, int per
     return c;
 }
 
-// Sums or moments of the block's threads, group by group.  Every thread brings
-// the value of its packets, all of one group but in blocks of one group only.
+// take(g, packets of a group) for the block's groups g, one warp each.
 template <typename F>
-__device__ __forceinline__ void by_group(const GroupNormProblem &p, const Columns &c, int V, F take) {
+__device__ __forceinline__ void by_group(const Columns &c, F take) {
     const int warp = threadIdx.x >> 5, ppg = c.packets / c.groups;
     for (int g = warp; g < c.groups; g += kThreads / 32) take(g, ppg);
 }
@@ -727,7 +727,7 @@ __global__ void __launch_bounds__(kThreads) seq_stats_kernel(GroupNormProblem p,
     mom[1][threadIdx.x] = mean;
     mom[2][threadIdx.x] = m2;
     __syncthreads();
-    by_group(p, c, V, [&](int g, int ppg) {
+    by_group(c, [&](int g, int ppg) {
         const bool whole = c.packets >= kThreads && c.groups == 1;
         const int count = whole ? kThreads : ppg * c.lanes;
         const float center = mom[1][whole ? 0 : g * ppg];
@@ -884,7 +884,7 @@ seq_sums_kernel(GroupNormProblem p, int rows, int per_block, int slots, float2 *
         if (!some) continue;
         red[threadIdx.x] = s;
         __syncthreads();
-        by_group(p, c, V, [&](int g, int ppg) {
+        by_group(c, [&](int g, int ppg) {
             float2 a = make_float2(0.f, 0.f);
             const bool whole = c.packets >= kThreads && c.groups == 1;
             const int count = whole ? kThreads : ppg * c.lanes;
@@ -1199,9 +1199,9 @@ int cluster_walkers(int n_seq, long blocks) { return (int)std::min<long>(n_seq, 
 // bytes a token, and so many blocks that a thread's packets of the longest
 // sequence there can be fit shared memory, three blocks to a multiprocessor where
 // that goes.  (8 sequences of 2048 tokens of 2048 bf16 columns in 32 groups:
-// 47 us; with two blocks to a multiprocessor 52, in tiles 64.  Forward and
-// gradient of 1531 fp32 tokens of 330 columns in 6 groups and 5 sequences: 64,
-// and 84 in tiles.)
+// 44 us; with two blocks to a multiprocessor 46, in tiles 62.  Forward and
+// gradient of those 140, 142 and 203; of 1531 fp32 tokens of 330 columns in 6
+// groups and 5 sequences 50, 56 and 62.)
 struct ClusterShape {
     int per_block, blocks, smem;
 };
@@ -1242,7 +1242,7 @@ void spread(const GroupNormProblem &p, TokenShape &t, long most) {
 // The gradient's blocks: two of 256 threads to a multiprocessor, as many as are
 // there at once, since each lane of tokens leaves a row of the parameters' sums
 // behind.  (16384 tokens of 16 groups of 128 bf16 columns, gate: forward and
-// gradient 124 us; with one block 154, three 141, four 123.)
+// gradient 114 us; with one block 140, three 129, four 119.)
 TokenShape token_shape(const GroupNormProblem &p, int V, bool bwd) {
     TokenShape t;
     const long P = (p.D / p.G) / V;
@@ -1304,8 +1304,8 @@ cudaError_t token_launch(const GroupNormProblem &p, TokenShape t, float *part, b
     }
     // The forward takes two whole waves: blocks end at different times, and the
     // second one's fill the gaps.  (32768 tokens of 16 groups of 128 columns,
-    // gate.  bf16, three blocks to a multiprocessor at once: in all 5 96 us, 6 85,
-    // 7 98, 8 92, 12 90; fp32, four: 5 171, 6 150, 7 141, 8 134, 12 135.)
+    // gate.  bf16, three blocks to a multiprocessor at once: in all 5 92 us, 6 81,
+    // 7 93, 8 89, 12 85; fp32, four: 5 167, 6 146, 7 137, 8 130, 12 132.)
     spread(p, t, 1L << 30);
     if (t.blocks > 152) {
         int resident = 1;
