@@ -716,8 +716,8 @@ size_t mdn_linear_attn_bwd_workspace_size(int n_seq, int T_total, int H, int Hkv
  * the formulas' rounded to bf16 once, states as exact as in fp32.  fp32 rows are multiplied as three
  * bf16 parts each, as exactly as in fp32; their values are expected below 3e38.
  * Infinite and NaN rows reach what the formulas carry them to and, beyond that,
- * the other tokens of their sequence's run of 64 tokens, where they may appear
- * as NaN; no other sequence and no other head.
+ * the other tokens of their sequence's run of 64 tokens, those before them too;
+ * an infinity may appear as NaN.  They reach no other sequence and no other head.
  * Errors: as mdn_short_conv_fwd; MDN_ERR_UNSUPPORTED for dk or dv above 128.
  */
 mdn_status mdn_linear_attn_fwd(const void *q, const void *k, const void *v,
